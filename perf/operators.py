@@ -161,7 +161,7 @@ def prepare(case, seed):
     n = lay["offsets"].tolist()
     s["N"] = n[-1]
     s["cap"] = max(1, max(b - a for a, b in zip(n, n[1:])))
-    s["live"] = torch.tensor([e for e in range(El) if n[e + 1] > n[e]], dtype=torch.long, device=DEV)
+    s["live"] = torch.tensor([e for e in range(El) if n[e + 1] > n[e]] or [0], dtype=torch.long, device=DEV)
     if c["op"] == "experts":
         F = c["F"]
         for name, rows, K in (("w1", F, d), ("w3", F, d), ("w2", d, F)):
@@ -216,7 +216,7 @@ def _weight(codes, scales, live):
     El, rows, half = codes.shape
     codes = codes[live]
     q = torch.stack((codes & 15, codes >> 4), -1).reshape(-1, 2 * half)
-    sc = scales.reshape(-1, El, rows, 4)[:, live].permute(1, 2, 0, 3).reshape(q.shape[0], -1)
+    sc = scales.reshape(scales.shape[0], El, rows, 4)[:, live].permute(1, 2, 0, 3).reshape(q.shape[0], half // 16)
     return _values(q, sc).reshape(-1, rows, 2 * half)
 
 
