@@ -61,8 +61,10 @@ extern "C" {
 typedef enum {
   MOE_F32 = 0,   /* fp32 rows and weights, fp32 arithmetic */
   MOE_BF16 = 1,  /* bf16 rows and weights, fp32 accumulation, bf16 h and outputs */
-  MOE_MXFP8 = 2  /* bf16 token rows and outputs; the expert GEMMs in MXFP8: E4M3 elements
+  MOE_MXFP8 = 2, /* bf16 token rows and outputs; the expert GEMMs in MXFP8: E4M3 elements
                     with one E8M0 scale per 32 consecutive K values (see moe_mx_quantize) */
+  MOE_MXFP4 = 3  /* the same in MXFP4: E2M1 elements, two a byte, with the same scales (see
+                    moe_mx_quantize_to); forward only, for serving */
 } moe_dtype_t;
 
 typedef struct {
@@ -85,10 +87,10 @@ typedef struct {
  * i.e. one 32-bit word per (128-value K tile, row), K tiles outermost: [K/128][rows][4].
  * The grouped GEMM reads the words of 64 consecutive rows of one K tile at once.
  *
- * Block scales of MXFP8 expert weights (moe_mx_quantize of the bf16 weights), DEVICE
- * pointers, 4-byte aligned.  Used only when dtype is MOE_MXFP8, where the weight pointers
- * w1, w3, w2 hold E4M3 codes of the same [E_local][F][d] / [E_local][d][F] shapes (one byte
- * per value); each scale array covers the whole tensor as one matrix of E_local*F (or
+ * Block scales of MXFP8 or MXFP4 expert weights (moe_mx_quantize, moe_mx_quantize_to of the
+ * bf16 weights), DEVICE pointers, 4-byte aligned.  Used only when dtype is MOE_MXFP8 or
+ * MOE_MXFP4, where the weight pointers w1, w3, w2 hold codes of the same [E_local][F][d] /
+ * [E_local][d][F] shapes (one byte per value, or half a byte); each scale array covers the whole tensor as one matrix of E_local*F (or
  * E_local*d) rows. */
 typedef struct {
   const uint8_t* w1;   /* [d/128][E_local*F][4] */
@@ -143,6 +145,34 @@ int moe_mx_quantize(const void* src, int32_t src_dtype, int64_t rows, int32_t K,
                     uint8_t* scales, void* stream);
 
 /*
+ * moe_mx_quantize_to -- moe_mx_quantize for either block-scaled format (MOE_MXFP8 or
+ * MOE_MXFP4).  With MOE_MXFP8 it is moe_mx_quantize.  MOE_MXFP4 (OCP Microscaling v1.0):
+ * for every block of 32 consecutive values v of a row, amax = max |v|;
+ *   amax == 0: scale code 0 and 32 zero codes;
+ *   a NaN or an infinity among them: scale code 255 (E8M0's NaN) and 32 zero codes, which
+ *     moe_mx_dequantize and the expert GEMMs turn into NaN;
+ *   otherwise e = clamp(floor(log2 amax) - 2, -127, 127), scale code e + 127, and
+ *   code_i = E2M1(v_i / 2^e) rounded to nearest (ties to the even code), saturated to +-6.
+ * codes: [rows][K / 2] bytes, 16-byte aligned, value 2i of a row in the low half of byte i
+ * and value 2i + 1 in the high half; scales: as moe_mx_quantize, 4-byte aligned.
+ * K % 128 == 0 (else MOE_EALIGN).  Bit-exact.  rows == 0 launches nothing.
+ */
+int moe_mx_quantize_to(const void* src, int32_t src_dtype, int64_t rows, int32_t K, int32_t format, uint8_t* codes,
+                       uint8_t* scales, void* stream);
+
+/*
+ * moe_mx_dequantize -- the values that codes and scales of either format stand for:
+ *   dst[r][i] = element(code) * 2^(scale code - 127), NaN where the scale code is 255 (or an
+ *   E4M3 code is NaN).
+ * dst: [rows][K] of dst_dtype (MOE_BF16 or MOE_F32), 16-byte aligned; codes 16-byte, scales
+ * 4-byte aligned.  K % 128 == 0 (else MOE_EALIGN).  Exact wherever the value fits the type;
+ * a larger one becomes an infinity (as the largest scale codes can make it), and below
+ * the bf16 subnormals an E4M3 value is rounded to nearest even.
+ */
+int moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t format, int64_t rows, int32_t K, void* dst,
+                      int32_t dst_dtype, void* stream);
+
+/*
  * moe_layout -- routing and sort-free layout generation.
  *   [kucoin §01] the router picks several experts per token every step; the
  *   system counts each expert's tokens, decides where they land on the target and
@@ -179,6 +209,8 @@ int moe_layout(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t*
  * is quantised on its way (the moe_mx_quantize rule): xe receives [moe_max_pairs][d]
  * E4M3 codes and xe_scales their scale codes in the MXFP8 scale layout with
  * rows = moe_max_pairs ([d/128][moe_max_pairs][4], 4-byte aligned).
+ * MOE_MXFP4: the same with the moe_mx_quantize_to rule and codes of half a byte
+ * ([moe_max_pairs][d / 2]).
  * xe_scales is ignored for the other dtypes.
  */
 int moe_dispatch_pull(const moe_shape_t* s, const moe_placement_t* p, const void* const* x,
@@ -203,6 +235,11 @@ int moe_dispatch_pull(const moe_shape_t* s, const moe_placement_t* p, const void
  * error <= 5e-3; h is quantised from fp32, so an h code may differ from that reference's
  * by one E4M3 step where the value lies within fp32 rounding of the midpoint, and each
  * output element then lies within the effect of those steps plus one bf16 rounding.
+ * MOE_MXFP4: the same with E2M1 codes of half a byte throughout (xe, the weights, h); the
+ * products of 64 values are exact in the MFMA, so h and ye carry fp32 accumulation errors
+ * only.  d and F must be multiples of 128, and d * F < 2^32.  Accuracy against the fp64 forward
+ * on the dequantised operands: as stated for MXFP8, an h code may differ by one E2M1 step where
+ * h lies within its fp32 error of a midpoint; relative Frobenius error <= 5e-3.
  * xe_scales and w_scales are ignored for other dtypes.
  */
 int moe_expert_ffn(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t* ex,
@@ -228,7 +265,7 @@ int moe_expert_ffn(const moe_shape_t* s, const moe_placement_t* p, const moe_exe
  * x: NULL or R device pointers [T][d]; recv: R device pointers, each [T][k][d]; both
  *   16-byte aligned.  Other arguments, alignment and dtype rules as moe_expert_ffn.
  * Errors: MOE_EINVAL for a missing pull_src, slot_of or recv entry (or xe when x is NULL);
- *   MOE_EUNSUP for x != NULL with MOE_MXFP8 (its rows are quantised by the gather);
+ *   MOE_EUNSUP for x != NULL with MOE_MXFP8 or MOE_MXFP4 (their rows are quantised by the gather);
  *   otherwise as moe_expert_ffn.
  */
 int moe_expert_ffn_push(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t* ex,
@@ -268,9 +305,9 @@ int moe_combine_push(const moe_shape_t* s, const moe_placement_t* p, const void*
 
 /*
  * moe_forward -- the four calls above in order on one stream (the unfused,
- * multi-kernel path).  xe and ye are [moe_max_pairs][d] staging rows (xe holds E4M3
- * codes and xe_scales their scales for MOE_MXFP8; xe_scales and w_scales are ignored
- * for the other dtypes).
+ * multi-kernel path).  xe and ye are [moe_max_pairs][d] staging rows (xe holds the
+ * codes and xe_scales their scales for MOE_MXFP8 and MOE_MXFP4; xe_scales and w_scales are
+ * ignored for the other dtypes).
  */
 int moe_forward(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t* ex,
                 const float* const* logits, const void* const* x, const void* w1, const void* w3,
@@ -283,9 +320,9 @@ int moe_forward(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t
  * moe_forward_fused -- moe_layout, moe_expert_ffn_push and moe_weighted_merge in order on one
  *   stream: for fp32 and bf16 the pull is fused into the gate/up GEMM and the push into the
  *   down GEMM, so neither the dispatched rows (xe) nor the expert outputs (ye) are staged;
- *   for MXFP8, moe_dispatch_pull (which quantises the rows) runs first and only the push is
- *   fused.  recv (local-pair entries) and y are bit-identical to moe_forward's.  Arguments
- *   as moe_forward without ye; xe and xe_scales are only used (and required) for MXFP8.
+ *   for MXFP8 and MXFP4, moe_dispatch_pull (which quantises the rows) runs first and only the
+ *   push is fused.  recv (local-pair entries) and y are bit-identical to moe_forward's.  Arguments
+ *   as moe_forward without ye; xe and xe_scales are only used (and required) for MXFP8 and MXFP4.
  *   moe_backward reads xe and ye, which this call does not write: a caller that runs the
  *   backward after it runs moe_forward instead, or moe_forward_persistent and then
  *   moe_backward_ring (which reads the expert outputs from recv and the token rows from the
@@ -297,6 +334,74 @@ int moe_forward_fused(const moe_shape_t* s, const moe_placement_t* p, const moe_
                       void* const* recv, void* const* y, int32_t* topk_idx, float* topk_w, int32_t* counts,
                       int32_t* offsets, int32_t* pull_src, int32_t* slot_of, void* ws, size_t ws_bytes,
                       void* stream);
+
+/*
+ * The layer for GIVEN choices and gate weights -- for routers other than moe_layout's softmax
+ * over the top-k logits (sigmoid or biased scores, grouped selection, capacity drops), and for
+ * sources that lie on this GPU: the expert rows are merged where the FFN left them, without
+ * the receive buffers recv that moe_combine_push writes and reads again.  The moves are those
+ * of [kucoin §01-03] (one expert's rows contiguous, results back at their tokens, the weighted
+ * merge).  fp32 rows with MOE_F32, bf16 rows with every other dtype.
+ */
+
+/*
+ * moe_layout_choices -- moe_layout without its routing: counts, offsets, pull_src, slot_of and
+ * the tables in ws (read by moe_dispatch_pull, moe_expert_ffn and the calls below) for
+ *   topk_idx[r][t][j]: an expert id in [0, E), or -1 for no expert (a dropped pair, a padded
+ *     token: any number of them, anywhere)                             [R][T][k] int32
+ * A -1 pair counts nowhere and its slot_of is -1.  Rows of one expert lie in ascending (r, t, j)
+ * order, bit-exact.  An id outside [-1, E), or one token naming an expert twice, sets
+ * MOE_EINVAL in the status word and the layout yields N = 0 and slot_of = -1 (counts are then
+ * unspecified), as a bad placement does.
+ */
+int moe_layout_choices(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t* ex, const int32_t* topk_idx,
+                       int32_t* counts, int32_t* offsets, int32_t* pull_src, int32_t* slot_of, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/*
+ * moe_combine_merge -- the expert rows back at their tokens with the gate weights applied:
+ *   y[r][t][:] = sum over ascending j with slot_of[r][t][j] >= 0 of
+ *                topk_w[r][t][j] * ye[slot_of[r][t][j]][:]
+ * fp32 accumulation, rounded once to the row type; exactly 0 for a token with no local pair.
+ * Deterministic; equal to moe_combine_push's y bit for bit.  ye: rows [0, N) of d elements (rows
+ * from N on, and the weights of pairs that are not local, are not read); topk_w: [R][T][k] fp32;
+ * y: R pointers [T][d].  ye and y 16-byte aligned.
+ */
+int moe_combine_merge(const moe_shape_t* s, const moe_placement_t* p, const void* ye, const int32_t* slot_of,
+                      const float* topk_w, void* const* y, void* stream);
+
+/*
+ * moe_combine_merge_backward -- its gradient for L = sum over (r, t) of <dy[r][t], y[r][t]>:
+ *   dye[s][:] = topk_w[r][t][j] * dy[r][t][:]  (rounded once) for the pair with slot_of == s;
+ *   dtopk_w[r][t][j] = <dy[r][t], ye[s]>       (fp32), 0 for a pair that is not local.
+ * Rows of dye from N on are left as they are.  dye may not overlap ye.  Deterministic.
+ * For the bf16 expert backward (moe_expert_ffn_backward), dye goes to the place that
+ * moe_backward_rows_info names.  Buffers 16-byte aligned.
+ */
+int moe_combine_merge_backward(const moe_shape_t* s, const moe_placement_t* p, const void* const* dy, const void* ye,
+                               const int32_t* slot_of, const float* topk_w, void* dye, float* dtopk_w, void* stream);
+
+/*
+ * moe_dispatch_pull_backward -- the gradient of moe_dispatch_pull's copies: dx[r][t][:] = sum
+ * over ascending j with slot_of[r][t][j] >= 0 of dxe[slot_of[r][t][j]][:], fp32 accumulation,
+ * rounded once; exactly 0 for a token with no local pair.  Deterministic.
+ */
+int moe_dispatch_pull_backward(const moe_shape_t* s, const moe_placement_t* p, const void* dxe, const int32_t* slot_of,
+                               void* const* dx, void* stream);
+
+/*
+ * moe_forward_choices -- moe_layout_choices, moe_dispatch_pull, moe_expert_ffn and
+ * moe_combine_merge in order on one stream, for every dtype.  Arguments as moe_forward, with
+ * the choices and their weights as inputs and without logits and recv; every stage's arguments
+ * are checked before the first launch.  xe, ye and pull_src need [moe_max_pairs] rows, of which
+ * [0, N) are touched (the scales in xe_scales keep moe_max_pairs rows a plane); a caller who
+ * knows N may pass N rows of ye and pull_src.
+ */
+int moe_forward_choices(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t* ex, const int32_t* topk_idx,
+                        const float* topk_w, const void* const* x, const void* w1, const void* w3, const void* w2,
+                        const moe_mx_scales_t* w_scales, void* xe, uint8_t* xe_scales, void* ye, void* const* y,
+                        int32_t* counts, int32_t* offsets, int32_t* pull_src, int32_t* slot_of, void* ws,
+                        size_t ws_bytes, void* stream);
 
 /*
  * moe_forward_persistent -- the whole share with dispatch, expert FFN and combine in one
@@ -351,7 +456,7 @@ int moe_forward_fused(const moe_shape_t* s, const moe_placement_t* p, const moe_
  * ring holds each pipeline's first chunks in layout order (all of them when the ring is large
  * enough), and the workspace records which slot holds which chunk, for moe_backward_ring.
  * Results are bit-identical to the layout order.
- * Errors: MOE_EUNSUP for an fp32 dtype, minibatch_rows not in {64, 128, 256}, or a device
+ * Errors: MOE_EUNSUP for an fp32 or MXFP4 dtype, minibatch_rows not in {64, 128, 256}, or a device
  * where one workgroup per CU cannot be resident; MOE_EINVAL for a missing MXFP8 w_scales or
  * when comm_cus leaves no CU for compute; MOE_EALIGN for misaligned scales; MOE_ENOSPC for a
  * ring below one 256-row tile or a small workspace.
@@ -517,6 +622,14 @@ int moe_dispatch_push_reverse(const moe_shape_t* s, const moe_placement_t* p, co
                               const int32_t* slot_of, const int32_t* topk_idx, const float* topk_w, const void* ws,
                               size_t ws_bytes, void* const* recv, void* const* dx, float* const* dlogits, void* bws,
                               size_t bws_bytes, void* stream);
+
+/* Where moe_expert_ffn_backward reads the gradients of the expert outputs and leaves those of
+ * the expert rows: byte offsets in bws of the bf16 rows [moe_max_pairs][d].  With them the
+ * layer trains under any router: moe_combine_merge_backward (dye = bws + *dye_offset),
+ * moe_expert_ffn_backward, moe_dispatch_pull_backward (dxe = bws + *dxe_offset).  No kernel is
+ * launched; MOE_EINVAL for a bad shape or a null pointer, MOE_EUNSUP for a dtype other than
+ * bf16. */
+int moe_backward_rows_info(const moe_shape_t* s, const moe_placement_t* p, size_t* dye_offset, size_t* dxe_offset);
 
 /*
  * moe_backward -- the three calls above in order on one stream, after moe_forward ran with

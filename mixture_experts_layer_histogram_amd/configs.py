@@ -19,7 +19,7 @@ class MoEConfig:
     E_local: int
     k: int
     F: int
-    dtype: str = "bf16"          # "f32" | "bf16" | "mxfp8"
+    dtype: str = "bf16"          # "f32" | "bf16" | "mxfp8" | "mxfp4"
     load: str = "router"         # "router": logits = x @ W_r ; "skew": Zipf/Gumbel logits
     zipf_s: float = 1.2
     tau: float = 0.5

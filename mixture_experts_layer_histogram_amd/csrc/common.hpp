@@ -59,6 +59,9 @@ struct WsLayout {
 
 inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
+// MXFP4 h staging: where the block scales lie behind the codes of max_pairs rows of F values
+inline size_t mx4_h_scales_offset(int64_t max_pairs, int F) { return align256(size_t(max_pairs) * (F / 2)); }
+
 inline WsLayout ws_layout(const moe_shape_t& s, int32_t E_local) {
   WsLayout w{};
   const int64_t tokens = int64_t(s.R) * s.T;
@@ -76,9 +79,11 @@ inline WsLayout ws_layout(const moe_shape_t& s, int32_t E_local) {
   w.blockbase = o;   o = align256(o + size_t(w.nb) * E_local * 4);
   // persistent-path control block (counters, task tables, one epoch word per ring slot)
   w.pctrl = o;       o = align256(o + size_t(sched::ctrl_layout(w.max_mtiles, kMaxRingSlots).words) * 4);
-  // h staging: fp32/bf16 rows, or MXFP8 codes followed (256-aligned) by their block scales
+  // h staging: fp32/bf16 rows, or MXFP8 / MXFP4 codes followed (256-aligned) by their block scales
   const size_t hbytes = (s.dtype == MOE_MXFP8)
                             ? align256(size_t(w.max_pairs) * s.F) + size_t(w.max_pairs) * (s.F / 32)
+                        : (s.dtype == MOE_MXFP4)
+                            ? mx4_h_scales_offset(w.max_pairs, s.F) + size_t(w.max_pairs) * (s.F / 32)
                             : size_t(w.max_pairs) * s.F * esz;
   w.hbuf = o;        o = align256(o + hbytes);
   // per local pair: the address of its recv row (the push fused into the down GEMM)

@@ -157,8 +157,10 @@ __device__ int block_excl_scan_1024(int v, int* tmp16, int* total) {
   return excl;
 }
 
+// choices: blockbase[b * El] holds, on entry, whether block b's given choices are invalid
+// (choices_hist_kernel); they are all read before blockbase is written
 __global__ __launch_bounds__(1024) void layout_scan_kernel(
-    const int32_t* __restrict__ e2l, int E, int El, int nb, int bm, int mb,
+    const int32_t* __restrict__ e2l, int E, int El, int nb, int bm, int mb, bool choices,
     const int32_t* __restrict__ blockhist, int32_t* __restrict__ blockbase,
     int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ l2g,
     int32_t* __restrict__ mtile_base, int32_t* __restrict__ chunk_base, int32_t* __restrict__ ctrl) {
@@ -197,6 +199,9 @@ __global__ __launch_bounds__(1024) void layout_scan_kernel(
   __syncthreads();
   for (int l = tid; l < El; l += 1024)
     if (seen[l] != 1) atomicOr(&bad, 1);
+  if (choices)
+    for (int b = tid; b < nb; b += 1024)
+      if (blockbase[size_t(b) * El]) atomicOr(&bad, 1);
   __syncthreads();
   if (bad) {
     for (int l = tid; l <= El; l += 1024) {
@@ -307,7 +312,10 @@ __global__ __launch_bounds__(64) void slot_assign_kernel(
     const int64_t p = pb + lane;
     const bool inr = p < p1;
     int l = -1;
-    if (inr && ok) l = map[topk_idx[p]];
+    if (inr && ok) {
+      const int e = topk_idx[p];              // ok: every choice lies in [-1, E)
+      if (e >= 0) l = map[e];
+    }
     const int key = l + 1;
     unsigned long long m = __ballot(l >= 0);
     for (int b = 0; b < nbits; ++b) {
@@ -341,6 +349,26 @@ static void launch_topk(dim3 grid, hipStream_t st, const RankPtrs<const float*>&
                      topk_w, blockhist);
 }
 
+hipError_t launch_choices_hist(const moe_shape_t& s, const int32_t* idx, int32_t* blockhist, int32_t* bad, int El,
+                               int nb, hipStream_t st);
+
+// scan and slots, from the choices and their block histograms
+static hipError_t launch_slots(const moe_shape_t& s, const int32_t* e2l, int El, int mb, const int32_t* topk_idx,
+                               int32_t* counts, int32_t* offsets, int32_t* pull_src, int32_t* slot_of, char* ws,
+                               const WsLayout& L, bool choices, hipStream_t st) {
+  int32_t* blockhist = reinterpret_cast<int32_t*>(ws + L.blockhist);
+  int32_t* blockbase = reinterpret_cast<int32_t*>(ws + L.blockbase);
+  int32_t* ctrl = reinterpret_cast<int32_t*>(ws + L.ctrl);
+  const int bm = (s.dtype == MOE_F32) ? kF32BM : kGemmBM;
+  hipLaunchKernelGGL(layout_scan_kernel, dim3(1 + (s.E + 63) / 64), dim3(1024), 0, st, e2l, s.E, El,
+                     L.nb, bm, mb, choices, blockhist, blockbase, counts, offsets,
+                     reinterpret_cast<int32_t*>(ws + L.l2g), reinterpret_cast<int32_t*>(ws + L.mtile_base),
+                     reinterpret_cast<int32_t*>(ws + L.chunk_base), ctrl);
+  hipLaunchKernelGGL(slot_assign_kernel, dim3(L.nb), dim3(64), 0, st, topk_idx, e2l, s.R, s.T, s.E, s.k, El,
+                     blockbase, ctrl, slot_of, pull_src);
+  return hipGetLastError();
+}
+
 hipError_t launch_layout(const moe_shape_t& s, const int32_t* e2l, int El, int mb,
                          const float* const* logits, int32_t* topk_idx, float* topk_w, int32_t* counts,
                          int32_t* offsets, int32_t* pull_src, int32_t* slot_of, char* ws,
@@ -348,8 +376,6 @@ hipError_t launch_layout(const moe_shape_t& s, const int32_t* e2l, int El, int m
   RankPtrs<const float*> lp{};
   for (int r = 0; r < s.R; ++r) lp.p[r] = logits[r];
   int32_t* blockhist = reinterpret_cast<int32_t*>(ws + L.blockhist);
-  int32_t* blockbase = reinterpret_cast<int32_t*>(ws + L.blockbase);
-  int32_t* ctrl = reinterpret_cast<int32_t*>(ws + L.ctrl);
   const dim3 grid(L.nb);
   const int vpl_need = (s.E + 15) / 16;
   if (vpl_need <= 1) launch_topk<1>(grid, st, lp, s, topk_idx, topk_w, blockhist);
@@ -360,14 +386,17 @@ hipError_t launch_layout(const moe_shape_t& s, const int32_t* e2l, int El, int m
   else if (vpl_need <= 32) launch_topk<32>(grid, st, lp, s, topk_idx, topk_w, blockhist);
   else launch_topk<64>(grid, st, lp, s, topk_idx, topk_w, blockhist);
 
-  const int bm = (s.dtype == MOE_F32) ? kF32BM : kGemmBM;
-  hipLaunchKernelGGL(layout_scan_kernel, dim3(1 + (s.E + 63) / 64), dim3(1024), 0, st, e2l, s.E, El,
-                     L.nb, bm, mb, blockhist, blockbase, counts, offsets,
-                     reinterpret_cast<int32_t*>(ws + L.l2g), reinterpret_cast<int32_t*>(ws + L.mtile_base),
-                     reinterpret_cast<int32_t*>(ws + L.chunk_base), ctrl);
-  hipLaunchKernelGGL(slot_assign_kernel, grid, dim3(64), 0, st, topk_idx, e2l, s.R, s.T, s.E, s.k, El,
-                     blockbase, ctrl, slot_of, pull_src);
-  return hipGetLastError();
+  return launch_slots(s, e2l, El, mb, topk_idx, counts, offsets, pull_src, slot_of, ws, L, false, st);
+}
+
+// the layout of given choices: no routing
+hipError_t launch_layout_choices(const moe_shape_t& s, const int32_t* e2l, int El, int mb, const int32_t* topk_idx,
+                                 int32_t* counts, int32_t* offsets, int32_t* pull_src, int32_t* slot_of, char* ws,
+                                 const WsLayout& L, hipStream_t st) {
+  const hipError_t e = launch_choices_hist(s, topk_idx, reinterpret_cast<int32_t*>(ws + L.blockhist),
+                                           reinterpret_cast<int32_t*>(ws + L.blockbase), El, L.nb, st);
+  if (e != hipSuccess) return e;
+  return launch_slots(s, e2l, El, mb, topk_idx, counts, offsets, pull_src, slot_of, ws, L, true, st);
 }
 
 }  // namespace moe

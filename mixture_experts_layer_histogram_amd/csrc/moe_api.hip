@@ -74,11 +74,31 @@ hipError_t launch_gemm1_bwd_mx(const uint8_t* xe, const uint8_t* xes, const uint
                                const uint8_t* w1s, const uint8_t* w3s, const uint16_t* dh, uint16_t* h, uint16_t* dab,
                                uint8_t* dabq, uint8_t* dabs, int d, int F, int64_t nmax, const int32_t* offsets,
                                const int32_t* mtb, const int32_t* ctrl, int El, int cus, hipStream_t st);
+hipError_t launch_layout_choices(const moe_shape_t& s, const int32_t* e2l, int El, int mb, const int32_t* topk_idx,
+                                 int32_t* counts, int32_t* offsets, int32_t* pull_src, int32_t* slot_of, char* ws,
+                                 const WsLayout& L, hipStream_t st);
+hipError_t launch_merge_rows(const moe_shape_t& s, const void* rows, const int32_t* slot_of, const float* w,
+                             void* const* y, int cus, hipStream_t st);
+hipError_t launch_merge_rows_bwd(const moe_shape_t& s, const void* const* dy, const void* ye, const int32_t* slot_of,
+                                 const float* w, void* dye, float* dw, int cus, hipStream_t st);
+hipError_t launch_mx4_quantize(const void* src, int src_dtype, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
+                               int cus, hipStream_t st);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int format, int64_t rows, int K, void* dst,
+                                int dst_dtype, int cus, hipStream_t st);
+hipError_t launch_dispatch_mx4(const moe_shape_t& s, const void* const* x, const int32_t* pull_src, uint8_t* xe,
+                               uint8_t* xe_scales, int64_t nmax, const int32_t* ctrl, int cus, hipStream_t st);
+hipError_t launch_ffn_mx4(const moe_shape_t& s, int El, const uint8_t* xe, const uint8_t* xe_scales,
+                          const int32_t* offsets, const uint8_t* w1, const uint8_t* w3, const uint8_t* w2,
+                          const moe_mx_scales_t& w_scales, void* ye, char* ws, const WsLayout& L, int cus,
+                          hipStream_t st, const uint64_t* row_dst);
 }  // namespace moe
 
 using namespace moe;
 
 namespace {
+
+// expert GEMMs on block-scaled codes: the rows are quantised by the gather and need scale arrays
+bool is_mx(const moe_shape_t* s) { return s->dtype == MOE_MXFP8 || s->dtype == MOE_MXFP4; }
 
 int check_shape(const moe_shape_t* s, const moe_placement_t* p) {
   if (!s || !p) return MOE_EINVAL;
@@ -86,11 +106,12 @@ int check_shape(const moe_shape_t* s, const moe_placement_t* p) {
   if (s->E < 1 || s->E > 1024 || s->k < 1 || s->k > 16 || s->k > s->E) return MOE_EINVAL;
   if (p->E_local < 1 || p->E_local > s->E) return MOE_EINVAL;
   if (int64_t(s->R) * s->T * s->k >= (int64_t(1) << 31)) return MOE_EINVAL;
-  if (s->dtype != MOE_F32 && s->dtype != MOE_BF16 && s->dtype != MOE_MXFP8) return MOE_EINVAL;
+  if (s->dtype != MOE_F32 && s->dtype != MOE_BF16 && s->dtype != MOE_MXFP8 && s->dtype != MOE_MXFP4) return MOE_EINVAL;
   const int esz = s->dtype == MOE_F32 ? 4 : 2;
   if ((int64_t(s->d) * esz) % 16 || (int64_t(s->F) * esz) % 16) return MOE_EALIGN;
   if (s->dtype == MOE_BF16 && (s->d % kGemmBK || s->F % kGemmBK)) return MOE_EALIGN;
-  if (s->dtype == MOE_MXFP8 && (s->d % 128 || s->F % 128)) return MOE_EALIGN;   // one 128-value GEMM stage
+  if (is_mx(s) && (s->d % 128 || s->F % 128)) return MOE_EALIGN;   // one 128-value GEMM stage (MXFP4: half of one)
+  if (s->dtype == MOE_MXFP4 && int64_t(s->d) * s->F >= (int64_t(1) << 32)) return MOE_EINVAL;   // 32-bit tile offsets
   return MOE_OK;
 }
 
@@ -211,6 +232,33 @@ int moe_mx_quantize(const void* src, int32_t src_dtype, int64_t rows, int32_t K,
                                    static_cast<hipStream_t>(stream)));
 }
 
+int moe_mx_quantize_to(const void* src, int32_t src_dtype, int64_t rows, int32_t K, int32_t format, uint8_t* codes,
+                       uint8_t* scales, void* stream) {
+  if (format == MOE_MXFP8) return moe_mx_quantize(src, src_dtype, rows, K, codes, scales, stream);
+  if (format != MOE_MXFP4) return MOE_EINVAL;
+  if (src_dtype != MOE_BF16 && src_dtype != MOE_F32) return MOE_EINVAL;
+  if (rows < 0 || K < 1 || rows > (int64_t(1) << 40) / K) return MOE_EINVAL;
+  if (K % 128) return MOE_EALIGN;                // whole 32-bit scale words per row
+  if (!src || !codes) return MOE_EINVAL;
+  if (!aligned16(src) || !aligned16(codes)) return MOE_EALIGN;
+  if (const int rc = check_scales(scales)) return rc;
+  return hip_rc(launch_mx4_quantize(src, src_dtype, rows, K, codes, scales, cu_count(),
+                                    static_cast<hipStream_t>(stream)));
+}
+
+int moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t format, int64_t rows, int32_t K, void* dst,
+                      int32_t dst_dtype, void* stream) {
+  if (format != MOE_MXFP8 && format != MOE_MXFP4) return MOE_EINVAL;
+  if (dst_dtype != MOE_BF16 && dst_dtype != MOE_F32) return MOE_EINVAL;
+  if (rows < 0 || K < 1 || rows > (int64_t(1) << 40) / K) return MOE_EINVAL;
+  if (K % 128) return MOE_EALIGN;
+  if (!codes || !dst) return MOE_EINVAL;
+  if (!aligned16(codes) || !aligned16(dst)) return MOE_EALIGN;
+  if (const int rc = check_scales(scales)) return rc;
+  return hip_rc(launch_mx_dequantize(codes, scales, format, rows, K, dst, dst_dtype, cu_count(),
+                                     static_cast<hipStream_t>(stream)));
+}
+
 int moe_layout(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t* ex,
                const float* const* logits, int32_t* topk_idx, float* topk_w, int32_t* counts,
                int32_t* offsets, int32_t* pull_src, int32_t* slot_of, void* ws, size_t ws_bytes,
@@ -235,7 +283,7 @@ int moe_dispatch_pull(const moe_shape_t* s, const moe_placement_t* p, const void
   if (rc) return rc;
   if (!pull_src || !offsets) return MOE_EINVAL;
   if (!aligned16(xe)) return xe ? MOE_EALIGN : MOE_EINVAL;
-  if (s->dtype == MOE_MXFP8 && (rc = check_scales(xe_scales))) return rc;
+  if (is_mx(s) && (rc = check_scales(xe_scales))) return rc;
   if ((rc = check_ptr_table(x, s->R))) return rc;
   if ((rc = check_ws(s, p, ws, ws_bytes))) return rc;
   const WsLayout L = ws_layout(*s, p->E_local);
@@ -243,6 +291,9 @@ int moe_dispatch_pull(const moe_shape_t* s, const moe_placement_t* p, const void
   if (s->dtype == MOE_MXFP8)
     return hip_rc(launch_dispatch_mx(*s, x, pull_src, static_cast<uint8_t*>(xe), xe_scales, L.max_pairs, ctrl,
                                      cu_count(), static_cast<hipStream_t>(stream)));
+  if (s->dtype == MOE_MXFP4)
+    return hip_rc(launch_dispatch_mx4(*s, x, pull_src, static_cast<uint8_t*>(xe), xe_scales, L.max_pairs, ctrl,
+                                      cu_count(), static_cast<hipStream_t>(stream)));
   return hip_rc(launch_dispatch(*s, x, pull_src, static_cast<char*>(xe), ctrl, cu_count(),
                                 static_cast<hipStream_t>(stream)));
 }
@@ -256,7 +307,7 @@ int moe_expert_ffn(const moe_shape_t* s, const moe_placement_t* p, const moe_exe
   const void* bufs[] = {xe, w1, w3, w2, ye};
   for (const void* b : bufs)
     if (!aligned16(b)) return b ? MOE_EALIGN : MOE_EINVAL;
-  if (s->dtype == MOE_MXFP8 && ((rc = check_scales(xe_scales)) || (rc = check_w_scales(w_scales)))) return rc;
+  if (is_mx(s) && ((rc = check_scales(xe_scales)) || (rc = check_w_scales(w_scales)))) return rc;
   if ((rc = check_ws(s, p, ws, ws_bytes))) return rc;
   const WsLayout L = ws_layout(*s, p->E_local);
   if (s->dtype == MOE_MXFP8)
@@ -264,6 +315,11 @@ int moe_expert_ffn(const moe_shape_t* s, const moe_placement_t* p, const moe_exe
                                 static_cast<const uint8_t*>(w1), static_cast<const uint8_t*>(w3),
                                 static_cast<const uint8_t*>(w2), w_scales->w1, w_scales->w3, w_scales->w2, ye,
                                 static_cast<char*>(ws), L, cu_count(), static_cast<hipStream_t>(stream), nullptr));
+  if (s->dtype == MOE_MXFP4)
+    return hip_rc(launch_ffn_mx4(*s, p->E_local, static_cast<const uint8_t*>(xe), xe_scales, offsets,
+                                 static_cast<const uint8_t*>(w1), static_cast<const uint8_t*>(w3),
+                                 static_cast<const uint8_t*>(w2), *w_scales, ye, static_cast<char*>(ws), L, cu_count(),
+                                 static_cast<hipStream_t>(stream), nullptr));
   return hip_rc(launch_ffn(*s, p->E_local, xe, offsets, w1, w3, w2, ye, static_cast<char*>(ws), L, cu_count(),
                            static_cast<hipStream_t>(stream), nullptr, nullptr));
 }
@@ -276,12 +332,12 @@ int moe_expert_ffn_push(const moe_shape_t* s, const moe_placement_t* p, const mo
   int rc = check_shape(s, p);
   if (rc || (rc = check_ex(ex))) return rc;
   if (!offsets || !pull_src || !slot_of) return MOE_EINVAL;
-  if (x && s->dtype == MOE_MXFP8) return MOE_EUNSUP;      // MXFP8 rows are quantised by the gather
+  if (x && is_mx(s)) return MOE_EUNSUP;      // MXFP8 and MXFP4 rows are quantised by the gather
   const void* bufs[] = {x ? w1 : xe, w1, w3, w2};
   for (const void* b : bufs)
     if (!aligned16(b)) return b ? MOE_EALIGN : MOE_EINVAL;
   if (x && (rc = check_ptr_table(x, s->R))) return rc;
-  if (s->dtype == MOE_MXFP8 && ((rc = check_scales(xe_scales)) || (rc = check_w_scales(w_scales)))) return rc;
+  if (is_mx(s) && ((rc = check_scales(xe_scales)) || (rc = check_w_scales(w_scales)))) return rc;
   if ((rc = check_ptr_table(recv, s->R))) return rc;
   if ((rc = check_ws(s, p, ws, ws_bytes))) return rc;
   const WsLayout L = ws_layout(*s, p->E_local);
@@ -297,6 +353,10 @@ int moe_expert_ffn_push(const moe_shape_t* s, const moe_placement_t* p, const mo
                                 static_cast<const uint8_t*>(w1), static_cast<const uint8_t*>(w3),
                                 static_cast<const uint8_t*>(w2), w_scales->w1, w_scales->w3, w_scales->w2, nullptr,
                                 w, L, cu_count(), st, dst));
+  if (s->dtype == MOE_MXFP4)
+    return hip_rc(launch_ffn_mx4(*s, p->E_local, static_cast<const uint8_t*>(xe), xe_scales, offsets,
+                                 static_cast<const uint8_t*>(w1), static_cast<const uint8_t*>(w3),
+                                 static_cast<const uint8_t*>(w2), *w_scales, nullptr, w, L, cu_count(), st, dst));
   return hip_rc(launch_ffn(*s, p->E_local, x ? nullptr : xe, offsets, w1, w3, w2, nullptr, w, L, cu_count(), st, dst,
                            src));
 }
@@ -339,7 +399,7 @@ int moe_forward(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t
   const void* bufs[] = {xe, ye, w1, w3, w2};
   for (const void* b : bufs)
     if (!aligned16(b)) return b ? MOE_EALIGN : MOE_EINVAL;
-  if (s->dtype == MOE_MXFP8 && ((rc = check_scales(xe_scales)) || (rc = check_w_scales(w_scales)))) return rc;
+  if (is_mx(s) && ((rc = check_scales(xe_scales)) || (rc = check_w_scales(w_scales)))) return rc;
   if ((rc = check_ptr_table(logits, s->R)) || (rc = check_ptr_table(x, s->R)) ||
       (rc = check_ptr_table(recv, s->R)) || (rc = check_ptr_table(y, s->R)))
     return rc;
@@ -364,7 +424,7 @@ int moe_forward_fused(const moe_shape_t* s, const moe_placement_t* p, const moe_
   // validate every stage's arguments before launching any of them
   if (!p->expert_to_local || !topk_idx || !topk_w || !counts || !offsets || !pull_src || !slot_of)
     return MOE_EINVAL;
-  const bool mx = s->dtype == MOE_MXFP8;      // only MXFP8 stages its rows (the gather quantises them)
+  const bool mx = is_mx(s);      // only MXFP8 and MXFP4 stage their rows (the gather quantises them)
   const void* bufs[] = {mx ? xe : w1, w1, w3, w2};
   for (const void* b : bufs)
     if (!aligned16(b)) return b ? MOE_EALIGN : MOE_EINVAL;
@@ -381,6 +441,73 @@ int moe_forward_fused(const moe_shape_t* s, const moe_placement_t* p, const moe_
                                 slot_of, recv, ws, ws_bytes, stream)))
     return rc;
   return moe_weighted_merge(s, p, slot_of, topk_w, recv, y, stream);
+}
+
+int moe_layout_choices(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t* ex, const int32_t* topk_idx,
+                       int32_t* counts, int32_t* offsets, int32_t* pull_src, int32_t* slot_of, void* ws, size_t ws_bytes,
+                       void* stream) {
+  int rc = check_shape(s, p);
+  if (rc || (rc = check_ex(ex))) return rc;
+  if (!p->expert_to_local || !topk_idx || !counts || !offsets || !pull_src || !slot_of) return MOE_EINVAL;
+  if ((rc = check_ws(s, p, ws, ws_bytes))) return rc;
+  return hip_rc(launch_layout_choices(*s, p->expert_to_local, p->E_local, minibatch_of(ex), topk_idx, counts, offsets,
+                                      pull_src, slot_of, static_cast<char*>(ws), ws_layout(*s, p->E_local),
+                                      static_cast<hipStream_t>(stream)));
+}
+
+int moe_combine_merge(const moe_shape_t* s, const moe_placement_t* p, const void* ye, const int32_t* slot_of,
+                      const float* topk_w, void* const* y, void* stream) {
+  int rc = check_shape(s, p);
+  if (rc) return rc;
+  if (!slot_of || !topk_w) return MOE_EINVAL;
+  if (!aligned16(ye)) return ye ? MOE_EALIGN : MOE_EINVAL;
+  if ((rc = check_ptr_table(y, s->R))) return rc;
+  return hip_rc(launch_merge_rows(*s, ye, slot_of, topk_w, y, cu_count(), static_cast<hipStream_t>(stream)));
+}
+
+int moe_combine_merge_backward(const moe_shape_t* s, const moe_placement_t* p, const void* const* dy, const void* ye,
+                               const int32_t* slot_of, const float* topk_w, void* dye, float* dtopk_w, void* stream) {
+  int rc = check_shape(s, p);
+  if (rc) return rc;
+  if (!slot_of || !topk_w || !dtopk_w) return MOE_EINVAL;
+  const void* bufs[] = {ye, dye};
+  for (const void* b : bufs)
+    if (!aligned16(b)) return b ? MOE_EALIGN : MOE_EINVAL;
+  if ((rc = check_ptr_table(dy, s->R))) return rc;
+  return hip_rc(launch_merge_rows_bwd(*s, dy, ye, slot_of, topk_w, dye, dtopk_w, cu_count(),
+                                      static_cast<hipStream_t>(stream)));
+}
+
+int moe_dispatch_pull_backward(const moe_shape_t* s, const moe_placement_t* p, const void* dxe, const int32_t* slot_of,
+                               void* const* dx, void* stream) {
+  int rc = check_shape(s, p);
+  if (rc) return rc;
+  if (!slot_of) return MOE_EINVAL;
+  if (!aligned16(dxe)) return dxe ? MOE_EALIGN : MOE_EINVAL;
+  if ((rc = check_ptr_table(dx, s->R))) return rc;
+  return hip_rc(launch_merge_rows(*s, dxe, slot_of, nullptr, dx, cu_count(), static_cast<hipStream_t>(stream)));
+}
+
+int moe_forward_choices(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t* ex, const int32_t* topk_idx,
+                        const float* topk_w, const void* const* x, const void* w1, const void* w3, const void* w2,
+                        const moe_mx_scales_t* w_scales, void* xe, uint8_t* xe_scales, void* ye, void* const* y,
+                        int32_t* counts, int32_t* offsets, int32_t* pull_src, int32_t* slot_of, void* ws,
+                        size_t ws_bytes, void* stream) {
+  int rc = check_shape(s, p);
+  if (rc || (rc = check_ex(ex))) return rc;
+  // validate every stage's arguments before launching any of them
+  if (!p->expert_to_local || !topk_idx || !topk_w || !counts || !offsets || !pull_src || !slot_of) return MOE_EINVAL;
+  const void* bufs[] = {xe, ye, w1, w3, w2};
+  for (const void* b : bufs)
+    if (!aligned16(b)) return b ? MOE_EALIGN : MOE_EINVAL;
+  if (is_mx(s) && ((rc = check_scales(xe_scales)) || (rc = check_w_scales(w_scales)))) return rc;
+  if ((rc = check_ptr_table(x, s->R)) || (rc = check_ptr_table(y, s->R))) return rc;
+  if ((rc = check_ws(s, p, ws, ws_bytes))) return rc;
+  if ((rc = moe_layout_choices(s, p, ex, topk_idx, counts, offsets, pull_src, slot_of, ws, ws_bytes, stream))) return rc;
+  if ((rc = moe_dispatch_pull(s, p, x, pull_src, offsets, xe, xe_scales, ws, ws_bytes, stream))) return rc;
+  if ((rc = moe_expert_ffn(s, p, ex, xe, xe_scales, offsets, w1, w3, w2, w_scales, ye, ws, ws_bytes, stream)))
+    return rc;
+  return moe_combine_merge(s, p, ye, slot_of, topk_w, y, stream);
 }
 
 size_t moe_ring_slot_bytes(const moe_shape_t* s, const moe_exec_t* ex) {
@@ -557,6 +684,17 @@ int moe_forward_persistent(const moe_shape_t* s, const moe_placement_t* p, const
 size_t moe_backward_workspace_bytes(const moe_shape_t* s, const moe_placement_t* p) {
   if (check_shape(s, p) != MOE_OK || (s->dtype != MOE_BF16 && s->dtype != MOE_MXFP8)) return 0;
   return bwd_layout(*s, p->E_local).total;
+}
+
+int moe_backward_rows_info(const moe_shape_t* s, const moe_placement_t* p, size_t* dye_offset, size_t* dxe_offset) {
+  int rc = check_shape(s, p);
+  if (rc) return rc;
+  if (!dye_offset || !dxe_offset) return MOE_EINVAL;
+  if (s->dtype != MOE_BF16) return MOE_EUNSUP;
+  const BwdLayout B = bwd_layout(*s, p->E_local);
+  *dye_offset = B.dO;
+  *dxe_offset = B.dX;
+  return MOE_OK;
 }
 
 int moe_backward_prepare_mx(const moe_shape_t* s, const moe_placement_t* p, const void* w1, const void* w3,

@@ -1,0 +1,229 @@
+// MXFP4 quantiser, the dequantiser of both MX formats, and the pull dispatch that quantises
+// each gathered token row to MXFP4 (the pull itself: MoK article, kucoin.com/es "Cursor's MoK
+// logra un aumento del 2.37x ...", section 02).
+//
+// All are HBM-bound: per value the quantiser reads 2 (bf16) or 4 (fp32) bytes and writes
+// 17/32; the dequantiser the reverse.  A wave takes 512 consecutive values of one row at a
+// time (16 bytes of bf16 per lane, an aligned lane quad holds one 32-value block), a workgroup
+// 32 rows x 512 values, so that its scale words -- four K-tile planes of 32 rows -- leave as
+// four runs of 128 bytes instead of single words (each a partial write of its own line).
+#include "mx4.hpp"
+
+namespace moe {
+
+constexpr int kQuantRows = 32, kQuantCols = 512;
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void mx4_quantize_kernel(const void* __restrict__ src, int64_t rows, int K,
+                                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  __shared__ uint32_t s_sc[4][kQuantRows];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int nct = (K + kQuantCols - 1) / kQuantCols;
+  const int64_t tasks = (rows + kQuantRows - 1) / kQuantRows * nct;
+  uint32_t* const words = reinterpret_cast<uint32_t*>(scales);
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int64_t r0 = task / nct * kQuantRows;
+    const int ct = int(task % nct);
+    const int k = ct * kQuantCols + lane * 8;              // K % 128 == 0: whole 16-lane groups are in or out
+    const bool in = k < K;
+    const int nr = int(min(int64_t(kQuantRows), rows - r0));
+    constexpr int U = 8;                                   // rows in flight per wave
+    u32x4 v[U][BF16 ? 1 : 2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int rr = u * 4 + wave;
+#pragma unroll
+      for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
+        v[u][h] = u32x4{0, 0, 0, 0};
+        if (in && rr < nr)
+          v[u][h] = __builtin_nontemporal_load(
+              reinterpret_cast<const u32x4*>(static_cast<const char*>(src) + ((r0 + rr) * K + k) * (BF16 ? 2 : 4)) + h);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int rr = u * 4 + wave;
+      uint32_t sc;
+      uint32_t q;
+      if constexpr (BF16) q = mx4_quant8_bf16(v[u][0], &sc);          // all lanes: quad permutations inside
+      else q = mx4_quant8_f32(__builtin_bit_cast(f32x4, v[u][0]), __builtin_bit_cast(f32x4, v[u][1]), &sc);
+      const uint32_t sw = mx_scale_word(sc);
+      if (in && rr < nr) *reinterpret_cast<uint32_t*>(codes + ((r0 + rr) * K + k) / 2) = q;
+      if ((lane & 15) == 0) s_sc[lane >> 4][rr] = sw;
+    }
+    __syncthreads();
+    if (threadIdx.x < 4 * kQuantRows) {
+      const int p = threadIdx.x >> 5, rr = threadIdx.x & 31;
+      const int plane = ct * 4 + p;
+      if (plane < (K >> 7) && rr < nr) words[int64_t(plane) * rows + r0 + rr] = s_sc[p][rr];
+    }
+    __syncthreads();
+  }
+}
+
+// FP4: 4-bit codes, else E4M3 codes; BF16: bf16 values out, else fp32
+template <bool FP4, bool BF16>
+__global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* __restrict__ codes,
+                                                            const uint8_t* __restrict__ scales, int64_t rows, int K,
+                                                            void* __restrict__ dst) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int nct = (K + kQuantCols - 1) / kQuantCols;
+  const int64_t tasks = (rows + kQuantRows - 1) / kQuantRows * nct;
+  const uint32_t* const words = reinterpret_cast<const uint32_t*>(scales);
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int64_t r0 = task / nct * kQuantRows;
+    const int ct = int(task % nct);
+    const int k = ct * kQuantCols + lane * 8;
+    if (k >= K) continue;
+    const int nr = int(min(int64_t(kQuantRows), rows - r0));
+    constexpr int U = 8;
+    uint2 q[U];
+    uint32_t sw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int rr = u * 4 + wave;
+      q[u] = make_uint2(0, 0);
+      sw[u] = 0;
+      if (rr < nr) {
+        const int64_t at = (r0 + rr) * K + k;
+        if (FP4) q[u].x = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(codes + at / 2));
+        else {
+          q[u].x = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(codes + at));
+          q[u].y = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(codes + at) + 1);
+        }
+        sw[u] = words[int64_t(k >> 7) * rows + r0 + rr];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int rr = u * 4 + wave;
+      if (rr >= nr) continue;
+      const float f = e8m0_f32((sw[u] >> (8 * ((k >> 5) & 3))) & 0xFFu);
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f32v2 p;
+        if constexpr (FP4) {
+          p = i == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u].x, 1.0f, 0)
+              : i == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u].x, 1.0f, 1)
+              : i == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u].x, 1.0f, 2)
+                       : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u].x, 1.0f, 3);
+        } else {
+          const int w = int(i < 2 ? q[u].x : q[u].y);
+          p = (i & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8(w, true) : __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
+        }
+        o[2 * i] = p[0] * f;              // exact, or an infinity past the type's range
+        o[2 * i + 1] = p[1] * f;
+      }
+      char* d = static_cast<char*>(dst) + ((r0 + rr) * K + k) * (BF16 ? 2 : 4);
+      if constexpr (BF16) {
+        const u32x4 w = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                         pack_bf16x2(o[6], o[7])};
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(d));
+      } else {
+        __builtin_nontemporal_store(f32x4{o[0], o[1], o[2], o[3]}, reinterpret_cast<f32x4*>(d));
+        __builtin_nontemporal_store(f32x4{o[4], o[5], o[6], o[7]}, reinterpret_cast<f32x4*>(d) + 1);
+      }
+    }
+  }
+}
+
+// xe[s] / xe_scales[s] = MXFP4(x[pull_src[s].rank][pull_src[s].token]); one wave per row, as
+// the MXFP8 gather: a workgroup takes `cr` consecutive rows, keeps their scale words in LDS
+// and writes each K-tile plane's words as one run.
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 8))) void dispatch_pull_mx4_kernel(
+    RankPtrs<const char*> x, const int32_t* __restrict__ pull_src, const int32_t* __restrict__ ctrl,
+    uint8_t* __restrict__ xe, uint8_t* __restrict__ xes, int d, int64_t nmax, int cr) {
+  constexpr int UNROLL = 16;
+  extern __shared__ uint32_t s_sc[];           // [cr][nq + 1]
+  const int N = ctrl[kCtrlN];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n16 = d >> 3;            // 16-byte source vectors per row (d % 128 == 0: whole 16-lane groups)
+  const int nq = d >> 7;             // scale words (K-tile planes) per row
+  const int nchunks = (N + cr - 1) / cr;
+  uint32_t* xw = reinterpret_cast<uint32_t*>(xes);
+  for (int c = blockIdx.x; c < nchunks; c += gridDim.x) {
+    const int s0 = c * cr, rows = min(cr, N - s0);
+    for (int rr = wave; rr < rows; rr += 4) {
+      const int s = s0 + rr;
+      const int r = pull_src[2 * int64_t(s)];
+      const int t = pull_src[2 * int64_t(s) + 1];
+      const u32x4* src = reinterpret_cast<const u32x4*>(x.p[r] + int64_t(t) * d * 2);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(xe + int64_t(s) * (d >> 1));
+      for (int base = 0; base < n16; base += 64 * UNROLL) {
+        u32x4 v[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+          const int i = base + u * 64 + lane;
+          v[u] = u32x4{0, 0, 0, 0};
+          if (i < n16) v[u] = __builtin_nontemporal_load(src + i);
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+          const int i = base + u * 64 + lane;
+          uint32_t sc;
+          const uint32_t q = mx4_quant8_bf16(v[u], &sc);   // all lanes: quad permutations inside
+          const uint32_t sw = mx_scale_word(sc);            // all lanes: row shifts inside
+          if (i < n16) {
+            dst[i] = q;
+            if ((i & 15) == 0) s_sc[rr * (nq + 1) + (i >> 4)] = sw;
+          }
+        }
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < nq * cr; e += 256) {
+      const int q = e / cr, rr = e - q * cr;
+      if (rr < rows) xw[nmax * q + s0 + rr] = s_sc[rr * (nq + 1) + q];
+    }
+    __syncthreads();                 // the next chunk's waves overwrite s_sc
+  }
+}
+
+constexpr int kQuant4BlocksPerCU = 8, kGatherMx4BlocksPerCU = 4;
+
+static int quant_grid(int64_t rows, int K, int cus) {
+  const int64_t tasks = (rows + kQuantRows - 1) / kQuantRows * ((K + kQuantCols - 1) / kQuantCols);
+  return int(tasks < int64_t(cus) * kQuant4BlocksPerCU ? tasks : int64_t(cus) * kQuant4BlocksPerCU);
+}
+
+hipError_t launch_mx4_quantize(const void* src, int src_dtype, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
+                               int cus, hipStream_t st) {
+  if (rows == 0) return hipSuccess;
+  const dim3 grid(quant_grid(rows, K, cus));
+  if (src_dtype == MOE_BF16)
+    hipLaunchKernelGGL(mx4_quantize_kernel<true>, grid, dim3(256), 0, st, src, rows, K, codes, scales);
+  else
+    hipLaunchKernelGGL(mx4_quantize_kernel<false>, grid, dim3(256), 0, st, src, rows, K, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int format, int64_t rows, int K, void* dst,
+                                int dst_dtype, int cus, hipStream_t st) {
+  if (rows == 0) return hipSuccess;
+  const dim3 grid(quant_grid(rows, K, cus));
+  if (format == MOE_MXFP4) {
+    if (dst_dtype == MOE_BF16)
+      hipLaunchKernelGGL((mx_dequantize_kernel<true, true>), grid, dim3(256), 0, st, codes, scales, rows, K, dst);
+    else
+      hipLaunchKernelGGL((mx_dequantize_kernel<true, false>), grid, dim3(256), 0, st, codes, scales, rows, K, dst);
+  } else {
+    if (dst_dtype == MOE_BF16)
+      hipLaunchKernelGGL((mx_dequantize_kernel<false, true>), grid, dim3(256), 0, st, codes, scales, rows, K, dst);
+    else
+      hipLaunchKernelGGL((mx_dequantize_kernel<false, false>), grid, dim3(256), 0, st, codes, scales, rows, K, dst);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch_mx4(const moe_shape_t& s, const void* const* x, const int32_t* pull_src, uint8_t* xe,
+                               uint8_t* xe_scales, int64_t nmax, const int32_t* ctrl, int cus, hipStream_t st) {
+  RankPtrs<const char*> xp{};
+  for (int r = 0; r < s.R; ++r) xp.p[r] = static_cast<const char*>(x[r]);
+  const int cr = mx_chunk_rows(s.d);
+  hipLaunchKernelGGL(dispatch_pull_mx4_kernel, dim3(cus * kGatherMx4BlocksPerCU), dim3(256),
+                     size_t(cr) * ((s.d >> 7) + 1) * 4, st, xp, pull_src, ctrl, xe, xe_scales, s.d, nmax, cr);
+  return hipGetLastError();
+}
+
+}  // namespace moe

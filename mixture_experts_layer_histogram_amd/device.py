@@ -37,7 +37,7 @@ class DeviceProblem:
         self.w3 = _to_device_store(inp.w3_store, dt, self.device)
         self.w2 = _to_device_store(inp.w2_store, dt, self.device)
         self.w_scales = None
-        if dt == "mxfp8":
+        if dt in ("mxfp8", "mxfp4"):
             self.quantize_weights()
         self.nmax = moe.moe_max_pairs(self.shape, self.placement)
         self.ws_bytes = moe.moe_workspace_bytes(self.shape, self.placement, self.ex)
@@ -48,22 +48,23 @@ class DeviceProblem:
             self.alloc_outputs()
 
     def quantize_weights(self, stream=None):
-        """MXFP8 codes and block scales of the bf16 expert weights (the offline step, on the device)."""
+        """MXFP8 or MXFP4 codes and block scales of the bf16 expert weights (the offline step, on the device)."""
         torch = self.torch
+        per_byte = 2 if self.cfg.dtype == "mxfp4" else 1
         self.wq, self.ws_codes = [], []
         for w in (self.w1, self.w3, self.w2):
             K = w.shape[-1]
             rows = w.numel() // K
-            q = torch.empty(w.shape, dtype=torch.uint8, device=self.device)
+            q = torch.empty((*w.shape[:-1], K // per_byte), dtype=torch.uint8, device=self.device)
             sc = torch.empty((K // 128, rows, 4), dtype=torch.uint8, device=self.device)   # K-tile-major
-            moe.moe_mx_quantize(w, moe.MOE_BF16, rows, K, q, sc, stream=stream)
+            moe.moe_mx_quantize_to(w, moe.MOE_BF16, rows, K, self.shape.dtype, q, sc, stream=stream)
             self.wq.append(q)
             self.ws_codes.append(sc)
         self.w_scales = moe.MXScales(*(t.data_ptr() for t in self.ws_codes))
 
     def weights(self):
-        """The weight tensors the FFN reads: bf16/fp32 rows, or MXFP8 codes."""
-        return self.wq if self.cfg.dtype == "mxfp8" else (self.w1, self.w3, self.w2)
+        """The weight tensors the FFN reads: bf16/fp32 rows, or MXFP8 / MXFP4 codes."""
+        return self.wq if self.cfg.dtype in ("mxfp8", "mxfp4") else (self.w1, self.w3, self.w2)
 
     def alloc_outputs(self):
         torch, cfg, dev = self.torch, self.cfg, self.device
@@ -75,8 +76,8 @@ class DeviceProblem:
         self.offsets = torch.empty(cfg.E_local + 1, dtype=torch.int32, device=dev)
         self.pull_src = torch.empty((self.nmax, 2), dtype=torch.int32, device=dev)
         self.slot_of = torch.empty((R, T, k), dtype=torch.int32, device=dev)
-        if cfg.dtype == "mxfp8":
-            self.xe = torch.empty((self.nmax, d), dtype=torch.uint8, device=dev)
+        if cfg.dtype in ("mxfp8", "mxfp4"):
+            self.xe = torch.empty((self.nmax, d // 2 if cfg.dtype == "mxfp4" else d), dtype=torch.uint8, device=dev)
             self.xe_scales = torch.empty((d // 128, self.nmax, 4), dtype=torch.uint8, device=dev)
         else:
             self.xe = torch.empty((self.nmax, d), dtype=ed, device=dev)
@@ -127,6 +128,13 @@ class DeviceProblem:
         moe.moe_forward(self.shape, self.placement, self.ex, self.logits, self.x, w1, w3, w2, self.xe, self.ye,
                         self.recv, self.y, self.topk_idx, self.topk_w, self.counts, self.offsets, self.pull_src,
                         self.slot_of, self.ws, stream=stream, w_scales=self.w_scales, xe_scales=self.xe_scales)
+
+    def forward_choices(self, topk_idx, topk_w, stream=None):
+        """The layer for given choices and gate weights (this problem's logits and recv are not used)."""
+        w1, w3, w2 = self.weights()
+        moe.moe_forward_choices(self.shape, self.placement, self.ex, topk_idx, topk_w, self.x, w1, w3, w2, self.xe,
+                                self.ye, self.y, self.counts, self.offsets, self.pull_src, self.slot_of, self.ws,
+                                stream=stream, w_scales=self.w_scales, xe_scales=self.xe_scales)
 
     # ---- backward (bf16) ----
     def alloc_backward(self, dy_bits=None):

@@ -14,14 +14,16 @@ import os
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoe.so")
 
-MOE_F32, MOE_BF16, MOE_MXFP8 = 0, 1, 2
-DTYPE_CODE = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp8": MOE_MXFP8}
+MOE_F32, MOE_BF16, MOE_MXFP8, MOE_MXFP4 = 0, 1, 2, 3
+DTYPE_CODE = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp8": MOE_MXFP8, "mxfp4": MOE_MXFP4}
 MOE_MAX_RANKS = 64
 ERRORS = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_EALIGN", -3: "MOE_ENOSPC", -4: "MOE_EHIP",
           -5: "MOE_ETIMEOUT", -6: "MOE_EUNSUP", -7: "MOE_EINCOMPLETE"}
 
 # every symbol include/moe.h declares
-EXPORTS = ["moe_max_pairs", "moe_workspace_bytes", "moe_mx_quantize", "moe_layout", "moe_dispatch_pull",
+EXPORTS = ["moe_max_pairs", "moe_workspace_bytes", "moe_mx_quantize", "moe_mx_quantize_to", "moe_mx_dequantize",
+           "moe_layout", "moe_layout_choices", "moe_combine_merge", "moe_combine_merge_backward",
+           "moe_dispatch_pull_backward", "moe_forward_choices", "moe_backward_rows_info", "moe_dispatch_pull",
            "moe_expert_ffn", "moe_expert_ffn_push", "moe_weighted_merge", "moe_combine_push", "moe_forward",
            "moe_forward_fused", "moe_forward_persistent", "moe_persistent_dispatch_ffn_combine",
            "moe_forward_persistent_noalloc", "moe_ring_slot_bytes", "moe_persistent_workspace_bytes", "moe_persistent_trace_info",
@@ -78,6 +80,16 @@ def lib() -> ctypes.CDLL:
         L.moe_workspace_bytes.argtypes = [S, PL, EX]
         L.moe_workspace_bytes.restype = SZ
         L.moe_mx_quantize.argtypes = [VP, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, VP, VP, VP]
+        L.moe_mx_quantize_to.argtypes = [VP, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, VP, VP,
+                                         VP]
+        L.moe_mx_dequantize.argtypes = [VP, VP, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, VP, ctypes.c_int32, VP]
+        L.moe_layout_choices.argtypes = [S, PL, EX, VP, VP, VP, VP, VP, VP, SZ, VP]
+        L.moe_combine_merge.argtypes = [S, PL, VP, VP, VP, VP, VP]
+        L.moe_combine_merge_backward.argtypes = [S, PL, VP, VP, VP, VP, VP, VP, VP]
+        L.moe_dispatch_pull_backward.argtypes = [S, PL, VP, VP, VP, VP]
+        L.moe_forward_choices.argtypes = [S, PL, EX, VP, VP, VP, VP, VP, VP, MS, VP, VP, VP, VP, VP, VP, VP, VP, VP,
+                                          SZ, VP]
+        L.moe_backward_rows_info.argtypes = [S, PL, P(SZ), P(SZ)]
         L.moe_layout.argtypes = [S, PL, EX, VP, VP, VP, VP, VP, VP, VP, VP, SZ, VP]
         L.moe_dispatch_pull.argtypes = [S, PL, VP, VP, VP, VP, VP, VP, SZ, VP]
         L.moe_expert_ffn.argtypes = [S, PL, EX, VP, VP, VP, VP, VP, VP, MS, VP, VP, SZ, VP]
@@ -124,7 +136,9 @@ def lib() -> ctypes.CDLL:
         L.moe_strerror.argtypes = [I32]
         L.moe_strerror.restype = ctypes.c_char_p
         L.moe_version.restype = ctypes.c_char_p
-        for f in ("moe_mx_quantize", "moe_layout", "moe_dispatch_pull", "moe_expert_ffn", "moe_combine_push",
+        for f in ("moe_mx_quantize", "moe_mx_quantize_to", "moe_mx_dequantize", "moe_layout", "moe_layout_choices",
+                  "moe_combine_merge", "moe_combine_merge_backward", "moe_dispatch_pull_backward",
+                  "moe_forward_choices", "moe_backward_rows_info", "moe_dispatch_pull", "moe_expert_ffn", "moe_combine_push",
                   "moe_expert_ffn_push", "moe_weighted_merge", "moe_forward_fused",
                   "moe_forward", "moe_forward_persistent", "moe_persistent_dispatch_ffn_combine",
                   "moe_forward_persistent_noalloc",
@@ -192,6 +206,61 @@ def _ref(st):
 def moe_mx_quantize(src, src_dtype, rows, K, codes, scales, stream=None, check=True):
     rc = lib().moe_mx_quantize(_p(src), int(src_dtype), int(rows), int(K), _p(codes), _p(scales), _stream(stream))
     return _check(rc, "moe_mx_quantize") if check else rc
+
+
+def moe_mx_quantize_to(src, src_dtype, rows, K, format, codes, scales, stream=None, check=True):
+    rc = lib().moe_mx_quantize_to(_p(src), int(src_dtype), int(rows), int(K), int(format), _p(codes), _p(scales),
+                                  _stream(stream))
+    return _check(rc, "moe_mx_quantize_to") if check else rc
+
+
+def moe_mx_dequantize(codes, scales, format, rows, K, dst, dst_dtype, stream=None, check=True):
+    rc = lib().moe_mx_dequantize(_p(codes), _p(scales), int(format), int(rows), int(K), _p(dst), int(dst_dtype),
+                                 _stream(stream))
+    return _check(rc, "moe_mx_dequantize") if check else rc
+
+
+def moe_layout_choices(shape, placement, ex, topk_idx, counts, offsets, pull_src, slot_of, ws, ws_bytes=None,
+                       stream=None, check=True):
+    rc = lib().moe_layout_choices(ctypes.byref(shape), ctypes.byref(placement), _ref(ex), _p(topk_idx), _p(counts),
+                                  _p(offsets), _p(pull_src), _p(slot_of), _p(ws),
+                                  ws.numel() if ws_bytes is None else ws_bytes, _stream(stream))
+    return _check(rc, "moe_layout_choices") if check else rc
+
+
+def moe_combine_merge(shape, placement, ye, slot_of, topk_w, y, stream=None, check=True):
+    rc = lib().moe_combine_merge(ctypes.byref(shape), ctypes.byref(placement), _p(ye), _p(slot_of), _p(topk_w),
+                                 _table(y), _stream(stream))
+    return _check(rc, "moe_combine_merge") if check else rc
+
+
+def moe_combine_merge_backward(shape, placement, dy, ye, slot_of, topk_w, dye, dtopk_w, stream=None, check=True):
+    rc = lib().moe_combine_merge_backward(ctypes.byref(shape), ctypes.byref(placement), _table(dy), _p(ye),
+                                          _p(slot_of), _p(topk_w), _p(dye), _p(dtopk_w), _stream(stream))
+    return _check(rc, "moe_combine_merge_backward") if check else rc
+
+
+def moe_dispatch_pull_backward(shape, placement, dxe, slot_of, dx, stream=None, check=True):
+    rc = lib().moe_dispatch_pull_backward(ctypes.byref(shape), ctypes.byref(placement), _p(dxe), _p(slot_of),
+                                          _table(dx), _stream(stream))
+    return _check(rc, "moe_dispatch_pull_backward") if check else rc
+
+
+def moe_forward_choices(shape, placement, ex, topk_idx, topk_w, x, w1, w3, w2, xe, ye, y, counts, offsets, pull_src,
+                        slot_of, ws, ws_bytes=None, stream=None, check=True, w_scales=None, xe_scales=None):
+    rc = lib().moe_forward_choices(ctypes.byref(shape), ctypes.byref(placement), _ref(ex), _p(topk_idx), _p(topk_w),
+                                   _table(x), _p(w1), _p(w3), _p(w2), _ref(w_scales), _p(xe), _p(xe_scales), _p(ye),
+                                   _table(y), _p(counts), _p(offsets), _p(pull_src), _p(slot_of), _p(ws),
+                                   ws.numel() if ws_bytes is None else ws_bytes, _stream(stream))
+    return _check(rc, "moe_forward_choices") if check else rc
+
+
+def moe_backward_rows_info(shape, placement):
+    """Byte offsets in the backward workspace of the rows that moe_expert_ffn_backward reads and leaves."""
+    a, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib().moe_backward_rows_info(ctypes.byref(shape), ctypes.byref(placement), ctypes.byref(a),
+                                        ctypes.byref(b)), "moe_backward_rows_info")
+    return a.value, b.value
 
 
 def moe_layout(shape, placement, ex, logits, topk_idx, topk_w, counts, offsets, pull_src, slot_of,

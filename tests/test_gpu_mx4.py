@@ -1,0 +1,345 @@
+"""GPU parity of MXFP4: the codec bit for bit, and the expert path against its 64-bit formula.
+
+Bars.  Codec: bit-exact.  Expert outputs: every element of ye lies within what its own
+arithmetic allows, derived per element (_bound): the h codes that may legitimately differ
+from the 64-bit h's -- those whose value lies closer to an E2M1 midpoint (or whose block
+maximum lies closer to a power of two) than the fp32 error of h -- times W2, the fp32
+accumulation of the down product, and one bf16 rounding (2^-8 of the value: half a step).
+A dropped block, a wrong scale or nibble order moves outputs by tens of percent.
+"""
+import numpy as np
+import pytest
+
+from oracle import moe_oracle as O
+from oracle import mx4_oracle as M4
+from oracle import mx_oracle as M8
+from mixture_experts_layer_histogram_amd import configs, inputs, moe
+
+pytestmark = pytest.mark.gpu
+
+GUARD = 0x5A
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _rowmajor(scales, rows, K):
+    """Scale codes [rows][K/32] of the plane-wise device layout [K/128][rows][4]."""
+    return scales.reshape(K // 128, rows, 4).transpose(1, 0, 2).reshape(rows, K // 32)
+
+
+def _gpu_quantize(v, src, fmt=moe.MOE_MXFP4):
+    """moe_mx_quantize_to of rows of fp32 values; codes and scales lie between guard bytes."""
+    torch = _torch()
+    rows, K = v.shape
+    x = torch.from_numpy(np.ascontiguousarray(v, dtype=np.float32)).cuda()
+    if src == "bf16":
+        x = x.to(torch.bfloat16)
+        assert np.array_equal(x.float().cpu().numpy(), v, equal_nan=True), "inputs must be bf16 values"
+    nb = rows * K // (2 if fmt == moe.MOE_MXFP4 else 1)
+    q = torch.full((nb + 256,), GUARD, dtype=torch.uint8, device="cuda")
+    s = torch.full((rows * K // 32 + 256,), GUARD, dtype=torch.uint8, device="cuda")
+    moe.moe_mx_quantize_to(x, moe.MOE_BF16 if src == "bf16" else moe.MOE_F32, rows, K, fmt, q, s)
+    q, s = q.cpu().numpy(), s.cpu().numpy()
+    assert (q[nb:] == GUARD).all() and (s[rows * K // 32:] == GUARD).all()
+    return q[:nb].reshape(rows, -1), _rowmajor(s[: rows * K // 32], rows, K)
+
+
+def _bf16_values():
+    return (np.arange(65536, dtype=np.uint32) << 16).view(np.float32).copy()
+
+
+# --------------------------------------------------------------------------- codec
+@pytest.mark.parametrize("order", ["natural", "shuffled", "near", "finite"])
+def test_quantize_every_bf16_value(order):
+    v = _bf16_values()
+    if order == "finite":
+        v[~np.isfinite(v)] = 0.0
+    if order == "shuffled":                       # almost every block has an infinity, a NaN or a huge value
+        v = v[np.random.default_rng(1).permutation(v.size)]
+    elif order == "near":                         # blocks of neighbouring magnitudes
+        v = v[np.argsort(np.abs(v), kind="stable")].reshape(-1, 32)
+        v = v[np.random.default_rng(2).permutation(len(v))].reshape(-1)
+    v = v.reshape(-1, 1024)
+    codes, scales = _gpu_quantize(v, "bf16")
+    rc, rs, _ = M4.quantize(v)
+    assert np.array_equal(scales, rs)
+    assert np.array_equal(M4.unpack(codes), rc)
+
+
+@pytest.mark.parametrize("src", ["bf16", "f32"])
+def test_quantize_midpoints_at_every_scale(src):
+    """Values on and next to every midpoint, blocks scaled by every power of two of the type."""
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0, 7.5, 0.5, 1.0, 3.0, 0.125, 0.0])
+    if src == "f32":
+        m32 = mids.astype(np.float32)
+        base = np.concatenate([mids, np.nextafter(m32, np.float32(0)), np.nextafter(m32, np.float32(9))])[:31]
+    else:
+        base = np.concatenate([mids, mids[:7] * (1 + 2.0 ** -7), mids[:7] * (1 - 2.0 ** -7)])[:31]
+    rng = np.random.default_rng(3)
+    blocks = []
+    for e in range(-149, 126):
+        b = np.concatenate([[4.0 + rng.integers(0, 4)], rng.permutation(np.resize(base, 31))])
+        blocks.append(np.ldexp(b * np.where(rng.random(32) < 0.5, -1.0, 1.0), e))
+    blocks += [np.zeros(32)] * ((-len(blocks)) % 4)
+    v = np.array(blocks).astype(np.float32).reshape(-1, 128)
+    if src == "bf16":
+        v = inputs.f32_to_bf16_bits(v).astype(np.uint32)
+        v = (v << 16).view(np.float32).reshape(-1, 128)
+    codes, scales = _gpu_quantize(v, src)
+    rc, rs, _ = M4.quantize(v)
+    assert np.array_equal(scales, rs)
+    assert np.array_equal(M4.unpack(codes), rc)
+
+
+@pytest.mark.parametrize("rows,K", [(1, 128), (1, 7168), (31, 384), (32, 512), (33, 640), (65, 1408), (257, 128)])
+@pytest.mark.parametrize("src", ["bf16", "f32"])
+def test_quantize_dequantize_shapes(rows, K, src):
+    torch = _torch()
+    rng = np.random.default_rng(rows * K)
+    v = rng.standard_normal((rows, K)).astype(np.float32)
+    v[rng.random((rows, K // 32)).repeat(32, 1) < 0.1] = 0.0          # whole zero blocks
+    if src == "bf16":
+        v = (inputs.f32_to_bf16_bits(v).astype(np.uint32) << 16).view(np.float32).reshape(rows, K)
+    v[rows // 2, 5], v[0, K - 1] = np.nan, -np.inf
+    for fmt in (moe.MOE_MXFP4, moe.MOE_MXFP8):
+        w = v if fmt == moe.MOE_MXFP4 else np.nan_to_num(v, nan=0.0, neginf=0.0)
+        codes, scales = _gpu_quantize(w, src, fmt)
+        rc, rs, want = M4.quantize(w) if fmt == moe.MOE_MXFP4 else M8.quantize(w)
+        assert np.array_equal(M4.unpack(codes) if fmt == moe.MOE_MXFP4 else codes, rc) and np.array_equal(scales, rs)
+        planes = torch.from_numpy(np.ascontiguousarray(rs.reshape(rows, K // 128, 4).transpose(1, 0, 2))).cuda()
+        for code, kind in ((moe.MOE_BF16, torch.bfloat16), (moe.MOE_F32, torch.float32)):
+            out = torch.full((rows * K + 64,), 7.0, dtype=kind, device="cuda")
+            moe.moe_mx_dequantize(torch.from_numpy(codes.copy()).cuda(), planes, fmt, rows, K, out, code)
+            assert (out[rows * K:] == 7.0).all()
+            assert np.array_equal(out[: rows * K].double().cpu().numpy().reshape(rows, K), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("fmt", [moe.MOE_MXFP4, moe.MOE_MXFP8])
+def test_dequantize_every_code_at_every_scale(fmt):
+    torch = _torch()
+    if fmt == moe.MOE_MXFP4:
+        q = M4.unpack(np.arange(256, dtype=np.uint8)[None])[0]                 # every byte: 512 codes
+        elem, stored = M4.e2m1_decode(q), np.arange(256, dtype=np.uint8)
+    else:
+        stored = np.arange(256, dtype=np.uint8)
+        elem = M8.e4m3_decode(stored)
+    K = elem.size
+    codes = np.tile(stored, (256, 1))
+    scales = np.repeat(np.arange(256, dtype=np.uint8)[:, None], K // 32, axis=1)
+    planes = torch.from_numpy(np.ascontiguousarray(scales.reshape(256, K // 128, 4).transpose(1, 0, 2))).cuda()
+    with np.errstate(over="ignore"):
+        want = torch.from_numpy((elem[None] * M4.scale_value(scales[:, :1])).astype(np.float32))   # exact, or infinite
+    for code, kind in ((moe.MOE_F32, torch.float32), (moe.MOE_BF16, torch.bfloat16)):
+        out = torch.empty(256, K, dtype=kind, device="cuda")
+        moe.moe_mx_dequantize(torch.from_numpy(codes).cuda(), planes, fmt, 256, K, out, code)
+        assert torch.equal(torch.nan_to_num(out.cpu().float(), nan=12345.0),
+                           torch.nan_to_num(want.to(kind).float(), nan=12345.0))
+
+
+# --------------------------------------------------------------------------- expert products
+def _cfg(name, **kw):
+    base = dict(R=1, T=64, d=256, E=8, E_local=8, k=2, F=256, dtype="mxfp4")
+    base.update(kw)
+    return configs.DSV3_MX.scaled(name=name, **base)
+
+
+CASES = {
+    "one-token": _cfg("mx4 one token", T=1, d=256, F=128),
+    "one-token-wide": _cfg("mx4 one token d1408", T=1, d=1408, F=640, E=16, E_local=16, k=6),
+    "k1-one-expert": _cfg("mx4 one expert", T=7, d=128, F=128, E=1, E_local=1, k=1),
+    "half-tails": _cfg("mx4 half tails", R=2, T=45, d=384, F=1408, E=4, E_local=2, k=2),
+    "rows-33": _cfg("mx4 rows 33", T=33, d=640, F=384, E=1, E_local=1, k=1),
+    "rows-64": _cfg("mx4 rows 64", T=64, d=512, F=256, E=1, E_local=1, k=1),
+    "rows-129": _cfg("mx4 rows 129", T=129, d=256, F=512, E=1, E_local=1, k=1),
+    "rows-257": _cfg("mx4 rows 257", T=257, d=1152, F=128, E=2, E_local=2, k=2),
+    "several-tiles": _cfg("mx4 several tiles", R=2, T=600, d=1024, F=512, E=16, E_local=8, k=4),
+    "skew": _cfg("mx4 skew", R=2, T=256, d=768, F=384, E=32, E_local=8, k=4, load="skew"),
+}
+
+
+def _problem(cfg, seed=0, mutate=None):
+    from mixture_experts_layer_histogram_amd.device import DeviceProblem
+    inp = inputs.make_inputs(cfg, seed=seed)
+    if mutate:
+        mutate(inp)
+    return inp, DeviceProblem(cfg, inp)
+
+
+def _bound(x, w1, w3, w2):
+    """(ye, per-element allowance without the bf16 rounding) of one expert in 64 bits.  The MFMA adds
+    64 exact products at a time to an fp32 accumulator: K / 64 roundings, each at most 2^-23 of the
+    running sum of magnitudes (a truncating adder's step), and the scale product; exp and the quotient of
+    silu: (|a| + 8) 2^-22 relative."""
+    a, b = x @ w1.T, x @ w3.T
+    ax, aw1, aw3 = np.abs(x), np.abs(w1), np.abs(w3)
+    n = x.shape[1] / 64 + 4
+    da, db = n * 2.0 ** -23 * (ax @ aw1.T), n * 2.0 ** -23 * (ax @ aw3.T)
+    h = O.silu(a) * b
+    dh = 1.1 * da * np.abs(b) + np.abs(O.silu(a)) * db + (np.abs(a) + 8) * 2.0 ** -22 * np.abs(h) + 2.0 ** -130
+    _, sc, hq = M4.quantize(h)
+    scale = np.repeat(M4.scale_value(sc), 32, axis=-1)
+    y, dy = np.abs(h) / scale, dh / scale
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    steps = np.array([0.5, 0.5, 0.5, 0.5, 1.0, 1.0, 2.0])
+    near = np.abs(y[..., None] - mids) <= dy[..., None]
+    slack = (near * steps).sum(-1) * scale
+    hb = np.abs(h).reshape(*h.shape[:-1], -1, 32)
+    top = hb.max(-1)
+    dtop = np.take_along_axis(dh.reshape(hb.shape), hb.argmax(-1)[..., None], -1)[..., 0]
+    _, e_lo = np.frexp(np.maximum(top - dtop, 0))
+    _, e_hi = np.frexp(top + dtop)
+    moved = np.repeat(e_lo != e_hi, 32, axis=-1)                 # the block's scale may differ: up to 2 units either side
+    slack = np.where(moved, 8 * scale, slack)
+    aw2 = np.abs(w2)
+    acc = (w2.shape[1] / 64 + 4) * 2.0 ** -23 * ((np.abs(hq) + slack) @ aw2.T)
+    return hq @ w2.T, slack @ aw2.T + acc
+
+
+def _weights64(P):
+    """The device's packed weights in 64 bits, and that they are the oracle's quantisation."""
+    out = []
+    for w, q, s in zip((P.w1, P.w3, P.w2), P.wq, P.ws_codes):
+        El, rows, K = w.shape
+        v = w.float().cpu().numpy().astype(np.float64).reshape(El * rows, K)
+        codes, sc, val = M4.quantize(v)
+        assert np.array_equal(M4.unpack(q.cpu().numpy().reshape(El * rows, K // 2)), codes)
+        assert np.array_equal(_rowmajor(s.cpu().numpy().reshape(-1), El * rows, K), sc)
+        out.append(val.reshape(El, rows, K))
+    return out
+
+
+def _check_rows(P, ye, x64, w):
+    """Every row of ye (device, bf16) within its bound; returns the 64-bit rows."""
+    off = P.offsets.cpu().numpy()
+    N = int(off[-1])
+    ref = np.zeros((N, x64.shape[-1]))
+    src = P.pull_src.cpu().numpy()
+    got = ye[:N].double().cpu().numpy()
+    for l in range(len(off) - 1):
+        a, b = int(off[l]), int(off[l + 1])
+        if a == b:
+            continue
+        rows = M4.quantize(x64[src[a:b, 0], src[a:b, 1]])[2]
+        ref[a:b], allow = _bound(rows, w[0][l], w[1][l], w[2][l])
+        err = np.abs(got[a:b] - ref[a:b])
+        lim = allow + (np.abs(ref[a:b]) + allow) * 2.0 ** -8 + 1e-38
+        assert (err <= lim).all(), (l, float((err / lim).max()), np.argwhere(err > lim)[:4].tolist())
+    return ref
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_expert_rows_within_their_bounds(name):
+    torch = _torch()
+    cfg = CASES[name]
+    print(f"[mx4] {cfg.name}", flush=True)
+    inp, P = _problem(cfg)
+    P.xe.fill_(GUARD)
+    P.ye.fill_(3.0)
+    P.xe_scales.fill_(GUARD)
+    P.forward()
+    assert P.status() == 0
+    torch.cuda.synchronize()
+    N = int(P.offsets[-1])
+    x64 = np.stack([P.rows_f64(t) for t in P.x]).reshape(cfg.R, cfg.T, cfg.d)
+    src = P.pull_src.cpu().numpy()[:N]
+    codes, sc, _ = M4.quantize(x64[src[:, 0], src[:, 1]])
+    assert np.array_equal(M4.unpack(P.xe[:N].cpu().numpy()), codes)
+    assert np.array_equal(P.xe_scales[:, :N].permute(1, 0, 2).reshape(N, -1).cpu().numpy(), sc)
+    assert (P.xe[N:] == GUARD).all() and (P.xe_scales[:, N:] == GUARD).all() and (P.ye[N:] == 3.0).all()
+    w = _weights64(P)
+    ref = _check_rows(P, P.ye, x64, w)
+    err = np.linalg.norm(P.ye[:N].double().cpu().numpy() - ref) / np.linalg.norm(ref)
+    print(f"[mx4] {cfg.name}: N {N}, relative error {err:.2e}", flush=True)
+    assert err <= 5e-3                      # the header's figure
+    # the fused path and the path for given choices give the same bits
+    y = [t.clone() for t in P.y]
+    for t in P.y:
+        t.fill_(float("nan"))
+    P.forward_fused()
+    assert P.status() == 0 and all(torch.equal(a, b) for a, b in zip(y, P.y))
+    idx, wgt, lay = P.topk_idx.clone(), P.topk_w.clone(), P.slot_of.clone()
+    for t in P.y:
+        t.fill_(float("nan"))
+    P.ye.fill_(float("nan"))
+    P.forward_choices(idx, wgt)
+    assert P.status() == 0 and torch.equal(lay, P.slot_of) and all(torch.equal(a, b) for a, b in zip(y, P.y))
+
+
+def test_tokens_without_a_value_stay_apart():
+    """A NaN, an infinity or both in a token's row makes that token NaN and touches no other."""
+    torch = _torch()
+    cfg = _cfg("mx4 non-finite tokens", T=70, d=512, F=256, E=4, E_local=4, k=2)
+    inp, P = _problem(cfg)
+    P.forward()
+    clean = P.y[0].clone()
+    x = P.x[0].clone()
+    P.x[0][3, 17] = float("nan")
+    P.x[0][40, 511] = float("inf")
+    P.x[0][69, 0], P.x[0][69, 1] = float("-inf"), float("nan")
+    P.forward_choices(P.topk_idx.clone(), P.topk_w.clone())
+    bad = [3, 40, 69]
+    assert torch.isnan(P.y[0][bad]).all()
+    good = [t for t in range(70) if t not in bad]
+    assert torch.equal(P.y[0][good], clean[good])
+    P.x[0].copy_(x)
+    P.forward_choices(P.topk_idx.clone(), P.topk_w.clone())
+    assert torch.equal(P.y[0], clean)
+
+
+def test_zero_and_extreme_rows():
+    """Rows of zeros give zeros; rows at the ends of bf16's range keep their scales."""
+    torch = _torch()
+    cfg = _cfg("mx4 extreme rows", T=8, d=256, F=128, E=2, E_local=2, k=1)
+    inp, P = _problem(cfg)
+    P.x[0][0] = 0.0
+    P.x[0][1] *= 2.0 ** -120
+    P.x[0][2] *= 2.0 ** 60
+    P.forward()
+    assert (P.y[0][0] == 0).all()
+    x64 = P.rows_f64(P.x[0]).reshape(1, 8, 256)
+    codes = M4.quantize(x64[0])[0]
+    src = P.pull_src.cpu().numpy()[:, 1]
+    assert np.array_equal(M4.unpack(P.xe.cpu().numpy()), codes[src])
+    assert torch.isfinite(P.y[0][[0, 1, 3, 4, 5, 6, 7]]).all()
+
+
+def test_no_local_rows_and_all_dropped():
+    torch = _torch()
+    cfg = _cfg("mx4 nothing", T=5, d=256, F=128, E=8, E_local=2, k=2)
+    inp, P = _problem(cfg)
+    P.forward_choices(torch.full((1, 5, 2), -1, dtype=torch.int32, device="cuda"), torch.ones(1, 5, 2, device="cuda"))
+    assert P.status() == 0 and (P.y[0] == 0).all() and (P.offsets == 0).all() and (P.slot_of == -1).all()
+    away = torch.tensor([[[6, 7]] * 5], dtype=torch.int32, device="cuda")        # experts 0 and 1 are local
+    P.forward_choices(away, torch.ones(1, 5, 2, device="cuda"))
+    assert P.status() == 0 and (P.y[0] == 0).all()
+    assert P.counts.tolist() == [0, 0, 0, 0, 0, 0, 5, 5]
+
+
+def test_graph_replays_and_two_streams():
+    torch = _torch()
+    cfg = CASES["half-tails"]
+    inp, A = _problem(cfg, seed=1)
+    _, B = _problem(cfg, seed=2)
+    for P in (A, B):
+        P.forward()
+    want = [[t.clone() for t in P.y] for P in (A, B)]
+    ch = [(P.topk_idx.clone(), P.topk_w.clone()) for P in (A, B)]
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        A.forward_choices(*ch[0])
+    for i in range(3):
+        for P in (A, B):
+            for t in P.y:
+                t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        other = torch.cuda.Stream()
+        B.forward_choices(*ch[1], stream=other)
+        torch.cuda.synchronize()
+        for P, w in zip((A, B), want):
+            assert all(torch.equal(a, b) for a, b in zip(P.y, w)), i
