@@ -1,12 +1,10 @@
-// The layer for given expert choices and gate weights (any router) on gfx950: the layout of
-// the choices, the expert rows back at their tokens, and the gradients of both moves.
+// The layer for given expert choices and gate weights (any router) on gfx950: the expert rows
+// back at their tokens, and the gradients of both moves (the layout of the choices itself is in
+// layout.hip).
 //
 // Operations (the moves themselves: MoK article, kucoin.com/es "Cursor's MoK logra un aumento
-// del 2.37x ...", sections 01-03: one expert's rows contiguous, results returned to their
-// tokens, the weighted merge):
-//   layout:  slot(p) = offsets[l] + rank of pair p among the pairs of local expert l, in
-//            (rank, token, j) order
-//   merge:   y[t]   = sum_j w[t][j] ye[slot(t, j)]
+// del 2.37x ...", sections 01-03: results returned to their tokens, the weighted merge):
+//   merge:               y[t] = sum_j w[t][j] ye[slot(t, j)]
 //   its gradient:        dye[slot(t, j)] = w[t][j] dy[t],   dw[t][j] = <dy[t], ye[slot(t, j)]>
 //   the pull's gradient: dx[t] = sum_j dxe[slot(t, j)]
 // Every source lies on this GPU, so merge reads the expert rows where the FFN left them: no
@@ -18,43 +16,17 @@
 
 namespace moe {
 
-// Histogram of one block's kTokPerLayoutBlock tokens.  A choice outside [-1, E) or an expert
-// named twice by one token marks the block in `bad` (one word per block): rows are counted on
-// at most one pair per token and expert, so such choices could overrun the tables.
-__global__ __launch_bounds__(256) void choices_hist_kernel(const int32_t* __restrict__ idx, int64_t RT, int E, int k,
-                                                           int32_t* __restrict__ blockhist, int32_t* __restrict__ bad,
-                                                           int bad_stride) {
-  __shared__ int hist[1024];
-  __shared__ int wrong;
-  const int tid = threadIdx.x;
-  for (int e = tid; e < E; e += 256) hist[e] = 0;
-  if (tid == 0) wrong = 0;
-  __syncthreads();
-  const int64_t g0 = int64_t(blockIdx.x) * kTokPerLayoutBlock;
-  const int64_t p0 = g0 * k, p1 = min(g0 + kTokPerLayoutBlock, RT) * k;
-  for (int64_t p = p0 + tid; p < p1; p += 256) {
-    const int e = idx[p];
-    if (e < -1 || e >= E) {
-      wrong = 1;
-    } else if (e >= 0) {
-      const int64_t first = p - p % k;
-      bool twice = false;
-      for (int64_t q = first; q < p; ++q) twice |= idx[q] == e;
-      if (twice) wrong = 1;
-      else atomicAdd(&hist[e], 1);
-    }
-  }
-  __syncthreads();
-  for (int e = tid; e < E; e += 256) blockhist[size_t(blockIdx.x) * E + e] = hist[e];
-  if (tid == 0) bad[size_t(blockIdx.x) * bad_stride] = wrong;
-}
-
 namespace {
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
   return v;
+}
+
+// lane j's value, j the same in every lane
+__device__ __forceinline__ float read_lane(float v, int j) {
+  return __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(v)), j)));
 }
 
 template <bool BF16>
@@ -83,8 +55,9 @@ __device__ __forceinline__ u32x4 pack(const float* f) {
 }  // namespace
 
 // y[r][t] = sum over ascending j with slot >= 0 of w[r][t][j] rows[slot] (w = 1 when null); a
-// token with none gets zeros.  A wave task is one column segment of 64 * VPL vectors.
-template <bool BF16, int VPL>
+// token with none gets zeros.  A wave task is one column segment of 64 * VPL vectors of one
+// token's row; JB of the token's expert rows are in flight at once.
+template <bool BF16, int VPL, int JB>
 __global__ __launch_bounds__(256) void merge_rows_kernel(const char* __restrict__ rows, RankPtrs<char*> y,
                                                          const int32_t* __restrict__ slot_of,
                                                          const float* __restrict__ w, int R, int T, int k, int d) {
@@ -107,24 +80,34 @@ __global__ __launch_bounds__(256) void merge_rows_kernel(const char* __restrict_
     for (int u = 0; u < VPL; ++u)
 #pragma unroll
       for (int e = 0; e < EPV; ++e) acc[u][e] = 0.0f;
-    for (unsigned long long m = __ballot(slot >= 0); m; m &= m - 1) {
-      const int j = __builtin_ctzll(m);
-      const int sj = __shfl(slot, j, 64);
-      const float wj = __shfl(wl, j, 64);
-      const u32x4* src = reinterpret_cast<const u32x4*>(rows + int64_t(sj) * row_bytes);
-      u32x4 v[VPL];
+    for (unsigned long long m = __ballot(slot >= 0); m;) {
+      const int n = __popcll(m);             // rows left (the same in every lane)
+      u32x4 v[JB][VPL];
+      float wj[JB];
 #pragma unroll
-      for (int u = 0; u < VPL; ++u) {
-        const int i = cb + u * 64 + lane;
-        if (i < n16) v[u] = __builtin_nontemporal_load(src + i);
+      for (int b = 0; b < JB; ++b) {
+        if (b >= n) continue;
+        const int j = __builtin_ctzll(m);
+        m &= m - 1;
+        wj[b] = read_lane(wl, j);
+        const u32x4* src = reinterpret_cast<const u32x4*>(rows + int64_t(__builtin_amdgcn_readlane(slot, j)) * row_bytes);
+#pragma unroll
+        for (int u = 0; u < VPL; ++u) {
+          const int i = cb + u * 64 + lane;
+          if (i < n16) v[b][u] = __builtin_nontemporal_load(src + i);
+        }
       }
 #pragma unroll
-      for (int u = 0; u < VPL; ++u) {
-        if (cb + u * 64 + lane < n16) {
-          float f[EPV];
-          unpack<BF16>(v[u], f);
+      for (int b = 0; b < JB; ++b) {
+        if (b >= n) continue;
 #pragma unroll
-          for (int e = 0; e < EPV; ++e) acc[u][e] = fmaf(wj, f[e], acc[u][e]);
+        for (int u = 0; u < VPL; ++u) {
+          if (cb + u * 64 + lane < n16) {
+            float f[EPV];
+            unpack<BF16>(v[b][u], f);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) acc[u][e] = fmaf(wj[b], f[e], acc[u][e]);
+          }
         }
       }
     }
@@ -137,21 +120,24 @@ __global__ __launch_bounds__(256) void merge_rows_kernel(const char* __restrict_
   }
 }
 
-// dye[slot] = w dy (rounded once), dw = <dy, ye[slot]> (fp32): one wave per token.  The row goes
-// in segments of 64 * VPL vectors; each holds its part of dy in registers for all the token's
-// rows, and lane j collects the dot product of pair j.
-template <bool BF16, int VPL>
+// dye[slot] = w dy (rounded once), dw = <dy, ye[slot]> (fp32).  WPT waves (1 or the workgroup's 4)
+// share a token; the row goes in segments of 64 * VPL vectors, wave after wave; a segment of dy
+// stays in registers for all the token's rows, JB of which are in flight at once, and lane j
+// collects the dot product of pair j.
+template <bool BF16, int VPL, int JB, int WPT>
 __global__ __launch_bounds__(256) void merge_rows_bwd_kernel(RankPtrs<const char*> dy, const char* __restrict__ ye,
                                                              const int32_t* __restrict__ slot_of,
                                                              const float* __restrict__ w, char* __restrict__ dye,
                                                              float* __restrict__ dw, int R, int T, int k, int d) {
   constexpr int EPV = BF16 ? 8 : 4;
-  const int lane = threadIdx.x & 63;
+  __shared__ float part[4][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row_bytes = int64_t(d) * (BF16 ? 2 : 4);
   const int n16 = int(row_bytes >> 4);
   const int64_t RT = int64_t(R) * T;
-  const int64_t nw = int64_t(gridDim.x) * 4;
-  for (int64_t g = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); g < RT; g += nw) {
+  const int first = WPT == 1 ? 0 : wave;
+  const int64_t step = int64_t(gridDim.x) * (4 / WPT);
+  for (int64_t g = WPT == 1 ? int64_t(blockIdx.x) * 4 + wave : int64_t(blockIdx.x); g < RT; g += step) {
     const int r = int(g / T);
     const int t = int(g - int64_t(r) * T);
     const int slot = lane < k ? slot_of[g * k + lane] : -1;
@@ -159,71 +145,96 @@ __global__ __launch_bounds__(256) void merge_rows_bwd_kernel(RankPtrs<const char
     const unsigned long long local = __ballot(slot >= 0);
     float mine = 0.0f;                      // lane j: the dot product of pair j
     const u32x4* dyr = reinterpret_cast<const u32x4*>(dy.p[r] + int64_t(t) * row_bytes);
-    if (local) {
-      for (int cb = 0; cb < n16; cb += 64 * VPL) {
-        u32x4 dv[VPL];
+    for (int cb = first * 64 * VPL; local && cb < n16; cb += WPT * 64 * VPL) {
+      u32x4 dv[VPL];
 #pragma unroll
-        for (int u = 0; u < VPL; ++u) {
-          const int i = cb + u * 64 + lane;
-          dv[u] = u32x4{0, 0, 0, 0};
-          if (i < n16) dv[u] = __builtin_nontemporal_load(dyr + i);
-        }
-        for (unsigned long long m = local; m; m &= m - 1) {
-          const int j = __builtin_ctzll(m);
-          const int64_t at = int64_t(__shfl(slot, j, 64)) * row_bytes;
-          const float wj = __shfl(wl, j, 64);
-          const u32x4* src = reinterpret_cast<const u32x4*>(ye + at);
-          u32x4* dst = reinterpret_cast<u32x4*>(dye + at);
-          u32x4 v[VPL];
+      for (int u = 0; u < VPL; ++u) {
+        const int i = cb + u * 64 + lane;
+        dv[u] = u32x4{0, 0, 0, 0};
+        if (i < n16) dv[u] = __builtin_nontemporal_load(dyr + i);
+      }
+      for (unsigned long long m = local; m;) {
+        const int n = __popcll(m);
+        u32x4 v[JB][VPL];
+        int js[JB];
+        int64_t at[JB];
+#pragma unroll
+        for (int b = 0; b < JB; ++b) {
+          if (b >= n) continue;
+          js[b] = __builtin_ctzll(m);
+          m &= m - 1;
+          at[b] = int64_t(__builtin_amdgcn_readlane(slot, js[b])) * row_bytes;
+          const u32x4* src = reinterpret_cast<const u32x4*>(ye + at[b]);
 #pragma unroll
           for (int u = 0; u < VPL; ++u) {
             const int i = cb + u * 64 + lane;
-            v[u] = u32x4{0, 0, 0, 0};
-            if (i < n16) v[u] = __builtin_nontemporal_load(src + i);
+            v[b][u] = u32x4{0, 0, 0, 0};
+            if (i < n16) v[b][u] = __builtin_nontemporal_load(src + i);
           }
+        }
+#pragma unroll
+        for (int b = 0; b < JB; ++b) {
+          if (b >= n) continue;
+          const float wj = read_lane(wl, js[b]);
+          u32x4* dst = reinterpret_cast<u32x4*>(dye + at[b]);
           float dot = 0.0f;
 #pragma unroll
           for (int u = 0; u < VPL; ++u) {
             const int i = cb + u * 64 + lane;
-            float a[EPV], b[EPV];
-            unpack<BF16>(dv[u], a);
-            unpack<BF16>(v[u], b);
+            float x[EPV], z[EPV];
+            unpack<BF16>(dv[u], x);
+            unpack<BF16>(v[b][u], z);
 #pragma unroll
             for (int e = 0; e < EPV; ++e) {
-              dot = fmaf(a[e], b[e], dot);
-              a[e] *= wj;
+              dot = fmaf(x[e], z[e], dot);
+              x[e] *= wj;
             }
-            if (i < n16) dst[i] = pack<BF16>(a);
+            if (i < n16) dst[i] = pack<BF16>(x);
           }
           dot = wave_sum(dot);
-          if (lane == j) mine += dot;
+          if (lane == js[b]) mine += dot;
         }
       }
     }
-    if (lane < k) dw[g * k + lane] = mine;
+    if constexpr (WPT > 1) {
+      if (lane < k) part[wave][lane] = mine;
+      __syncthreads();
+      if (wave == 0 && lane < k) dw[g * k + lane] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+      __syncthreads();
+    } else {
+      if (lane < k) dw[g * k + lane] = mine;
+    }
   }
 }
 
 constexpr int kMergeRowsBlocksPerCU = 16, kMergeBwdBlocksPerCU = 8;
 
-hipError_t launch_choices_hist(const moe_shape_t& s, const int32_t* idx, int32_t* blockhist, int32_t* bad, int El,
-                               int nb, hipStream_t st) {
-  hipLaunchKernelGGL(choices_hist_kernel, dim3(nb), dim3(256), 0, st, idx, int64_t(s.R) * s.T, s.E, s.k, blockhist, bad,
-                     El);
-  return hipGetLastError();
-}
+// workgroups for `n` of them, at most `most`: a few tokens do not pay for the launch of
+// thousands of empty workgroups
+static int grid_of(int64_t n, int most) { return int(n < most ? n : most); }
 
 hipError_t launch_merge_rows(const moe_shape_t& s, const void* rows, const int32_t* slot_of, const float* w,
                              void* const* y, int cus, hipStream_t st) {
   RankPtrs<char*> yp{};
   for (int r = 0; r < s.R; ++r) yp.p[r] = static_cast<char*>(y[r]);
-  const dim3 grid(cus * kMergeRowsBlocksPerCU);
-  if (s.dtype != MOE_F32)
-    hipLaunchKernelGGL((merge_rows_kernel<true, 4>), grid, dim3(256), 0, st, static_cast<const char*>(rows), yp, slot_of,
-                       w, s.R, s.T, s.k, s.d);
-  else
-    hipLaunchKernelGGL((merge_rows_kernel<false, 4>), grid, dim3(256), 0, st, static_cast<const char*>(rows), yp, slot_of,
-                       w, s.R, s.T, s.k, s.d);
+  const char* src = static_cast<const char*>(rows);
+  const int64_t RT = int64_t(s.R) * s.T;
+  const int n16 = s.d * (s.dtype == MOE_F32 ? 4 : 2) / 16;
+  // Long segments once they give every SIMD a wave; below that short ones with all rows in flight.
+  const bool few = RT * ((n16 + 255) / 256) < int64_t(cus) * 4;
+  const int most = cus * kMergeRowsBlocksPerCU;
+  const dim3 grid(few ? grid_of((RT * ((n16 + 63) / 64) + 3) / 4, most) : grid_of((RT * ((n16 + 255) / 256) + 3) / 4, most));
+  if (s.dtype != MOE_F32) {
+    if (few)
+      hipLaunchKernelGGL((merge_rows_kernel<true, 1, 8>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
+    else
+      hipLaunchKernelGGL((merge_rows_kernel<true, 4, 2>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
+  } else {
+    if (few)
+      hipLaunchKernelGGL((merge_rows_kernel<false, 1, 8>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
+    else
+      hipLaunchKernelGGL((merge_rows_kernel<false, 4, 2>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
+  }
   return hipGetLastError();
 }
 
@@ -231,13 +242,27 @@ hipError_t launch_merge_rows_bwd(const moe_shape_t& s, const void* const* dy, co
                                  const float* w, void* dye, float* dw, int cus, hipStream_t st) {
   RankPtrs<const char*> dp{};
   for (int r = 0; r < s.R; ++r) dp.p[r] = static_cast<const char*>(dy[r]);
-  const dim3 grid(cus * kMergeBwdBlocksPerCU);
-  if (s.dtype != MOE_F32)
-    hipLaunchKernelGGL((merge_rows_bwd_kernel<true, 4>), grid, dim3(256), 0, st, dp, static_cast<const char*>(ye),
-                       slot_of, w, static_cast<char*>(dye), dw, s.R, s.T, s.k, s.d);
-  else
-    hipLaunchKernelGGL((merge_rows_bwd_kernel<false, 4>), grid, dim3(256), 0, st, dp, static_cast<const char*>(ye),
-                       slot_of, w, static_cast<char*>(dye), dw, s.R, s.T, s.k, s.d);
+  const char* src = static_cast<const char*>(ye);
+  char* dst = static_cast<char*>(dye);
+  const int64_t RT = int64_t(s.R) * s.T;
+  // a wave per token once that gives every SIMD two; below that a workgroup per token
+  const bool few = RT < int64_t(cus) * 8;
+  const dim3 grid(grid_of(few ? RT : (RT + 3) / 4, cus * kMergeBwdBlocksPerCU));
+  if (s.dtype != MOE_F32) {
+    if (few)
+      hipLaunchKernelGGL((merge_rows_bwd_kernel<true, 1, 4, 4>), grid, dim3(256), 0, st, dp, src, slot_of, w, dst, dw, s.R,
+                         s.T, s.k, s.d);
+    else
+      hipLaunchKernelGGL((merge_rows_bwd_kernel<true, 4, 1, 1>), grid, dim3(256), 0, st, dp, src, slot_of, w, dst, dw, s.R,
+                         s.T, s.k, s.d);
+  } else {
+    if (few)
+      hipLaunchKernelGGL((merge_rows_bwd_kernel<false, 1, 4, 4>), grid, dim3(256), 0, st, dp, src, slot_of, w, dst, dw, s.R,
+                         s.T, s.k, s.d);
+    else
+      hipLaunchKernelGGL((merge_rows_bwd_kernel<false, 4, 1, 1>), grid, dim3(256), 0, st, dp, src, slot_of, w, dst, dw, s.R,
+                         s.T, s.k, s.d);
+  }
   return hipGetLastError();
 }
 

@@ -25,8 +25,13 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
     const uint8_t* __restrict__ B1, const uint8_t* __restrict__ Bs0, const uint8_t* __restrict__ Bs1,
     void* __restrict__ C, uint8_t* __restrict__ Cs, const int32_t* __restrict__ offsets,
     const int32_t* __restrict__ mtile_base, const int32_t* __restrict__ ctrl, int El, int K, int Nout,
-    int64_t nmax, const uint64_t* __restrict__ RowDst) {
+    int64_t nmax, const uint64_t* __restrict__ RowDst, int min_rows) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
+  if (min_rows > 0) {      // few rows expected: often the streaming kernel has taken every expert
+    int any = 0;
+    for (int l = threadIdx.x; l < El; l += kGemmThreads) any |= offsets[l + 1] - offsets[l] >= min_rows;
+    if (!__syncthreads_or(any)) return;
+  }
   const int cols_per_tile = (MODE == 0) ? kGemmBN / 2 : kGemmBN;
   const int NT = (Nout + cols_per_tile - 1) / cols_per_tile;
   const int total = ctrl[kCtrlMTiles] * NT;
@@ -41,6 +46,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
     const int mtg = tau / NT;
     const int l = find_expert(mtile_base, El, mtg);
     const int mt0 = mtile_base[l];
+    if (offsets[l + 1] - offsets[l] < min_rows) continue;      // the streaming kernel's
     const int mtl = mtile_base[l + 1] - mt0;
     const int i_in = tau - mt0 * NT;
     const int nt = i_in / mtl, mt = i_in - nt * mtl;
@@ -69,6 +75,11 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
   }
 }
 
+hipError_t launch_thin_mx4(bool gate_up, const uint8_t* a, const uint8_t* as, const uint8_t* b0, const uint8_t* b1,
+                           const uint8_t* bs0, const uint8_t* bs1, void* o, uint8_t* os, const int32_t* offsets,
+                           const uint64_t* row_dst, int64_t nmax, int El, int64_t experts, int K, int Nout, int cus,
+                           hipStream_t st);
+
 hipError_t launch_ffn_mx4(const moe_shape_t& s, int El, const uint8_t* xe, const uint8_t* xe_scales,
                           const int32_t* offsets, const uint8_t* w1, const uint8_t* w3, const uint8_t* w2,
                           const moe_mx_scales_t& w_scales, void* ye, char* ws, const WsLayout& L, int cus,
@@ -88,11 +99,33 @@ hipError_t launch_ffn_mx4(const moe_shape_t& s, int El, const uint8_t* xe, const
   uint8_t* hq = reinterpret_cast<uint8_t*>(ws + L.hbuf);
   uint8_t* hs = hq + mx4_h_scales_offset(L.max_pairs, s.F);
   const int grid = (cus / 8) * 8;
-  hipLaunchKernelGGL(grouped_gemm_mx4_kernel<0>, dim3(grid), dim3(kGemmThreads), kMx4Lds, st, xe, xe_scales, w1, w3,
-                     w_scales.w1, w_scales.w3, static_cast<void*>(hq), hs, offsets, mtb, ctrl, El, s.d, s.F,
-                     int64_t(L.max_pairs), nullptr);
-  hipLaunchKernelGGL(grouped_gemm_mx4_kernel<1>, dim3(grid), dim3(kGemmThreads), kMx4Lds, st, hq, hs, w2, nullptr,
-                     w_scales.w2, nullptr, ye, nullptr, offsets, mtb, ctrl, El, s.F, s.d, int64_t(L.max_pairs), row_dst);
+  // Which experts have few rows is known on the device only.  An expert has at most R T rows (a
+  // token names it once) and, under an even load, R T k / E.  So with at most kThinRows tokens the
+  // streaming kernel does it all; with kThinRows rows expected of an expert or more the tile
+  // kernel does; in between both run, each on its experts.
+  const int64_t tokens = int64_t(s.R) * s.T;
+  const bool thin = tokens <= kThinRows || tokens * s.k <= int64_t(kThinRows) * s.E;
+  const bool wide = tokens > kThinRows;
+  const int min_rows = thin ? kThinRows + 1 : 0;
+  const int64_t nmax = L.max_pairs;
+  const int64_t experts = El < nmax ? El : nmax;             // with a row, at most
+  if (thin) {
+    const hipError_t e = launch_thin_mx4(true, xe, xe_scales, w1, w3, w_scales.w1, w_scales.w3, hq, hs, offsets, nullptr,
+                                         nmax, El, experts, s.d, s.F, cus, st);
+    if (e != hipSuccess) return e;
+  }
+  if (wide)
+    hipLaunchKernelGGL(grouped_gemm_mx4_kernel<0>, dim3(grid), dim3(kGemmThreads), kMx4Lds, st, xe, xe_scales, w1, w3,
+                       w_scales.w1, w_scales.w3, static_cast<void*>(hq), hs, offsets, mtb, ctrl, El, s.d, s.F, nmax,
+                       nullptr, min_rows);
+  if (thin) {
+    const hipError_t e = launch_thin_mx4(false, hq, hs, w2, w2, w_scales.w2, w_scales.w2, ye, nullptr, offsets, row_dst,
+                                         nmax, El, experts, s.F, s.d, cus, st);
+    if (e != hipSuccess) return e;
+  }
+  if (wide)
+    hipLaunchKernelGGL(grouped_gemm_mx4_kernel<1>, dim3(grid), dim3(kGemmThreads), kMx4Lds, st, hq, hs, w2, nullptr,
+                       w_scales.w2, nullptr, ye, nullptr, offsets, mtb, ctrl, El, s.F, s.d, nmax, row_dst, min_rows);
   return hipGetLastError();
 }
 

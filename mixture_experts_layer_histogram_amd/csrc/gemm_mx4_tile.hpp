@@ -26,6 +26,21 @@ struct TileMX4 {
   const uint64_t* row_dst;  // MODE 1: null, or per tile row the address its output row goes to
 };
 
+// The order the scheduler is asked for in a sub-step of eight MFMAs: a read after each, so that the
+// eight waves' LDS requests do not arrive in bursts.
+#define MOE_MX4_PAIR                             \
+  __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); \
+  __builtin_amdgcn_sched_group_barrier(0x100, 1, 0)
+#define MOE_MX4_SPREAD \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR
+
 // MODE 0: h = MX4(silu(A B0^T) * (A B1^T)), 128 f columns of Nout = F per tile; MODE 1: bf16 A B0^T, 256
 // columns.  b0/b1: this expert's weight codes ([Nout][K / 2]); bs0/bs1: the scale word of its row 0 in
 // plane 0; bs_plane: bytes between the weights' K-tile planes.
@@ -79,24 +94,27 @@ __device__ __forceinline__ void gemm_mx4_tile(const TileMX4& io, const uint8_t* 
     const uint32_t stage = uint32_t((ks & 1) * kMx4StageBytes);
     const uint32_t da = lds_dst0 + stage, db = da + uint32_t(kGemmBM * kMx4RowBytes);
     const uint32_t ls = lds_sc0 + stage;
-    uint32_t koff = uint32_t(ks) * kMx4RowBytes;
-    uint32_t ke = koff, ko = koff;
-    const bool tail = half_tail && ks == nk - 1;
-    if (tail) {       // chunks 4..7 lie past the row's end: re-read chunks 0..3 (never used)
-      ke -= uint32_t(lch_even & 4) * 16;
-      ko -= uint32_t(lch_odd & 4) * 16;
+    // the K offset goes into the scalar bases: no vector address work per fill
+    const uint8_t* ak = abase + size_t(ks) * kMx4RowBytes;
+    const uint8_t* bk = bbase + size_t(ks) * kMx4RowBytes;
+    const uint8_t* s0 = sp + (2 * ks) * splane;
+    const uint8_t* s1 = s0 + splane;
+    uint32_t te = 0, to = 0;
+    if (half_tail && ks == nk - 1) {  // chunks 4..7 lie past the row's end: re-read chunks 0..3 (never used)
+      te = uint32_t(lch_even & 4) * 16;
+      to = uint32_t(lch_odd & 4) * 16;
+      s1 = s0;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t k = (i & 1) ? ko : ke;
-      __builtin_amdgcn_global_load_lds(static_cast<const void*>(abase + (aoff[i] + k)),
+      const uint32_t t = (i & 1) ? to : te;
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(ak + (aoff[i] - t)),
                                        (lds_void_ptr)(uintptr_t)(da + uint32_t(i * 1024)), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds(static_cast<const void*>(bbase + (boff[i] + k)),
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(bk + (boff[i] - t)),
                                        (lds_void_ptr)(uintptr_t)(db + uint32_t(i * 1024)), 16, 0, 0);
     }
-    const uint8_t* s0 = sp + (2 * ks) * splane;
     __builtin_amdgcn_global_load_lds(static_cast<const void*>(s0), (lds_void_ptr)(uintptr_t)ls, 4, 0, 0);
-    __builtin_amdgcn_global_load_lds(static_cast<const void*>(tail ? s0 : s0 + splane),
+    __builtin_amdgcn_global_load_lds(static_cast<const void*>(s1),
                                      (lds_void_ptr)(uintptr_t)(ls + uint32_t(4 * (kGemmBM + kGemmBN))), 4, 0, 0);
   };
 
@@ -143,8 +161,8 @@ __device__ __forceinline__ void gemm_mx4_tile(const TileMX4& io, const uint8_t* 
   const int mv = __builtin_amdgcn_readfirstlane(min(2, max(0, (rows - wm * 64 + 31) >> 5)));
   auto kloop = [&](auto mvc) {
     constexpr int MV = decltype(mvc)::value;
-    i32x4 fa[2][2], fb[2][4];
-    int sa[2], sb[4];
+    i32x4 fa[2][2], fb[2][4];            // fragments, two sets
+    int sa[2][2], sb[2][4];              // scale words of a stage's two halves
     auto load = [&](int buf, const char* stg, int st) {
 #pragma unroll
       for (int m = 0; m < MV; ++m) fa[buf][m] = frag(stg, offA[st], m);
@@ -153,54 +171,71 @@ __device__ __forceinline__ void gemm_mx4_tile(const TileMX4& io, const uint8_t* 
     };
     auto scales = [&](const char* stg, int w) {
 #pragma unroll
-      for (int m = 0; m < MV; ++m) sa[m] = scl(stg, offSA, w, m);
+      for (int m = 0; m < MV; ++m) sa[w][m] = scl(stg, offSA, w, m);
 #pragma unroll
-      for (int n = 0; n < 4; ++n) sb[n] = scl(stg, offSB, w, n);
+      for (int n = 0; n < 4; ++n) sb[w][n] = scl(stg, offSB, w, n);
     };
-    auto mfmas = [&](int buf, int st) {
+    auto mfmas = [&](int st) {           // sub-step st: fragment set st & 1, scale word st >> 1
+      const int buf = st & 1, w = st >> 1;
 #pragma unroll
       for (int m = 0; m < MV; ++m)
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           if (st & 1)
             acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(fa[buf][m]), wide(fb[buf][n]), acc[m][n], 4,
-                                                                        4, 2, sa[m], 2, sb[n]);
+                                                                        4, 2, sa[w][m], 2, sb[w][n]);
           else
             acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(fa[buf][m]), wide(fb[buf][n]), acc[m][n], 4,
-                                                                        4, 0, sa[m], 0, sb[n]);
+                                                                        4, 0, sa[w][m], 0, sb[w][n]);
         }
     };
-    if constexpr (MV > 0) {
-      load(0, smem, 0);
-      scales(smem, 0);
-    }
-    for (int ks = 0; ks < nk; ++ks) {
-      const char* cs = smem + (ks & 1) * kMx4StageBytes;
-      const char* ns = smem + ((ks + 1) & 1) * kMx4StageBytes;   // after the last stage: stale, unused
-      const bool full = !(half_tail && ks == nk - 1);
-      if constexpr (MV > 0) {
-        load(1, cs, 1);
-        mfmas(0, 0);
-        if (full) load(0, cs, 2);
-        mfmas(1, 1);
-        if (full) {
-          scales(cs, 1);
-          load(1, cs, 3);
-          mfmas(0, 2);
-        }
-      }
-      // this wave's fills of stage ks + 1 and its reads of stage ks are done; then everyone's.
-      // The accumulators pass through the statement, so no MFMA moves across the barrier.
+    // this wave's fills of the next stage and its reads of this one are done; then everyone's.
+    // The accumulators pass through the statement, so no MFMA moves across the barrier.
+    auto meet = [&]() {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier"
                    : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[0][2]), "+v"(acc[0][3]), "+v"(acc[1][0]),
                      "+v"(acc[1][1]), "+v"(acc[1][2]), "+v"(acc[1][3])
                    :
                    : "memory");
+    };
+    if constexpr (MV > 0) {
+      load(0, smem, 0);
+      scales(smem, 0);
+    }
+    const int nfull = half_tail ? nk - 1 : nk;
+    for (int ks = 0; ks < nfull; ++ks) {
+      const char* cs = smem + (ks & 1) * kMx4StageBytes;
+      const char* ns = smem + ((ks + 1) & 1) * kMx4StageBytes;   // after the last stage: stale, unused
+      asm volatile("" : "+v"(offA[0]), "+v"(offA[1]), "+v"(offA[2]), "+v"(offA[3]), "+v"(offB[0]), "+v"(offB[1]),
+                   "+v"(offB[2]), "+v"(offB[3]), "+v"(offSA), "+v"(offSB));
+      if constexpr (MV > 0) {
+        load(1, cs, 1);
+        mfmas(0);
+        load(0, cs, 2);
+        scales(cs, 1);
+        mfmas(1);
+        load(1, cs, 3);
+        mfmas(2);
+        if constexpr (MV == 2) {
+          MOE_MX4_SPREAD;
+          MOE_MX4_SPREAD;
+          MOE_MX4_SPREAD;
+        }
+      }
+      meet();
       if (ks + 2 < nk) issue(ks + 2);     // into stage ks, which nobody reads any more
       if constexpr (MV > 0) {
         load(0, ns, 0);
-        if (full) mfmas(1, 3);
         scales(ns, 0);
+        mfmas(3);
+        if constexpr (MV == 2) MOE_MX4_SPREAD;
+      }
+    }
+    if (half_tail) {                      // the last stage's first half: sub-steps 0 and 1
+      if constexpr (MV > 0) {
+        load(1, smem + (nfull & 1) * kMx4StageBytes, 1);
+        mfmas(0);
+        mfmas(1);
       }
     }
   };
@@ -208,6 +243,13 @@ __device__ __forceinline__ void gemm_mx4_tile(const TileMX4& io, const uint8_t* 
   else if (mv == 1) kloop(std::integral_constant<int, 1>{});
   else kloop(std::integral_constant<int, 0>{});
   __syncthreads();                        // the epilogues reuse the stages
+
+  // The epilogue's lane indices are re-derived through an opaque copy, so the compiler cannot
+  // hoist its store offsets above the main loop, where they would hold registers.
+  int lane_o = lane;
+  asm volatile("" : "+v"(lane_o));
+  const int r32o = lane_o & 31, hio = lane_o >> 5;
+  const int tido = wave * 64 + lane_o;
 
   // Epilogue through LDS, as the MXFP8 tile: a row-major tile whose rows are padded by 16 bytes;
   // the lane layout of the accumulators is column r32, rows 8*(e/4) + 4*hi + e%4 of each block.
@@ -225,20 +267,20 @@ __device__ __forceinline__ void gemm_mx4_tile(const TileMX4& io, const uint8_t* 
     if (MODE == 0) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const int fc = (wn * 2 + q) * 32 + r32;
+        const int fc = (wn * 2 + q) * 32 + r32o;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int row = rb0 + 8 * (e >> 2) + 4 * hi + (e & 3);
+          const int row = rb0 + 8 * (e >> 2) + 4 * hio + (e & 3);
           *reinterpret_cast<float*>(ot + row * kPitch + fc * 4) = silu_f32(acc[m][2 * q][e]) * acc[m][2 * q + 1][e];
         }
       }
     } else {
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        const int cc = wn * 128 + n * 32 + r32;
+        const int cc = wn * 128 + n * 32 + r32o;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int row = rb0 + 8 * (e >> 2) + 4 * hi + (e & 3);
+          const int row = rb0 + 8 * (e >> 2) + 4 * hio + (e & 3);
           *reinterpret_cast<uint16_t*>(ot + row * kPitch + cc * 2) = uint16_t(pack_bf16x2(acc[m][n][e], 0.0f));
         }
       }
@@ -247,7 +289,7 @@ __device__ __forceinline__ void gemm_mx4_tile(const TileMX4& io, const uint8_t* 
   __syncthreads();
   if (MODE == 0) {
     uint8_t* hq = static_cast<uint8_t*>(io.o);
-    for (int b = tid; b < kGemmBM * 4; b += kGemmThreads) {    // 4 blocks of 32 f per row
+    for (int b = tido; b < kGemmBM * 4; b += kGemmThreads) {    // 4 blocks of 32 f per row
       const int row = b >> 2, blk = b & 3;
       if (row >= rows) continue;
       const f32x4* src = reinterpret_cast<const f32x4*>(ot + row * kPitch + blk * 128);
@@ -272,7 +314,7 @@ __device__ __forceinline__ void gemm_mx4_tile(const TileMX4& io, const uint8_t* 
   } else {
     uint16_t* orow0 = static_cast<uint16_t*>(io.o);
     const int ncols = min(kGemmBN, Nout - c0);
-    for (int v = tid; v < kGemmBM * (kGemmBN / 8); v += kGemmThreads) {
+    for (int v = tido; v < kGemmBM * (kGemmBN / 8); v += kGemmThreads) {
       const int row = v >> 5, cv = v & 31;                   // 32 vectors of 8 bf16 per row
       if (row < rows && cv * 8 < ncols) {
         uint16_t* orow = io.row_dst ? reinterpret_cast<uint16_t*>(io.row_dst[row]) : orow0 + size_t(row) * Nout;

@@ -157,10 +157,8 @@ __device__ int block_excl_scan_1024(int v, int* tmp16, int* total) {
   return excl;
 }
 
-// choices: blockbase[b * El] holds, on entry, whether block b's given choices are invalid
-// (choices_hist_kernel); they are all read before blockbase is written
 __global__ __launch_bounds__(1024) void layout_scan_kernel(
-    const int32_t* __restrict__ e2l, int E, int El, int nb, int bm, int mb, bool choices,
+    const int32_t* __restrict__ e2l, int E, int El, int nb, int bm, int mb,
     const int32_t* __restrict__ blockhist, int32_t* __restrict__ blockbase,
     int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ l2g,
     int32_t* __restrict__ mtile_base, int32_t* __restrict__ chunk_base, int32_t* __restrict__ ctrl) {
@@ -199,9 +197,6 @@ __global__ __launch_bounds__(1024) void layout_scan_kernel(
   __syncthreads();
   for (int l = tid; l < El; l += 1024)
     if (seen[l] != 1) atomicOr(&bad, 1);
-  if (choices)
-    for (int b = tid; b < nb; b += 1024)
-      if (blockbase[size_t(b) * El]) atomicOr(&bad, 1);
   __syncthreads();
   if (bad) {
     for (int l = tid; l <= El; l += 1024) {
@@ -312,10 +307,7 @@ __global__ __launch_bounds__(64) void slot_assign_kernel(
     const int64_t p = pb + lane;
     const bool inr = p < p1;
     int l = -1;
-    if (inr && ok) {
-      const int e = topk_idx[p];              // ok: every choice lies in [-1, E)
-      if (e >= 0) l = map[e];
-    }
+    if (inr && ok) l = map[topk_idx[p]];
     const int key = l + 1;
     unsigned long long m = __ballot(l >= 0);
     for (int b = 0; b < nbits; ++b) {
@@ -349,26 +341,6 @@ static void launch_topk(dim3 grid, hipStream_t st, const RankPtrs<const float*>&
                      topk_w, blockhist);
 }
 
-hipError_t launch_choices_hist(const moe_shape_t& s, const int32_t* idx, int32_t* blockhist, int32_t* bad, int El,
-                               int nb, hipStream_t st);
-
-// scan and slots, from the choices and their block histograms
-static hipError_t launch_slots(const moe_shape_t& s, const int32_t* e2l, int El, int mb, const int32_t* topk_idx,
-                               int32_t* counts, int32_t* offsets, int32_t* pull_src, int32_t* slot_of, char* ws,
-                               const WsLayout& L, bool choices, hipStream_t st) {
-  int32_t* blockhist = reinterpret_cast<int32_t*>(ws + L.blockhist);
-  int32_t* blockbase = reinterpret_cast<int32_t*>(ws + L.blockbase);
-  int32_t* ctrl = reinterpret_cast<int32_t*>(ws + L.ctrl);
-  const int bm = (s.dtype == MOE_F32) ? kF32BM : kGemmBM;
-  hipLaunchKernelGGL(layout_scan_kernel, dim3(1 + (s.E + 63) / 64), dim3(1024), 0, st, e2l, s.E, El,
-                     L.nb, bm, mb, choices, blockhist, blockbase, counts, offsets,
-                     reinterpret_cast<int32_t*>(ws + L.l2g), reinterpret_cast<int32_t*>(ws + L.mtile_base),
-                     reinterpret_cast<int32_t*>(ws + L.chunk_base), ctrl);
-  hipLaunchKernelGGL(slot_assign_kernel, dim3(L.nb), dim3(64), 0, st, topk_idx, e2l, s.R, s.T, s.E, s.k, El,
-                     blockbase, ctrl, slot_of, pull_src);
-  return hipGetLastError();
-}
-
 hipError_t launch_layout(const moe_shape_t& s, const int32_t* e2l, int El, int mb,
                          const float* const* logits, int32_t* topk_idx, float* topk_w, int32_t* counts,
                          int32_t* offsets, int32_t* pull_src, int32_t* slot_of, char* ws,
@@ -376,6 +348,8 @@ hipError_t launch_layout(const moe_shape_t& s, const int32_t* e2l, int El, int m
   RankPtrs<const float*> lp{};
   for (int r = 0; r < s.R; ++r) lp.p[r] = logits[r];
   int32_t* blockhist = reinterpret_cast<int32_t*>(ws + L.blockhist);
+  int32_t* blockbase = reinterpret_cast<int32_t*>(ws + L.blockbase);
+  int32_t* ctrl = reinterpret_cast<int32_t*>(ws + L.ctrl);
   const dim3 grid(L.nb);
   const int vpl_need = (s.E + 15) / 16;
   if (vpl_need <= 1) launch_topk<1>(grid, st, lp, s, topk_idx, topk_w, blockhist);
@@ -386,17 +360,317 @@ hipError_t launch_layout(const moe_shape_t& s, const int32_t* e2l, int El, int m
   else if (vpl_need <= 32) launch_topk<32>(grid, st, lp, s, topk_idx, topk_w, blockhist);
   else launch_topk<64>(grid, st, lp, s, topk_idx, topk_w, blockhist);
 
-  return launch_slots(s, e2l, El, mb, topk_idx, counts, offsets, pull_src, slot_of, ws, L, false, st);
+  const int bm = (s.dtype == MOE_F32) ? kF32BM : kGemmBM;
+  hipLaunchKernelGGL(layout_scan_kernel, dim3(1 + (s.E + 63) / 64), dim3(1024), 0, st, e2l, s.E, El,
+                     L.nb, bm, mb, blockhist, blockbase, counts, offsets,
+                     reinterpret_cast<int32_t*>(ws + L.l2g), reinterpret_cast<int32_t*>(ws + L.mtile_base),
+                     reinterpret_cast<int32_t*>(ws + L.chunk_base), ctrl);
+  hipLaunchKernelGGL(slot_assign_kernel, grid, dim3(64), 0, st, topk_idx, e2l, s.R, s.T, s.E, s.k, El,
+                     blockbase, ctrl, slot_of, pull_src);
+  return hipGetLastError();
 }
 
-// the layout of given choices: no routing
+// ---------------------------------------------------------------------------
+// Layout of given choices (any router; -1 = no expert).  Same outputs and tables as above.
+//
+// The choices are [R][T][k] in (r, t, j) order, so a block of consecutive pairs needs only how
+// many pairs of each expert came before it.  At most kChoiceBlocks blocks, each at least
+// 4096 pairs: choices_count_kernel writes every block's histogram, and choices_slots_kernel
+// sums the blocks before its own (and all of them, for the offsets) itself, so there is no scan
+// kernel between them; up to 4096 pairs one workgroup does it all in one launch.  Bound by the
+// latency of its dependent steps, not by bytes, so a wave holds its pairs' choices in registers
+// through all phases where they are four groups of 64 (HELD), and few pairs and experts take a
+// workgroup of 256 threads, whose barriers are cheaper.
+// ---------------------------------------------------------------------------
+constexpr int kChoiceBlocks = 128, kChoiceHeld = 4;
+
+// exclusive prefixes over the block of three values at once, and their totals
+template <int NT>
+__device__ __forceinline__ void block_excl_scan3(const int (&v)[3], int (&ex)[3], int (&total)[3], int (*tmp)[16]) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    int x = v[i];
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int y = __shfl_up(x, off, 64);
+      if (lane >= off) x += y;
+    }
+    if (lane == 63) tmp[i][w] = x;
+    ex[i] = x - v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    int all = 0, before = 0;
+#pragma unroll
+    for (int q = 0; q < NT / 64; ++q) {
+      before += q < w ? tmp[i][q] : 0;
+      all += tmp[i][q];
+    }
+    ex[i] += before;
+    total[i] = all;
+  }
+}
+
+// A wave's run of whole 64-pair groups of a block's pairs [p0, p1)
+struct PairRun {
+  uint32_t begin, end;
+};
+template <int NT>
+__device__ __forceinline__ PairRun wave_pairs(uint32_t p0, uint32_t p1) {
+  const uint32_t run = ((p1 - p0 + NT - 1) / NT) * 64;
+  const uint32_t b = p0 + (threadIdx.x >> 6) * run;
+  return {b, min(p1, b + run)};
+}
+
+// calls f(group's first pair, this lane's choice or -1) for each group of the run, from `held` where
+// HELD (at most kChoiceHeld groups)
+template <bool HELD, typename F>
+__device__ __forceinline__ void each_group(const int32_t* __restrict__ idx, const PairRun r, const int (&held)[kChoiceHeld],
+                                           F f) {
+  const int lane = threadIdx.x & 63;
+  if constexpr (HELD) {
+#pragma unroll
+    for (int i = 0; i < kChoiceHeld; ++i)
+      if (r.begin + i * 64 < r.end) f(r.begin + i * 64, held[i]);
+  } else {
+    for (uint32_t pb = r.begin; pb < r.end; pb += 64) f(pb, pb + lane < r.end ? idx[pb + lane] : -1);
+  }
+}
+
+template <bool HELD>
+__device__ __forceinline__ void hold(const int32_t* __restrict__ idx, const PairRun r, int (&held)[kChoiceHeld]) {
+#pragma unroll
+  for (int i = 0; i < kChoiceHeld; ++i) {
+    const uint32_t p = r.begin + i * 64 + (threadIdx.x & 63);
+    held[i] = HELD && p < r.end ? idx[p] : -1;
+  }
+}
+
+// adds a run's pairs to hist; sets *wrong for a choice outside [-1, E) or an expert that a token
+// names twice (the tables hold at most one row per token and expert)
+template <bool HELD>
+__device__ __forceinline__ void count_choices(const int32_t* __restrict__ idx, const PairRun r,
+                                              const int (&held)[kChoiceHeld], int E, int k, int* hist, int* wrong) {
+  const int lane = threadIdx.x & 63;
+  const bool aligned = 64 % k == 0;          // no token crosses a group of 64 (runs begin at multiples of 64)
+  each_group<HELD>(idx, r, held, [&](uint32_t pb, int e) {
+    const uint32_t p = pb + lane;
+    const int j = int(p % uint32_t(k));
+    bool twice = false;
+    for (int o = 1; o < k; ++o) {            // the token's earlier choices: other lanes', or past the group's edge
+      int q = __shfl_up(e, o, 64);
+      if (!aligned && j >= o && lane < o && p < r.end) q = idx[p - o];
+      twice |= j >= o && q == e;
+    }
+    if (e < -1 || e >= E || (twice && e >= 0)) *wrong = 1;
+    else if (e >= 0) atomicAdd(&hist[e], 1);
+  });
+}
+
+// table[b][E + 1]: block b's histogram over the experts, then whether its choices are invalid
+template <bool HELD>
+__global__ __launch_bounds__(1024) void choices_count_kernel(const int32_t* __restrict__ idx, uint32_t P, uint32_t PB,
+                                                             int E, int k, int32_t* __restrict__ table) {
+  __shared__ int hist[1024];
+  __shared__ int wrong;
+  const uint32_t p0 = blockIdx.x * PB;
+  const PairRun run = wave_pairs<1024>(p0, min(P, p0 + PB));
+  int held[kChoiceHeld];
+  hold<HELD>(idx, run, held);
+  for (int e = threadIdx.x; e < E; e += 1024) hist[e] = 0;
+  if (threadIdx.x == 0) wrong = 0;
+  __syncthreads();
+  count_choices<HELD>(idx, run, held, E, k, hist, &wrong);
+  __syncthreads();
+  int32_t* row = table + size_t(blockIdx.x) * (E + 1);
+  for (int e = threadIdx.x; e < E; e += 1024) row[e] = hist[e];
+  if (threadIdx.x == 0) row[E] = wrong;
+}
+
+// E <= MAXE, El <= NT
+template <int NT, int MAXE, bool HELD>
+__global__ __launch_bounds__(NT) void choices_slots_kernel(
+    const int32_t* __restrict__ idx, uint32_t P, uint32_t PB, const int32_t* __restrict__ e2l, int T, int E, int El,
+    int k, int bm, int mb, const int32_t* __restrict__ table, int32_t* __restrict__ counts,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ l2g, int32_t* __restrict__ mtile_base,
+    int32_t* __restrict__ chunk_base, int32_t* __restrict__ ctrl, int32_t* __restrict__ slot_of,
+    int32_t* __restrict__ pull_src) {
+  constexpr int kWaves = NT / 64;
+  extern __shared__ int cnt[];               // [kWaves][El]: the next slot of (wave, local expert)
+  __shared__ int total[MAXE], before[MAXE];  // pairs of a global expert: of all blocks, of earlier ones
+  __shared__ int map[MAXE], seen[MAXE], home[MAXE];
+  __shared__ int tmp[3][16];
+  __shared__ int bad;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int nb = gridDim.x, blk = blockIdx.x;
+  const uint32_t p0 = blk * PB, p1 = min(P, p0 + PB);        // P < 2^31, PB a multiple of 64 * kWaves
+  const PairRun run = wave_pairs<NT>(p0, p1);
+  int held[kChoiceHeld];
+  hold<HELD>(idx, run, held);
+  for (int e = tid; e < E; e += NT) {
+    total[e] = 0;
+    before[e] = 0;
+    map[e] = e2l[e];
+    seen[e] = 0;
+  }
+  for (int i = tid; i < kWaves * El; i += NT) cnt[i] = 0;
+  if (tid == 0) bad = 0;
+  __syncthreads();
+  for (int e = tid; e < E; e += NT) {
+    const int l = map[e];
+    if (l < -1 || l >= El) {
+      bad = 1;
+    } else if (l >= 0) {
+      atomicAdd(&seen[l], 1);
+      home[l] = e;
+    }
+  }
+  if (nb == 1) {
+    count_choices<HELD>(idx, run, held, E, k, total, &bad);
+  } else {
+    int pe = 1;
+    while (pe < E) pe <<= 1;
+    const int per = NT / pe;                 // threads of one expert's column (E <= 1024 = NT here: at least one)
+    const int e = tid & (pe - 1), g = tid / pe;
+    if (e < E) {
+      int t = 0, u = 0;
+#pragma unroll 8
+      for (int b = g; b < nb; b += per) {
+        const int v = table[size_t(b) * (E + 1) + e];
+        t += v;
+        u += b < blk ? v : 0;
+      }
+      atomicAdd(&total[e], t);
+      atomicAdd(&before[e], u);
+    }
+    for (int b = tid; b < nb; b += NT)
+      if (table[size_t(b) * (E + 1) + E]) bad = 1;
+  }
+  // this wave's pairs of each local expert (a choice outside [-1, E) has no place in the map)
+  each_group<HELD>(idx, run, held, [&](uint32_t, int e) {
+    const int l = e >= 0 && e < E ? map[e] : -1;
+    if (l >= 0 && l < El) atomicAdd(&cnt[wave * El + l], 1);
+  });
+  __syncthreads();
+  if (tid < El && seen[tid] != 1) bad = 1;
+  __syncthreads();
+  if (bad) {                                 // nothing is local; slots say so
+    for (uint32_t p = p0 + tid; p < p1; p += NT) slot_of[p] = -1;
+    if (blk == 0) {
+      for (int l = tid; l <= El; l += NT) {
+        offsets[l] = 0;
+        mtile_base[l] = 0;
+        chunk_base[l] = 0;
+      }
+      if (tid == 0) {
+        ctrl[kCtrlStatus] = MOE_EINVAL;
+        ctrl[kCtrlN] = 0;
+        ctrl[kCtrlMTiles] = 0;
+        ctrl[kCtrlChunks] = 0;
+      }
+    }
+    return;
+  }
+  const int rows = tid < El ? total[home[tid]] : 0;
+  const int v[3] = {rows, (rows + bm - 1) / bm, (rows + mb - 1) / mb};
+  int ex[3], all[3];                         // offsets, row tiles, chunks
+  block_excl_scan3<NT>(v, ex, all, tmp);
+  if (tid < El) {
+    int next = ex[0] + before[home[tid]];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const int c = cnt[w * El + tid];
+      cnt[w * El + tid] = next;
+      next += c;
+    }
+  }
+  if (blk == 0) {
+    for (int e = tid; e < E; e += NT) counts[e] = total[e];
+    if (tid < El) {
+      offsets[tid] = ex[0];
+      l2g[tid] = home[tid];
+      mtile_base[tid] = ex[1];
+      chunk_base[tid] = ex[2];
+    }
+    if (tid == 0) {
+      offsets[El] = all[0];
+      mtile_base[El] = all[1];
+      chunk_base[El] = all[2];
+      ctrl[kCtrlN] = all[0];
+      ctrl[kCtrlMTiles] = all[1];
+      ctrl[kCtrlChunks] = all[2];
+      ctrl[kCtrlStatus] = MOE_OK;
+    }
+  }
+  __syncthreads();
+  const int nbits = 32 - __clz(El);          // bits of (l + 1) in [0, El]
+  const unsigned long long below = (1ull << lane) - 1ull;
+  each_group<HELD>(idx, run, held, [&](uint32_t pb, int e) {
+    const uint32_t p = pb + lane;
+    const int l = e >= 0 ? map[e] : -1;
+    const int key = l + 1;
+    unsigned long long m = __ballot(l >= 0);
+    for (int b = 0; b < nbits; ++b) {
+      const bool bit = (key >> b) & 1;
+      const unsigned long long bb = __ballot(bit);
+      m &= bit ? bb : ~bb;
+    }
+    int slot = -1;
+    if (l >= 0) slot = cnt[wave * El + l] + __popcll(m & below);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // every lane has read before one of them adds
+    if (l >= 0 && (m >> lane) == 1ull) cnt[wave * El + l] = slot + 1;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (p < run.end) slot_of[p] = slot;
+    if (slot >= 0) {
+      const uint32_t t = p / uint32_t(k), r = t / uint32_t(T);
+      reinterpret_cast<int2*>(pull_src)[slot] = make_int2(int(r), int(t - r * uint32_t(T)));
+    }
+  });
+}
+
 hipError_t launch_layout_choices(const moe_shape_t& s, const int32_t* e2l, int El, int mb, const int32_t* topk_idx,
                                  int32_t* counts, int32_t* offsets, int32_t* pull_src, int32_t* slot_of, char* ws,
                                  const WsLayout& L, hipStream_t st) {
-  const hipError_t e = launch_choices_hist(s, topk_idx, reinterpret_cast<int32_t*>(ws + L.blockhist),
-                                           reinterpret_cast<int32_t*>(ws + L.blockbase), El, L.nb, st);
-  if (e != hipSuccess) return e;
-  return launch_slots(s, e2l, El, mb, topk_idx, counts, offsets, pull_src, slot_of, ws, L, true, st);
+  static std::atomic<uint64_t> attr_set{0};
+  const hipError_t ea = once_per_device(attr_set, [] {
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(choices_slots_kernel<1024, 1024, true>),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, 16 * 1024 * 4);
+    if (e == hipSuccess)
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(choices_slots_kernel<1024, 1024, false>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, 16 * 1024 * 4);
+    return e;
+  });
+  if (ea != hipSuccess) return ea;
+  const int64_t P = int64_t(s.R) * s.T * s.k;
+  int64_t PB = (P + kChoiceBlocks - 1) / kChoiceBlocks;
+  const bool held = PB <= 1024 * kChoiceHeld;
+  PB = held ? 1024 * kChoiceHeld : (PB + 1023) / 1024 * 1024;
+  const int nb = int((P + PB - 1) / PB);
+  // the histogram region holds E words for each of ceil(R T / 64) token blocks: with k <= 16 there
+  // are at most a quarter as many pair blocks (of at least 4096 pairs, so of 256 tokens), rounded up
+  int32_t* table = reinterpret_cast<int32_t*>(ws + L.blockhist);
+  int32_t* ctrl = reinterpret_cast<int32_t*>(ws + L.ctrl);
+  const int bm = (s.dtype == MOE_F32) ? kF32BM : kGemmBM;
+  const uint32_t p = uint32_t(P), pb = uint32_t(PB);
+  int32_t* l2g = reinterpret_cast<int32_t*>(ws + L.l2g);
+  int32_t* mtb = reinterpret_cast<int32_t*>(ws + L.mtile_base);
+  int32_t* chb = reinterpret_cast<int32_t*>(ws + L.chunk_base);
+  if (P <= 256 * kChoiceHeld && s.E <= 256) {
+    hipLaunchKernelGGL((choices_slots_kernel<256, 256, true>), dim3(1), dim3(256), size_t(4) * El * 4, st, topk_idx, p, pb,
+                       e2l, s.T, s.E, El, s.k, bm, mb, table, counts, offsets, l2g, mtb, chb, ctrl, slot_of, pull_src);
+  } else if (held) {
+    if (nb > 1)
+      hipLaunchKernelGGL(choices_count_kernel<true>, dim3(nb), dim3(1024), 0, st, topk_idx, p, pb, s.E, s.k, table);
+    hipLaunchKernelGGL((choices_slots_kernel<1024, 1024, true>), dim3(nb), dim3(1024), size_t(16) * El * 4, st, topk_idx, p,
+                       pb, e2l, s.T, s.E, El, s.k, bm, mb, table, counts, offsets, l2g, mtb, chb, ctrl, slot_of, pull_src);
+  } else {
+    hipLaunchKernelGGL(choices_count_kernel<false>, dim3(nb), dim3(1024), 0, st, topk_idx, p, pb, s.E, s.k, table);
+    hipLaunchKernelGGL((choices_slots_kernel<1024, 1024, false>), dim3(nb), dim3(1024), size_t(16) * El * 4, st, topk_idx, p,
+                       pb, e2l, s.T, s.E, El, s.k, bm, mb, table, counts, offsets, l2g, mtb, chb, ctrl, slot_of, pull_src);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace moe

@@ -23,6 +23,7 @@ typedef __bf16 bf16v2 __attribute__((ext_vector_type(2)));
 typedef float f32v2 __attribute__((ext_vector_type(2)));
 
 constexpr uint32_t kMx4NaNScale = 255;
+constexpr int kThinRows = 32;             // experts with at most this many rows take the streaming kernel
 
 // E8M0 code -> fp32 (code 0 is 2^-127, a subnormal; code 255 is NaN)
 __device__ __forceinline__ float e8m0_f32(uint32_t code) {

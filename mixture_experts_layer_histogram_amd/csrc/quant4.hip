@@ -128,45 +128,52 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* __res
   }
 }
 
-// xe[s] / xe_scales[s] = MXFP4(x[pull_src[s].rank][pull_src[s].token]); one wave per row, as
-// the MXFP8 gather: a workgroup takes `cr` consecutive rows, keeps their scale words in LDS
-// and writes each K-tile plane's words as one run.
+// xe[s] / xe_scales[s] = MXFP4(x[pull_src[s].rank][pull_src[s].token]); one wave per row, UNROLL
+// 16-byte vectors of it in flight per lane (the whole row for the widths below).  A workgroup
+// takes up to `most` consecutive rows at a time -- fewer when there are not enough rows to give
+// every workgroup that many, since one row alone takes two microseconds of waiting -- keeps
+// their scale words in LDS and writes each K-tile plane's words as one run.
+template <int UNROLL>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 8))) void dispatch_pull_mx4_kernel(
     RankPtrs<const char*> x, const int32_t* __restrict__ pull_src, const int32_t* __restrict__ ctrl,
-    uint8_t* __restrict__ xe, uint8_t* __restrict__ xes, int d, int64_t nmax, int cr) {
-  constexpr int UNROLL = 16;
-  extern __shared__ uint32_t s_sc[];           // [cr][nq + 1]
+    uint8_t* __restrict__ xe, uint8_t* __restrict__ xes, int d, int64_t nmax, int most) {
+  extern __shared__ uint32_t s_sc[];           // [most][nq + 1]
   const int N = ctrl[kCtrlN];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n16 = d >> 3;            // 16-byte source vectors per row (d % 128 == 0: whole 16-lane groups)
   const int nq = d >> 7;             // scale words (K-tile planes) per row
+  const int even = (N + int(gridDim.x) - 1) / int(gridDim.x);
+  const int cr = min(most, max(4, (even + 3) & ~3));
   const int nchunks = (N + cr - 1) / cr;
   uint32_t* xw = reinterpret_cast<uint32_t*>(xes);
   for (int c = blockIdx.x; c < nchunks; c += gridDim.x) {
     const int s0 = c * cr, rows = min(cr, N - s0);
-    for (int rr = wave; rr < rows; rr += 4) {
-      const int s = s0 + rr;
-      const int r = pull_src[2 * int64_t(s)];
-      const int t = pull_src[2 * int64_t(s) + 1];
+    // where this wave's rows (wave, wave + 4, ...: at most 8) come from, one load for all
+    const int mine = s0 + wave + 4 * (lane & 7);
+    int2 from = make_int2(0, 0);
+    if (mine < s0 + rows) from = reinterpret_cast<const int2*>(pull_src)[mine];
+    for (int i = 0; wave + 4 * i < rows; ++i) {
+      const int rr = wave + 4 * i;
+      const int r = __builtin_amdgcn_readlane(from.x, i), t = __builtin_amdgcn_readlane(from.y, i);
       const u32x4* src = reinterpret_cast<const u32x4*>(x.p[r] + int64_t(t) * d * 2);
-      uint32_t* dst = reinterpret_cast<uint32_t*>(xe + int64_t(s) * (d >> 1));
+      uint32_t* dst = reinterpret_cast<uint32_t*>(xe + int64_t(s0 + rr) * (d >> 1));
       for (int base = 0; base < n16; base += 64 * UNROLL) {
         u32x4 v[UNROLL];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-          const int i = base + u * 64 + lane;
+          const int q = base + u * 64 + lane;
           v[u] = u32x4{0, 0, 0, 0};
-          if (i < n16) v[u] = __builtin_nontemporal_load(src + i);
+          if (q < n16) v[u] = __builtin_nontemporal_load(src + q);
         }
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-          const int i = base + u * 64 + lane;
+          const int q = base + u * 64 + lane;
           uint32_t sc;
-          const uint32_t q = mx4_quant8_bf16(v[u], &sc);   // all lanes: quad permutations inside
-          const uint32_t sw = mx_scale_word(sc);            // all lanes: row shifts inside
-          if (i < n16) {
-            dst[i] = q;
-            if ((i & 15) == 0) s_sc[rr * (nq + 1) + (i >> 4)] = sw;
+          const uint32_t code = mx4_quant8_bf16(v[u], &sc);   // all lanes: quad permutations inside
+          const uint32_t sw = mx_scale_word(sc);               // all lanes: row shifts inside
+          if (q < n16) {
+            dst[q] = code;
+            if ((q & 15) == 0) s_sc[rr * (nq + 1) + (q >> 4)] = sw;
           }
         }
       }
@@ -180,7 +187,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 8))) voi
   }
 }
 
-constexpr int kQuant4BlocksPerCU = 8, kGatherMx4BlocksPerCU = 4;
+constexpr int kQuant4BlocksPerCU = 8;
 
 static int quant_grid(int64_t rows, int K, int cus) {
   const int64_t tasks = (rows + kQuantRows - 1) / kQuantRows * ((K + kQuantCols - 1) / kQuantCols);
@@ -221,8 +228,15 @@ hipError_t launch_dispatch_mx4(const moe_shape_t& s, const void* const* x, const
   RankPtrs<const char*> xp{};
   for (int r = 0; r < s.R; ++r) xp.p[r] = static_cast<const char*>(x[r]);
   const int cr = mx_chunk_rows(s.d);
-  hipLaunchKernelGGL(dispatch_pull_mx4_kernel, dim3(cus * kGatherMx4BlocksPerCU), dim3(256),
-                     size_t(cr) * ((s.d >> 7) + 1) * 4, st, xp, pull_src, ctrl, xe, xe_scales, s.d, nmax, cr);
+  const size_t lds = size_t(cr) * ((s.d >> 7) + 1) * 4;
+  const int n16 = s.d >> 3;
+  const dim3 grid(cus * (n16 <= 64 * 8 ? 8 : 4));       // short rows leave registers for more waves
+  if (n16 <= 64 * 4)
+    hipLaunchKernelGGL(dispatch_pull_mx4_kernel<4>, grid, dim3(256), lds, st, xp, pull_src, ctrl, xe, xe_scales, s.d, nmax, cr);
+  else if (n16 <= 64 * 8)
+    hipLaunchKernelGGL(dispatch_pull_mx4_kernel<8>, grid, dim3(256), lds, st, xp, pull_src, ctrl, xe, xe_scales, s.d, nmax, cr);
+  else
+    hipLaunchKernelGGL(dispatch_pull_mx4_kernel<14>, grid, dim3(256), lds, st, xp, pull_src, ctrl, xe, xe_scales, s.d, nmax, cr);
   return hipGetLastError();
 }
 

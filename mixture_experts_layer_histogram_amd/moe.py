@@ -160,17 +160,19 @@ def _p(t):
 
 
 def _table(ts):
-    """Host array of R device pointers."""
+    """Host array of R device pointers (passed as it is: a cast would cost a microsecond and leave a
+    reference cycle to collect)."""
     if ts is None:
         return None
-    ptrs = [_p(t) for t in ts]
-    return ctypes.cast((ctypes.c_void_p * len(ptrs))(*ptrs), ctypes.c_void_p)
+    return (ctypes.c_void_p * len(ts))(*[_p(t) for t in ts])
 
 
 def _stream(stream):
     if stream is None:
+        # the current stream of the current device, without the Stream object that
+        # torch.cuda.current_stream() builds (2.9 us of a small call's 9; this takes 0.2)
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
