@@ -232,7 +232,7 @@ __global__ __launch_bounds__(256, 1) void thin_mx4_kernel(ThinArgs g) {
         float h[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          h[e] = silu_f32(acc[0][e]) * acc[1][e];
+          h[e] = mx4_silu(acc[0][e]) * acc[1][e];
           mx = max(mx, __float_as_uint(h[e]) & 0x7FFFFFFFu);
         }
         mx = max(mx, uint32_t(__shfl_xor(int(mx), 32, 64)));

@@ -271,7 +271,7 @@ __device__ __forceinline__ void gemm_mx4_tile(const TileMX4& io, const uint8_t* 
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int row = rb0 + 8 * (e >> 2) + 4 * hio + (e & 3);
-          *reinterpret_cast<float*>(ot + row * kPitch + fc * 4) = silu_f32(acc[m][2 * q][e]) * acc[m][2 * q + 1][e];
+          *reinterpret_cast<float*>(ot + row * kPitch + fc * 4) = mx4_silu(acc[m][2 * q][e]) * acc[m][2 * q + 1][e];
         }
       }
     } else {
