@@ -11,12 +11,53 @@
 // rows with the same XOR swizzle, direct global->LDS fills), so a stage holds 256 K values and
 // two scale words per row, and four MFMA sub-steps of 64.  K is a multiple of 128: the last
 // stage may hold only half, whose second half is neither read past the rows' ends nor used.
-#include "gemm_mx4_tile.hpp"
+//
+// Weights are the MFMA's first operand and token rows its second, so a lane ends up with 16 of 32
+// columns of one token row and its partner in the other half with the rest: the epilogues work in
+// registers (half exchanges instead of a tile in LDS), and the next tile's first two stages fill
+// while they run; the waits for those fills leave the epilogue's stores in flight.
+#include "gemm_tile.hpp"
+#include "mx4.hpp"
 
 namespace moe {
 
+constexpr int kMx4BK = 256;                                               // K values per stage: 128-byte LDS rows
+constexpr int kMx4RowBytes = kMx4BK / 2;
+constexpr int kMx4DataBytes = (kGemmBM + kGemmBN) * kMx4RowBytes;         // 64 KiB
+constexpr int kMx4ScaleBytes = 2 * (kGemmBM + kGemmBN) * 4;               // two K-tile planes of a word per row
+constexpr int kMx4StageBytes = kMx4DataBytes + kMx4ScaleBytes;
+constexpr int kMx4Lds = 2 * kMx4StageBytes;                               // 136 KiB
+
+// The order the scheduler is asked for in a sub-step of eight MFMAs: a read after each, so that the
+// eight waves' LDS requests do not arrive in bursts.
+#define MOE_MX4_PAIR                             \
+  __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); \
+  __builtin_amdgcn_sched_group_barrier(0x100, 1, 0)
+#define MOE_MX4_SPREAD \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR;        \
+  MOE_MX4_PAIR
+
+// exchanges: the upper half (odd 16-lane rows) of `a` with the lower half (even rows) of `b`
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap_rows16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
 // MODE 0: A = xe codes [*][d/2], B0/B1 = W1/W3 -> h codes [*][F/2] + scales   (256 rows x 128 f)
 // MODE 1: A = h codes [*][F/2],  B0 = W2 -> bf16 [*][d]                        (256 x 256)
+// MODE 2: the same, each row to the address that RowDst holds for it (the fused push)
 // Tile enumeration as in the other grouped GEMMs: a persistent grid walks 8 contiguous
 // per-XCD ranges of the expert-major tile list.
 template <int MODE>
@@ -32,46 +73,330 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
     for (int l = threadIdx.x; l < El; l += kGemmThreads) any |= offsets[l + 1] - offsets[l] >= min_rows;
     if (!__syncthreads_or(any)) return;
   }
-  const int cols_per_tile = (MODE == 0) ? kGemmBN / 2 : kGemmBN;
-  const int NT = (Nout + cols_per_tile - 1) / cols_per_tile;
+  constexpr int kCols = (MODE == 0) ? kGemmBN / 2 : kGemmBN;
+  const int NT = (Nout + kCols - 1) / kCols;
   const int total = ctrl[kCtrlMTiles] * NT;
   const int per_xcd = (total + 7) >> 3;
   const int xcd = blockIdx.x & 7;
   const int wg_per_xcd = gridDim.x >> 3;
-  const int64_t bs_plane = 4 * int64_t(El) * Nout;    // weight scale planes hold every expert's rows
 
-  for (int tt = blockIdx.x >> 3; tt < per_xcd; tt += wg_per_xcd) {
-    const int tau = xcd * per_xcd + tt;
-    if (tau >= total) break;
-    const int mtg = tau / NT;
-    const int l = find_expert(mtile_base, El, mtg);
-    const int mt0 = mtile_base[l];
-    if (offsets[l + 1] - offsets[l] < min_rows) continue;      // the streaming kernel's
-    const int mtl = mtile_base[l + 1] - mt0;
-    const int i_in = tau - mt0 * NT;
-    const int nt = i_in / mtl, mt = i_in - nt * mtl;
-    const int row0 = offsets[l] + mt * kGemmBM;
-    TileMX4 io;
-    io.a = A + size_t(row0) * (K >> 1);
-    io.as = As + 4 * size_t(row0);
-    io.as_plane = 4 * nmax;
-    io.rows = min(kGemmBM, offsets[l + 1] - row0);
-    if (MODE == 0) {
-      io.o = static_cast<uint8_t*>(C) + size_t(row0) * (Nout >> 1);
-      io.os = Cs + 4 * size_t(row0);
-      io.os_plane = 4 * nmax;
-      io.row_dst = nullptr;
-    } else {
-      io.o = C ? static_cast<uint16_t*>(C) + size_t(row0) * Nout : nullptr;   // null C: with RowDst
-      io.os = nullptr;
-      io.os_plane = 0;
-      io.row_dst = RowDst ? RowDst + row0 : nullptr;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int r32 = lane & 31, hi = lane >> 5;
+  const int lch_even = (lane & 7) ^ (lane >> 4);     // fill lane: row lane / 8 of eight, chunk lane % 8 swizzled
+  const int nk = (K + kMx4BK - 1) / kMx4BK;
+  const bool half_tail = (K & 128) != 0;      // the last stage holds 128 K values
+  const uint32_t rb = uint32_t(K >> 1);       // bytes of a row
+
+  // the tiles of this workgroup, in ascending order
+  struct Tile {
+    int l, row0, rows, c0;                    // expert, first row, valid rows (1..256), first column (f)
+  };
+  typedef const __attribute__((address_space(4))) int32_t* sload_t;     // scalar loads: a vector load's wait
+  const sload_t mbase = (sload_t)reinterpret_cast<uintptr_t>(mtile_base);   // would drain the fills in flight
+  const sload_t offs = (sload_t)reinterpret_cast<uintptr_t>(offsets);
+  int tt = int(blockIdx.x >> 3) - wg_per_xcd;
+  Tile next{-1, 0, 0, 0};
+  auto advance = [&]() -> bool {
+    for (;;) {
+      tt += wg_per_xcd;
+      const int tau = xcd * per_xcd + tt;
+      if (tt >= per_xcd || tau >= total) return false;
+      const int mtg = tau / NT;
+      int l = next.l;
+      if (l < 0) l = __builtin_amdgcn_readfirstlane(find_expert(mtile_base, El, mtg));
+      while (l + 1 < El && mbase[l + 1] <= mtg) ++l;
+      next.l = l;
+      const int mt0 = mbase[l], mtl = mbase[l + 1] - mt0;
+      const int o0 = offs[l], o1 = offs[l + 1];
+      if (o1 - o0 < min_rows) continue;       // the streaming kernel's
+      const int i_in = tau - mt0 * NT;
+      const int nt = i_in / mtl, mt = i_in - nt * mtl;
+      next.row0 = o0 + mt * kGemmBM;
+      next.rows = min(kGemmBM, o1 - next.row0);
+      next.c0 = nt * kCols;
+      return true;
     }
-    const size_t wb = size_t(l) * Nout * (K >> 1);
-    const uint8_t* bs0 = Bs0 + 4 * size_t(l) * Nout;
-    const uint8_t* bs1 = (MODE == 0) ? Bs1 + 4 * size_t(l) * Nout : bs0;
-    gemm_mx4_tile<MODE>(io, B0 + wb, (MODE == 0) ? B1 + wb : B0 + wb, bs0, bs1, bs_plane, nt * cols_per_tile, Nout, K,
-                        smem);
+  };
+
+  // fills: this wave's row groups g = wave*4 + i (rows g*8 + lrow) of the A and B tiles, as in
+  // the bf16 and MXFP8 tiles (wave-uniform bases, 32-bit offsets); scale words: waves 0-3 fetch A
+  // rows 64*wave + lane, waves 4-7 B rows 64*(wave-4) + lane.  Rows past the last re-read it.
+  const uint8_t *abase, *bbase, *sp;
+  uint32_t aoff[4], boff[4];
+  const int64_t splane = wave < 4 ? 4 * nmax : 4 * int64_t(El) * Nout;   // weight planes hold every expert's rows
+  auto column = [&](int c0, int row) -> int {
+    return (MODE == 0) ? min(c0 + (row >> 6) * 32 + (row & 31), Nout - 1) : min(c0 + row, Nout - 1);
+  };
+  auto aim = [&](const Tile& t) {
+    int lane_o = lane;                        // opaque: nothing of this is hoisted out of the tile loop,
+    asm volatile("" : "+v"(lane_o));          // where it would hold registers
+    const int lrow = lane_o >> 3, lpos = lane_o & 7;
+    const int lch_even = lpos ^ (lrow >> 1), lch_odd = lpos ^ (4 + (lrow >> 1));
+    abase = wave_uniform(A + size_t(t.row0) * rb);
+    bbase = wave_uniform(((MODE == 0 && (wave & 1)) ? B1 : B0) + size_t(t.l) * Nout * rb);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = (wave * 4 + i) * 8 + lrow;
+      const int lch = (i & 1) ? lch_odd : lch_even;
+      aoff[i] = uint32_t(min(row, t.rows - 1)) * rb + lch * 16;
+      boff[i] = uint32_t(column(t.c0, row)) * rb + lch * 16;
+    }
+    const int row = (wave & 3) * 64 + lane_o;
+    if (wave < 4) sp = As + 4 * size_t(t.row0 + min(row, t.rows - 1));
+    else sp = ((MODE == 0 && ((row >> 5) & 1)) ? Bs1 : Bs0) + 4 * (size_t(t.l) * Nout + column(t.c0, row));
+  };
+  const uint32_t lds_dst0 = __builtin_amdgcn_readfirstlane(lds_addr(smem + wave * 4 * 1024));
+  const uint32_t lds_sc0 = __builtin_amdgcn_readfirstlane(lds_addr(smem + kMx4DataBytes + wave * 256));
+  auto issue = [&](int ks) {
+    const uint32_t stage = uint32_t((ks & 1) * kMx4StageBytes);
+    const uint32_t da = lds_dst0 + stage, db = da + uint32_t(kGemmBM * kMx4RowBytes);
+    const uint32_t ls = lds_sc0 + stage;
+    // the K offset goes into the scalar bases: no vector address work per fill
+    const uint8_t* ak = abase + size_t(ks) * kMx4RowBytes;
+    const uint8_t* bk = bbase + size_t(ks) * kMx4RowBytes;
+    const uint8_t* s0 = sp + (2 * ks) * splane;
+    const uint8_t* s1 = s0 + splane;
+    uint32_t te = 0, to = 0;
+    if (half_tail && ks == nk - 1) {  // chunks 4..7 lie past the row's end: re-read chunks 0..3 (never used)
+      te = uint32_t(lch_even & 4) * 16;
+      to = uint32_t(~lch_even & 4) * 16;       // odd row groups: the chunk ^ 4
+      s1 = s0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t t = (i & 1) ? to : te;
+      uint32_t ao = aoff[i] - t, bo = boff[i] - t;           // opaque: kept as one register each, not as pairs
+      asm volatile("" : "+v"(ao), "+v"(bo));
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(ak + ao), (lds_void_ptr)(uintptr_t)(da + uint32_t(i * 1024)),
+                                       16, 0, 0);
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(bk + bo), (lds_void_ptr)(uintptr_t)(db + uint32_t(i * 1024)),
+                                       16, 0, 0);
+    }
+    __builtin_amdgcn_global_load_lds(static_cast<const void*>(s0), (lds_void_ptr)(uintptr_t)ls, 4, 0, 0);
+    __builtin_amdgcn_global_load_lds(static_cast<const void*>(s1),
+                                     (lds_void_ptr)(uintptr_t)(ls + uint32_t(4 * (kGemmBM + kGemmBN))), 4, 0, 0);
+  };
+
+  f32x16 acc[2][4];
+  // Software pipeline over K, four sub-steps of 64 per 256-value stage.  The fragments of the
+  // next sub-step are read while this one's MFMAs run (an FP4 fragment is 4 registers, so both
+  // sets fit).  The stage's barrier sits before its last sub-step, whose fragments are in
+  // registers by then: the fill two stages ahead goes into the stage nobody reads any more, and
+  // the last sub-step's MFMAs cover the reads of the next stage's first fragments and scales.
+  // Lane (row r32, half hi) supplies the 32 K values of block hi of the 64-value step (16 bytes)
+  // and that block's scale: byte 2 (st & 1) + hi of the row's word st >> 1.
+  int offA[4], offB[4];
+#pragma unroll
+  for (int st = 0; st < 4; ++st) {
+    offA[st] = swz_off(wm * 64 + r32, 2 * st + hi);
+    offB[st] = kGemmBM * kMx4RowBytes + swz_off(wn * 128 + r32, 2 * st + hi);
+  }
+  int offSA = kMx4DataBytes + 4 * (wm * 64 + r32);
+  int offSB = kMx4DataBytes + 4 * (kGemmBM + wn * 128 + r32);
+  auto frag = [&](const char* stg, int off, int m) -> i32x4 {
+    return *reinterpret_cast<const i32x4*>(stg + off + m * 4096);
+  };
+  auto scl = [&](const char* stg, int off, int w, int m) -> int {
+    return int(*reinterpret_cast<const uint32_t*>(stg + off + w * 4 * (kGemmBM + kGemmBN) + 128 * m) >> (8 * hi));
+  };
+  auto wide = [](const i32x4& v) -> i32x8 { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; };
+
+  // stores an epilogue certainly issues for a whole tile (waits may leave so many operations in flight)
+  constexpr int kFills = 10, kStores = (MODE == 0) ? 4 : 16;
+  auto kloop = [&](auto mvc, int behind) {
+    constexpr int MV = decltype(mvc)::value;
+    i32x4 fa[2][2], fb[2][4];            // fragments, two sets
+    int sa[2][2], sb[2][4];              // scale words of a stage's two halves
+    auto load = [&](int buf, const char* stg, int st) {
+#pragma unroll
+      for (int m = 0; m < MV; ++m) fa[buf][m] = frag(stg, offA[st], m);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) fb[buf][n] = frag(stg, offB[st], n);
+    };
+    auto scales = [&](const char* stg, int w) {
+#pragma unroll
+      for (int m = 0; m < MV; ++m) sa[w][m] = scl(stg, offSA, w, m);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) sb[w][n] = scl(stg, offSB, w, n);
+    };
+    auto mfmas = [&](int st) {           // sub-step st: fragment set st & 1, scale word st >> 1
+      const int buf = st & 1, w = st >> 1;
+#pragma unroll
+      for (int m = 0; m < MV; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          if (st & 1)
+            acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(fb[buf][n]), wide(fa[buf][m]), acc[m][n], 4,
+                                                                        4, 2, sb[w][n], 2, sa[w][m]);
+          else
+            acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(fb[buf][n]), wide(fa[buf][m]), acc[m][n], 4,
+                                                                        4, 0, sb[w][n], 0, sa[w][m]);
+        }
+    };
+    // this wave's fills of the next stage and its reads of this one are done; then everyone's.  Stage 1
+    // was filled before the last epilogue's stores, which may still fly; the later stages after them.
+    // The accumulators pass through, so no MFMA moves across the barrier.
+    auto meet = [&]() {                   // one block of code: a branch here would split the schedule
+      asm volatile("s_waitcnt vmcnt(%c9)\n\ts_cmp_lg_u32 %8, 0\n\ts_cbranch_scc1 1f\n\ts_waitcnt vmcnt(0)\n1:\n\t"
+                   "s_waitcnt lgkmcnt(0)\n\ts_barrier"
+                   : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[0][2]), "+v"(acc[0][3]), "+v"(acc[1][0]),
+                     "+v"(acc[1][1]), "+v"(acc[1][2]), "+v"(acc[1][3])
+                   : "s"(behind), "n"(kStores)
+                   : "memory", "scc");
+      behind = 0;                         // opaque below, or the compiler peels the first iteration
+      asm volatile("" : "+s"(behind));
+    };
+    if constexpr (MV > 0) {
+      load(0, smem, 0);
+      scales(smem, 0);
+    }
+    const int nfull = half_tail ? nk - 1 : nk;
+    for (int ks = 0; ks < nfull; ++ks) {
+      const char* cs = smem + (ks & 1) * kMx4StageBytes;
+      const char* ns = smem + ((ks + 1) & 1) * kMx4StageBytes;   // after the last stage: stale, unused
+      asm volatile("" : "+v"(offA[0]), "+v"(offA[1]), "+v"(offA[2]), "+v"(offA[3]), "+v"(offB[0]), "+v"(offB[1]),
+                   "+v"(offB[2]), "+v"(offB[3]), "+v"(offSA), "+v"(offSB));
+      if constexpr (MV > 0) {
+        load(1, cs, 1);
+        mfmas(0);
+        load(0, cs, 2);
+        scales(cs, 1);
+        mfmas(1);
+        load(1, cs, 3);
+        mfmas(2);
+        if constexpr (MV == 2) {
+          MOE_MX4_SPREAD;
+          MOE_MX4_SPREAD;
+          MOE_MX4_SPREAD;
+        }
+      }
+      meet();
+      if (ks + 2 < nk) issue(ks + 2);     // into stage ks, which nobody reads any more
+      if constexpr (MV > 0) {
+        load(0, ns, 0);
+        scales(ns, 0);
+        mfmas(3);
+        if constexpr (MV == 2) MOE_MX4_SPREAD;
+      }
+    }
+    if (half_tail) {                      // the last stage's first half: sub-steps 0 and 1
+      if constexpr (MV > 0) {
+        load(1, smem + (nfull & 1) * kMx4StageBytes, 1);
+        mfmas(0);
+        mfmas(1);
+      }
+    }
+  };
+
+  if (!advance()) return;
+  aim(next);
+  issue(0);
+  if (nk > 1) issue(1);
+  int stores = 0;                       // the fills in flight are followed by kStores stores at least
+  for (;;) {
+    const Tile t = next;
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.0f;
+    // stage 0 landed
+    if (nk > 1 && stores) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kFills + kStores) : "memory");
+    else if (nk > 1) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kFills) : "memory");
+    else if (stores) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kStores) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    // Row padding: a wave whose 32-row blocks lie wholly past the tile's valid rows skips their
+    // fragment reads and MFMAs; it still fills and meets every barrier.
+    const int mv = __builtin_amdgcn_readfirstlane(min(2, max(0, (t.rows - wm * 64 + 31) >> 5)));
+    if (mv == 2) kloop(std::integral_constant<int, 2>{}, stores);
+    else if (mv == 1) kloop(std::integral_constant<int, 1>{}, stores);
+    else kloop(std::integral_constant<int, 0>{}, stores);
+    const bool more = advance();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // every wave has read both stages
+    if (more) {
+      aim(next);
+      issue(0);
+      if (nk > 1) issue(1);
+    }
+    stores = t.rows == kGemmBM && (MODE == 0 || t.c0 + kGemmBN <= Nout);
+
+    // Epilogue.  The lane indices are re-derived through an opaque copy, so the compiler cannot
+    // hoist its offsets above the main loop, where they would hold registers.  Value 4 c + j of an
+    // accumulator is column 8 c + 4 hi + j of its block of 32, of token row r32.  No store moves up past
+    // the fills (the memory clobber): the waits above count on their order.
+    int lane_o = lane;
+    asm volatile("" : "+v"(lane_o) : : "memory");
+    const int r32o = lane_o & 31, hio = lane_o >> 5;
+    if constexpr (MODE == 0) {
+      // h is rounded once, from fp32 to E2M1 under its block's scale: 4-bit activations are what this
+      // dtype means.  Half s stores block 2 wn + s of its row: 16 code bytes and the scale.
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int row = wm * 64 + m * 32 + r32o;
+        uint32_t lo[2], up[2], sc[2];         // codes of this half's columns c = 0, 1 and c = 2, 3
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float h[16];
+          uint32_t mx = 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            h[e] = mx4_silu(acc[m][2 * q][e]) * acc[m][2 * q + 1][e];
+            mx = max(mx, __float_as_uint(h[e]) & 0x7FFFFFFFu);
+          }
+          mx = max(mx, uint32_t(__shfl_xor(int(mx), 32, 64)));
+          sc[q] = mx4_scale_code(mx);
+          const float f = e8m0_f32(sc[q]);
+          lo[q] = mx4_blank(mx) ? 0u : mx4_pack8(f32x4{h[0], h[1], h[2], h[3]}, f32x4{h[4], h[5], h[6], h[7]}, f);
+          up[q] = mx4_blank(mx) ? 0u : mx4_pack8(f32x4{h[8], h[9], h[10], h[11]}, f32x4{h[12], h[13], h[14], h[15]}, f);
+        }
+        swap_halves(lo[0], lo[1]);            // now [0]: the lower half's codes of block s, [1]: the upper half's
+        swap_halves(up[0], up[1]);
+        const u32x4 code = {(lo[0] & 0xFFFFu) | (lo[1] << 16), (lo[0] >> 16) | (lo[1] & 0xFFFF0000u),
+                            (up[0] & 0xFFFFu) | (up[1] << 16), (up[0] >> 16) | (up[1] & 0xFFFF0000u)};
+        if (row < t.rows) {
+          const int blk = wn * 2 + hio;
+          *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(C) + size_t(t.row0 + row) * (Nout >> 1) + (t.c0 >> 1) + blk * 16) = code;
+          Cs[(t.c0 >> 7) * (4 * nmax) + 4 * size_t(t.row0 + row) + blk] = uint8_t(hio ? sc[1] : sc[0]);
+        }
+      }
+    } else if (t.c0 + wn * 128 < Nout) {
+      // bf16 rows, rounded once from fp32 (the row type of this library's expert outputs).  Two
+      // exchanges turn a block's column quads into 16 rows x 64 bytes: lane group g = lane / 16 holds
+      // columns 16 (g & 1) + 8 (g >> 1) .. + 7 of row lane % 16 (first store) and of row + 16 (second).
+      const int r16 = lane_o & 15, g = lane_o >> 4;
+      const int col = t.c0 + wn * 128 + (g & 1) * 16 + (g >> 1) * 8;
+      typedef __attribute__((address_space(1))) u32x4* grow_t;      // global, or a row's address makes flat stores
+      auto row_at = [&](int r, int c) -> grow_t {
+        const int row = t.row0 + min(r, t.rows - 1);
+        uintptr_t p = reinterpret_cast<uintptr_t>(C) + size_t(row) * Nout * 2;
+        if constexpr (MODE == 2) p = RowDst[row];
+        return (grow_t)(p + size_t(c) * 2);
+      };
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int ra = wm * 64 + m * 32 + r16;
+        grow_t pa = row_at(ra, col), pb = row_at(ra + 16, col);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          uint32_t v[2][4];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) v[p][w] = pack_bf16x2(acc[m][n][8 * p + 2 * w], acc[m][n][8 * p + 2 * w + 1]);
+            swap_halves(v[p][0], v[p][2]);
+            swap_halves(v[p][1], v[p][3]);
+          }
+#pragma unroll
+          for (int w = 0; w < 4; ++w) swap_rows16(v[0][w], v[1][w]);
+          if (ra < t.rows) pa[4 * n] = u32x4{v[0][0], v[0][1], v[0][2], v[0][3]};
+          if (ra + 16 < t.rows) pb[4 * n] = u32x4{v[1][0], v[1][1], v[1][2], v[1][3]};
+        }
+      }
+    }
+    if (!more) break;
   }
 }
 
@@ -90,6 +415,9 @@ hipError_t launch_ffn_mx4(const moe_shape_t& s, int El, const uint8_t* xe, const
                                        hipFuncAttributeMaxDynamicSharedMemorySize, kMx4Lds);
     if (e == hipSuccess)
       e = hipFuncSetAttribute(reinterpret_cast<const void*>(grouped_gemm_mx4_kernel<1>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, kMx4Lds);
+    if (e == hipSuccess)
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(grouped_gemm_mx4_kernel<2>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, kMx4Lds);
     return e;
   });
@@ -123,9 +451,11 @@ hipError_t launch_ffn_mx4(const moe_shape_t& s, int El, const uint8_t* xe, const
                                          nmax, El, experts, s.F, s.d, cus, st);
     if (e != hipSuccess) return e;
   }
-  if (wide)
-    hipLaunchKernelGGL(grouped_gemm_mx4_kernel<1>, dim3(grid), dim3(kGemmThreads), kMx4Lds, st, hq, hs, w2, nullptr,
-                       w_scales.w2, nullptr, ye, nullptr, offsets, mtb, ctrl, El, s.F, s.d, nmax, row_dst, min_rows);
+  if (wide) {
+    const auto kernel = row_dst ? grouped_gemm_mx4_kernel<2> : grouped_gemm_mx4_kernel<1>;
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kGemmThreads), kMx4Lds, st, hq, hs, w2, nullptr, w_scales.w2, nullptr, ye,
+                       nullptr, offsets, mtb, ctrl, El, s.F, s.d, nmax, row_dst, min_rows);
+  }
   return hipGetLastError();
 }
 
