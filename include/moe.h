@@ -90,8 +90,8 @@ typedef struct {
  * Block scales of MXFP8 or MXFP4 expert weights (moe_mx_quantize, moe_mx_quantize_to of the
  * bf16 weights), DEVICE pointers, 4-byte aligned.  Used only when dtype is MOE_MXFP8 or
  * MOE_MXFP4, where the weight pointers w1, w3, w2 hold codes of the same [E_local][F][d] /
- * [E_local][d][F] shapes (one byte per value, or half a byte); each scale array covers the whole tensor as one matrix of E_local*F (or
- * E_local*d) rows. */
+ * [E_local][d][F] shapes (one byte per value, or half a byte); each scale array covers the
+ * whole tensor as one matrix of E_local*F (or E_local*d) rows. */
 typedef struct {
   const uint8_t* w1;   /* [d/128][E_local*F][4] */
   const uint8_t* w3;   /* [d/128][E_local*F][4] */
@@ -365,7 +365,8 @@ int moe_layout_choices(const moe_shape_t* s, const moe_placement_t* p, const moe
  * fp32 accumulation, rounded once to the row type; exactly 0 for a token with no local pair.
  * Deterministic; equal to moe_combine_push's y bit for bit.  ye: rows [0, N) of d elements (rows
  * from N on, and the weights of pairs that are not local, are not read); topk_w: [R][T][k] fp32;
- * y: R pointers [T][d].  ye and y 16-byte aligned.
+ * y: R pointers [T][d], which may not overlap ye (MOE_EINVAL where a y is ye itself).  ye and y
+ * 16-byte aligned.
  */
 int moe_combine_merge(const moe_shape_t* s, const moe_placement_t* p, const void* ye, const int32_t* slot_of,
                       const float* topk_w, void* const* y, void* stream);
@@ -374,7 +375,8 @@ int moe_combine_merge(const moe_shape_t* s, const moe_placement_t* p, const void
  * moe_combine_merge_backward -- its gradient for L = sum over (r, t) of <dy[r][t], y[r][t]>:
  *   dye[s][:] = topk_w[r][t][j] * dy[r][t][:]  (rounded once) for the pair with slot_of == s;
  *   dtopk_w[r][t][j] = <dy[r][t], ye[s]>       (fp32), 0 for a pair that is not local.
- * Rows of dye from N on are left as they are.  dye may not overlap ye.  Deterministic.
+ * Rows of dye from N on are left as they are.  dye may overlap neither ye nor a dy (MOE_EINVAL
+ * where it is one of them).  Deterministic.
  * For the bf16 expert backward (moe_expert_ffn_backward), dye goes to the place that
  * moe_backward_rows_info names.  Buffers 16-byte aligned.
  */
@@ -384,7 +386,8 @@ int moe_combine_merge_backward(const moe_shape_t* s, const moe_placement_t* p, c
 /*
  * moe_dispatch_pull_backward -- the gradient of moe_dispatch_pull's copies: dx[r][t][:] = sum
  * over ascending j with slot_of[r][t][j] >= 0 of dxe[slot_of[r][t][j]][:], fp32 accumulation,
- * rounded once; exactly 0 for a token with no local pair.  Deterministic.
+ * rounded once; exactly 0 for a token with no local pair.  A dx may not overlap dxe (MOE_EINVAL
+ * where it is dxe itself).  Deterministic.
  */
 int moe_dispatch_pull_backward(const moe_shape_t* s, const moe_placement_t* p, const void* dxe, const int32_t* slot_of,
                                void* const* dx, void* stream);

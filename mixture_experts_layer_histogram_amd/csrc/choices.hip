@@ -219,7 +219,7 @@ hipError_t launch_merge_rows(const moe_shape_t& s, const void* rows, const int32
   for (int r = 0; r < s.R; ++r) yp.p[r] = static_cast<char*>(y[r]);
   const char* src = static_cast<const char*>(rows);
   const int64_t RT = int64_t(s.R) * s.T;
-  const int n16 = s.d * (s.dtype == MOE_F32 ? 4 : 2) / 16;
+  const int64_t n16 = int64_t(s.d) * (s.dtype == MOE_F32 ? 4 : 2) / 16;
   // Long segments once they give every SIMD a wave; below that short ones with all rows in flight.
   const bool few = RT * ((n16 + 255) / 256) < int64_t(cus) * 4;
   const int most = cus * kMergeRowsBlocksPerCU;

@@ -130,6 +130,13 @@ int check_ptr_table(const T* const* tab, int R) {
   return MOE_OK;
 }
 
+// rows that tokens are gathered from or scattered to may not be a rank's rows themselves
+int check_not_in(const void* p, const void* const* t, int R) {
+  for (int r = 0; r < R; ++r)
+    if (t[r] == p) return MOE_EINVAL;
+  return MOE_OK;
+}
+
 int aligned16(const void* q) { return q && !(reinterpret_cast<uintptr_t>(q) & 15); }
 
 // non-null and 4-byte aligned (scale arrays, read as 32-bit words)
@@ -461,7 +468,7 @@ int moe_combine_merge(const moe_shape_t* s, const moe_placement_t* p, const void
   if (rc) return rc;
   if (!slot_of || !topk_w) return MOE_EINVAL;
   if (!aligned16(ye)) return ye ? MOE_EALIGN : MOE_EINVAL;
-  if ((rc = check_ptr_table(y, s->R))) return rc;
+  if ((rc = check_ptr_table(y, s->R)) || (rc = check_not_in(ye, y, s->R))) return rc;
   return hip_rc(launch_merge_rows(*s, ye, slot_of, topk_w, y, cu_count(), static_cast<hipStream_t>(stream)));
 }
 
@@ -473,7 +480,8 @@ int moe_combine_merge_backward(const moe_shape_t* s, const moe_placement_t* p, c
   const void* bufs[] = {ye, dye};
   for (const void* b : bufs)
     if (!aligned16(b)) return b ? MOE_EALIGN : MOE_EINVAL;
-  if ((rc = check_ptr_table(dy, s->R))) return rc;
+  if ((rc = check_ptr_table(dy, s->R)) || (rc = check_not_in(dye, dy, s->R))) return rc;
+  if (dye == ye) return MOE_EINVAL;
   return hip_rc(launch_merge_rows_bwd(*s, dy, ye, slot_of, topk_w, dye, dtopk_w, cu_count(),
                                       static_cast<hipStream_t>(stream)));
 }
@@ -484,7 +492,7 @@ int moe_dispatch_pull_backward(const moe_shape_t* s, const moe_placement_t* p, c
   if (rc) return rc;
   if (!slot_of) return MOE_EINVAL;
   if (!aligned16(dxe)) return dxe ? MOE_EALIGN : MOE_EINVAL;
-  if ((rc = check_ptr_table(dx, s->R))) return rc;
+  if ((rc = check_ptr_table(dx, s->R)) || (rc = check_not_in(dxe, dx, s->R))) return rc;
   return hip_rc(launch_merge_rows(*s, dxe, slot_of, nullptr, dx, cu_count(), static_cast<hipStream_t>(stream)));
 }
 
@@ -502,7 +510,7 @@ int moe_forward_choices(const moe_shape_t* s, const moe_placement_t* p, const mo
     if (!aligned16(b)) return b ? MOE_EALIGN : MOE_EINVAL;
   if (is_mx(s) && ((rc = check_scales(xe_scales)) || (rc = check_w_scales(w_scales)))) return rc;
   if ((rc = check_ptr_table(x, s->R)) || (rc = check_ptr_table(y, s->R))) return rc;
-  if ((rc = check_ws(s, p, ws, ws_bytes))) return rc;
+  if ((rc = check_ws(s, p, ws, ws_bytes)) || (rc = check_not_in(ye, y, s->R))) return rc;
   if ((rc = moe_layout_choices(s, p, ex, topk_idx, counts, offsets, pull_src, slot_of, ws, ws_bytes, stream))) return rc;
   if ((rc = moe_dispatch_pull(s, p, x, pull_src, offsets, xe, xe_scales, ws, ws_bytes, stream))) return rc;
   if ((rc = moe_expert_ffn(s, p, ex, xe, xe_scales, offsets, w1, w3, w2, w_scales, ye, ws, ws_bytes, stream)))

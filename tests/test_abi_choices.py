@@ -84,6 +84,16 @@ def test_bad_shapes(name, kw, El, code):
     assert _call(name, _shape(**kw), _fill(CALLS[name]), moe.Placement(FAKE, El)) == code
 
 
+def test_outputs_in_place_of_inputs():
+    """A row moved onto rows that other tokens still read: the same pointer is refused."""
+    s, other = _shape(), FAKE + (1 << 30)
+    both = _tab(last=other)                                              # rank 0's rows are at FAKE
+    assert _call("moe_combine_merge", s, [FAKE, FAKE, FAKE, both, None]) == -1
+    assert _call("moe_combine_merge", s, [other, FAKE, FAKE, both, None]) == -1
+    assert _call("moe_combine_merge_backward", s, [both, other + 64, FAKE, FAKE, other + 64, FAKE, None]) == -1
+    assert _call("moe_dispatch_pull_backward", s, [other, FAKE, both, None]) == -1
+
+
 def test_small_workspace_and_exec_knobs():
     for name in ("moe_layout_choices", "moe_forward_choices"):
         spec = list(CALLS[name])

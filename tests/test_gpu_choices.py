@@ -128,6 +128,42 @@ def test_bad_choices_are_refused_on_the_device(what, T):
     assert L.layout(dup) == 0
 
 
+@pytest.mark.parametrize("R,T,E,El,k,drop", [(8, 8192, 16, 8, 9, 0.1), (3, 7000, 256, 32, 6, 0.02),
+                                              (64, 513, 1024, 1000, 16, 0.0)])
+def test_layout_of_many_choices(R, T, E, El, k, drop):
+    """Many workgroups, tokens across the groups and blocks they split the pairs at (k does not divide 64), and
+    more pairs than the workgroups hold in registers (more than 524288); slots by a stable sort."""
+    print(f"[choices] layout R{R} T{T} E{E}/{El} k{k}", flush=True)
+    rng = np.random.default_rng(11)
+    idx = np.argsort(rng.random((R * T, E), dtype=np.float32), axis=1)[:, :k].astype(np.int32).reshape(R, T, k)
+    idx[rng.random(idx.shape) < drop] = -1
+    e2l = _e2l(rng, E, El)
+    L = Layer(R, T, 128, E, El, k, "bf16", e2l)
+    assert L.layout(idx) == 0
+    flat = idx.reshape(-1)
+    l = np.where(flat >= 0, e2l[flat], -1)
+    local = np.flatnonzero(l >= 0)
+    order = local[np.argsort(l[local], kind="stable")]
+    slot = np.full(flat.shape, -1, dtype=np.int32)
+    slot[order] = np.arange(len(order), dtype=np.int32)
+    assert np.array_equal(L.slot_of.cpu().numpy().reshape(-1), slot)
+    assert np.array_equal(L.counts.cpu().numpy(), np.bincount(flat[flat >= 0], minlength=E))
+    assert np.array_equal(L.offsets.cpu().numpy(), np.concatenate([[0], np.cumsum(np.bincount(l[local], minlength=El))]))
+    src = L.pull_src.cpu().numpy()[:len(order)]
+    assert np.array_equal(src[:, 0], order // (T * k)) and np.array_equal(src[:, 1], order // k % T)
+    # one bad choice anywhere refuses all of it: across a group's edge, across a block's, in the last token
+    for at in (63 // k, 4096 // k, (R * T * k // 2) // k, R * T - 1):
+        bad = idx.reshape(-1, k).copy()
+        bad[at] = np.arange(k)
+        bad[at, k - 1] = bad[at, 0]
+        assert L.layout(bad.reshape(R, T, k)) == -1, at
+        assert (L.slot_of == -1).all() and (L.offsets == 0).all()
+    bad = idx.copy()
+    bad[R - 1, T - 1, k - 1] = E
+    assert L.layout(bad) == -1
+    assert L.layout(idx) == 0 and np.array_equal(L.slot_of.cpu().numpy().reshape(-1), slot)
+
+
 MOVES = [  # R, T, d, E, El, k, drop, dtype
     (1, 1, 64, 4, 4, 1, 0.0, "bf16"), (1, 1, 4, 4, 4, 2, 0.0, "f32"), (1, 3, 12, 8, 3, 8, 0.4, "f32"),
     (2, 65, 128, 16, 16, 4, 0.2, "bf16"), (1, 130, 2048, 64, 64, 6, 0.0, "bf16"), (3, 50, 7168, 32, 8, 8, 0.1, "bf16"),

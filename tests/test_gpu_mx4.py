@@ -268,6 +268,85 @@ def test_expert_rows_within_their_bounds(name):
     assert P.status() == 0 and torch.equal(lay, P.slot_of) and all(torch.equal(a, b) for a, b in zip(y, P.y))
 
 
+def _check_some_rows(P, ye, rows, w):
+    """The given rows of ye within their bounds."""
+    off = P.offsets.cpu().numpy()
+    src = P.pull_src.cpu().numpy()
+    for l in range(len(off) - 1):
+        r = rows[(rows >= off[l]) & (rows < off[l + 1])]
+        if not len(r):
+            continue
+        x = np.stack([P.x[src[i, 0]][src[i, 1]].double().cpu().numpy() for i in r])
+        ref, allow = _bound(M4.quantize(x)[2], w[0][l], w[1][l], w[2][l])
+        err = np.abs(ye[r].double().cpu().numpy() - ref)
+        lim = allow + (np.abs(ref) + allow) * 2.0 ** -8 + 1e-38
+        assert (err <= lim).all(), (l, float((err / lim).max()), r[np.argwhere(err > lim)[:4, 0]].tolist())
+
+
+def _push(P, idx, wgt):
+    """The choices' layer with the push fused into the down product; the merged rows."""
+    torch = _torch()
+    w1, w3, w2 = P.weights()
+    for t in P.recv:
+        t.fill_(float("nan"))
+    moe.moe_layout_choices(P.shape, P.placement, P.ex, idx, P.counts, P.offsets, P.pull_src, P.slot_of, P.ws)
+    P.dispatch()
+    moe.moe_expert_ffn_push(P.shape, P.placement, P.ex, P.xe, P.offsets, w1, w3, w2, P.pull_src, P.slot_of, P.recv, P.ws,
+                            w_scales=P.w_scales, xe_scales=P.xe_scales)
+    y = [torch.full_like(t, float("nan")) for t in P.y]
+    moe.moe_weighted_merge(P.shape, P.placement, P.slot_of, wgt, P.recv, y)
+    return y
+
+
+@pytest.mark.parametrize("T,d,F,E,k", [(26000, 512, 1024, 4, 1), (140000, 256, 128, 4, 1), (9000, 1152, 896, 8, 4)])
+def test_many_tiles_a_workgroup(T, d, F, E, k):
+    """Three and more tiles a workgroup, whole and partial ones in turn, of one, two and several stages, with
+    half stages and half columns: the next tile's fills run under the last one's stores."""
+    torch = _torch()
+    cfg = _cfg(f"mx4 many tiles T{T} d{d} F{F} E{E} k{k}", T=T, d=d, F=F, E=E, E_local=E, k=k)
+    print(f"[mx4] {cfg.name}", flush=True)
+    inp, P = _problem(cfg)
+    P.ye.fill_(float("nan"))
+    P.forward()
+    assert P.status() == 0
+    off = P.offsets.cpu().numpy()
+    N = int(off[-1])
+    assert N == T * k and torch.isfinite(P.ye[:N]).all()
+    edges = np.concatenate([np.concatenate([np.arange(a, b, 256), np.arange(a, b, 256) + 255]) for a, b in zip(off, off[1:])])
+    rows = np.unique(np.concatenate([edges[edges < N][:: max(1, len(edges) // 400)], [0, N - 1],
+                                     np.random.default_rng(3).integers(0, N, 200)]))
+    _check_some_rows(P, P.ye, rows, _weights64(P))
+    y = [t.clone() for t in P.y]
+    for _ in range(3):                        # the same bits whatever the timing, and through the fused push
+        P.ye.fill_(float("nan"))
+        P.forward_choices(P.topk_idx.clone(), P.topk_w.clone())
+        assert all(torch.equal(a, b) for a, b in zip(y, P.y))
+    assert all(torch.equal(a, b) for a, b in zip(y, _push(P, P.topk_idx.clone(), P.topk_w.clone())))
+
+
+def test_few_and_many_rows_in_one_call():
+    """Experts of 100, 33, 32, 31, 1 and 0 rows where few are expected: each of the two product kernels
+    takes its own."""
+    torch = _torch()
+    cfg = _cfg("mx4 few and many rows", T=100, d=640, F=384, E=16, E_local=16, k=2)
+    inp, P = _problem(cfg)
+    idx = np.full((1, 100, 2), -1, dtype=np.int32)
+    idx[0, :, 0] = 0
+    for e, (a, b) in enumerate([(0, 33), (33, 65), (65, 96), (96, 97)], start=1):
+        idx[0, a:b, 1] = e
+    idx = torch.from_numpy(idx).cuda()
+    wgt = torch.rand(1, 100, 2, device="cuda") - 0.5
+    P.ye.fill_(3.0)
+    P.forward_choices(idx, wgt)
+    assert P.status() == 0 and P.counts.tolist() == [100, 33, 32, 31, 1] + [0] * 11
+    N = int(P.offsets[-1])
+    assert (P.ye[N:] == 3.0).all()
+    x64 = P.rows_f64(P.x[0]).reshape(1, cfg.T, cfg.d)
+    _check_rows(P, P.ye, x64, _weights64(P))
+    y = P.y[0].clone()
+    assert torch.equal(y, _push(P, idx, wgt)[0])
+
+
 def test_tokens_without_a_value_stay_apart():
     """A NaN, an infinity or both in a token's row makes that token NaN and touches no other."""
     torch = _torch()
