@@ -384,32 +384,42 @@ hipError_t launch_layout(const moe_shape_t& s, const int32_t* e2l, int El, int m
 // ---------------------------------------------------------------------------
 constexpr int kChoiceBlocks = 128, kChoiceHeld = 4;
 
-// exclusive prefixes over the block of three values at once, and their totals
-template <int NT>
-__device__ __forceinline__ void block_excl_scan3(const int (&v)[3], int (&ex)[3], int (&total)[3], int (*tmp)[16]) {
+// the sum of this and all lower lanes: within rows of 16 lanes, then a row's last lane to the next
+// row, then lane 31 to the upper half
+__device__ __forceinline__ int wave_incl_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
+  return x;
+}
+
+// exclusive prefixes over the block's first `waves` waves of three values at once, and their totals
+// (the other waves' values are zero)
+__device__ __forceinline__ void block_excl_scan3(const int (&v)[3], int (&ex)[3], int (&total)[3], int (*tmp)[16],
+                                                 int waves) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  if (w < waves) {
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    int x = v[i];
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int y = __shfl_up(x, off, 64);
-      if (lane >= off) x += y;
+    for (int i = 0; i < 3; ++i) {
+      const int x = wave_incl_scan(v[i]);
+      if (lane == 63) tmp[i][w] = x;
+      ex[i] = x - v[i];
     }
-    if (lane == 63) tmp[i][w] = x;
-    ex[i] = x - v[i];
   }
   __syncthreads();
+  if (w >= waves) return;
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    int all = 0, before = 0;
+  for (int i = 0; i < 3; ++i) total[i] = 0;
+  for (int q = 0; q < waves; ++q) {
 #pragma unroll
-    for (int q = 0; q < NT / 64; ++q) {
-      before += q < w ? tmp[i][q] : 0;
-      all += tmp[i][q];
+    for (int i = 0; i < 3; ++i) {
+      const int x = tmp[i][q];
+      ex[i] += q < w ? x : 0;
+      total[i] += x;
     }
-    ex[i] += before;
-    total[i] = all;
   }
 }
 
@@ -424,21 +434,6 @@ __device__ __forceinline__ PairRun wave_pairs(uint32_t p0, uint32_t p1) {
   return {b, min(p1, b + run)};
 }
 
-// calls f(group's first pair, this lane's choice or -1) for each group of the run, from `held` where
-// HELD (at most kChoiceHeld groups)
-template <bool HELD, typename F>
-__device__ __forceinline__ void each_group(const int32_t* __restrict__ idx, const PairRun r, const int (&held)[kChoiceHeld],
-                                           F f) {
-  const int lane = threadIdx.x & 63;
-  if constexpr (HELD) {
-#pragma unroll
-    for (int i = 0; i < kChoiceHeld; ++i)
-      if (r.begin + i * 64 < r.end) f(r.begin + i * 64, held[i]);
-  } else {
-    for (uint32_t pb = r.begin; pb < r.end; pb += 64) f(pb, pb + lane < r.end ? idx[pb + lane] : -1);
-  }
-}
-
 template <bool HELD>
 __device__ __forceinline__ void hold(const int32_t* __restrict__ idx, const PairRun r, int (&held)[kChoiceHeld]) {
 #pragma unroll
@@ -448,25 +443,69 @@ __device__ __forceinline__ void hold(const int32_t* __restrict__ idx, const Pair
   }
 }
 
-// adds a run's pairs to hist; sets *wrong for a choice outside [-1, E) or an expert that a token
-// names twice (the tables hold at most one row per token and expert)
-template <bool HELD>
-__device__ __forceinline__ void count_choices(const int32_t* __restrict__ idx, const PairRun r,
-                                              const int (&held)[kChoiceHeld], int E, int k, int* hist, int* wrong) {
+// G groups of 64 pairs from pair pb on, this lane's choice of each in e (-1: none).  m: the lanes of a
+// group that chose what this lane chose, by ballots over the bits of e + 1.  A choice outside [-1, E)
+// or an expert that a token names twice (the tables hold at most one row per token and expert)
+// sets *wrong; the former becomes -1.
+template <int G>
+__device__ __forceinline__ void match_choices(const int32_t* __restrict__ idx, uint32_t pb, uint32_t end, int (&e)[G],
+                                              int E, int k, unsigned long long (&m)[G], int* wrong) {
   const int lane = threadIdx.x & 63;
-  const bool aligned = 64 % k == 0;          // no token crosses a group of 64 (runs begin at multiples of 64)
-  each_group<HELD>(idx, r, held, [&](uint32_t pb, int e) {
-    const uint32_t p = pb + lane;
-    const int j = int(p % uint32_t(k));
-    bool twice = false;
-    for (int o = 1; o < k; ++o) {            // the token's earlier choices: other lanes', or past the group's edge
-      int q = __shfl_up(e, o, 64);
-      if (!aligned && j >= o && lane < o && p < r.end) q = idx[p - o];
-      twice |= j >= o && q == e;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    if (e[i] < -1 || e[i] >= E) {
+      bad = true;
+      e[i] = -1;
     }
-    if (e < -1 || e >= E || (twice && e >= 0)) *wrong = 1;
-    else if (e >= 0) atomicAdd(&hist[e], 1);
-  });
+    m[i] = __ballot(e[i] >= 0);
+  }
+#pragma nounroll                             // executed once: short code costs less than its fetching
+  for (int b = 32 - __clz(E); --b >= 0;)
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const bool bit = ((e[i] + 1) >> b) & 1;
+      const unsigned long long bb = __ballot(bit);
+      m[i] &= bit ? bb : ~bb;
+    }
+  int j = int((pb + lane) % uint32_t(k));    // this lane's place in its token
+  const int step = 64 % k;
+  const unsigned long long token = (1ull << k) - 1ull;
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const int first = lane - j;              // the lane of the token's first choice; in an earlier group if < 0
+    const unsigned long long others = (first >= 0 ? token << first : token >> -first) & ~(1ull << lane);
+    if (e[i] >= 0) {
+      bad |= (m[i] & others) != 0;
+      const uint32_t p = pb + i * 64 + lane;
+      for (int o = lane + 1; o <= j; ++o) bad |= idx[p - o] == e[i];
+    }
+    j += step;
+    if (j >= k) j -= k;
+  }
+  if (bad) *wrong = 1;
+}
+
+// adds a wave's run of pairs to hist; sets *wrong as above
+template <bool HELD>
+__device__ __forceinline__ void count_choices(const int32_t* __restrict__ idx, const PairRun r, int (&held)[kChoiceHeld],
+                                              int E, int k, int* hist, int* wrong) {
+  const int lane = threadIdx.x & 63;
+  const unsigned long long below = (1ull << lane) - 1ull;
+  if constexpr (HELD) {
+    unsigned long long m[kChoiceHeld];
+    match_choices<kChoiceHeld>(idx, r.begin, r.end, held, E, k, m, wrong);
+#pragma unroll
+    for (int i = 0; i < kChoiceHeld; ++i)
+      if (held[i] >= 0 && !(m[i] & below)) atomicAdd(&hist[held[i]], __popcll(m[i]));
+  } else {
+    for (uint32_t pb = r.begin; pb < r.end; pb += 64) {
+      int e[1] = {pb + lane < r.end ? idx[pb + lane] : -1};
+      unsigned long long m[1];
+      match_choices<1>(idx, pb, r.end, e, E, k, m, wrong);
+      if (e[0] >= 0 && !(m[0] & below)) atomicAdd(&hist[e[0]], __popcll(m[0]));
+    }
+  }
 }
 
 // table[b][E + 1]: block b's histogram over the experts, then whether its choices are invalid
@@ -489,7 +528,8 @@ __global__ __launch_bounds__(1024) void choices_count_kernel(const int32_t* __re
   if (threadIdx.x == 0) row[E] = wrong;
 }
 
-// E <= MAXE, El <= NT
+// E <= MAXE, El <= NT.  A pair's slot = its expert's offset + the expert's pairs in earlier blocks
+// (both in `total` after the scan) + in earlier waves and groups (cnt) + in earlier lanes.
 template <int NT, int MAXE, bool HELD>
 __global__ __launch_bounds__(NT) void choices_slots_kernel(
     const int32_t* __restrict__ idx, uint32_t P, uint32_t PB, const int32_t* __restrict__ e2l, int T, int E, int El,
@@ -498,8 +538,8 @@ __global__ __launch_bounds__(NT) void choices_slots_kernel(
     int32_t* __restrict__ chunk_base, int32_t* __restrict__ ctrl, int32_t* __restrict__ slot_of,
     int32_t* __restrict__ pull_src) {
   constexpr int kWaves = NT / 64;
-  extern __shared__ int cnt[];               // [kWaves][El]: the next slot of (wave, local expert)
-  __shared__ int total[MAXE], before[MAXE];  // pairs of a global expert: of all blocks, of earlier ones
+  extern __shared__ int cnt[];               // [kWaves][E]: pairs of (wave, expert), then of those before them
+  __shared__ int total[MAXE], before[MAXE];  // pairs of an expert: of all blocks, of earlier ones
   __shared__ int map[MAXE], seen[MAXE], home[MAXE];
   __shared__ int tmp[3][16];
   __shared__ int bad;
@@ -509,13 +549,28 @@ __global__ __launch_bounds__(NT) void choices_slots_kernel(
   const PairRun run = wave_pairs<NT>(p0, p1);
   int held[kChoiceHeld];
   hold<HELD>(idx, run, held);
+  int pe = 1;
+  while (pe < E) pe <<= 1;
+  const int per = NT / pe, ge = tid & (pe - 1);  // threads of one expert's column of the table (nb > 1: E <= 1024 = NT)
+  int sum_all = 0, sum_before = 0, wrong = 0;
+  if (nb > 1) {
+    if (ge < E) {
+#pragma unroll 8
+      for (int b = tid / pe; b < nb; b += per) {
+        const int v = table[size_t(b) * (E + 1) + ge];
+        sum_all += v;
+        sum_before += b < blk ? v : 0;
+      }
+    }
+    for (int b = tid; b < nb; b += NT) wrong |= table[size_t(b) * (E + 1) + E];
+  }
   for (int e = tid; e < E; e += NT) {
     total[e] = 0;
     before[e] = 0;
     map[e] = e2l[e];
     seen[e] = 0;
   }
-  for (int i = tid; i < kWaves * El; i += NT) cnt[i] = 0;
+  for (int i = tid; i < kWaves * E; i += NT) cnt[i] = 0;
   if (tid == 0) bad = 0;
   __syncthreads();
   for (int e = tid; e < E; e += NT) {
@@ -527,33 +582,46 @@ __global__ __launch_bounds__(NT) void choices_slots_kernel(
       home[l] = e;
     }
   }
-  if (nb == 1) {
-    count_choices<HELD>(idx, run, held, E, k, total, &bad);
-  } else {
-    int pe = 1;
-    while (pe < E) pe <<= 1;
-    const int per = NT / pe;                 // threads of one expert's column (E <= 1024 = NT here: at least one)
-    const int e = tid & (pe - 1), g = tid / pe;
-    if (e < E) {
-      int t = 0, u = 0;
-#pragma unroll 8
-      for (int b = g; b < nb; b += per) {
-        const int v = table[size_t(b) * (E + 1) + e];
-        t += v;
-        u += b < blk ? v : 0;
-      }
-      atomicAdd(&total[e], t);
-      atomicAdd(&before[e], u);
+  // rank: a held pair's place among the wave's pairs of its expert.  The first lane that chose an expert
+  // takes the places of all in its group from the wave's counter; the groups' counters are asked
+  // for one after another (the LDS keeps a wave's order) before the first answer is needed.
+  int* const mine = cnt + wave * E;
+  const unsigned long long below = (1ull << lane) - 1ull;
+  int rank[kChoiceHeld];
+  if constexpr (HELD) {
+    unsigned long long m[kChoiceHeld];
+    int old[kChoiceHeld];
+    match_choices<kChoiceHeld>(idx, run.begin, run.end, held, E, k, m, &bad);
+#pragma unroll
+    for (int i = 0; i < kChoiceHeld; ++i) {
+      old[i] = 0;
+      if (held[i] >= 0 && !(m[i] & below)) old[i] = atomicAdd(&mine[held[i]], __popcll(m[i]));
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // another lane may ask for the same counter next
     }
-    for (int b = tid; b < nb; b += NT)
-      if (table[size_t(b) * (E + 1) + E]) bad = 1;
+#pragma unroll
+    for (int i = 0; i < kChoiceHeld; ++i)
+      rank[i] = __shfl(old[i], held[i] >= 0 ? __builtin_ctzll(m[i]) : 0, 64) + __popcll(m[i] & below);
+  } else {
+    count_choices<false>(idx, run, held, E, k, mine, &bad);
   }
-  // this wave's pairs of each local expert (a choice outside [-1, E) has no place in the map)
-  each_group<HELD>(idx, run, held, [&](uint32_t, int e) {
-    const int l = e >= 0 && e < E ? map[e] : -1;
-    if (l >= 0 && l < El) atomicAdd(&cnt[wave * El + l], 1);
-  });
+  if (nb > 1) {
+    if (ge < E) {
+      atomicAdd(&total[ge], sum_all);
+      atomicAdd(&before[ge], sum_before);
+    }
+    if (wrong) bad = 1;
+  }
   __syncthreads();
+  for (int e = tid; e < E; e += NT) {
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const int c = cnt[w * E + e];
+      cnt[w * E + e] = sum;
+      sum += c;
+    }
+    if (nb == 1) total[e] = sum;
+  }
   if (tid < El && seen[tid] != 1) bad = 1;
   __syncthreads();
   if (bad) {                                 // nothing is local; slots say so
@@ -573,61 +641,69 @@ __global__ __launch_bounds__(NT) void choices_slots_kernel(
     }
     return;
   }
-  const int rows = tid < El ? total[home[tid]] : 0;
+  const int e_of = tid < El ? home[tid] : 0;
+  const int rows = tid < El ? total[e_of] : 0;
+  if (blk == 0)
+    for (int e = tid; e < E; e += NT) counts[e] = total[e];
   const int v[3] = {rows, (rows + bm - 1) / bm, (rows + mb - 1) / mb};
   int ex[3], all[3];                         // offsets, row tiles, chunks
-  block_excl_scan3<NT>(v, ex, all, tmp);
+  block_excl_scan3(v, ex, all, tmp, (El + 63) >> 6);     // its barrier: everyone has read total
   if (tid < El) {
-    int next = ex[0] + before[home[tid]];
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const int c = cnt[w * El + tid];
-      cnt[w * El + tid] = next;
-      next += c;
-    }
-  }
-  if (blk == 0) {
-    for (int e = tid; e < E; e += NT) counts[e] = total[e];
-    if (tid < El) {
+    total[e_of] = ex[0] + before[e_of];
+    if (blk == 0) {
       offsets[tid] = ex[0];
-      l2g[tid] = home[tid];
+      l2g[tid] = e_of;
       mtile_base[tid] = ex[1];
       chunk_base[tid] = ex[2];
     }
-    if (tid == 0) {
-      offsets[El] = all[0];
-      mtile_base[El] = all[1];
-      chunk_base[El] = all[2];
-      ctrl[kCtrlN] = all[0];
-      ctrl[kCtrlMTiles] = all[1];
-      ctrl[kCtrlChunks] = all[2];
-      ctrl[kCtrlStatus] = MOE_OK;
-    }
+  }
+  if (blk == 0 && tid == 0) {
+    offsets[El] = all[0];
+    mtile_base[El] = all[1];
+    chunk_base[El] = all[2];
+    ctrl[kCtrlN] = all[0];
+    ctrl[kCtrlMTiles] = all[1];
+    ctrl[kCtrlChunks] = all[2];
+    ctrl[kCtrlStatus] = MOE_OK;
   }
   __syncthreads();
-  const int nbits = 32 - __clz(El);          // bits of (l + 1) in [0, El]
-  const unsigned long long below = (1ull << lane) - 1ull;
-  each_group<HELD>(idx, run, held, [&](uint32_t pb, int e) {
-    const uint32_t p = pb + lane;
-    const int l = e >= 0 ? map[e] : -1;
-    const int key = l + 1;
-    unsigned long long m = __ballot(l >= 0);
-    for (int b = 0; b < nbits; ++b) {
-      const bool bit = (key >> b) & 1;
-      const unsigned long long bb = __ballot(bit);
-      m &= bit ? bb : ~bb;
-    }
-    int slot = -1;
-    if (l >= 0) slot = cnt[wave * El + l] + __popcll(m & below);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // every lane has read before one of them adds
-    if (l >= 0 && (m >> lane) == 1ull) cnt[wave * El + l] = slot + 1;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  auto put = [&](uint32_t p, uint32_t t, int e, int rank_in_wave) {
+    const int slot = e >= 0 && map[e] >= 0 ? total[e] + rank_in_wave : -1;
     if (p < run.end) slot_of[p] = slot;
     if (slot >= 0) {
-      const uint32_t t = p / uint32_t(k), r = t / uint32_t(T);
+      const uint32_t r = t / uint32_t(T);
       reinterpret_cast<int2*>(pull_src)[slot] = make_int2(int(r), int(t - r * uint32_t(T)));
     }
-  });
+  };
+  const uint32_t pl = run.begin + lane, tl = pl / uint32_t(k);
+  uint32_t t = tl, j = pl - tl * uint32_t(k);                // pair pl is choice j of token t
+  const uint32_t tstep = 64 / k, jstep = 64 % k;
+  auto further = [&]() {
+    t += tstep;
+    j += jstep;
+    if (j >= uint32_t(k)) {
+      j -= k;
+      ++t;
+    }
+  };
+  if constexpr (HELD) {
+#pragma unroll
+    for (int i = 0; i < kChoiceHeld; ++i) {
+      put(pl + i * 64, t, held[i], held[i] >= 0 ? mine[held[i]] + rank[i] : 0);
+      further();
+    }
+  } else {
+    for (uint32_t pb = run.begin; pb < run.end; pb += 64) {
+      int e[1] = {pb + lane < run.end ? idx[pb + lane] : -1};
+      unsigned long long m[1];
+      match_choices<1>(idx, pb, run.end, e, E, k, m, &bad);
+      int old = 0;
+      if (e[0] >= 0 && !(m[0] & below)) old = atomicAdd(&mine[e[0]], __popcll(m[0]));
+      old = __shfl(old, e[0] >= 0 ? __builtin_ctzll(m[0]) : 0, 64);
+      put(pb + lane, t, e[0], old + __popcll(m[0] & below));
+      further();
+    }
+  }
 }
 
 hipError_t launch_layout_choices(const moe_shape_t& s, const int32_t* e2l, int El, int mb, const int32_t* topk_idx,
@@ -658,16 +734,16 @@ hipError_t launch_layout_choices(const moe_shape_t& s, const int32_t* e2l, int E
   int32_t* mtb = reinterpret_cast<int32_t*>(ws + L.mtile_base);
   int32_t* chb = reinterpret_cast<int32_t*>(ws + L.chunk_base);
   if (P <= 256 * kChoiceHeld && s.E <= 256) {
-    hipLaunchKernelGGL((choices_slots_kernel<256, 256, true>), dim3(1), dim3(256), size_t(4) * El * 4, st, topk_idx, p, pb,
+    hipLaunchKernelGGL((choices_slots_kernel<256, 256, true>), dim3(1), dim3(256), size_t(4) * s.E * 4, st, topk_idx, p, pb,
                        e2l, s.T, s.E, El, s.k, bm, mb, table, counts, offsets, l2g, mtb, chb, ctrl, slot_of, pull_src);
   } else if (held) {
     if (nb > 1)
       hipLaunchKernelGGL(choices_count_kernel<true>, dim3(nb), dim3(1024), 0, st, topk_idx, p, pb, s.E, s.k, table);
-    hipLaunchKernelGGL((choices_slots_kernel<1024, 1024, true>), dim3(nb), dim3(1024), size_t(16) * El * 4, st, topk_idx, p,
+    hipLaunchKernelGGL((choices_slots_kernel<1024, 1024, true>), dim3(nb), dim3(1024), size_t(16) * s.E * 4, st, topk_idx, p,
                        pb, e2l, s.T, s.E, El, s.k, bm, mb, table, counts, offsets, l2g, mtb, chb, ctrl, slot_of, pull_src);
   } else {
     hipLaunchKernelGGL(choices_count_kernel<false>, dim3(nb), dim3(1024), 0, st, topk_idx, p, pb, s.E, s.k, table);
-    hipLaunchKernelGGL((choices_slots_kernel<1024, 1024, false>), dim3(nb), dim3(1024), size_t(16) * El * 4, st, topk_idx, p,
+    hipLaunchKernelGGL((choices_slots_kernel<1024, 1024, false>), dim3(nb), dim3(1024), size_t(16) * s.E * 4, st, topk_idx, p,
                        pb, e2l, s.T, s.E, El, s.k, bm, mb, table, counts, offsets, l2g, mtb, chb, ctrl, slot_of, pull_src);
   }
   return hipGetLastError();
