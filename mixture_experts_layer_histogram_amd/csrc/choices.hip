@@ -189,7 +189,7 @@ __global__ __launch_bounds__(256) void merge_rows_bwd_kernel(RankPtrs<const char
               dot = fmaf(x[e], z[e], dot);
               x[e] *= wj;
             }
-            if (i < n16) dst[i] = pack<BF16>(x);
+            if (i < n16) __builtin_nontemporal_store(pack<BF16>(x), dst + i);
           }
           dot = wave_sum(dot);
           if (lane == js[b]) mine += dot;
@@ -207,11 +207,9 @@ __global__ __launch_bounds__(256) void merge_rows_bwd_kernel(RankPtrs<const char
   }
 }
 
-constexpr int kMergeRowsBlocksPerCU = 16, kMergeBwdBlocksPerCU = 8;
-
-// workgroups for `n` of them, at most `most`: a few tokens do not pay for the launch of
-// thousands of empty workgroups
-static int grid_of(int64_t n, int most) { return int(n < most ? n : most); }
+// One task per wave: a capped grid whose waves loop over tasks is slower (16 workgroups a CU 165 us,
+// 64 a CU 151, uncapped 145 for the merge below; 8 a CU 243 us, uncapped 216 for its gradient).
+static int grid_of(int64_t n) { return int(n < (int64_t(1) << 30) ? n : int64_t(1) << 30); }
 
 hipError_t launch_merge_rows(const moe_shape_t& s, const void* rows, const int32_t* slot_of, const float* w,
                              void* const* y, int cus, hipStream_t st) {
@@ -220,20 +218,22 @@ hipError_t launch_merge_rows(const moe_shape_t& s, const void* rows, const int32
   const char* src = static_cast<const char*>(rows);
   const int64_t RT = int64_t(s.R) * s.T;
   const int64_t n16 = int64_t(s.d) * (s.dtype == MOE_F32 ? 4 : 2) / 16;
-  // Long segments once they give every SIMD a wave; below that short ones with all rows in flight.
+  // Segments of 2 KiB with two rows in flight once 4-KiB ones would give every SIMD a wave (32768 tokens
+  // of 7168 bf16: 142 us, 6.0 TB/s; 1-KiB ones with eight rows 179); below that short ones with all
+  // rows in flight (61 tokens of 2048 fp32: 3.8 us against 4.7).
   const bool few = RT * ((n16 + 255) / 256) < int64_t(cus) * 4;
-  const int most = cus * kMergeRowsBlocksPerCU;
-  const dim3 grid(few ? grid_of((RT * ((n16 + 63) / 64) + 3) / 4, most) : grid_of((RT * ((n16 + 255) / 256) + 3) / 4, most));
+  const int64_t seg = few ? 64 : 128;
+  const dim3 grid(grid_of((RT * ((n16 + seg - 1) / seg) + 3) / 4));
   if (s.dtype != MOE_F32) {
     if (few)
       hipLaunchKernelGGL((merge_rows_kernel<true, 1, 8>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
     else
-      hipLaunchKernelGGL((merge_rows_kernel<true, 4, 2>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
+      hipLaunchKernelGGL((merge_rows_kernel<true, 2, 2>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
   } else {
     if (few)
       hipLaunchKernelGGL((merge_rows_kernel<false, 1, 8>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
     else
-      hipLaunchKernelGGL((merge_rows_kernel<false, 4, 2>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
+      hipLaunchKernelGGL((merge_rows_kernel<false, 2, 2>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
   }
   return hipGetLastError();
 }
@@ -245,23 +245,23 @@ hipError_t launch_merge_rows_bwd(const moe_shape_t& s, const void* const* dy, co
   const char* src = static_cast<const char*>(ye);
   char* dst = static_cast<char*>(dye);
   const int64_t RT = int64_t(s.R) * s.T;
-  // a wave per token once that gives every SIMD two; below that a workgroup per token
+  // A wave per token once that gives every SIMD two, with the whole row in registers up to 14 KiB (32768
+  // tokens of 7168 bf16: 187 us, 5.6 TB/s; segments of 4 KiB 216, of 7 KiB 194); below that a workgroup
+  // per token (258 tokens of 1408 fp32: 6.5 us against 8.2).
   const bool few = RT < int64_t(cus) * 8;
-  const dim3 grid(grid_of(few ? RT : (RT + 3) / 4, cus * kMergeBwdBlocksPerCU));
+  const bool wide = int64_t(s.d) * (s.dtype == MOE_F32 ? 4 : 2) > 4096;
+  const dim3 grid(grid_of(few ? RT : (RT + 3) / 4));
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, dp, src, slot_of, w, dst, dw, s.R, s.T, s.k, s.d);
+  };
   if (s.dtype != MOE_F32) {
-    if (few)
-      hipLaunchKernelGGL((merge_rows_bwd_kernel<true, 1, 4, 4>), grid, dim3(256), 0, st, dp, src, slot_of, w, dst, dw, s.R,
-                         s.T, s.k, s.d);
-    else
-      hipLaunchKernelGGL((merge_rows_bwd_kernel<true, 4, 1, 1>), grid, dim3(256), 0, st, dp, src, slot_of, w, dst, dw, s.R,
-                         s.T, s.k, s.d);
+    if (few) launch(merge_rows_bwd_kernel<true, 1, 4, 4>);
+    else if (wide) launch(merge_rows_bwd_kernel<true, 14, 1, 1>);
+    else launch(merge_rows_bwd_kernel<true, 4, 1, 1>);
   } else {
-    if (few)
-      hipLaunchKernelGGL((merge_rows_bwd_kernel<false, 1, 4, 4>), grid, dim3(256), 0, st, dp, src, slot_of, w, dst, dw, s.R,
-                         s.T, s.k, s.d);
-    else
-      hipLaunchKernelGGL((merge_rows_bwd_kernel<false, 4, 1, 1>), grid, dim3(256), 0, st, dp, src, slot_of, w, dst, dw, s.R,
-                         s.T, s.k, s.d);
+    if (few) launch(merge_rows_bwd_kernel<false, 1, 4, 4>);
+    else if (wide) launch(merge_rows_bwd_kernel<false, 14, 1, 1>);
+    else launch(merge_rows_bwd_kernel<false, 4, 1, 1>);
   }
   return hipGetLastError();
 }

@@ -82,9 +82,9 @@ hipError_t launch_merge_rows(const moe_shape_t& s, const void* rows, const int32
 hipError_t launch_merge_rows_bwd(const moe_shape_t& s, const void* const* dy, const void* ye, const int32_t* slot_of,
                                  const float* w, void* dye, float* dw, int cus, hipStream_t st);
 hipError_t launch_mx4_quantize(const void* src, int src_dtype, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
-                               int cus, hipStream_t st);
+                               hipStream_t st);
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int format, int64_t rows, int K, void* dst,
-                                int dst_dtype, int cus, hipStream_t st);
+                                int dst_dtype, hipStream_t st);
 hipError_t launch_dispatch_mx4(const moe_shape_t& s, const void* const* x, const int32_t* pull_src, uint8_t* xe,
                                uint8_t* xe_scales, int64_t nmax, const int32_t* ctrl, int cus, hipStream_t st);
 hipError_t launch_ffn_mx4(const moe_shape_t& s, int El, const uint8_t* xe, const uint8_t* xe_scales,
@@ -249,8 +249,7 @@ int moe_mx_quantize_to(const void* src, int32_t src_dtype, int64_t rows, int32_t
   if (!src || !codes) return MOE_EINVAL;
   if (!aligned16(src) || !aligned16(codes)) return MOE_EALIGN;
   if (const int rc = check_scales(scales)) return rc;
-  return hip_rc(launch_mx4_quantize(src, src_dtype, rows, K, codes, scales, cu_count(),
-                                    static_cast<hipStream_t>(stream)));
+  return hip_rc(launch_mx4_quantize(src, src_dtype, rows, K, codes, scales, static_cast<hipStream_t>(stream)));
 }
 
 int moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t format, int64_t rows, int32_t K, void* dst,
@@ -262,7 +261,7 @@ int moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t forma
   if (!codes || !dst) return MOE_EINVAL;
   if (!aligned16(codes) || !aligned16(dst)) return MOE_EALIGN;
   if (const int rc = check_scales(scales)) return rc;
-  return hip_rc(launch_mx_dequantize(codes, scales, format, rows, K, dst, dst_dtype, cu_count(),
+  return hip_rc(launch_mx_dequantize(codes, scales, format, rows, K, dst, dst_dtype,
                                      static_cast<hipStream_t>(stream)));
 }
 
