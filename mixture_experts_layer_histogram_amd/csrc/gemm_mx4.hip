@@ -28,20 +28,30 @@ constexpr int kMx4ScaleBytes = 2 * (kGemmBM + kGemmBN) * 4;               // two
 constexpr int kMx4StageBytes = kMx4DataBytes + kMx4ScaleBytes;
 constexpr int kMx4Lds = 2 * kMx4StageBytes;                               // 136 KiB
 
-// The order the scheduler is asked for in a sub-step of eight MFMAs: a read after each, so that the
-// eight waves' LDS requests do not arrive in bursts.
-#define MOE_MX4_PAIR                             \
-  __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); \
-  __builtin_amdgcn_sched_group_barrier(0x100, 1, 0)
-#define MOE_MX4_SPREAD \
-  MOE_MX4_PAIR;        \
-  MOE_MX4_PAIR;        \
-  MOE_MX4_PAIR;        \
-  MOE_MX4_PAIR;        \
-  MOE_MX4_PAIR;        \
-  MOE_MX4_PAIR;        \
-  MOE_MX4_PAIR;        \
-  MOE_MX4_PAIR
+// The ten loads of a stage's fill in two parts (bits 0-3 A, 4-7 B, 8-9 scales): the token rows in the
+// last sub-step of the stage before the one before, the weights and scales in the first sub-step
+// after it.  All ten in one sub-step: 1146 us for the share of 32 experts of 2048 x 7168 (32700 rows)
+// instead of 1105; other splits, or three parts, 1115 to 1175.
+constexpr int kFirst = 0x00F, kSecond = 0x3F0;
+
+// The order the scheduler is asked for in a sub-step of eight MFMAs: the LDS reads of the next
+// fragments behind the first four, two each, so that the eight waves' requests do not arrive in one
+// burst (one each 1139 us, three 1123, in front of the MFMAs 1113), then this part's fills behind the
+// last four.
+template <int PART>
+__device__ __forceinline__ void spread() {
+  constexpr int kPer = (__builtin_popcount(PART) + 3) / 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x020, kPer, 0);
+  }
+}
 
 // exchanges: the upper half (odd 16-lane rows) of `a` with the lower half (even rows) of `b`
 __device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
@@ -149,7 +159,9 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
   };
   const uint32_t lds_dst0 = __builtin_amdgcn_readfirstlane(lds_addr(smem + wave * 4 * 1024));
   const uint32_t lds_sc0 = __builtin_amdgcn_readfirstlane(lds_addr(smem + kMx4DataBytes + wave * 256));
-  auto issue = [&](int ks) {
+  // part: which of a stage's ten loads (bits 0-3 A, 4-7 B, 8-9 the scales of its two K tiles)
+  auto issue_part = [&](int ks, auto part) {
+    constexpr int P = decltype(part)::value;
     const uint32_t stage = uint32_t((ks & 1) * kMx4StageBytes);
     const uint32_t da = lds_dst0 + stage, db = da + uint32_t(kGemmBM * kMx4RowBytes);
     const uint32_t ls = lds_sc0 + stage;
@@ -157,33 +169,36 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
     const uint8_t* ak = abase + size_t(ks) * kMx4RowBytes;
     const uint8_t* bk = bbase + size_t(ks) * kMx4RowBytes;
     const uint8_t* s0 = sp + (2 * ks) * splane;
-    const uint8_t* s1 = s0 + splane;
-    uint32_t te = 0, to = 0;
-    if (half_tail && ks == nk - 1) {  // chunks 4..7 lie past the row's end: re-read chunks 0..3 (never used)
-      te = uint32_t(lch_even & 4) * 16;
-      to = uint32_t(~lch_even & 4) * 16;       // odd row groups: the chunk ^ 4
-      s1 = s0;
-    }
+    const uint8_t* s1 = s0 + ((half_tail && ks == nk - 1) ? 0 : splane);
+    // chunks 4..7 of a half stage lie past the row's end: re-read chunks 0..3 (never used)
+    const bool tail = half_tail && ks == nk - 1;
+    const uint32_t te = uint32_t(lch_even & (tail ? 4 : 0)) * 16, to = uint32_t(~lch_even & (tail ? 4 : 0)) * 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t t = (i & 1) ? to : te;
       uint32_t ao = aoff[i] - t, bo = boff[i] - t;           // opaque: kept as one register each, not as pairs
       asm volatile("" : "+v"(ao), "+v"(bo));
-      __builtin_amdgcn_global_load_lds(static_cast<const void*>(ak + ao), (lds_void_ptr)(uintptr_t)(da + uint32_t(i * 1024)),
-                                       16, 0, 0);
-      __builtin_amdgcn_global_load_lds(static_cast<const void*>(bk + bo), (lds_void_ptr)(uintptr_t)(db + uint32_t(i * 1024)),
-                                       16, 0, 0);
+      if ((P >> i) & 1)
+        __builtin_amdgcn_global_load_lds(static_cast<const void*>(ak + ao), (lds_void_ptr)(uintptr_t)(da + uint32_t(i * 1024)),
+                                         16, 0, 0);
+      if ((P >> (4 + i)) & 1)
+        __builtin_amdgcn_global_load_lds(static_cast<const void*>(bk + bo), (lds_void_ptr)(uintptr_t)(db + uint32_t(i * 1024)),
+                                         16, 0, 0);
     }
-    __builtin_amdgcn_global_load_lds(static_cast<const void*>(s0), (lds_void_ptr)(uintptr_t)ls, 4, 0, 0);
-    __builtin_amdgcn_global_load_lds(static_cast<const void*>(s1),
+    if constexpr ((P >> 8) & 1)
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(s0), (lds_void_ptr)(uintptr_t)ls, 4, 0, 0);
+    if constexpr ((P >> 9) & 1)
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(s1),
                                      (lds_void_ptr)(uintptr_t)(ls + uint32_t(4 * (kGemmBM + kGemmBN))), 4, 0, 0);
   };
+
+  auto issue = [&](int ks) { issue_part(ks, std::integral_constant<int, 0x3FF>{}); };
 
   f32x16 acc[2][4];
   // Software pipeline over K, four sub-steps of 64 per 256-value stage.  The fragments of the
   // next sub-step are read while this one's MFMAs run (an FP4 fragment is 4 registers, so both
   // sets fit).  The stage's barrier sits before its last sub-step, whose fragments are in
-  // registers by then: the fill two stages ahead goes into the stage nobody reads any more, and
+  // registers by then: the fill two stages ahead starts into the stage nobody reads any more, and
   // the last sub-step's MFMAs cover the reads of the next stage's first fragments and scales.
   // Lane (row r32, half hi) supplies the 32 K values of block hi of the 64-value step (16 bytes)
   // and that block's scale: byte 2 (st & 1) + hi of the row's word st >> 1.
@@ -253,34 +268,46 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
       scales(smem, 0);
     }
     const int nfull = half_tail ? nk - 1 : nk;
-    for (int ks = 0; ks < nfull; ++ks) {
+    int ks = 0;
+    // `early`: the last sub-step starts the fill of stage ks + 2, into stage ks, which nobody reads any
+    // more; `late`: the first sub-step issues the rest of stage ks + 1's.
+    auto stage = [&](auto early, auto late) {
+      constexpr bool E = decltype(early)::value, L = decltype(late)::value;
       const char* cs = smem + (ks & 1) * kMx4StageBytes;
       const char* ns = smem + ((ks + 1) & 1) * kMx4StageBytes;   // after the last stage: stale, unused
       asm volatile("" : "+v"(offA[0]), "+v"(offA[1]), "+v"(offA[2]), "+v"(offA[3]), "+v"(offB[0]), "+v"(offB[1]),
                    "+v"(offB[2]), "+v"(offB[3]), "+v"(offSA), "+v"(offSB));
+      if constexpr (MV > 0) load(1, cs, 1);
+      if constexpr (L) issue_part(ks + 1, std::integral_constant<int, kSecond>{});
       if constexpr (MV > 0) {
-        load(1, cs, 1);
         mfmas(0);
         load(0, cs, 2);
         scales(cs, 1);
         mfmas(1);
         load(1, cs, 3);
         mfmas(2);
-        if constexpr (MV == 2) {
-          MOE_MX4_SPREAD;
-          MOE_MX4_SPREAD;
-          MOE_MX4_SPREAD;
-        }
+      }
+      if constexpr (MV == 2) {
+        spread<L ? kSecond : 0>();
+        spread<0>();
+        spread<0>();
       }
       meet();
-      if (ks + 2 < nk) issue(ks + 2);     // into stage ks, which nobody reads any more
       if constexpr (MV > 0) {
         load(0, ns, 0);
         scales(ns, 0);
-        mfmas(3);
-        if constexpr (MV == 2) MOE_MX4_SPREAD;
       }
+      if constexpr (E) issue_part(ks + 2, std::integral_constant<int, kFirst>{});
+      if constexpr (MV > 0) mfmas(3);
+      if constexpr (MV == 2) spread<E ? kFirst : 0>();
+    };
+    if (nk > 2) {
+      stage(std::true_type{}, std::false_type{});
+      for (++ks; ks + 2 < nk; ++ks) stage(std::true_type{}, std::true_type{});
+      stage(std::false_type{}, std::true_type{});
+      ++ks;
     }
+    for (; ks < nfull; ++ks) stage(std::false_type{}, std::false_type{});
     if (half_tail) {                      // the last stage's first half: sub-steps 0 and 1
       if constexpr (MV > 0) {
         load(1, smem + (nfull & 1) * kMx4StageBytes, 1);
