@@ -61,6 +61,10 @@ __global__ __launch_bounds__(256, 1) void thin_mx4_kernel(ThinArgs g) {
   __shared__ int16_t list[1024];          // the experts with 1..kThinRows rows, ascending
   __shared__ int n_list;
   constexpr int kStages = thin_stages(SPLIT);
+  // Many items: the weights pass by once and would only push each other and the token rows out of the
+  // caches (non-temporal: 151 us for the layer on 32 experts of 2048 x 7168, 512 rows, instead of
+  // 167; the scale words stay cached, their lines serve two loads: 149 against 154).  Few: they may well be there still from the last token (27.5 us against 28.4).
+  constexpr int kWeightPolicy = SPLIT == 1 ? 2 : 0;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r32 = lane & 31, hi = lane >> 5;
   if (wave == 0) {
@@ -119,7 +123,7 @@ __global__ __launch_bounds__(256, 1) void thin_mx4_kernel(ThinArgs g) {
     for (int i = 0; i < 8; ++i) {
       const uint8_t* base = (i < 4 ? t.w0 : t.w1) + size_t((i & 3) * 8) * rb + koff;
       __builtin_amdgcn_global_load_lds(static_cast<const void*>(base + ((i & 1) ? odd - to : even - te)),
-                                       (lds_void_ptr)(uintptr_t)(dst + uint32_t(i * 1024)), 16, 0, 0);
+                                       (lds_void_ptr)(uintptr_t)(dst + uint32_t(i * 1024)), 16, 0, kWeightPolicy);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {               // token rows past the last re-read it, are not stored

@@ -142,10 +142,37 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 8))) voi
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n16 = d >> 3;            // 16-byte source vectors per row (d % 128 == 0: whole 16-lane groups)
   const int nq = d >> 7;             // scale words (K-tile planes) per row
+  uint32_t* xw = reinterpret_cast<uint32_t*>(xes);
+  if (N <= int(gridDim.x)) {         // a row for a workgroup: its waves share it, a quarter of its vectors each
+    const int row = blockIdx.x;
+    if (row >= N) return;
+    const u32x4* src = reinterpret_cast<const u32x4*>(x.p[pull_src[2 * row]] + int64_t(pull_src[2 * row + 1]) * d * 2);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(xe + int64_t(row) * (d >> 1));
+    constexpr int U = 4;
+    for (int base = int(threadIdx.x); base - int(threadIdx.x) < n16; base += 256 * U) {
+      u32x4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        v[u] = u32x4{0, 0, 0, 0};
+        if (base + u * 256 < n16) v[u] = src[base + u * 256];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int q = base + u * 256;
+        uint32_t sc;
+        const uint32_t code = mx4_quant8_bf16(v[u], &sc);       // all lanes: quad permutations inside
+        const uint32_t sw = mx_scale_word(sc);                   // all lanes: row shifts inside
+        if (q < n16) {
+          dst[q] = code;
+          if ((q & 15) == 0) xw[nmax * (q >> 4) + row] = sw;
+        }
+      }
+    }
+    return;
+  }
   const int even = (N + int(gridDim.x) - 1) / int(gridDim.x);
   const int cr = min(most, max(4, (even + 3) & ~3));
   const int nchunks = (N + cr - 1) / cr;
-  uint32_t* xw = reinterpret_cast<uint32_t*>(xes);
   for (int c = blockIdx.x; c < nchunks; c += gridDim.x) {
     const int s0 = c * cr, rows = min(cr, N - s0);
     // where this wave's rows (wave, wave + 4, ...: at most 8) come from, one load for all
