@@ -169,6 +169,7 @@ MOVES = [  # R, T, d, E, El, k, drop, dtype
     (2, 65, 128, 16, 16, 4, 0.2, "bf16"), (1, 130, 2048, 64, 64, 6, 0.0, "bf16"), (3, 50, 7168, 32, 8, 8, 0.1, "bf16"),
     (1, 64, 1408, 16, 8, 16, 0.1, "f32"), (2, 40, 2052, 8, 8, 3, 0.0, "f32"), (1, 37, 8256, 4, 4, 4, 0.0, "bf16"),
     (1, 9, 512, 16, 4, 4, 1.0, "bf16"), (1, 2100, 192, 12, 12, 5, 0.05, "bf16"),
+    (1, 2060, 2176, 8, 8, 3, 0.1, "bf16"), (2, 1040, 1032, 8, 4, 2, 0.1, "f32"), (1, 2050, 8256, 4, 4, 2, 0.0, "bf16"),
 ]
 
 

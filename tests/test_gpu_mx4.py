@@ -324,6 +324,27 @@ def test_many_tiles_a_workgroup(T, d, F, E, k):
     assert all(torch.equal(a, b) for a, b in zip(y, _push(P, P.topk_idx.clone(), P.topk_w.clone())))
 
 
+@pytest.mark.parametrize("d", [384, 2176, 7168, 8320])
+def test_gather_of_more_rows_than_workgroups(d):
+    """Codes and scales bit for bit where workgroups take several rows, and rows wider than a wave holds."""
+    torch = _torch()
+    cfg = _cfg(f"mx4 gather d{d}", T=3000, d=d, F=128, E=5, E_local=4, k=2)
+    print(f"[mx4] {cfg.name}", flush=True)
+    inp, P = _problem(cfg)
+    P.xe.fill_(GUARD)
+    P.xe_scales.fill_(GUARD)
+    P.layout()
+    P.dispatch()
+    assert P.status() == 0
+    N = int(P.offsets[-1])
+    assert 4096 < N < P.nmax
+    codes, sc, _ = M4.quantize(P.rows_f64(P.x[0]).reshape(cfg.T, d))
+    src = P.pull_src.cpu().numpy()[:N, 1]
+    assert np.array_equal(M4.unpack(P.xe[:N].cpu().numpy()), codes[src])
+    assert np.array_equal(P.xe_scales[:, :N].permute(1, 0, 2).reshape(N, -1).cpu().numpy(), sc[src])
+    assert (P.xe[N:] == GUARD).all() and (P.xe_scales[:, N:] == GUARD).all()
+
+
 def test_few_and_many_rows_in_one_call():
     """Experts of 100, 33, 32, 31, 1 and 0 rows where few are expected: each of the two product kernels
     takes its own."""
