@@ -23,7 +23,8 @@ typedef __bf16 bf16v2 __attribute__((ext_vector_type(2)));
 typedef float f32v2 __attribute__((ext_vector_type(2)));
 
 constexpr uint32_t kMx4NaNScale = 255;
-constexpr int kThinRows = 32;             // experts with at most this many rows take the streaming kernel
+constexpr int kThinRows = 32;             // experts with at most this many rows may take the streaming kernel,
+constexpr int kThinMean = 20;             // and do where this many are expected of one at most
 
 // silu with the reciprocal instruction (1 ulp) in place of the division sequence: six instructions a
 // value instead of some twenty, and the epilogue of a GEMM1 tile is 64 of them a lane
