@@ -192,7 +192,12 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
                                      (lds_void_ptr)(uintptr_t)(ls + uint32_t(4 * (kGemmBM + kGemmBN))), 4, 0, 0);
   };
 
-  auto issue = [&](int ks) { issue_part(ks, std::integral_constant<int, 0x3FF>{}); };
+  // waves whose 64 token rows lie wholly past the tile's valid rows do not fill their share of the rows
+  bool lean = false;
+  auto issue = [&](int ks) {
+    if (lean) issue_part(ks, std::integral_constant<int, kSecond>{});
+    else issue_part(ks, std::integral_constant<int, kFirst | kSecond>{});
+  };
 
   f32x16 acc[2][4];
   // Software pipeline over K, four sub-steps of 64 per 256-value stage.  The fragments of the
@@ -219,7 +224,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
   auto wide = [](const i32x4& v) -> i32x8 { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; };
 
   // stores an epilogue certainly issues for a whole tile (waits may leave so many operations in flight)
-  constexpr int kFills = 10, kStores = (MODE == 0) ? 4 : 16;
+  constexpr int kStores = (MODE == 0) ? 4 : 16;
   auto kloop = [&](auto mvc, int behind) {
     constexpr int MV = decltype(mvc)::value;
     i32x4 fa[2][2], fb[2][4];            // fragments, two sets
@@ -297,7 +302,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
         load(0, ns, 0);
         scales(ns, 0);
       }
-      if constexpr (E) issue_part(ks + 2, std::integral_constant<int, kFirst>{});
+      if constexpr (E && MV > 0) issue_part(ks + 2, std::integral_constant<int, kFirst>{});
       if constexpr (MV > 0) mfmas(3);
       if constexpr (MV == 2) spread<E ? kFirst : 0>();
     };
@@ -319,6 +324,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
 
   if (!advance()) return;
   aim(next);
+  lean = __builtin_amdgcn_readfirstlane(next.rows <= wm * 64);
   issue(0);
   if (nk > 1) issue(1);
   int stores = 0;                       // the fills in flight are followed by kStores stores at least
@@ -330,21 +336,26 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
       for (int b = 0; b < 4; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.0f;
-    // stage 0 landed
-    if (nk > 1 && stores) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kFills + kStores) : "memory");
-    else if (nk > 1) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kFills) : "memory");
-    else if (stores) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kStores) : "memory");
-    else asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    // stage 0 landed: behind its fills are stage 1's and the stores
+    auto landed = [&](auto fills) {
+      constexpr int n = decltype(fills)::value;
+      if (stores) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(n + kStores) : "memory");
+      else asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(n) : "memory");
+    };
+    if (nk == 1) landed(std::integral_constant<int, 0>{});
+    else if (lean) landed(std::integral_constant<int, __builtin_popcount(kSecond)>{});
+    else landed(std::integral_constant<int, __builtin_popcount(kFirst | kSecond)>{});
     // Row padding: a wave whose 32-row blocks lie wholly past the tile's valid rows skips their
     // fragment reads and MFMAs; it still fills and meets every barrier.
     const int mv = __builtin_amdgcn_readfirstlane(min(2, max(0, (t.rows - wm * 64 + 31) >> 5)));
-    if (mv == 2) kloop(std::integral_constant<int, 2>{}, stores);
-    else if (mv == 1) kloop(std::integral_constant<int, 1>{}, stores);
-    else kloop(std::integral_constant<int, 0>{}, stores);
+    if (mv == 2) kloop(std::integral_constant<int, 2>{}, __builtin_amdgcn_readfirstlane(stores));
+    else if (mv == 1) kloop(std::integral_constant<int, 1>{}, __builtin_amdgcn_readfirstlane(stores));
+    else kloop(std::integral_constant<int, 0>{}, __builtin_amdgcn_readfirstlane(stores));
     const bool more = advance();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // every wave has read both stages
     if (more) {
       aim(next);
+      lean = __builtin_amdgcn_readfirstlane(next.rows <= wm * 64);
       issue(0);
       if (nk > 1) issue(1);
     }
