@@ -7,6 +7,8 @@
 // time (16 bytes of bf16 per lane, an aligned lane quad holds one 32-value block), a workgroup
 // 32 rows x 512 values, so that its scale words -- four K-tile planes of 32 rows -- leave as
 // four runs of 128 bytes instead of single words (each a partial write of its own line).
+// Measured on 229376 rows of 2048 bf16 values: quantise 187 us, dequantise 194 us (1.19 GB: 6.3 and
+// 6.1 TB/s; a device copy of 2 GiB reaches 4.9); the gather of 32768 rows of 7168, 111 us (5.3 TB/s).
 #include "mx4.hpp"
 
 namespace moe {
@@ -132,7 +134,8 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* __res
 // 16-byte vectors of each in flight per lane (the whole row for the widths below).  A workgroup
 // takes up to `most` consecutive rows at a time -- fewer when there are not enough rows to give
 // every workgroup that many, since one row alone takes two microseconds of waiting -- keeps
-// their scale words in LDS and writes each K-tile plane's words as one run.
+// their scale words in LDS and writes each K-tile plane's words as one run.  With no more rows than
+// workgroups each takes one, its waves a quarter of the row each (512 rows of 7168: 5.6 us against 8.4).
 template <int UNROLL, int ROWS>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 8))) void dispatch_pull_mx4_kernel(
     RankPtrs<const char*> x, const int32_t* __restrict__ pull_src, const int32_t* __restrict__ ctrl,
