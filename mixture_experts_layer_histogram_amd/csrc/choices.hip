@@ -210,7 +210,8 @@ __global__ __launch_bounds__(256) void merge_rows_bwd_kernel(RankPtrs<const char
 
 // One task per wave: a capped grid whose waves loop over tasks is slower (16 workgroups a CU 165 us,
 // 64 a CU 151, uncapped 145 for the merge below; 8 a CU 243 us, uncapped 216 for its gradient).
-static int grid_of(int64_t n) { return int(n < (int64_t(1) << 30) ? n : int64_t(1) << 30); }
+// The cap that is left keeps a launch below 2^32 threads; the waves loop beyond it.
+static int grid_of(int64_t n) { return int(n < (1 << 22) ? n : 1 << 22); }
 
 hipError_t launch_merge_rows(const moe_shape_t& s, const void* rows, const int32_t* slot_of, const float* w,
                              void* const* y, int cus, hipStream_t st) {

@@ -20,14 +20,14 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void* __restric
                                                            uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   __shared__ uint32_t s_sc[4][kQuantRows];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int nct = (K + kQuantCols - 1) / kQuantCols;
+  const int nct = int((uint32_t(K) + kQuantCols - 1) / kQuantCols);
   const int64_t tasks = (rows + kQuantRows - 1) / kQuantRows * nct;
   uint32_t* const words = reinterpret_cast<uint32_t*>(scales);
   for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
     const int64_t r0 = task / nct * kQuantRows;
     const int ct = int(task % nct);
-    const int k = ct * kQuantCols + lane * 8;              // K % 128 == 0: whole 16-lane groups are in or out
-    const bool in = k < K;
+    const uint32_t k = uint32_t(ct) * kQuantCols + lane * 8;   // K % 128 == 0: whole 16-lane groups are in or out
+    const bool in = k < uint32_t(K);
     const int nr = int(min(int64_t(kQuantRows), rows - r0));
     constexpr int U = 8;                                   // rows in flight per wave
     u32x4 v[U][BF16 ? 1 : 2];
@@ -69,14 +69,14 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t* __res
                                                             const uint8_t* __restrict__ scales, int64_t rows, int K,
                                                             void* __restrict__ dst) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int nct = (K + kQuantCols - 1) / kQuantCols;
+  const int nct = int((uint32_t(K) + kQuantCols - 1) / kQuantCols);
   const int64_t tasks = (rows + kQuantRows - 1) / kQuantRows * nct;
   const uint32_t* const words = reinterpret_cast<const uint32_t*>(scales);
   for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
     const int64_t r0 = task / nct * kQuantRows;
     const int ct = int(task % nct);
-    const int k = ct * kQuantCols + lane * 8;
-    if (k >= K) continue;
+    const uint32_t k = uint32_t(ct) * kQuantCols + lane * 8;
+    if (k >= uint32_t(K)) continue;
     const int nr = int(min(int64_t(kQuantRows), rows - r0));
     constexpr int U = 8;
     uint2 q[U];
@@ -229,8 +229,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 8))) voi
 
 // a task per workgroup: 189 us for 229376 rows of 2048 bf16; 8 workgroups a CU that loop take 204
 static int quant_grid(int64_t rows, int K) {
-  const int64_t tasks = (rows + kQuantRows - 1) / kQuantRows * ((K + kQuantCols - 1) / kQuantCols);
-  return int(tasks < (int64_t(1) << 30) ? tasks : int64_t(1) << 30);
+  const int64_t tasks = (rows + kQuantRows - 1) / kQuantRows * ((int64_t(K) + kQuantCols - 1) / kQuantCols);
+  return int(tasks < (1 << 22) ? tasks : 1 << 22);        // a launch has less than 2^32 threads
 }
 
 hipError_t launch_mx4_quantize(const void* src, int src_dtype, int64_t rows, int K, uint8_t* codes, uint8_t* scales,

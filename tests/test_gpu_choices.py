@@ -448,3 +448,29 @@ def test_rows_past_4_gib():
         assert torch.equal(dxe[s], (x[0][t].float() * w[0, t][:, None]).to(torch.bfloat16))
     # every pair of a token holds the token's own row: its weight gradients are |x|^2 all
     assert torch.allclose(dw, x[0].double().square().sum(-1)[None, :, None].expand_as(w).float(), rtol=1e-4)
+
+
+def test_more_tokens_than_a_launch_has_waves():
+    """17 million tokens of one 16-byte vector: waves take several tokens.  One term a token, so the merge and
+    the row gradient are single products, and a weight's gradient four products and their sum."""
+    torch = _torch()
+    T = 17_000_000
+    shape, pl = moe.Shape(1, T, 4, 4, 1, 128, moe.MOE_F32), moe.Placement(1, 4)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    ye, dy = (torch.randn(T, 4, device="cuda", generator=g) for _ in range(2))
+    w = torch.randn(T, device="cuda", generator=g)
+    slot = torch.randperm(T, device="cuda", generator=g).to(torch.int32)
+    slot[:: 1000] = -1
+    local = slot >= 0
+    at = slot[local].long()
+    y, dx = (torch.full((T, 4), float("nan"), device="cuda") for _ in range(2))
+    moe.moe_combine_merge(shape, pl, ye, slot, w, [y])
+    assert torch.equal(y[local], w[local, None] * ye[at]) and (y[~local] == 0).all()
+    moe.moe_dispatch_pull_backward(shape, pl, ye, slot, [dx])
+    assert torch.equal(dx[local], ye[at]) and (dx[~local] == 0).all()
+    dye, dw = torch.full((T, 4), 9.0, device="cuda"), torch.full((T,), float("nan"), device="cuda")
+    moe.moe_combine_merge_backward(shape, pl, [dy], ye, slot, w, dye, dw)
+    assert torch.equal(dye[at], w[local, None] * dy[local]) and (dw[~local] == 0).all()
+    assert int((dye == 9.0).all(1).sum()) == T - int(local.sum())
+    terms = dy[local].double() * ye[at].double()
+    assert ((dw[local].double() - terms.sum(1)).abs() <= 4 * 2.0 ** -24 * terms.abs().sum(1)).all()

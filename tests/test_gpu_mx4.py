@@ -117,6 +117,31 @@ def test_quantize_dequantize_shapes(rows, K, src):
             assert np.array_equal(out[: rows * K].double().cpu().numpy().reshape(rows, K), want, equal_nan=True)
 
 
+def test_more_rows_than_a_launch_has_workgroups():
+    """134 million rows of 128: workgroups take several blocks of rows (checked around the seam and at the end)."""
+    torch = _torch()
+    rows, K = (1 << 22) * 32 + 37, 128
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    places = [slice(0, 40), slice((1 << 22) * 32 - 40, rows)]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for p in places:
+        x[p] = torch.randn(x[p].shape, generator=g, device="cuda").to(torch.bfloat16)
+    q = torch.full((rows, K // 2), GUARD, dtype=torch.uint8, device="cuda")
+    s = torch.full((rows, 4), GUARD, dtype=torch.uint8, device="cuda")
+    moe.moe_mx_quantize_to(x, moe.MOE_BF16, rows, K, moe.MOE_MXFP4, q, s)
+    values = []
+    for p in places:
+        codes, sc, val = M4.quantize(x[p].double().cpu().numpy())
+        assert np.array_equal(M4.unpack(q[p].cpu().numpy()), codes) and np.array_equal(s[p].cpu().numpy(), sc)
+        values.append(val)
+    assert not q[40:(1 << 22) * 32 - 40].any() and not s[40:(1 << 22) * 32 - 40].any()
+    x.fill_(float("nan"))
+    moe.moe_mx_dequantize(q, s, moe.MOE_MXFP4, rows, K, x, moe.MOE_BF16)
+    for p, val in zip(places, values):
+        assert np.array_equal(x[p].double().cpu().numpy(), val)
+    assert not x[40:(1 << 22) * 32 - 40].any()
+
+
 @pytest.mark.parametrize("fmt", [moe.MOE_MXFP4, moe.MOE_MXFP8])
 def test_dequantize_every_code_at_every_scale(fmt):
     torch = _torch()
