@@ -446,12 +446,12 @@ __device__ __forceinline__ void hold(const int32_t* __restrict__ idx, const Pair
 }
 
 // G groups of 64 pairs from pair pb on, this lane's choice of each in e (-1: none).  m: the lanes of a
-// group that chose what this lane chose, by ballots over the bits of e + 1.  A choice outside [-1, E)
-// or an expert that a token names twice (the tables hold at most one row per token and expert)
-// sets *wrong; the former becomes -1.
+// group that chose what this lane chose, by ballots over the bits of e.  A choice outside [-1, E) or,
+// where `check`, an expert that a token names twice (the tables hold at most one row per token and
+// expert) sets *wrong; the former becomes -1.
 template <int G>
 __device__ __forceinline__ void match_choices(const int32_t* __restrict__ idx, uint32_t pb, uint32_t end, int (&e)[G],
-                                              int E, int k, unsigned long long (&m)[G], int* wrong) {
+                                              int E, int k, unsigned long long (&m)[G], int* wrong, bool check) {
   const int lane = threadIdx.x & 63;
   bool bad = false;
 #pragma unroll
@@ -463,13 +463,17 @@ __device__ __forceinline__ void match_choices(const int32_t* __restrict__ idx, u
     m[i] = __ballot(e[i] >= 0);
   }
 #pragma nounroll                             // executed once: short code costs less than its fetching
-  for (int b = 32 - __clz(E); --b >= 0;)
+  for (int b = 32 - __clz(E - 1); --b >= 0;)
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-      const bool bit = ((e[i] + 1) >> b) & 1;
+      const bool bit = (e[i] >> b) & 1;
       const unsigned long long bb = __ballot(bit);
       m[i] &= bit ? bb : ~bb;
     }
+  if (!check) {
+    if (bad) *wrong = 1;
+    return;
+  }
   int j = int((pb + lane) % uint32_t(k));    // this lane's place in its token
   const int step = 64 % k;
   const unsigned long long token = (1ull << k) - 1ull;
@@ -491,12 +495,12 @@ __device__ __forceinline__ void match_choices(const int32_t* __restrict__ idx, u
 // adds a wave's run of pairs to hist; sets *wrong as above
 template <bool HELD>
 __device__ __forceinline__ void count_choices(const int32_t* __restrict__ idx, const PairRun r, int (&held)[kChoiceHeld],
-                                              int E, int k, int* hist, int* wrong) {
+                                              int E, int k, int* hist, int* wrong, bool check) {
   const int lane = threadIdx.x & 63;
   const unsigned long long below = (1ull << lane) - 1ull;
   if constexpr (HELD) {
     unsigned long long m[kChoiceHeld];
-    match_choices<kChoiceHeld>(idx, r.begin, r.end, held, E, k, m, wrong);
+    match_choices<kChoiceHeld>(idx, r.begin, r.end, held, E, k, m, wrong, check);
 #pragma unroll
     for (int i = 0; i < kChoiceHeld; ++i)
       if (held[i] >= 0 && !(m[i] & below)) atomicAdd(&hist[held[i]], __popcll(m[i]));
@@ -504,7 +508,7 @@ __device__ __forceinline__ void count_choices(const int32_t* __restrict__ idx, c
     for (uint32_t pb = r.begin; pb < r.end; pb += 64) {
       int e[1] = {pb + lane < r.end ? idx[pb + lane] : -1};
       unsigned long long m[1];
-      match_choices<1>(idx, pb, r.end, e, E, k, m, wrong);
+      match_choices<1>(idx, pb, r.end, e, E, k, m, wrong, check);
       if (e[0] >= 0 && !(m[0] & below)) atomicAdd(&hist[e[0]], __popcll(m[0]));
     }
   }
@@ -523,7 +527,7 @@ __global__ __launch_bounds__(1024) void choices_count_kernel(const int32_t* __re
   for (int e = threadIdx.x; e < E; e += 1024) hist[e] = 0;
   if (threadIdx.x == 0) wrong = 0;
   __syncthreads();
-  count_choices<HELD>(idx, run, held, E, k, hist, &wrong);
+  count_choices<HELD>(idx, run, held, E, k, hist, &wrong, true);
   __syncthreads();
   int32_t* row = table + size_t(blockIdx.x) * (E + 1);
   for (int e = threadIdx.x; e < E; e += 1024) row[e] = hist[e];
@@ -593,7 +597,7 @@ __global__ __launch_bounds__(NT) void choices_slots_kernel(
   if constexpr (HELD) {
     unsigned long long m[kChoiceHeld];
     int old[kChoiceHeld];
-    match_choices<kChoiceHeld>(idx, run.begin, run.end, held, E, k, m, &bad);
+    match_choices<kChoiceHeld>(idx, run.begin, run.end, held, E, k, m, &bad, nb == 1);   // else checked by the count
 #pragma unroll
     for (int i = 0; i < kChoiceHeld; ++i) {
       old[i] = 0;
@@ -604,7 +608,7 @@ __global__ __launch_bounds__(NT) void choices_slots_kernel(
     for (int i = 0; i < kChoiceHeld; ++i)
       rank[i] = __shfl(old[i], held[i] >= 0 ? __builtin_ctzll(m[i]) : 0, 64) + __popcll(m[i] & below);
   } else {
-    count_choices<false>(idx, run, held, E, k, mine, &bad);
+    count_choices<false>(idx, run, held, E, k, mine, &bad, nb == 1);
   }
   if (nb > 1) {
     if (ge < E) {
@@ -698,7 +702,7 @@ __global__ __launch_bounds__(NT) void choices_slots_kernel(
     for (uint32_t pb = run.begin; pb < run.end; pb += 64) {
       int e[1] = {pb + lane < run.end ? idx[pb + lane] : -1};
       unsigned long long m[1];
-      match_choices<1>(idx, pb, run.end, e, E, k, m, &bad);
+      match_choices<1>(idx, pb, run.end, e, E, k, m, &bad, false);
       int old = 0;
       if (e[0] >= 0 && !(m[0] & below)) old = atomicAdd(&mine[e[0]], __popcll(m[0]));
       old = __shfl(old, e[0] >= 0 ? __builtin_ctzll(m[0]) : 0, 64);

@@ -255,14 +255,15 @@ __global__ __launch_bounds__(256) void weighted_merge_kernel(RankPtrs<const char
   }
 }
 
-constexpr int kGatherBlocksPerCU = 4, kPushBlocksPerCU = 8, kMergeBlocksPerCU = 16;
+// dispatch: 32700 rows of 14 KiB with the layout before it 165 us; 4 workgroups a CU 170, 8 a CU 172
+constexpr int kDispatchBlocksPerCU = 16, kGatherBlocksPerCU = 4, kPushBlocksPerCU = 8, kMergeBlocksPerCU = 16;
 
 hipError_t launch_dispatch(const moe_shape_t& s, const void* const* x, const int32_t* pull_src, char* xe,
                            const int32_t* ctrl, int cus, hipStream_t st) {
   RankPtrs<const char*> xp{};
   for (int r = 0; r < s.R; ++r) xp.p[r] = static_cast<const char*>(x[r]);
   const int row_bytes = s.d * (s.dtype == MOE_F32 ? 4 : 2);
-  hipLaunchKernelGGL(dispatch_pull_kernel, dim3(cus * kGatherBlocksPerCU), dim3(256), 0, st, xp, pull_src, ctrl, xe,
+  hipLaunchKernelGGL(dispatch_pull_kernel, dim3(cus * kDispatchBlocksPerCU), dim3(256), 0, st, xp, pull_src, ctrl, xe,
                      row_bytes);
   return hipGetLastError();
 }
