@@ -379,8 +379,8 @@ hipError_t launch_layout(const moe_shape_t& s, const int32_t* e2l, int El, int m
 // sums the blocks before its own (and all of them, for the offsets) itself, so there is no scan
 // kernel between them; up to 4096 pairs one workgroup does it all in one launch.  Bound by the
 // latency of its dependent steps and of fetching its code, not by bytes, so a wave holds its pairs'
-// choices in registers through all phases where they are four groups of 64 (HELD; 262144 pairs: 6.3 +
-// 12.4 us, reading them again 7.2 + 14.4), one match by ballots serves the checks and the places, and
+// choices in registers through all phases where they are four groups of 64 (HELD; 262144 pairs: 5.8 +
+// 9.8 us, reading them again 7.2 + 14.4), one match by ballots serves the checks and the places, and
 // few pairs and experts take a workgroup of 256 threads, whose barriers are cheaper (512 pairs: 4.5
 // us against 5.3 with 1024).  4096 pairs: 8.6 us.
 // ---------------------------------------------------------------------------
