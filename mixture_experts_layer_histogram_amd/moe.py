@@ -152,11 +152,12 @@ def lib() -> ctypes.CDLL:
 # --------------------------------------------------------------------------- marshalling
 def _p(t):
     """Device pointer of a tensor (or an int address / None)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
+
+
+_TABLES = {}      # number of ranks -> array type
 
 
 def _table(ts):
@@ -164,15 +165,27 @@ def _table(ts):
     reference cycle to collect)."""
     if ts is None:
         return None
-    return (ctypes.c_void_p * len(ts))(*[_p(t) for t in ts])
+    n = len(ts)
+    kind = _TABLES.get(n)
+    if kind is None:
+        kind = _TABLES[n] = ctypes.c_void_p * n
+    return kind(*map(_p, ts))
+
+
+_current = None   # (the current device, a device's current stream): torch's calls, once it is initialised
 
 
 def _stream(stream):
+    global _current
     if stream is None:
         # the current stream of the current device, without the Stream object that
         # torch.cuda.current_stream() builds (2.9 us of a small call's 9; this takes 0.2)
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _current is None:
+            import torch
+            torch.cuda.current_device()
+            _current = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        device, raw = _current
+        return raw(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
