@@ -398,7 +398,9 @@ int moe_dispatch_pull_backward(const moe_shape_t* s, const moe_placement_t* p, c
  * the choices and their weights as inputs and without logits and recv; every stage's arguments
  * are checked before the first launch.  xe, ye and pull_src need [moe_max_pairs] rows, of which
  * [0, N) are touched (the scales in xe_scales keep moe_max_pairs rows a plane); a caller who
- * knows N may pass N rows of ye and pull_src.
+ * knows N may pass N rows of ye and pull_src.  With MOE_MXFP4 and moe_max_pairs * d * 4 <= 16 MiB the
+ * expert rows stay in fp32 in ws instead (ye is left as it is), and y is rounded once; otherwise y
+ * is moe_forward's bit for bit for the choices and weights that moe_layout takes.
  */
 int moe_forward_choices(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t* ex, const int32_t* topk_idx,
                         const float* topk_w, const void* const* x, const void* w1, const void* w3, const void* w2,

@@ -57,8 +57,9 @@ __device__ __forceinline__ u32x4 pack(const float* f) {
 
 // y[r][t] = sum over ascending j with slot >= 0 of w[r][t][j] rows[slot] (w = 1 when null); a
 // token with none gets zeros.  A wave task is one column segment of 64 * VPL vectors of one
-// token's row; JB of the token's expert rows are in flight at once.
-template <bool BF16, int VPL, int JB>
+// token's row; JB of the token's expert rows are in flight at once.  BF16: bf16 rows and y; else fp32 rows,
+// and fp32 or (Y16) bf16 y.
+template <bool BF16, int VPL, int JB, bool Y16 = BF16>
 __global__ __launch_bounds__(256) void merge_rows_kernel(const char* __restrict__ rows, RankPtrs<char*> y,
                                                          const int32_t* __restrict__ slot_of,
                                                          const float* __restrict__ w, int R, int T, int k, int d) {
@@ -112,11 +113,15 @@ __global__ __launch_bounds__(256) void merge_rows_kernel(const char* __restrict_
         }
       }
     }
-    u32x4* yrow = reinterpret_cast<u32x4*>(y.p[r] + int64_t(t) * row_bytes);
+    char* const yrow = y.p[r] + int64_t(t) * d * (Y16 ? 2 : 4);
 #pragma unroll
     for (int u = 0; u < VPL; ++u) {
       const int i = cb + u * 64 + lane;
-      if (i < n16) __builtin_nontemporal_store(pack<BF16>(acc[u]), yrow + i);
+      if (i >= n16) continue;
+      if constexpr (Y16 && !BF16)
+        reinterpret_cast<uint2*>(yrow)[i] = make_uint2(pack_bf16x2(acc[u][0], acc[u][1]), pack_bf16x2(acc[u][2], acc[u][3]));
+      else
+        __builtin_nontemporal_store(pack<BF16>(acc[u]), reinterpret_cast<u32x4*>(yrow) + i);
     }
   }
 }
@@ -213,30 +218,26 @@ __global__ __launch_bounds__(256) void merge_rows_bwd_kernel(RankPtrs<const char
 // The cap that is left keeps a launch below 2^32 threads; the waves loop beyond it.
 static int grid_of(int64_t n) { return int(n < (1 << 22) ? n : 1 << 22); }
 
-hipError_t launch_merge_rows(const moe_shape_t& s, const void* rows, const int32_t* slot_of, const float* w,
+// rows32: fp32 rows whatever the dtype (and y of the row type)
+hipError_t launch_merge_rows(const moe_shape_t& s, const void* rows, bool rows32, const int32_t* slot_of, const float* w,
                              void* const* y, int cus, hipStream_t st) {
   RankPtrs<char*> yp{};
   for (int r = 0; r < s.R; ++r) yp.p[r] = static_cast<char*>(y[r]);
   const char* src = static_cast<const char*>(rows);
   const int64_t RT = int64_t(s.R) * s.T;
-  const int64_t n16 = int64_t(s.d) * (s.dtype == MOE_F32 ? 4 : 2) / 16;
+  const int64_t n16 = int64_t(s.d) * (s.dtype == MOE_F32 || rows32 ? 4 : 2) / 16;
   // Segments of 2 KiB with two rows in flight once 4-KiB ones would give every SIMD a wave (32768 tokens
   // of 7168 bf16: 142 us; 1-KiB ones with eight rows 179); below that short ones with all
   // rows in flight (61 tokens of 2048 fp32: 3.8 us against 4.7).
   const bool few = RT * ((n16 + 255) / 256) < int64_t(cus) * 4;
   const int64_t seg = few ? 64 : 128;
   const dim3 grid(grid_of((RT * ((n16 + seg - 1) / seg) + 3) / 4));
-  if (s.dtype != MOE_F32) {
-    if (few)
-      hipLaunchKernelGGL((merge_rows_kernel<true, 1, 8>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
-    else
-      hipLaunchKernelGGL((merge_rows_kernel<true, 2, 2>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
-  } else {
-    if (few)
-      hipLaunchKernelGGL((merge_rows_kernel<false, 1, 8>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
-    else
-      hipLaunchKernelGGL((merge_rows_kernel<false, 2, 2>), grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
-  }
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, src, yp, slot_of, w, s.R, s.T, s.k, s.d);
+  };
+  if (s.dtype == MOE_F32) launch(few ? merge_rows_kernel<false, 1, 8> : merge_rows_kernel<false, 2, 2>);
+  else if (rows32) launch(few ? merge_rows_kernel<false, 1, 8, true> : merge_rows_kernel<false, 2, 2, true>);
+  else launch(few ? merge_rows_kernel<true, 1, 8> : merge_rows_kernel<true, 2, 2>);
   return hipGetLastError();
 }
 

@@ -51,7 +51,7 @@ enum CtrlSlot {
 constexpr int kMaxRingSlots = 65536;
 
 struct WsLayout {
-  size_t ctrl, l2g, mtile_base, chunk_base, blockhist, blockbase, pctrl, hbuf, push_dst, pull_addr, total;
+  size_t ctrl, l2g, mtile_base, chunk_base, blockhist, blockbase, pctrl, hbuf, push_dst, pull_addr, rows32, total;
   int32_t nb;        // layout blocks
   int64_t max_pairs;
   int32_t max_mtiles;
@@ -61,6 +61,10 @@ inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // MXFP4 h staging: where the block scales lie behind the codes of max_pairs rows of F values
 inline size_t mx4_h_scales_offset(int64_t max_pairs, int F) { return align256(size_t(max_pairs) * (F / 2)); }
+
+// Expert outputs of moe_forward_choices in MXFP4 stay in fp32 (in the workspace) up to this many bytes:
+// they stay in the caches then, and y is rounded once instead of twice.
+constexpr int64_t kRows32Bytes = int64_t(16) << 20;
 
 inline WsLayout ws_layout(const moe_shape_t& s, int32_t E_local) {
   WsLayout w{};
@@ -90,6 +94,11 @@ inline WsLayout ws_layout(const moe_shape_t& s, int32_t E_local) {
   w.push_dst = o;    o = align256(o + size_t(w.max_pairs) * 8);
   // per local pair: the address of its source token row (the pull fused into the gate/up GEMM)
   w.pull_addr = o;   o = align256(o + size_t(w.max_pairs) * 8);
+  w.rows32 = 0;                        // none
+  if (s.dtype == MOE_MXFP4 && w.max_pairs * s.d * 4 <= kRows32Bytes) {
+    w.rows32 = o;
+    o = align256(o + size_t(w.max_pairs) * s.d * 4);
+  }
   w.total = o;
   return w;
 }

@@ -75,6 +75,7 @@ __device__ __forceinline__ void swap_rows16(uint32_t& a, uint32_t& b) {
 // MODE 0: A = xe codes [*][d/2], B0/B1 = W1/W3 -> h codes [*][F/2] + scales   (256 rows x 128 f)
 // MODE 1: A = h codes [*][F/2],  B0 = W2 -> bf16 [*][d]                        (256 x 256)
 // MODE 2: the same, each row to the address that RowDst holds for it (the fused push)
+// MODE 3: the same, fp32 rows
 // Tile enumeration as in the other grouped GEMMs: a persistent grid walks 8 contiguous
 // per-XCD ranges of the expert-major tile list.
 template <int MODE>
@@ -231,7 +232,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
   auto wide = [](const i32x4& v) -> i32x8 { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; };
 
   // stores an epilogue certainly issues for a whole tile (waits may leave so many operations in flight)
-  constexpr int kStores = (MODE == 0) ? 4 : 16;
+  constexpr int kStores = (MODE == 0) ? 4 : (MODE == 3) ? 32 : 16;
   auto kloop = [&](auto mvc, int behind) {
     constexpr int MV = decltype(mvc)::value;
     i32x4 fa[2][2], fb[2][4];            // fragments, two sets
@@ -407,6 +408,19 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
           Cs[(t.c0 >> 7) * (4 * nmax) + 4 * size_t(t.row0 + row) + blk] = uint8_t(hio ? sc[1] : sc[0]);
         }
       }
+    } else if (MODE == 3 && t.c0 + wn * 128 < Nout) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int row = wm * 64 + m * 32 + r32o;
+        f32x4* const dst = reinterpret_cast<f32x4*>(static_cast<float*>(C) + size_t(t.row0 + min(row, t.rows - 1)) * Nout +
+                                                    t.c0 + wn * 128 + hio * 4);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (row < t.rows)
+              dst[8 * n + 2 * c] = f32x4{acc[m][n][4 * c], acc[m][n][4 * c + 1], acc[m][n][4 * c + 2], acc[m][n][4 * c + 3]};
+      }
     } else if (t.c0 + wn * 128 < Nout) {
       // bf16 rows, rounded once from fp32 (the row type of this library's expert outputs).  Two
       // exchanges turn a block's column quads into 16 rows x 64 bytes: lane group g = lane / 16 holds
@@ -447,13 +461,13 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_mx4_kernel(
 
 hipError_t launch_thin_mx4(bool gate_up, const uint8_t* a, const uint8_t* as, const uint8_t* b0, const uint8_t* b1,
                            const uint8_t* bs0, const uint8_t* bs1, void* o, uint8_t* os, const int32_t* offsets,
-                           const uint64_t* row_dst, int64_t nmax, int El, int64_t experts, int K, int Nout, int cus,
-                           hipStream_t st);
+                           const uint64_t* row_dst, bool rows32, int64_t nmax, int El, int64_t experts, int K, int Nout,
+                           int cus, hipStream_t st);
 
 hipError_t launch_ffn_mx4(const moe_shape_t& s, int El, const uint8_t* xe, const uint8_t* xe_scales,
                           const int32_t* offsets, const uint8_t* w1, const uint8_t* w3, const uint8_t* w2,
                           const moe_mx_scales_t& w_scales, void* ye, char* ws, const WsLayout& L, int cus,
-                          hipStream_t st, const uint64_t* row_dst) {
+                          hipStream_t st, const uint64_t* row_dst, bool rows32) {
   static std::atomic<uint64_t> attr_set{0};
   const hipError_t ea = once_per_device(attr_set, [] {
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(grouped_gemm_mx4_kernel<0>),
@@ -463,6 +477,9 @@ hipError_t launch_ffn_mx4(const moe_shape_t& s, int El, const uint8_t* xe, const
                               hipFuncAttributeMaxDynamicSharedMemorySize, kMx4Lds);
     if (e == hipSuccess)
       e = hipFuncSetAttribute(reinterpret_cast<const void*>(grouped_gemm_mx4_kernel<2>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, kMx4Lds);
+    if (e == hipSuccess)
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(grouped_gemm_mx4_kernel<3>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, kMx4Lds);
     return e;
   });
@@ -486,7 +503,7 @@ hipError_t launch_ffn_mx4(const moe_shape_t& s, int El, const uint8_t* xe, const
   const int64_t experts = El < nmax ? El : nmax;             // with a row, at most
   if (thin) {
     const hipError_t e = launch_thin_mx4(true, xe, xe_scales, w1, w3, w_scales.w1, w_scales.w3, hq, hs, offsets, nullptr,
-                                         nmax, El, experts, s.d, s.F, cus, st);
+                                         false, nmax, El, experts, s.d, s.F, cus, st);
     if (e != hipSuccess) return e;
   }
   if (wide)
@@ -495,11 +512,11 @@ hipError_t launch_ffn_mx4(const moe_shape_t& s, int El, const uint8_t* xe, const
                        nullptr, min_rows);
   if (thin) {
     const hipError_t e = launch_thin_mx4(false, hq, hs, w2, w2, w_scales.w2, w_scales.w2, ye, nullptr, offsets, row_dst,
-                                         nmax, El, experts, s.F, s.d, cus, st);
+                                         rows32, nmax, El, experts, s.F, s.d, cus, st);
     if (e != hipSuccess) return e;
   }
   if (wide) {
-    const auto kernel = row_dst ? grouped_gemm_mx4_kernel<2> : grouped_gemm_mx4_kernel<1>;
+    const auto kernel = row_dst ? grouped_gemm_mx4_kernel<2> : rows32 ? grouped_gemm_mx4_kernel<3> : grouped_gemm_mx4_kernel<1>;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(kGemmThreads), kMx4Lds, st, hq, hs, w2, nullptr, w_scales.w2, nullptr, ye,
                        nullptr, offsets, mtb, ctrl, El, s.F, s.d, nmax, row_dst, min_rows);
   }

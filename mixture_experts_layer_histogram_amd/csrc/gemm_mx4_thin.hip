@@ -41,11 +41,11 @@ constexpr int thin_lds(int split) {
 struct ThinArgs {
   const uint8_t* a;       // token rows' codes, row stride K / 2; scales as, planes of 4 * nmax bytes
   const uint8_t* as;
-  const uint8_t* b0;      // weight codes [El][Nout][K / 2] (MODE 0: W1 and W3, MODE 1: W2 for both)
+  const uint8_t* b0;      // weight codes [El][Nout][K / 2] (MODE 0: W1 and W3, MODE 1 and 2: W2 for both)
   const uint8_t* b1;
   const uint8_t* bs0;     // their scales, planes of 4 * El * Nout bytes
   const uint8_t* bs1;
-  void* o;                // MODE 0: h codes, row stride Nout / 2; MODE 1: bf16 rows, stride Nout (or row_dst)
+  void* o;                // MODE 0: h codes, row stride Nout / 2; MODE 1: bf16 rows, stride Nout (or row_dst); MODE 2: fp32 rows
   uint8_t* os;            // MODE 0: h scales, planes of 4 * nmax bytes
   const int32_t* offsets;
   const uint64_t* row_dst;
@@ -259,6 +259,15 @@ __global__ __launch_bounds__(256, 1) void thin_mx4_kernel(ThinArgs g) {
           }
           if (hi == 0) g.os[(t.cb >> 2) * 4 * g.nmax + 4 * row + (t.cb & 3)] = uint8_t(sc);
         }
+      } else if (MODE == 2) {
+        f32x4* dst = reinterpret_cast<f32x4*>(static_cast<float*>(g.o) + size_t(row) * g.Nout + t.cb * 64 + hi * 4);
+        if (r32 < t.rows) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              dst[8 * q + 2 * c] = f32x4{acc[q][4 * c], acc[q][4 * c + 1], acc[q][4 * c + 2], acc[q][4 * c + 3]};
+        }
       } else if (r32 < t.rows) {
         uint16_t* orow = g.row_dst ? reinterpret_cast<uint16_t*>(g.row_dst[row])
                                    : static_cast<uint16_t*>(g.o) + size_t(row) * g.Nout;
@@ -277,8 +286,8 @@ __global__ __launch_bounds__(256, 1) void thin_mx4_kernel(ThinArgs g) {
 // `experts`: how many may have rows at most (the host's bound: local experts and pairs)
 hipError_t launch_thin_mx4(bool gate_up, const uint8_t* a, const uint8_t* as, const uint8_t* b0, const uint8_t* b1,
                            const uint8_t* bs0, const uint8_t* bs1, void* o, uint8_t* os, const int32_t* offsets,
-                           const uint64_t* row_dst, int64_t nmax, int El, int64_t experts, int K, int Nout, int cus,
-                           hipStream_t st) {
+                           const uint64_t* row_dst, bool rows32, int64_t nmax, int El, int64_t experts, int K, int Nout,
+                           int cus, hipStream_t st) {
   static std::atomic<uint64_t> attr_set{0};
   const hipError_t ea = once_per_device(attr_set, [] {
     const struct {
@@ -287,7 +296,9 @@ hipError_t launch_thin_mx4(bool gate_up, const uint8_t* a, const uint8_t* as, co
     } ks[] = {{reinterpret_cast<const void*>(thin_mx4_kernel<0, 1>), thin_lds(1)},
               {reinterpret_cast<const void*>(thin_mx4_kernel<0, 4>), thin_lds(4)},
               {reinterpret_cast<const void*>(thin_mx4_kernel<1, 1>), thin_lds(1)},
-              {reinterpret_cast<const void*>(thin_mx4_kernel<1, 4>), thin_lds(4)}};
+              {reinterpret_cast<const void*>(thin_mx4_kernel<1, 4>), thin_lds(4)},
+              {reinterpret_cast<const void*>(thin_mx4_kernel<2, 1>), thin_lds(1)},
+              {reinterpret_cast<const void*>(thin_mx4_kernel<2, 4>), thin_lds(4)}};
     for (const auto& k : ks) {
       const hipError_t e = hipFuncSetAttribute(k.f, hipFuncAttributeMaxDynamicSharedMemorySize, k.lds);
       if (e != hipSuccess) return e;
@@ -302,6 +313,8 @@ hipError_t launch_thin_mx4(bool gate_up, const uint8_t* a, const uint8_t* as, co
   const dim3 grid(int(wgs < cus ? wgs : cus));               // one workgroup per CU (LDS)
   if (gate_up && alone) hipLaunchKernelGGL((thin_mx4_kernel<0, 1>), grid, dim3(256), thin_lds(1), st, g);
   else if (gate_up) hipLaunchKernelGGL((thin_mx4_kernel<0, 4>), grid, dim3(256), thin_lds(4), st, g);
+  else if (rows32 && alone) hipLaunchKernelGGL((thin_mx4_kernel<2, 1>), grid, dim3(256), thin_lds(1), st, g);
+  else if (rows32) hipLaunchKernelGGL((thin_mx4_kernel<2, 4>), grid, dim3(256), thin_lds(4), st, g);
   else if (alone) hipLaunchKernelGGL((thin_mx4_kernel<1, 1>), grid, dim3(256), thin_lds(1), st, g);
   else hipLaunchKernelGGL((thin_mx4_kernel<1, 4>), grid, dim3(256), thin_lds(4), st, g);
   return hipGetLastError();

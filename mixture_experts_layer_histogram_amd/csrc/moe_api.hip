@@ -77,7 +77,7 @@ hipError_t launch_gemm1_bwd_mx(const uint8_t* xe, const uint8_t* xes, const uint
 hipError_t launch_layout_choices(const moe_shape_t& s, const int32_t* e2l, int El, int mb, const int32_t* topk_idx,
                                  int32_t* counts, int32_t* offsets, int32_t* pull_src, int32_t* slot_of, char* ws,
                                  const WsLayout& L, hipStream_t st);
-hipError_t launch_merge_rows(const moe_shape_t& s, const void* rows, const int32_t* slot_of, const float* w,
+hipError_t launch_merge_rows(const moe_shape_t& s, const void* rows, bool rows32, const int32_t* slot_of, const float* w,
                              void* const* y, int cus, hipStream_t st);
 hipError_t launch_merge_rows_bwd(const moe_shape_t& s, const void* const* dy, const void* ye, const int32_t* slot_of,
                                  const float* w, void* dye, float* dw, int cus, hipStream_t st);
@@ -90,7 +90,7 @@ hipError_t launch_dispatch_mx4(const moe_shape_t& s, const void* const* x, const
 hipError_t launch_ffn_mx4(const moe_shape_t& s, int El, const uint8_t* xe, const uint8_t* xe_scales,
                           const int32_t* offsets, const uint8_t* w1, const uint8_t* w3, const uint8_t* w2,
                           const moe_mx_scales_t& w_scales, void* ye, char* ws, const WsLayout& L, int cus,
-                          hipStream_t st, const uint64_t* row_dst);
+                          hipStream_t st, const uint64_t* row_dst, bool rows32);
 }  // namespace moe
 
 using namespace moe;
@@ -325,7 +325,7 @@ int moe_expert_ffn(const moe_shape_t* s, const moe_placement_t* p, const moe_exe
     return hip_rc(launch_ffn_mx4(*s, p->E_local, static_cast<const uint8_t*>(xe), xe_scales, offsets,
                                  static_cast<const uint8_t*>(w1), static_cast<const uint8_t*>(w3),
                                  static_cast<const uint8_t*>(w2), *w_scales, ye, static_cast<char*>(ws), L, cu_count(),
-                                 static_cast<hipStream_t>(stream), nullptr));
+                                 static_cast<hipStream_t>(stream), nullptr, false));
   return hip_rc(launch_ffn(*s, p->E_local, xe, offsets, w1, w3, w2, ye, static_cast<char*>(ws), L, cu_count(),
                            static_cast<hipStream_t>(stream), nullptr, nullptr));
 }
@@ -362,7 +362,7 @@ int moe_expert_ffn_push(const moe_shape_t* s, const moe_placement_t* p, const mo
   if (s->dtype == MOE_MXFP4)
     return hip_rc(launch_ffn_mx4(*s, p->E_local, static_cast<const uint8_t*>(xe), xe_scales, offsets,
                                  static_cast<const uint8_t*>(w1), static_cast<const uint8_t*>(w3),
-                                 static_cast<const uint8_t*>(w2), *w_scales, nullptr, w, L, cu_count(), st, dst));
+                                 static_cast<const uint8_t*>(w2), *w_scales, nullptr, w, L, cu_count(), st, dst, false));
   return hip_rc(launch_ffn(*s, p->E_local, x ? nullptr : xe, offsets, w1, w3, w2, nullptr, w, L, cu_count(), st, dst,
                            src));
 }
@@ -468,7 +468,7 @@ int moe_combine_merge(const moe_shape_t* s, const moe_placement_t* p, const void
   if (!slot_of || !topk_w) return MOE_EINVAL;
   if (!aligned16(ye)) return ye ? MOE_EALIGN : MOE_EINVAL;
   if ((rc = check_ptr_table(y, s->R)) || (rc = check_not_in(ye, y, s->R))) return rc;
-  return hip_rc(launch_merge_rows(*s, ye, slot_of, topk_w, y, cu_count(), static_cast<hipStream_t>(stream)));
+  return hip_rc(launch_merge_rows(*s, ye, false, slot_of, topk_w, y, cu_count(), static_cast<hipStream_t>(stream)));
 }
 
 int moe_combine_merge_backward(const moe_shape_t* s, const moe_placement_t* p, const void* const* dy, const void* ye,
@@ -492,7 +492,7 @@ int moe_dispatch_pull_backward(const moe_shape_t* s, const moe_placement_t* p, c
   if (!slot_of) return MOE_EINVAL;
   if (!aligned16(dxe)) return dxe ? MOE_EALIGN : MOE_EINVAL;
   if ((rc = check_ptr_table(dx, s->R)) || (rc = check_not_in(dxe, dx, s->R))) return rc;
-  return hip_rc(launch_merge_rows(*s, dxe, slot_of, nullptr, dx, cu_count(), static_cast<hipStream_t>(stream)));
+  return hip_rc(launch_merge_rows(*s, dxe, false, slot_of, nullptr, dx, cu_count(), static_cast<hipStream_t>(stream)));
 }
 
 int moe_forward_choices(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t* ex, const int32_t* topk_idx,
@@ -512,6 +512,16 @@ int moe_forward_choices(const moe_shape_t* s, const moe_placement_t* p, const mo
   if ((rc = check_ws(s, p, ws, ws_bytes)) || (rc = check_not_in(ye, y, s->R))) return rc;
   if ((rc = moe_layout_choices(s, p, ex, topk_idx, counts, offsets, pull_src, slot_of, ws, ws_bytes, stream))) return rc;
   if ((rc = moe_dispatch_pull(s, p, x, pull_src, offsets, xe, xe_scales, ws, ws_bytes, stream))) return rc;
+  const WsLayout L = ws_layout(*s, p->E_local);
+  if (L.rows32) {            // MXFP4 and few rows: they stay in fp32, y is rounded once
+    char* const rows = static_cast<char*>(ws) + L.rows32;
+    const hipError_t e = launch_ffn_mx4(
+        *s, p->E_local, static_cast<const uint8_t*>(xe), xe_scales, offsets, static_cast<const uint8_t*>(w1),
+        static_cast<const uint8_t*>(w3), static_cast<const uint8_t*>(w2), *w_scales, rows, static_cast<char*>(ws), L,
+        cu_count(), static_cast<hipStream_t>(stream), nullptr, true);
+    if (e != hipSuccess) return hip_rc(e);
+    return hip_rc(launch_merge_rows(*s, rows, true, slot_of, topk_w, y, cu_count(), static_cast<hipStream_t>(stream)));
+  }
   if ((rc = moe_expert_ffn(s, p, ex, xe, xe_scales, offsets, w1, w3, w2, w_scales, ye, ws, ws_bytes, stream)))
     return rc;
   return moe_combine_merge(s, p, ye, slot_of, topk_w, y, stream);

@@ -123,8 +123,12 @@ def test_paths_that_mxfp4_does_not_have():
     assert L.moe_backward_prepare_mx(S, P, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None) == -6
     a, b = ctypes.c_size_t(), ctypes.c_size_t()
     assert L.moe_backward_rows_info(S, P, ctypes.byref(a), ctypes.byref(b)) == -6
-    # h is half a byte a value: the workspace is smaller than MXFP8's
-    assert 0 < moe.moe_workspace_bytes(s, p) < moe.moe_workspace_bytes(_shape(dtype=moe.MOE_MXFP8), p)
+    # h is half a byte a value: the workspace is smaller than MXFP8's ...
+    many, m8 = _shape(dtype=moe.MOE_MXFP4, T=4096), _shape(dtype=moe.MOE_MXFP8, T=4096)
+    assert 0 < moe.moe_workspace_bytes(many, p) < moe.moe_workspace_bytes(m8, p)
+    # ... but holds fp32 expert rows up to 16 MiB of them: 4096 rows of 1024, not 4104
+    at, past = (moe.moe_workspace_bytes(_shape(dtype=moe.MOE_MXFP4, T=t), p) for t in (512, 513))
+    assert at > (16 << 20) > past
     # and the calls it shares with MXFP8 need its scales
     assert L.moe_dispatch_pull(S, P, t, FAKE, FAKE, FAKE, None, FAKE, BIG, None) == -1
     assert L.moe_expert_ffn(S, P, None, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, FAKE, FAKE, BIG, None) == -1
