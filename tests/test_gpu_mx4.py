@@ -501,3 +501,39 @@ def test_graph_replays_and_two_streams():
         torch.cuda.synchronize()
         for P, w in zip((A, B), want):
             assert all(torch.equal(a, b) for a, b in zip(P.y, w)), i
+
+
+@pytest.mark.parametrize("T", [9, 300])
+def test_two_graphs_over_one_workspace(T):
+    """Two captured layers with choices of their own over the same buffers, replayed in turn with eager
+    calls between: every call leaves its own result, whatever the tables held."""
+    torch = _torch()
+    cfg = _cfg(f"mx4 two graphs T{T}", T=T, d=512, F=384, E=12, E_local=6, k=3)
+    inp, P = _problem(cfg)
+    rng = np.random.default_rng(5)
+    ch = []
+    for drop in (0.0, 0.3, 1.0):
+        idx = np.argsort(rng.random((1, T, 12)), -1)[..., :3].astype(np.int32)
+        idx[rng.random(idx.shape) < drop] = -1
+        ch.append((torch.from_numpy(idx).cuda(), torch.rand(1, T, 3, device="cuda")))
+    want = []
+    for c in ch:
+        P.forward_choices(*c)
+        want.append(P.y[0].clone())
+    assert not torch.equal(want[0], want[1]) and (want[2] == 0).all()
+    graphs = []
+    s = torch.cuda.Stream()
+    for c in ch[:2]:
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            P.forward_choices(*c)
+        graphs.append(g)
+    for i in (0, 1, 1, 2, 0, 2, 1):
+        P.y[0].fill_(float("nan"))
+        if i < 2:
+            graphs[i].replay()
+        else:
+            P.forward_choices(*ch[2])
+        torch.cuda.synchronize()
+        assert torch.equal(P.y[0], want[i]), i
