@@ -124,7 +124,11 @@ typedef struct {
 /* Worst-case local pairs: R * T * min(k, E_local).  Sizes of xe/ye/pull_src below. */
 int64_t moe_max_pairs(const moe_shape_t* s, const moe_placement_t* p);
 
-/* Workspace bytes needed by every call below for this shape (a pure host function). */
+/* Workspace bytes for every call below with this shape (a pure host function).  A workspace made for a
+ * shape serves every shape with fewer ranks or tokens and the same other fields: the calls refuse
+ * (MOE_ENOSPC) only what is smaller than their tables and staging rows, which grow with R * T.  With
+ * MOE_MXFP4 the figure may be larger for fewer tokens, since it then has room for the fp32 rows of
+ * moe_forward_choices, which that call does without where they do not fit. */
 size_t moe_workspace_bytes(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t* ex);
 
 /*
@@ -398,8 +402,10 @@ int moe_dispatch_pull_backward(const moe_shape_t* s, const moe_placement_t* p, c
  * the choices and their weights as inputs and without logits and recv; every stage's arguments
  * are checked before the first launch.  xe, ye and pull_src need [moe_max_pairs] rows, of which
  * [0, N) are touched (the scales in xe_scales keep moe_max_pairs rows a plane); a caller who
- * knows N may pass N rows of ye and pull_src.  With MOE_MXFP4 and moe_max_pairs * d * 4 <= 16 MiB the
- * expert rows stay in fp32 in ws instead (ye is left as it is), and y is rounded once; otherwise y
+ * knows N may pass N rows of ye and pull_src.  With MOE_MXFP4, moe_max_pairs * d * 4 <= 16 MiB
+ * and ws_bytes of at least this shape's moe_workspace_bytes, the expert rows stay in fp32 in ws
+ * instead (ye is left as it is, so nothing may read it afterwards), and y is rounded once; otherwise,
+ * also with a smaller workspace that was made for more tokens, they are bf16 rows in ye, and y
  * is moe_forward's bit for bit for the choices and weights that moe_layout takes.
  */
 int moe_forward_choices(const moe_shape_t* s, const moe_placement_t* p, const moe_exec_t* ex, const int32_t* topk_idx,

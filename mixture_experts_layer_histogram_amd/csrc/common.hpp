@@ -51,7 +51,7 @@ enum CtrlSlot {
 constexpr int kMaxRingSlots = 65536;
 
 struct WsLayout {
-  size_t ctrl, l2g, mtile_base, chunk_base, blockhist, blockbase, pctrl, hbuf, push_dst, pull_addr, rows32, total;
+  size_t ctrl, l2g, mtile_base, chunk_base, blockhist, blockbase, pctrl, hbuf, push_dst, pull_addr, need, rows32, total;
   int32_t nb;        // layout blocks
   int64_t max_pairs;
   int32_t max_mtiles;
@@ -94,6 +94,9 @@ inline WsLayout ws_layout(const moe_shape_t& s, int32_t E_local) {
   w.push_dst = o;    o = align256(o + size_t(w.max_pairs) * 8);
   // per local pair: the address of its source token row (the pull fused into the gate/up GEMM)
   w.pull_addr = o;   o = align256(o + size_t(w.max_pairs) * 8);
+  // What every call needs ends here, and grows with the tokens.  The fp32 rows behind it do not: a
+  // workspace made for more tokens may end before them, and then the rows go to ye in bf16.
+  w.need = o;
   w.rows32 = 0;                        // none
   if (s.dtype == MOE_MXFP4 && w.max_pairs * s.d * 4 <= kRows32Bytes) {
     w.rows32 = o;

@@ -118,7 +118,7 @@ int check_shape(const moe_shape_t* s, const moe_placement_t* p) {
 int check_ws(const moe_shape_t* s, const moe_placement_t* p, const void* ws, size_t ws_bytes) {
   if (!ws) return MOE_EINVAL;
   if (reinterpret_cast<uintptr_t>(ws) & 255) return MOE_EALIGN;
-  if (ws_bytes < ws_layout(*s, p->E_local).total) return MOE_ENOSPC;
+  if (ws_bytes < ws_layout(*s, p->E_local).need) return MOE_ENOSPC;
   return MOE_OK;
 }
 
@@ -513,7 +513,7 @@ int moe_forward_choices(const moe_shape_t* s, const moe_placement_t* p, const mo
   if ((rc = moe_layout_choices(s, p, ex, topk_idx, counts, offsets, pull_src, slot_of, ws, ws_bytes, stream))) return rc;
   if ((rc = moe_dispatch_pull(s, p, x, pull_src, offsets, xe, xe_scales, ws, ws_bytes, stream))) return rc;
   const WsLayout L = ws_layout(*s, p->E_local);
-  if (L.rows32) {            // MXFP4 and few rows: they stay in fp32, y is rounded once
+  if (L.rows32 && ws_bytes >= L.total) {       // MXFP4, few rows and room for them: they stay in fp32, y is rounded once
     char* const rows = static_cast<char*>(ws) + L.rows32;
     const hipError_t e = launch_ffn_mx4(
         *s, p->E_local, static_cast<const uint8_t*>(xe), xe_scales, offsets, static_cast<const uint8_t*>(w1),

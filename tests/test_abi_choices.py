@@ -167,3 +167,28 @@ def test_codec_refusals(fmt):
     assert dq(FAKE, FAKE + 2, fmt, 4, 128, FAKE, moe.MOE_F32, None) == -2
     assert q(FAKE, moe.MOE_BF16, 0, 128, fmt, FAKE, FAKE, None) == 0                 # nothing to do, nothing launched
     assert dq(FAKE, FAKE, fmt, 0, 128, FAKE, moe.MOE_BF16, None) == 0
+
+
+@pytest.mark.parametrize("kw,El,Ts", [(dict(R=1, d=2048, F=1408, E=64, k=6), 64, (1, 128, 340, 341, 1024)),
+                                      (dict(R=2, d=1024, F=512, E=16, k=4), 8, (1, 33, 512, 513, 4096)),
+                                      (dict(R=8, d=7168, F=2048, E=256, k=8), 32, (1, 9, 10, 64, 4096))])
+def test_a_workspace_for_more_tokens_serves_fewer(kw, El, Ts):
+    """moe_workspace_bytes of T tokens suffices for every smaller T, although the fp32 rows make it smaller than
+    those of some of them.  (The calls check the workspace before ye is found among the outputs.)"""
+    other = FAKE + (1 << 40)
+
+    def forward(T, ws_bytes):
+        s = _shape(dtype=moe.MOE_MXFP4, T=T, **kw)
+        t = (ctypes.c_void_p * s.R)(*[FAKE] * s.R)
+        args = [None, FAKE, FAKE, t, FAKE, FAKE, FAKE, ctypes.byref(MX), other, FAKE, FAKE, t, FAKE, FAKE, FAKE, FAKE, FAKE,
+                ws_bytes, None]
+        return _call("moe_forward_choices", s, args, moe.Placement(FAKE, El))
+
+    size = {T: moe.moe_workspace_bytes(_shape(dtype=moe.MOE_MXFP4, T=T, **kw), moe.Placement(FAKE, El)) for T in Ts}
+    assert any(size[a] > size[b] for a in Ts for b in Ts if a < b)
+    for T in Ts:
+        for small in Ts:
+            if small <= T:
+                assert forward(small, size[T]) == -1, (small, T)            # not MOE_ENOSPC
+        assert forward(T, 4096) == -3
+    assert forward(Ts[-1], size[Ts[-1]] - 256) == -3 and forward(Ts[-1], size[Ts[0]]) == -3

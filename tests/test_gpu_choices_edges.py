@@ -1,0 +1,46 @@
+"""GPU tests of calls at the edges of what the header allows, for given choices and MXFP4 experts."""
+import pytest
+from mixture_experts_layer_histogram_amd import moe
+from tests.test_gpu_mx4 import _cfg, _check_merged, _check_rows, _problem, _push, _torch, _weights64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T,most", [(40, 3000), (200, 3000)])
+def test_every_call_in_a_workspace_made_for_more_tokens(T, most):
+    """The workspace of `most` tokens is smaller than that of T, which has room for fp32 rows.  Every call takes it, the
+    rows are bf16 in ye, y is moe_forward's, and nothing behind its end is written.  With the shape's own
+    workspace the rows stay in fp32 and ye is left alone."""
+    torch = _torch()
+    cfg = _cfg(f"mx4 workspace for {most} tokens, T{T}", T=T, d=1024, F=256, E=16, E_local=16, k=4)
+    inp, P = _problem(cfg)
+    own = P.ws
+    many = moe.Shape(1, most, cfg.d, cfg.E, cfg.k, cfg.F, P.shape.dtype)
+    size = moe.moe_workspace_bytes(many, P.placement)
+    if T == 200:
+        assert size < own.numel()
+    wide = torch.full((max(size, own.numel()) + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    P.ws = wide[:size]
+    if size > own.numel():                     # as small as the calls take: without the fp32 rows
+        P.ws = wide[:own.numel() - P.nmax * cfg.d * 4]
+    end = P.ws.numel()
+    P.forward()
+    assert P.status() == 0
+    y, rows = [t.clone() for t in P.y], P.ye.clone()
+    N = int(P.offsets[-1])
+    idx, w = P.topk_idx.clone(), P.topk_w.clone()
+    P.forward_fused()
+    assert P.status() == 0 and torch.equal(y[0], P.y[0])
+    assert torch.equal(y[0], _push(P, idx, w)[0])
+    P.ye.fill_(float("nan"))
+    P.y[0].fill_(float("nan"))
+    P.forward_choices(idx, w)
+    assert P.status() == 0 and torch.equal(y[0], P.y[0]) and torch.equal(rows[:N], P.ye[:N])
+    assert (wide[end:] == 0x5A).all()
+    P.ws = own
+    P.ye.fill_(float("nan"))
+    P.forward_choices(idx, w)
+    assert P.status() == 0 and torch.isnan(P.ye).all() and not torch.equal(y[0], P.y[0])
+    P.ye.copy_(rows)
+    x64 = P.rows_f64(P.x[0]).reshape(1, cfg.T, cfg.d)
+    _check_merged(P, *_check_rows(P, P.ye, x64, _weights64(P)), w)
