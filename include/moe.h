@@ -381,6 +381,9 @@ int moe_combine_merge(const moe_shape_t* s, const moe_placement_t* p, const void
  *   dtopk_w[r][t][j] = <dy[r][t], ye[s]>       (fp32), 0 for a pair that is not local.
  * Rows of dye from N on are left as they are.  dye may overlap neither ye nor a dy (MOE_EINVAL
  * where it is one of them).  Deterministic.
+ * MOE_MXFP4 returns MOE_EUNSUP: moe_forward_choices may keep its expert rows in fp32 and leave ye as it
+ * is.  The gates' gradient over frozen 4-bit experts takes the bf16 rows that moe_expert_ffn wrote, with
+ * a shape of dtype MOE_BF16.
  * For the bf16 expert backward (moe_expert_ffn_backward), dye goes to the place that
  * moe_backward_rows_info names.  Buffers 16-byte aligned.
  */

@@ -481,6 +481,7 @@ int moe_combine_merge_backward(const moe_shape_t* s, const moe_placement_t* p, c
     if (!aligned16(b)) return b ? MOE_EALIGN : MOE_EINVAL;
   if ((rc = check_ptr_table(dy, s->R)) || (rc = check_not_in(dye, dy, s->R))) return rc;
   if (dye == ye) return MOE_EINVAL;
+  if (s->dtype == MOE_MXFP4) return MOE_EUNSUP;      // forward only: moe_forward_choices may have left ye as it was
   return hip_rc(launch_merge_rows_bwd(*s, dy, ye, slot_of, topk_w, dye, dtopk_w, cu_count(),
                                       static_cast<hipStream_t>(stream)));
 }

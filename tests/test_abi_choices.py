@@ -192,3 +192,9 @@ def test_a_workspace_for_more_tokens_serves_fewer(kw, El, Ts):
                 assert forward(small, size[T]) == -1, (small, T)            # not MOE_ENOSPC
         assert forward(T, 4096) == -3
     assert forward(Ts[-1], size[Ts[-1]] - 256) == -3 and forward(Ts[-1], size[Ts[0]]) == -3
+
+
+def test_merge_backward_has_no_mxfp4_form():
+    """moe_forward_choices in MXFP4 writes ye or not by its size, so the gradient that reads ye refuses the dtype."""
+    args = [_tab(), FAKE + (1 << 40), FAKE, FAKE, FAKE + (2 << 40), FAKE, None]
+    assert _call("moe_combine_merge_backward", _shape(dtype=moe.MOE_MXFP4), args) == -6

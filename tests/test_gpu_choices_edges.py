@@ -44,3 +44,40 @@ def test_every_call_in_a_workspace_made_for_more_tokens(T, most):
     P.ye.copy_(rows)
     x64 = P.rows_f64(P.x[0]).reshape(1, cfg.T, cfg.d)
     _check_merged(P, *_check_rows(P, P.ye, x64, _weights64(P)), w)
+
+
+@pytest.mark.parametrize("T", [40, 1100])
+def test_gate_gradient_over_mxfp4_experts(T):
+    """Staged calls write ye at every size, and the gradient of the gates reads it with a bf16 shape; the MXFP4
+    shape is refused (at T = 40 moe_forward_choices leaves ye as it was, at 1100 it writes it)."""
+    torch = _torch()
+    cfg = _cfg(f"mx4 gate gradient T{T}", R=2, T=T, d=1024, F=256, E=16, E_local=8, k=4)
+    inp, P = _problem(cfg)
+    P.forward()
+    idx, w = P.topk_idx.clone(), P.topk_w.clone()
+    P.ye.fill_(float("nan"))
+    P.forward_choices(idx, w)
+    N = int(P.offsets[-1])
+    assert bool(torch.isnan(P.ye[:N]).any()) == (T == 40)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    dy = [torch.randn(T, cfg.d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    dye, dw = torch.full_like(P.ye, 9.0), torch.full_like(w, float("nan"))
+    args = (dy, P.ye, P.slot_of, w, dye, dw)
+    with pytest.raises(moe.MoEError):
+        moe.moe_combine_merge_backward(P.shape, P.placement, *args)
+    moe.moe_layout_choices(P.shape, P.placement, P.ex, idx, P.counts, P.offsets, P.pull_src, P.slot_of, P.ws)
+    P.dispatch()
+    P.ffn()
+    rows = moe.Shape(2, T, cfg.d, cfg.E, cfg.k, cfg.F, moe.MOE_BF16)
+    moe.moe_combine_merge_backward(rows, P.placement, *args)
+    slot = P.slot_of.long()
+    ye, dy64 = P.ye.double(), torch.stack(dy).double()[:, :, None]
+    at = torch.where(slot >= 0, slot, 0)
+    want = (dy64 * ye[at]).sum(-1)
+    size = (dy64.abs() * ye[at].abs()).sum(-1)
+    local = slot >= 0
+    # d products and their sum in fp32, d / 64 + 6 additions to a lane
+    assert ((dw.double() - want).abs() <= (cfg.d / 64 + 16) * 2.0 ** -24 * size)[local].all() and (dw[~local] == 0).all()
+    step = w.double()[local][:, None] * dy64.expand(-1, -1, cfg.k, -1)[local]
+    assert ((dye[slot[local]].double() - step).abs() <= (2.0 ** -8 + 2.0 ** -23) * step.abs()).all()
+    assert (dye[N:] == 9.0).all()
