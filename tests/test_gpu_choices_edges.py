@@ -1,7 +1,11 @@
 """GPU tests of calls at the edges of what the header allows, for given choices and MXFP4 experts."""
+import numpy as np
 import pytest
+
+from oracle import mx4_oracle as M4
 from mixture_experts_layer_histogram_amd import moe
-from tests.test_gpu_mx4 import _cfg, _check_merged, _check_rows, _problem, _push, _torch, _weights64
+from tests.mx4_packed import Packed
+from tests.test_gpu_mx4 import _bound, _cfg, _check_merged, _check_rows, _problem, _push, _torch, _weights64
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +85,34 @@ def test_gate_gradient_over_mxfp4_experts(T):
     step = w.double()[local][:, None] * dy64.expand(-1, -1, cfg.k, -1)[local]
     assert ((dye[slot[local]].double() - step).abs() <= (2.0 ** -8 + 2.0 ** -23) * step.abs()).all()
     assert (dye[N:] == 9.0).all()
+
+
+@pytest.mark.parametrize("T", [5, 4300])
+def test_rows_wider_than_the_gather_keeps_in_lds(T):
+    """d = 524288: the scale words of four rows pass 64 KiB, so they go straight to memory, a row for a workgroup
+    at a time (more rows than workgroups: 4300).  Codes bit for bit, and the layer of the few within its bounds."""
+    torch = _torch()
+    d = 1 << 19
+    rows = torch.randn(7, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).to(torch.bfloat16)
+    P = Packed(T, d, 128, 1, 1, seed=2, x=rows[torch.arange(T, device="cuda") % 7].contiguous())
+    print(f"[edges] d {d} T {T}", flush=True)
+    idx = torch.zeros(1, T, 1, dtype=torch.int32, device="cuda")
+    P.layout(idx)
+    P.xe.fill_(0x5A)
+    P.xe_scales.fill_(0x5A)
+    P.dispatch()
+    assert P.status() == 0
+    codes, sc, val = M4.quantize(rows.double().cpu().numpy())
+    codes = torch.from_numpy(M4.pack(codes)).cuda()
+    planes = torch.from_numpy(np.ascontiguousarray(sc.reshape(7, d // 128, 4).transpose(1, 0, 2))).cuda()
+    for t in range(0, T, 700):
+        n = min(700, T - t)
+        assert torch.equal(P.xe[t:t + n], codes.repeat(100, 1)[:n])
+        assert torch.equal(P.xe_scales[:, t:t + n], planes.repeat(1, 100, 1)[:, :n])
+    if T > 32:
+        return
+    w = torch.rand(1, T, 1, device="cuda") + 0.5
+    P.forward_choices(idx, w)
+    assert P.status() == 0
+    ref, allow = _bound(val[:T], *P.weights64(0))
+    _check_merged(P, ref, allow, w)
