@@ -15,7 +15,7 @@ namespace moe {
 
 // UNROLL = 16-byte vectors in flight per lane (16: a 16 KiB row in one round trip).
 // Measured on MI355X at the DeepSeek-V3 share: the gather (random source rows, sequential
-// destination) is fastest with 16 in flight and 4 resident blocks per CU; the push
+// destination) is fastest with 16 in flight (its launch: kDispatchBlocksPerCU below); the push
 // (sequential source, scattered destination) with 8 in flight and 8 blocks per CU.
 template <int UNROLL>
 __device__ __forceinline__ void copy_row(const u32x4* __restrict__ src, u32x4* __restrict__ dst, int n16,
@@ -39,11 +39,15 @@ __device__ __forceinline__ void copy_row(const u32x4* __restrict__ src, u32x4* _
 __global__ __launch_bounds__(256) void dispatch_pull_kernel(RankPtrs<const char*> x,
                                                             const int32_t* __restrict__ pull_src,
                                                             const int32_t* __restrict__ ctrl,
-                                                            char* __restrict__ xe, int row_bytes) {
+                                                            char* __restrict__ xe, int row_bytes, int cus) {
   const int N = ctrl[kCtrlN];
   const int lane = threadIdx.x & 63;
   const int n16 = row_bytes >> 4;
-  const int nw = gridDim.x * 4;
+  // Registers let 24 waves of a CU reside.  From 26 rows a CU, a row for a wave takes a second turn for the
+  // last few, and up to 32 rows two rows for each of 16 waves are done sooner (below).
+  const bool pairs = N > 26 * cus && N <= 32 * cus;
+  const int nw = pairs ? min(int(gridDim.x) * 4, cus * 16) : int(gridDim.x) * 4;
+  if (int(blockIdx.x) * 4 >= nw) return;
   for (int s = blockIdx.x * 4 + (threadIdx.x >> 6); s < N; s += nw) {
     const int r = pull_src[2 * int64_t(s)];
     const int t = pull_src[2 * int64_t(s) + 1];
@@ -255,7 +259,10 @@ __global__ __launch_bounds__(256) void weighted_merge_kernel(RankPtrs<const char
   }
 }
 
-// dispatch: 32700 rows of 14 KiB with the layout before it 165 us; 4 workgroups a CU 170, 8 a CU 172
+// The dispatch's launch: up to 16 workgroups a CU, but no more waves than the host's bound on the rows.
+// Rows of 14 KiB, 16 workgroups a CU (in brackets 4): 6000 rows 28.2 us (35.1), 12288 60 (64.8), 32768 188 (195);
+// 8192 rows 45.9 (43.1), hence the pairs above.  Rows of 1 KiB: 6000 rows 3.5 us (3.9), 32768 16.7 (19.8).
+// No row (R T = 1): 1.7 us, and 2.1 with every workgroup started.
 constexpr int kDispatchBlocksPerCU = 16, kGatherBlocksPerCU = 4, kPushBlocksPerCU = 8, kMergeBlocksPerCU = 16;
 
 hipError_t launch_dispatch(const moe_shape_t& s, const void* const* x, const int32_t* pull_src, char* xe,
@@ -263,8 +270,9 @@ hipError_t launch_dispatch(const moe_shape_t& s, const void* const* x, const int
   RankPtrs<const char*> xp{};
   for (int r = 0; r < s.R; ++r) xp.p[r] = static_cast<const char*>(x[r]);
   const int row_bytes = s.d * (s.dtype == MOE_F32 ? 4 : 2);
-  hipLaunchKernelGGL(dispatch_pull_kernel, dim3(cus * kDispatchBlocksPerCU), dim3(256), 0, st, xp, pull_src, ctrl, xe,
-                     row_bytes);
+  const int64_t most = (int64_t(s.R) * s.T * s.k + 3) / 4, full = int64_t(cus) * kDispatchBlocksPerCU;
+  hipLaunchKernelGGL(dispatch_pull_kernel, dim3(int(most < full ? most : full)), dim3(256), 0, st, xp, pull_src, ctrl, xe,
+                     row_bytes, cus);
   return hipGetLastError();
 }
 

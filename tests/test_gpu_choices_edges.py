@@ -116,3 +116,31 @@ def test_rows_wider_than_the_gather_keeps_in_lds(T):
     assert P.status() == 0
     ref, allow = _bound(val[:T], *P.weights64(0))
     _check_merged(P, ref, allow, w)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (1028, "f32")])
+@pytest.mark.parametrize("T,k,drop", [(1, 1, 0.0), (3, 3, 0.5), (6656, 1, 0.0), (6657, 1, 0.0), (3700, 2, 0.02), (8192, 1, 0.0),
+                                      (8193, 1, 0.0), (5000, 2, 0.2), (9000, 4, 0.05)])
+def test_dispatch_of_any_number_of_rows(T, k, drop, d, dtype):
+    """Row counts on both sides of those at which the gather's waves take one row or two, and grids bounded by the
+    pairs there can be: every row the token's own, rows behind the last untouched."""
+    torch = _torch()
+    E = 8
+    code, kind = {"f32": (moe.MOE_F32, torch.float32), "bf16": (moe.MOE_BF16, torch.bfloat16)}[dtype]
+    g = torch.Generator(device="cuda").manual_seed(T + k)
+    idx = torch.rand(1, T, E, device="cuda", generator=g).topk(k, -1).indices.int().contiguous()
+    idx[torch.rand(1, T, k, device="cuda", generator=g) < drop] = -1
+    e2l = torch.arange(E, dtype=torch.int32, device="cuda")
+    shape, pl = moe.Shape(1, T, d, E, k, 64, code), moe.Placement(e2l.data_ptr(), E)
+    n = moe.moe_max_pairs(shape, pl)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    counts, offsets = torch.empty(E, **i32), torch.empty(E + 1, **i32)
+    src, slot = torch.empty(n, 2, **i32), torch.empty(1, T, k, **i32)
+    ws = torch.empty(moe.moe_workspace_bytes(shape, pl), dtype=torch.uint8, device="cuda")
+    moe.moe_layout_choices(shape, pl, None, idx, counts, offsets, src, slot, ws)
+    x = torch.randn(T, d, device="cuda", generator=g).to(kind)
+    xe = torch.full((n + 1, d), 9.0, dtype=kind, device="cuda")
+    moe.moe_dispatch_pull(shape, pl, [x], src, offsets, xe, ws)
+    N = int(offsets[-1])
+    assert N == int((idx >= 0).sum())
+    assert torch.equal(xe[:N], x[src[:N, 1].long()]) and (xe[N:] == 9.0).all()
