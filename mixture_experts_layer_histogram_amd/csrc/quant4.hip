@@ -146,12 +146,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 8))) voi
   const int n16 = d >> 3;            // 16-byte source vectors per row (d % 128 == 0: whole 16-lane groups)
   const int nq = d >> 7;             // scale words (K-tile planes) per row
   uint32_t* xw = reinterpret_cast<uint32_t*>(xes);
-  // A row for a workgroup at a time: its waves share it, a quarter of its vectors each.  Also (most == 0)
-  // where the words of a few rows do not fit in the LDS.
-  const bool alone = most == 0 || N <= int(gridDim.x);
-  for (int row = blockIdx.x; alone && row < N; row += gridDim.x) {
-    const int2 from = reinterpret_cast<const int2*>(pull_src)[row];
-    const u32x4* src = reinterpret_cast<const u32x4*>(x.p[from.x] + int64_t(from.y) * d * 2);
+  if (N <= int(gridDim.x)) {         // a row for a workgroup: its waves share it, a quarter of its vectors each
+    const int row = blockIdx.x;
+    if (row >= N) return;
+    const u32x4* src = reinterpret_cast<const u32x4*>(x.p[pull_src[2 * row]] + int64_t(pull_src[2 * row + 1]) * d * 2);
     uint32_t* dst = reinterpret_cast<uint32_t*>(xe + int64_t(row) * (d >> 1));
     constexpr int U = 4;
     for (int base = int(threadIdx.x); base - int(threadIdx.x) < n16; base += 256 * U) {
@@ -173,8 +171,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 8))) voi
         }
       }
     }
+    return;
   }
-  if (alone) return;
   const int even = (N + int(gridDim.x) - 1) / int(gridDim.x);
   const int cr = min(most, max(4, (even + 3) & ~3));
   const int nchunks = (N + cr - 1) / cr;
@@ -268,12 +266,15 @@ hipError_t launch_dispatch_mx4(const moe_shape_t& s, const void* const* x, const
                                uint8_t* xe_scales, int64_t nmax, const int32_t* ctrl, int cus, hipStream_t st) {
   RankPtrs<const char*> xp{};
   for (int r = 0; r < s.R; ++r) xp.p[r] = static_cast<const char*>(x[r]);
-  // four rows at least; their words pass the 64 KiB that a launch may ask for from d = 524288 on
-  const size_t row_words = size_t(s.d >> 7) + 1;
-  const int cr = row_words * 4 * 4 <= 65536 ? mx_chunk_rows(s.d) : 0;
-  const size_t lds = cr * row_words * 4;
+  // From d = 524288 on the words of the four rows that a workgroup takes at least pass the 64 KiB of LDS a
+  // launch may ask for: then as many workgroups as rows there can be, which each take one row without LDS.
+  const int64_t row_words = (s.d >> 7) + 1;
+  const bool wide = 4 * row_words * 4 > 65536;
+  const int cr = wide ? 4 : mx_chunk_rows(s.d);
+  const size_t lds = wide ? 0 : cr * row_words * 4;
   const int n16 = s.d >> 3;
-  const dim3 grid(cus * 16);       // 32700 rows of 7168: 111 us; 8 workgroups a CU 114, 4 a CU 125
+  // 32700 rows of 7168: 111 us; 8 workgroups a CU 114, 4 a CU 125
+  const dim3 grid(wide ? int(nmax) : cus * 16);
   // two short rows at a time: 24.0 us against 26.6 for 23300 rows of 2048
   if (n16 <= 64 * 4)
     hipLaunchKernelGGL((dispatch_pull_mx4_kernel<4, 2>), grid, dim3(256), lds, st, xp, pull_src, ctrl, xe, xe_scales, s.d, nmax, cr);
