@@ -150,7 +150,8 @@ int moe_mx_quantize(const void* src, int32_t src_dtype, int64_t rows, int32_t K,
 
 /*
  * moe_mx_quantize_to -- moe_mx_quantize for either block-scaled format (MOE_MXFP8 or
- * MOE_MXFP4).  With MOE_MXFP8 it is moe_mx_quantize.  MOE_MXFP4 (OCP Microscaling v1.0):
+ * MOE_MXFP4).  With MOE_MXFP8 its codes and scales are moe_mx_quantize's, whose rule is for finite
+ * values (a block with a NaN or an infinity is outside the contract there).  MOE_MXFP4 (OCP Microscaling v1.0):
  * for every block of 32 consecutive values v of a row, amax = max |v|;
  *   amax == 0: scale code 0 and 32 zero codes;
  *   a NaN or an infinity among them: scale code 255 (E8M0's NaN) and 32 zero codes, which

@@ -241,14 +241,14 @@ int moe_mx_quantize(const void* src, int32_t src_dtype, int64_t rows, int32_t K,
 
 int moe_mx_quantize_to(const void* src, int32_t src_dtype, int64_t rows, int32_t K, int32_t format, uint8_t* codes,
                        uint8_t* scales, void* stream) {
-  if (format == MOE_MXFP8) return moe_mx_quantize(src, src_dtype, rows, K, codes, scales, stream);
-  if (format != MOE_MXFP4) return MOE_EINVAL;
+  if (format != MOE_MXFP8 && format != MOE_MXFP4) return MOE_EINVAL;
   if (src_dtype != MOE_BF16 && src_dtype != MOE_F32) return MOE_EINVAL;
   if (rows < 0 || K < 1 || rows > (int64_t(1) << 40) / K) return MOE_EINVAL;
   if (K % 128) return MOE_EALIGN;                // whole 32-bit scale words per row
   if (!src || !codes) return MOE_EINVAL;
   if (!aligned16(src) || !aligned16(codes)) return MOE_EALIGN;
-  if (const int rc = check_scales(scales)) return rc;
+  if (const int rc = check_scales(scales)) return rc;       // moe_mx_quantize writes bytes and takes any address
+  if (format == MOE_MXFP8) return moe_mx_quantize(src, src_dtype, rows, K, codes, scales, stream);
   return hip_rc(launch_mx4_quantize(src, src_dtype, rows, K, codes, scales, static_cast<hipStream_t>(stream)));
 }
 

@@ -198,3 +198,11 @@ def test_merge_backward_has_no_mxfp4_form():
     """moe_forward_choices in MXFP4 writes ye or not by its size, so the gradient that reads ye refuses the dtype."""
     args = [_tab(), FAKE + (1 << 40), FAKE, FAKE, FAKE + (2 << 40), FAKE, None]
     assert _call("moe_combine_merge_backward", _shape(dtype=moe.MOE_MXFP4), args) == -6
+
+
+@pytest.mark.parametrize("fmt", [moe.MOE_MXFP8, moe.MOE_MXFP4])
+@pytest.mark.parametrize("by", [1, 2, 3])
+def test_quantize_to_asks_for_aligned_scales_in_both_formats(fmt, by):
+    q = moe.lib().moe_mx_quantize_to
+    assert q(FAKE, moe.MOE_BF16, 4, 128, fmt, FAKE, FAKE + by, None) == -2
+    assert q(FAKE, moe.MOE_F32, 0, 128, fmt, FAKE, FAKE + by, None) == -2
