@@ -160,7 +160,8 @@ int moe_mx_quantize(const void* src, int32_t src_dtype, int64_t rows, int32_t K,
  *   code_i = E2M1(v_i / 2^e) rounded to nearest (ties to the even code), saturated to +-6.
  * codes: [rows][K / 2] bytes, 16-byte aligned, value 2i of a row in the low half of byte i
  * and value 2i + 1 in the high half; scales: as moe_mx_quantize, 4-byte aligned.
- * K % 128 == 0 (else MOE_EALIGN).  Bit-exact.  rows == 0 launches nothing.
+ * K % 128 == 0 (else MOE_EALIGN).  Bit-exact.  rows == 0 launches nothing, and
+ * its pointers may be NULL.
  */
 int moe_mx_quantize_to(const void* src, int32_t src_dtype, int64_t rows, int32_t K, int32_t format, uint8_t* codes,
                        uint8_t* scales, void* stream);
@@ -170,7 +171,7 @@ int moe_mx_quantize_to(const void* src, int32_t src_dtype, int64_t rows, int32_t
  *   dst[r][i] = element(code) * 2^(scale code - 127), NaN where the scale code is 255 (or an
  *   E4M3 code is NaN).
  * dst: [rows][K] of dst_dtype (MOE_BF16 or MOE_F32), 16-byte aligned; codes 16-byte, scales
- * 4-byte aligned.  K % 128 == 0 (else MOE_EALIGN).  Exact wherever the value fits the type;
+ * 4-byte aligned.  K % 128 == 0 (else MOE_EALIGN).  rows == 0 as above.  Exact wherever the value fits the type;
  * a larger one becomes an infinity (as the largest scale codes can make it), and below
  * the bf16 subnormals an E4M3 value is rounded to nearest even.
  */

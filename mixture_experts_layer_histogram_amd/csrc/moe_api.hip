@@ -145,6 +145,13 @@ int check_scales(const void* q) {
   return (reinterpret_cast<uintptr_t>(q) & 3) ? MOE_EALIGN : MOE_OK;
 }
 
+// values, codes and scales of the codec; no rows need no addresses
+int check_codec(const void* values, const void* codes, const void* scales, int64_t rows) {
+  if (rows > 0 && (!values || !codes || !scales)) return MOE_EINVAL;
+  const uintptr_t rows16 = reinterpret_cast<uintptr_t>(values) | reinterpret_cast<uintptr_t>(codes);
+  return ((rows16 & 15) || (reinterpret_cast<uintptr_t>(scales) & 3)) ? MOE_EALIGN : MOE_OK;
+}
+
 int check_w_scales(const moe_mx_scales_t* w) {
   if (!w) return MOE_EINVAL;
   int rc;
@@ -245,9 +252,8 @@ int moe_mx_quantize_to(const void* src, int32_t src_dtype, int64_t rows, int32_t
   if (src_dtype != MOE_BF16 && src_dtype != MOE_F32) return MOE_EINVAL;
   if (rows < 0 || K < 1 || rows > (int64_t(1) << 40) / K) return MOE_EINVAL;
   if (K % 128) return MOE_EALIGN;                // whole 32-bit scale words per row
-  if (!src || !codes) return MOE_EINVAL;
-  if (!aligned16(src) || !aligned16(codes)) return MOE_EALIGN;
-  if (const int rc = check_scales(scales)) return rc;       // moe_mx_quantize writes bytes and takes any address
+  if (const int rc = check_codec(src, codes, scales, rows)) return rc;   // moe_mx_quantize takes scales anywhere
+  if (rows == 0) return MOE_OK;
   if (format == MOE_MXFP8) return moe_mx_quantize(src, src_dtype, rows, K, codes, scales, stream);
   return hip_rc(launch_mx4_quantize(src, src_dtype, rows, K, codes, scales, static_cast<hipStream_t>(stream)));
 }
@@ -258,9 +264,8 @@ int moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t forma
   if (dst_dtype != MOE_BF16 && dst_dtype != MOE_F32) return MOE_EINVAL;
   if (rows < 0 || K < 1 || rows > (int64_t(1) << 40) / K) return MOE_EINVAL;
   if (K % 128) return MOE_EALIGN;
-  if (!codes || !dst) return MOE_EINVAL;
-  if (!aligned16(codes) || !aligned16(dst)) return MOE_EALIGN;
-  if (const int rc = check_scales(scales)) return rc;
+  if (const int rc = check_codec(dst, codes, scales, rows)) return rc;
+  if (rows == 0) return MOE_OK;
   return hip_rc(launch_mx_dequantize(codes, scales, format, rows, K, dst, dst_dtype,
                                      static_cast<hipStream_t>(stream)));
 }

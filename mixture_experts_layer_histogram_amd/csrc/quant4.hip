@@ -235,7 +235,6 @@ static int quant_grid(int64_t rows, int K) {
 
 hipError_t launch_mx4_quantize(const void* src, int src_dtype, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
                                hipStream_t st) {
-  if (rows == 0) return hipSuccess;
   const dim3 grid(quant_grid(rows, K));
   if (src_dtype == MOE_BF16)
     hipLaunchKernelGGL(mx4_quantize_kernel<true>, grid, dim3(256), 0, st, src, rows, K, codes, scales);
@@ -246,7 +245,6 @@ hipError_t launch_mx4_quantize(const void* src, int src_dtype, int64_t rows, int
 
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int format, int64_t rows, int K, void* dst,
                                 int dst_dtype, hipStream_t st) {
-  if (rows == 0) return hipSuccess;
   const dim3 grid(quant_grid(rows, K));
   if (format == MOE_MXFP4) {
     if (dst_dtype == MOE_BF16)

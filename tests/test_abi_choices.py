@@ -206,3 +206,15 @@ def test_quantize_to_asks_for_aligned_scales_in_both_formats(fmt, by):
     q = moe.lib().moe_mx_quantize_to
     assert q(FAKE, moe.MOE_BF16, 4, 128, fmt, FAKE, FAKE + by, None) == -2
     assert q(FAKE, moe.MOE_F32, 0, 128, fmt, FAKE, FAKE + by, None) == -2
+
+
+@pytest.mark.parametrize("fmt", [moe.MOE_MXFP8, moe.MOE_MXFP4])
+def test_codec_of_no_rows_takes_null_pointers(fmt):
+    """An empty tensor has no address: no rows are done whatever the pointers, once the sizes and types are right."""
+    L = moe.lib()
+    for ptr in (None, FAKE, FAKE + 1):
+        assert L.moe_mx_quantize_to(ptr, moe.MOE_BF16, 0, 128, fmt, ptr, ptr, None) == (-2 if ptr == FAKE + 1 else 0)
+        assert L.moe_mx_dequantize(ptr, ptr, fmt, 0, 128, ptr, moe.MOE_F32, None) == (-2 if ptr == FAKE + 1 else 0)
+    assert L.moe_mx_quantize_to(None, moe.MOE_BF16, 0, 64, fmt, None, None, None) == -2
+    assert L.moe_mx_quantize_to(None, moe.MOE_BF16, 1, 128, fmt, None, None, None) == -1
+    assert L.moe_mx_dequantize(None, None, fmt, 0, 128, None, fmt, None) == -1
