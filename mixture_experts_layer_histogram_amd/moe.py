@@ -165,6 +165,8 @@ def _table(ts):
     reference cycle to collect)."""
     if ts is None:
         return None
+    if not isinstance(ts, (list, tuple)):
+        ts = list(ts)                 # any iterable of tensors or addresses
     n = len(ts)
     kind = _TABLES.get(n)
     if kind is None:
