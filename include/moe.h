@@ -725,6 +725,9 @@ int moe_backward_prepare_mx(const moe_shape_t* s, const moe_placement_t* p, cons
  * decisions on fp32 / bf16 intermediates flip against fp64); weight gradients per row
  * within the bf16 row-relative 2e-2; dlogits as moe_backward.  As in moe_backward, the dX
  * GEMM stores each row straight to recv[r][t][j] (recv is written, then summed into dx).
+ * After moe_forward_choices, with its choices and gate weights for topk_idx and topk_w, dx and the weight
+ * gradients are those under any router (-1 is no pair); dlogits is the softmax rule's and is of no
+ * use then, and the gates' gradient is moe_combine_merge_backward's dtopk_w.
  */
 int moe_backward_mx(const moe_shape_t* s, const moe_placement_t* p, const void* const* dy, const void* const* x,
                     const uint8_t* xe, const uint8_t* xe_scales, const void* ye, const uint8_t* w1q, const uint8_t* w3q,

@@ -3,9 +3,11 @@ import numpy as np
 import pytest
 
 from oracle import mx4_oracle as M4
-from mixture_experts_layer_histogram_amd import moe
+from oracle import mx_oracle_bwd as QB
+from mixture_experts_layer_histogram_amd import configs, inputs, moe
 from tests.mx4_packed import Packed
 from tests.test_gpu_mx4 import _bound, _cfg, _check_merged, _check_rows, _problem, _push, _torch, _weights64
+from tests.test_gpu_mx_bwd import DL_TOL, DX_FRO, DX_ROW, W_TOL
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +146,55 @@ def test_dispatch_of_any_number_of_rows(T, k, drop, d, dtype):
     N = int(offsets[-1])
     assert N == int((idx >= 0).sum())
     assert torch.equal(xe[:N], x[src[:N, 1].long()]) and (xe[N:] == 9.0).all()
+
+
+def test_mxfp8_training_step_under_a_sigmoid_router(monkeypatch):
+    """moe_backward_mx after moe_forward_choices: dx and the weight gradients for gates sigmoid(logits) of the k best by
+    a biased score, some pairs dropped, against the MXFP8 backward oracle on the same choices (bars as for
+    moe_backward_mx under the softmax router); the gates' gradient from moe_combine_merge_backward."""
+    torch = _torch()
+    from mixture_experts_layer_histogram_amd.device import DeviceProblem
+    cfg = configs.MoEConfig("mxfp8 choices R2 T200 d256 F256 E16/8 k4", R=2, T=200, d=256, F=256, E=16, E_local=8, k=4,
+                            dtype="mxfp8")
+    inp = inputs.make_inputs(cfg, seed=5)
+    bits, dy = inputs.make_dy(cfg, seed=5)
+    P = DeviceProblem(cfg, inp)
+    P.alloc_backward(bits)
+    logits = torch.stack(P.logits).double()
+    bias = 0.05 * torch.cos(torch.arange(cfg.E, device="cuda").double())
+    idx = torch.topk(torch.sigmoid(logits) + bias, cfg.k, dim=-1).indices
+    w = torch.sigmoid(logits).gather(-1, idx).float().contiguous()
+    idx = idx.int().contiguous()
+    idx[:, ::7, 2] = -1
+    idx[1, -20:] = -1                                     # a padded tail
+    P.forward_choices(idx, w)
+    dye, dw = torch.empty_like(P.ye), torch.empty_like(w)
+    moe.moe_combine_merge_backward(P.shape, P.placement, P.dy, P.ye, P.slot_of, w, dye, dw)
+    P.prepare_backward_mx()
+    P.topk_idx, P.topk_w = idx, w
+    P.backward_mx()
+    assert P.status() == 0
+    ids, gates = idx.cpu().numpy(), w.double().cpu().numpy()
+    lay = M4.layout(ids, inp.expert_to_local, cfg.E_local)
+    monkeypatch.setattr(QB.O, "route", lambda *_: (ids, gates))
+    monkeypatch.setattr(QB.O, "layout", lambda *_: lay)
+    ref = QB.backward_q(inp.logits, inp.x_f32, inp.w1_f32, inp.w3_f32, inp.w2_f32, inp.expert_to_local, cfg.E_local, cfg.k,
+                        dy)
+    n = lambda t: t.double().cpu().numpy()                # noqa: E731
+    slot = lay["slot_of"]
+    assert np.array_equal(P.slot_of.cpu().numpy(), slot)
+    has = (slot >= 0).any(-1)
+    got = np.stack([n(t) for t in P.dx])
+    assert has.sum() > 300 and (got[~has] == 0).all() and not has[1, -20:].any()
+    row = np.abs(got - ref["dx"])[has].max(-1) / np.abs(ref["dx"][has]).max(-1)
+    fro = np.linalg.norm((got - ref["dx"])[has]) / np.linalg.norm(ref["dx"][has])
+    print(f"[edges] mxfp8 choices: dx row {row.max():.2e}, Frobenius {fro:.2e}", flush=True)
+    assert row.max() <= DX_ROW and fro <= DX_FRO
+    for key in ("dw1", "dw3", "dw2"):
+        for l in range(cfg.E_local):
+            top = np.abs(ref[key][l]).max(-1)
+            assert (np.abs(n(getattr(P, key)[l]) - ref[key][l]).max(-1) <= W_TOL * top + 1e-30).all(), (key, l)
+    at = np.maximum(slot, 0)
+    want = np.where(slot >= 0, (dy[:, :, None] * ref["ye"][at]).sum(-1), 0.0)
+    size = np.linalg.norm(dy, axis=-1)[:, :, None] * np.linalg.norm(ref["ye"][at], axis=-1)
+    assert (np.abs(n(dw) - want) <= DL_TOL * size + 1e-30).all() and (n(dw)[slot < 0] == 0).all()
