@@ -370,7 +370,7 @@ int moe_layout_choices(const moe_shape_t* s, const moe_placement_t* p, const moe
  *                topk_w[r][t][j] * ye[slot_of[r][t][j]][:]
  * fp32 accumulation, rounded once to the row type; exactly 0 for a token with no local pair.
  * Deterministic; equal to moe_combine_push's y bit for bit.  ye: rows [0, N) of d elements (rows
- * from N on, and the weights of pairs that are not local, are not read); topk_w: [R][T][k] fp32;
+ * from N on are not read, and the weights of pairs that are not local have no effect); topk_w: [R][T][k] fp32;
  * y: R pointers [T][d], which may not overlap ye (MOE_EINVAL where a y is ye itself).  ye and y
  * 16-byte aligned.
  */
@@ -407,7 +407,7 @@ int moe_dispatch_pull_backward(const moe_shape_t* s, const moe_placement_t* p, c
  * the choices and their weights as inputs and without logits and recv; every stage's arguments
  * are checked before the first launch.  xe, ye and pull_src need [moe_max_pairs] rows, of which
  * [0, N) are touched (the scales in xe_scales keep moe_max_pairs rows a plane); a caller who
- * knows N may pass N rows of ye and pull_src.  With MOE_MXFP4, moe_max_pairs * d * 4 <= 16 MiB
+ * knows N may pass N rows (one at least) of ye and pull_src.  With MOE_MXFP4, moe_max_pairs * d * 4 <= 16 MiB
  * and ws_bytes of at least this shape's moe_workspace_bytes, the expert rows stay in fp32 in ws
  * instead (ye is left as it is, so nothing may read it afterwards), and y is rounded once; otherwise,
  * also with a smaller workspace that was made for more tokens, they are bf16 rows in ye, and y

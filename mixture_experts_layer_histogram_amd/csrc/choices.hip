@@ -250,7 +250,9 @@ hipError_t launch_merge_rows_bwd(const moe_shape_t& s, const void* const* dy, co
   const int64_t RT = int64_t(s.R) * s.T;
   // A wave per token once that gives every SIMD two, with the whole row in registers up to 14 KiB (32768
   // tokens of 7168 bf16: 187 us; segments of 4 KiB 216, of 7 KiB 194); below that a workgroup
-  // per token (258 tokens of 1408 fp32: 6.5 us against 8.2).
+  // per token (258 tokens of 1408 fp32: 6.5 us against 8.2).  Other widths, 16384 tokens with 16400 rows,
+  // whole rows and segments of 4 KiB: rows of 14 KiB 116 and 130 us, 10 KiB 82 and 92, 8 KiB 66 and 75, 7 KiB 63.6
+  // and 63.4, 5.5 KiB 52.5 and 51.2, 4.5 KiB 50 and 48, 4.1 KiB 48 and 42; 16 KiB 148 and 162.
   const bool few = RT < int64_t(cus) * 8;
   const bool wide = int64_t(s.d) * (s.dtype == MOE_F32 ? 4 : 2) > 4096;
   const dim3 grid(grid_of(few ? RT : (RT + 3) / 4));

@@ -17,11 +17,14 @@
 // registers (half exchanges instead of a tile in LDS), and the next tile's first two stages fill
 // while they run; the waits for those fills leave the epilogue's stores in flight.
 //
-// Bound by power: MFMAs of this shape alone, on random operands, sustain 6.6 PFLOP/s of 9.8, and what the
-// fills, the LDS reads and the stores use comes on top (the clock stands at 1.9 GHz).  32 experts of
-// 2048 x 7168, 32768 rows: GEMM1 534 us (3.6 PFLOP/s; its MFMAs alone 370), GEMM2 369 us (2.6 PFLOP/s; its
-// MFMAs alone 193, its rows' stores 470 MB).  A tile staged in LDS by the epilogue took 1224 us for the
-// layer where this one takes 1101; 16x16x128 MFMAs, operands laid out by block, and token rows read
+// Bound by both its schedule and power.  32 experts of 2048 x 7168, 32768 rows: GEMM1 504 to 539 us by the card
+// and the clock (3.6 to 3.8 PFLOP/s), GEMM2 348 to 369 us (2.6 to 2.8 PFLOP/s; its rows' stores are 470 MB).
+// On all-zero codes, with the same fills, reads and stores, they take 440 and 315 us: 13 and 9 % are power
+// (the clock is 2.4 GHz there and 1.8 on random codes).  The rest is the schedule: the MFMA pipes are
+// busy in 49 % and 35 % of the cycles on random codes (42 and 31 % on zeros), although GEMM1's MFMAs with the
+// LDS reads and the epilogue but without fills take four fifths of its time.  MFMAs of this shape alone
+// sustain 6.6 PFLOP/s on random operands and 9.8 on zeros.  A tile staged in LDS by the epilogue took 1224 us for the
+// layer where this one takes 1092; 16x16x128 MFMAs, operands laid out by block, and token rows read
 // straight into registers were no faster.
 #include "gemm_tile.hpp"
 #include "mx4.hpp"
@@ -493,8 +496,12 @@ hipError_t launch_ffn_mx4(const moe_shape_t& s, int El, const uint8_t* xe, const
   // token names it once) and, under an even load, R T k / E.  So with at most kThinRows tokens the
   // streaming kernel does it all; with kThinMean rows expected of an expert or more the tile kernel
   // does; in between both run, each on its experts.  The layer on 32 of 256 experts of 2048 x 7168
-  // with both and with the tile kernel alone: 4 rows an expert 129 us and 177, 16 rows 149 and 187,
-  // 24 rows 199 and 196, 30 rows (of which many have more than 32) 251 and 200.
+  // with both and with the tile kernel alone: 4 rows an expert 130 us and 168, 16 rows 149 and 179,
+  // 24 rows 193 and 187, 30 rows (of which many have more than 32) 251 and 200.  64 experts of 1408 x 2048: 4 rows
+  // 70 and 78, 16 rows 80 and 86, 20 rows 83 and 86, 24 rows 105 and 89.  The rule sees no loads: where a
+  // few experts have most of the rows (Zipf's popularity), both in turn cost more than the tile kernel on all
+  // (64 experts of 1408 x 2048, 4 and 20 rows on average: 78 and 60, 120 and 94 us; 32 of 256 of 2048 x 7168 with
+  // 10 and 16 rows: 133 and 119, but 151 and 169).
   const int64_t tokens = int64_t(s.R) * s.T;
   const bool thin = tokens <= kThinRows || tokens * s.k <= int64_t(kThinMean) * s.E;
   const bool wide = tokens > kThinRows;

@@ -27,7 +27,9 @@ constexpr int kThinRows = 32;             // experts with at most this many rows
 constexpr int kThinMean = 20;             // and do where this many are expected of one at most
 
 // silu with the reciprocal instruction (1 ulp) in place of the division sequence: six instructions a
-// value instead of some twenty, and the epilogue of a GEMM1 tile is 64 of them a lane
+// value instead of some twenty, and the epilogue of a GEMM1 tile is 64 of them a lane.  The value is rounded
+// to four bits next.  Below a = -87.3, where the quotient of silu_f32 is under 1.2e-36, it may be 0: the
+// instruction does not make subnormals.
 __device__ __forceinline__ float mx4_silu(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
 
 // E8M0 code -> fp32 (code 0 is 2^-127, a subnormal; code 255 is NaN)

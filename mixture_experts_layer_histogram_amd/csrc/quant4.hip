@@ -7,8 +7,11 @@
 // time (16 bytes of bf16 per lane, an aligned lane quad holds one 32-value block), a workgroup
 // 32 rows x 512 values, so that its scale words -- four K-tile planes of 32 rows -- leave as
 // four runs of 128 bytes instead of single words (each a partial write of its own line).
-// Measured on 229376 rows of 2048 bf16 values: quantise 187 us, dequantise 194 us (1.19 GB: 6.3 and
-// 6.1 TB/s; a device copy of 2 GiB reaches 4.9); the gather of 32768 rows of 7168, 111 us (5.3 TB/s).
+// Measured on 229376 rows of 2048 bf16 values: quantise 185 to 188 us, dequantise 177 to 194 us by the card
+// (1.19 GB: 6.3 and 6.1 to 6.7 TB/s; a device copy of 2 GiB reaches 4.8 to 4.9); the gather of 32768 rows of
+// 7168, 111 us (5.3 TB/s).  2^28 values: from bf16 106 to 121 us at K = 256 to 7168, from fp32 221 to 242 us
+// (5.0 to 5.5 TB/s); to bf16 113 to 128, to fp32 298 to 316 (4.0 TB/s).  K = 128 uses 16 of a wave's 64
+// lanes: 214 us from bf16, 199 back.
 #include "mx4.hpp"
 
 namespace moe {
