@@ -274,13 +274,19 @@ def _blocks(v):
     return b, b.abs().amax(-1, keepdim=True)
 
 
+def _power(e):
+    """2^e in fp32 for whole e in [-127, 127], by its bits (torch.ldexp is a unit off for some exponents on the GPU, and what is
+    next to a border then falls on its other side)."""
+    return torch.where(e > -127, (e + 127) << 23, 1 << 22).int().view(torch.float32)
+
+
 def _nearest8(v):
     """MXFP8 of fp32 rows: E4M3 codes and E8M0 scale codes of blocks of 32, scale 2^(floor(log2 max) - 8), nearest even, at
     most 448."""
     b, top = _blocks(v)
     e = torch.where(top > 0, (torch.frexp(top).exponent - 9).clamp(-127, 127), torch.full_like(top, -127, dtype=torch.int32))
-    y = torch.ldexp(b, -e)
-    step = torch.ldexp(torch.ones_like(y), torch.frexp(y).exponent.clamp(min=-5) - 4)       # E4M3's step at |y|
+    y = b * _power(-e)
+    step = _power(torch.frexp(y).exponent.clamp(min=-5) - 4)       # E4M3's step at |y|
     q = (torch.round(y / step) * step).clamp(-448, 448)
     return q.to(torch.float8_e4m3fn).reshape(v.shape).view(torch.uint8), (e + 127).to(torch.uint8)[..., 0]
 
@@ -288,17 +294,17 @@ def _nearest8(v):
 def _values8(codes, scales):
     """fp32 values of codes [..., K] and of one scale code for 32 of them."""
     v = codes.view(torch.float8_e4m3fn).float()
-    return torch.ldexp(v.reshape(*v.shape[:-1], -1, 32), scales[..., None].int() - 127).reshape(v.shape)
+    return (v.reshape(*v.shape[:-1], -1, 32) * _power(scales[..., None].int() - 127)).reshape(v.shape)
 
 
 def _rounded8(v, r16, root):
     """MXFP8 of an optimiser's state, rounded up with the probability of what is cut off (r16: 16 random bits a value): the
     smallest scale that keeps the block's largest magnitude within 448; a positive root takes the smallest code at least."""
     b, top = _blocks(v)
-    e = torch.frexp(top).exponent - 9
-    e = e + (top > torch.ldexp(torch.full_like(top, 448.0), e)).int()
-    e = torch.where(top > 0, e.clamp(-127, 127), torch.full_like(e, -127))
-    y = torch.ldexp(b, -e).abs().reshape(-1)
+    e = (torch.frexp(top).exponent - 9).clamp(-127, 126)
+    e = e + (top > 448.0 * _power(e)).int()
+    e = torch.where(top > 0, e, torch.full_like(e, -127))
+    y = (b * _power(-e)).abs().reshape(-1)
     part = (r16 << 4).reshape(-1)
     normal = ((y.view(torch.int32) + part) >> 20) - (120 << 3)
     small = ((y * 2.0 ** 29).int() + part) >> 20
