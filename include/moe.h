@@ -738,6 +738,152 @@ int moe_backward_mx(const moe_shape_t* s, const moe_placement_t* p, const void* 
                     void* bws, size_t bws_bytes, void* stream);
 
 /*
+ * Before, beside and behind the layer: the norm ahead of it, the dispatch of rows that the norm has quantised already,
+ * products grouped by expert for experts of any form, and the optimiser's step.  They follow the conventions above, with
+ * these additions: a size of zero (rows, tensors) is valid and needs no pointers for what it leaves out; products and steps
+ * never read what lies past a group's or a tensor's end.
+ */
+
+/*
+ * moe_norm -- RMS norm of token rows, with the residual's addition ahead of it:
+ *   s = x + residual (x alone where residual is NULL), in fp32;
+ *   rstd = (sum over i of s[i]^2 / d + eps)^-1/2;   n[i] = s[i] * rstd * gamma[i] (gamma NULL: ones);
+ *   h = s, rounded once to the row type (NULL: not written);
+ *   y = n, rounded once to the row type (NULL: not written);
+ *   codes, scales = n in MXFP8 by the moe_mx_quantize rule, rounded once from fp32 ([rows][d] codes, scales in the MXFP8
+ *     scale layout of `rows` rows; both NULL: not written), where a block of 32 with a NaN or an infinity gets scale code
+ *     255 (E8M0's NaN) and zero codes.  d % 128 == 0 then (else MOE_EALIGN).
+ * x, residual, h, y: dense rows of d values of `dtype` (MOE_F32 or MOE_BF16), 16-byte aligned; gamma: [d] fp32, 4-byte
+ * aligned; codes 16-byte, scales 4-byte aligned.  h or y may be x or residual themselves (a row is read before it is
+ * written), but not each other (MOE_EINVAL), and the buffers may not overlap otherwise.  The sum of squares is held in fp32:
+ * rows with values from about 1e18 on pass its range.  1 <= d <= 32768, rows >= 0, rows * d < 2^40, eps >= 0 and finite
+ * (else MOE_EINVAL), one output at least (else MOE_EINVAL).  Deterministic.
+ */
+typedef struct {
+  int64_t rows;
+  int32_t d;
+  int32_t dtype; /* MOE_F32 or MOE_BF16 (else MOE_EUNSUP) */
+  float eps;
+} moe_norm_t;
+int moe_norm(const moe_norm_t* n, const void* x, const void* residual, const float* gamma, void* h, void* y,
+             uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * moe_norm_backward -- its gradients at the rows h (moe_norm's h, or its x where there was no residual), for the gradient dy
+ * of y (of n, where n went to MXFP8) and dh of h (NULL: none).  With u = gamma * dy and rstd of h:
+ *   dx = dh + rstd * (u - h * rstd^2 * <u, h> / d), rounded once (the residual's gradient is the same; NULL: not written);
+ *   dgamma[i] = sum over rows of dy[i] * h[i] * rstd, [d] fp32 (NULL: not written; zeros for no rows).
+ * dx may be dy, h or dh themselves.  ws: at least moe_norm_backward_workspace_bytes() bytes, 256-byte aligned, for dgamma
+ * (may be NULL where dgamma is).  Limits as moe_norm.  Deterministic (the sums' order goes by the sizes alone).
+ */
+size_t moe_norm_backward_workspace_bytes(const moe_norm_t* n);
+int moe_norm_backward(const moe_norm_t* n, const void* dy, const void* h, const float* gamma, const void* dh, void* dx,
+                      float* dgamma, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_dispatch_pull_codes -- moe_dispatch_pull for token rows that are in MXFP8 or MXFP4 already (codes and scales of
+ * moe_norm or moe_mx_quantize_to):
+ *   xe[s] = xq[r][t] and its scale words, for (r, t) = pull_src[s], s in [0, N).
+ * s->dtype: MOE_MXFP8 or MOE_MXFP4 (else MOE_EUNSUP).  xq: R device pointers, [T][d] codes ([T][d / 2] in MXFP4), 16-byte
+ * aligned; xq_scales: R device pointers, each in the MXFP8 scale layout of T rows ([d/128][T][4]), 4-byte aligned.  xe and
+ * xe_scales as moe_dispatch_pull writes them, for moe_expert_ffn and moe_expert_ffn_push; rows from N on are left as they
+ * are.  An xe may not be one of xq (MOE_EINVAL).  Bit-exact: for codes made by moe_mx_quantize_to of bf16 rows the result is
+ * moe_dispatch_pull's of those rows.  Other arguments and errors as moe_dispatch_pull.
+ */
+int moe_dispatch_pull_codes(const moe_shape_t* s, const moe_placement_t* p, const uint8_t* const* xq,
+                            const uint8_t* const* xq_scales, const int32_t* pull_src, const int32_t* offsets, uint8_t* xe,
+                            uint8_t* xe_scales, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Products grouped by expert, for experts of any form (the SwiGLU experts are moe_expert_ffn's).  Rows of one group are
+ * consecutive: group g has rows [offsets[g], offsets[g + 1]) of x and y, offsets an ascending DEVICE array of groups + 1
+ * int32 within [0, rows] (moe_layout's, for instance, whose first is 0; a first one above 0 is as good).  Offsets that
+ * descend or leave that range are found on the device: the call then computes nothing and sets *status to MOE_EINVAL.
+ */
+typedef struct {
+  int64_t rows;      /* rows that x and y have, at least offsets[groups]; < 2^31 */
+  int32_t groups;    /* 1 .. 1024 */
+  int32_t K, N;      /* values of an x row and of a y row */
+  int32_t dtype;     /* MOE_BF16 or MOE_F32 (else MOE_EUNSUP), of x, w and y */
+  int32_t w_layout;  /* 0: w[g] is [N][K], y = x w^T;  1: w[g] is [K][N], y = x w */
+  int64_t ldx, ldy;  /* row strides of x and y in values, at least K and N; 0 for dense rows */
+} moe_gemm_t;
+
+/*
+ * moe_grouped_gemm -- y[s][n] = sum over k of x[s][k] * w_g[n][k] (layout 0; w_g[k][n] in layout 1) for the rows s of every
+ * group g: fp32 accumulation, rounded once to the row type.  Rows of no group are left as they are.  The gradient by the
+ * rows is the same call on dy with K and N exchanged and the other layout: dx = dy w.
+ * w: [groups][N][K] or [groups][K][N], dense.  K, N, ldx and ldy are multiples of 16 bytes and so are the addresses (else
+ * MOE_EALIGN); K * N < 2^31, ldx and ldy <= 2^22.  y may be neither x nor w (MOE_EINVAL) and overlap neither.
+ * status: NULL, or a 4-byte-aligned DEVICE int32 that receives 0 or MOE_EINVAL (bad offsets).  No workspace.
+ * `rows` (not the rows that the groups have, which the host does not know) chooses between a kernel for few rows a group
+ * and one for many; either is right for any number.  Deterministic; a row's result depends on its own values and
+ * on `rows` and the sizes only.
+ */
+int moe_grouped_gemm(const moe_gemm_t* g, const void* x, const void* w, const int32_t* offsets, void* y,
+                     int32_t* status, void* stream);
+
+/*
+ * moe_grouped_gemm_wgrad -- the gradient by the weights, in w's own layout:
+ *   dw_g[n][k] (layout 1: dw_g[k][n]) = sum over the rows s of group g of dy[s][n] * x[s][k],
+ * fp32 accumulation, rounded once to dw_dtype: the row type, or MOE_F32.  A group with no rows gets zeros.
+ * accumulate != 0: added to what dw holds (MOE_F32 only, else MOE_EINVAL): gradients of several batches.
+ * dy: rows of N values with stride ldy.  ws: at least moe_grouped_gemm_wgrad_workspace_bytes() bytes, 256-byte aligned
+ * (NULL where that is 0).  Other arguments, limits and errors as moe_grouped_gemm; with bad offsets dw stays as it is.
+ */
+size_t moe_grouped_gemm_wgrad_workspace_bytes(const moe_gemm_t* g);
+int moe_grouped_gemm_wgrad(const moe_gemm_t* g, const void* x, const void* dy, const int32_t* offsets, void* dw,
+                           int32_t dw_dtype, int32_t accumulate, void* ws, size_t ws_bytes, int32_t* status,
+                           void* stream);
+
+/*
+ * moe_adamw -- one AdamW step over `count` tensors.  For every value, in fp32:
+ *   g = grad * *grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2;
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps).
+ * p is the master where there is one (the param then receives it rounded), else the param.
+ * state_dtype MOE_F32: m and v are fp32 [n].  MOE_MXFP8: m and v hold E4M3 codes of m and of sqrt(v), n rounded up to a
+ * multiple of 128 of them, with a scale byte for each 32 of them (m_scales, v_scales: that many / 32): MXFP8 matrices of
+ * rows of 128 values, which moe_mx_dequantize reads.  The scale is the smallest power of two that keeps the block's largest
+ * magnitude within 448; a positive root takes the smallest code at least; a block with a NaN or an infinity gets scale
+ * code 255, which stays a NaN in later steps.  p is computed before m and v are rounded.  Zeroed codes and scales are
+ * states of zero.
+ * stochastic != 0: states in 8 bits, and a bf16 param without a master, are rounded up with the probability of what is cut
+ * off (16 random bits each, a mixing of seed, step, the tensor's place in the list and the value's in the tensor); 0: to
+ * nearest even, which loses small changes.  The root is rounded without bias, so v, its square, gains the rounding's variance:
+ * up to a twentieth with beta2 = 0.999.
+ * A gradient that is NaN or infinite makes its value (and in 8 bits its block of states) NaN.
+ * tensors: a HOST array, read during the call only; a launch for every 40 tensors.  Pointers 16-byte aligned, scales
+ * 4-byte aligned; buffers of a tensor overlap neither each other nor another tensor's.
+ * MOE_EINVAL: a NULL pointer of a tensor with n > 0, n outside [0, 2^40], master != NULL beside an fp32 param, count < 0, step < 1
+ * (without device_step), beta1 or beta2 outside [0, 1), eps <= 0, a value that is not finite.  MOE_EUNSUP: a dtype other than
+ * named here.  Deterministic.
+ */
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;               /* 1 for the first */
+  int32_t state_dtype;        /* MOE_F32 or MOE_MXFP8 */
+  int32_t stochastic;
+  uint64_t seed;
+  const float* grad_scale;    /* DEVICE float, NULL for 1 (1 / loss scale, a clipping factor) */
+  const float* device_lr;     /* DEVICE float in place of lr, NULL for lr: for steps captured into a graph */
+  const int64_t* device_step; /* DEVICE int64 in place of step, likewise (read, not advanced) */
+} moe_adamw_t;
+typedef struct {
+  void* param;                /* [n] of param_dtype */
+  const void* grad;           /* [n] of grad_dtype */
+  float* master;              /* fp32 [n] behind a bf16 param, or NULL */
+  void* m;
+  void* v;
+  uint8_t* m_scales;          /* MOE_MXFP8 states only */
+  uint8_t* v_scales;
+  int64_t n;
+  float weight_decay;
+  int32_t param_dtype;        /* MOE_BF16 or MOE_F32 */
+  int32_t grad_dtype;         /* MOE_BF16 or MOE_F32 */
+} moe_adamw_tensor_t;
+int moe_adamw(const moe_adamw_t* a, const moe_adamw_tensor_t* tensors, int32_t count, void* stream);
+
+/*
  * Inter-partition signal latency on one GPU -- the one-GPU analogue of the pages'
  * signalling measurement [kucoin §02: after a push the destination has to collect a
  * completion signal from every peer; Cursor's multi-node microbenchmark put that latency

@@ -1,5 +1,6 @@
 // extern "C" entry points of libmoe: argument checks, workspace sizing, launches.
 // Every check runs before the first HIP call, so argument errors need no GPU.
+#include <math.h>
 #include <string.h>
 
 #include "common.hpp"
@@ -91,6 +92,19 @@ hipError_t launch_ffn_mx4(const moe_shape_t& s, int El, const uint8_t* xe, const
                           const int32_t* offsets, const uint8_t* w1, const uint8_t* w3, const uint8_t* w2,
                           const moe_mx_scales_t& w_scales, void* ye, char* ws, const WsLayout& L, int cus,
                           hipStream_t st, const uint64_t* row_dst, bool rows32);
+hipError_t launch_norm(const moe_norm_t& n, const void* x, const void* residual, const float* gamma, void* h, void* y,
+                       uint8_t* codes, uint8_t* scales, int cus, hipStream_t st);
+int norm_bwd_grid(int64_t rows, int d);
+hipError_t launch_norm_bwd(const moe_norm_t& n, const void* dy, const void* h, const float* gamma, const void* dh, void* dx,
+                           float* dgamma, float* parts, hipStream_t st);
+hipError_t launch_dispatch_codes(const moe_shape_t& s, const uint8_t* const* xq, const uint8_t* const* xq_scales,
+                                 const int32_t* pull_src, uint8_t* xe, uint8_t* xe_scales, int64_t nmax,
+                                 const int32_t* ctrl, int cus, hipStream_t st);
+hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, const int32_t* offsets, void* y,
+                          int32_t* status, int cus, hipStream_t st);
+hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* dy, const int32_t* offsets, void* dw,
+                                int dw_dtype, bool accumulate, int32_t* status, int cus, hipStream_t st);
+hipError_t launch_adamw(const moe_adamw_t& h, const moe_adamw_tensor_t* tensors, int count, int cus, hipStream_t st);
 }  // namespace moe
 
 using namespace moe;
@@ -218,6 +232,31 @@ int check_bwd(const moe_shape_t* s, const moe_placement_t* p, const void* ws, si
   if (reinterpret_cast<uintptr_t>(bws) & 255) return MOE_EALIGN;
   if (bws_bytes < bwd_layout(*s, p->E_local).total) return MOE_ENOSPC;
   return MOE_OK;
+}
+
+// rows, or anything else that must be present and 16-byte aligned; optional buffers may be null
+int check_rows(const void* q) { return aligned16(q) ? MOE_OK : q ? MOE_EALIGN : MOE_EINVAL; }
+int check_optional(const void* q, int align) { return (reinterpret_cast<uintptr_t>(q) & (align - 1)) ? MOE_EALIGN : MOE_OK; }
+
+int check_norm(const moe_norm_t* n) {
+  if (!n) return MOE_EINVAL;
+  if (n->dtype != MOE_F32 && n->dtype != MOE_BF16) return MOE_EUNSUP;
+  if (n->d < 1 || n->d > 32768 || n->rows < 0 || n->rows >= (int64_t(1) << 40) / n->d) return MOE_EINVAL;
+  if (!(n->eps >= 0.0f) || isinf(n->eps)) return MOE_EINVAL;
+  return n->d % (n->dtype == MOE_F32 ? 4 : 8) ? MOE_EALIGN : MOE_OK;
+}
+
+int check_gemm(const moe_gemm_t* g) {
+  if (!g) return MOE_EINVAL;
+  if (g->dtype != MOE_F32 && g->dtype != MOE_BF16) return MOE_EUNSUP;
+  if (g->rows < 0 || g->rows >= (int64_t(1) << 31) || g->groups < 1 || g->groups > 1024) return MOE_EINVAL;
+  if (g->K < 1 || g->N < 1 || int64_t(g->K) * g->N >= (int64_t(1) << 31)) return MOE_EINVAL;
+  if (g->w_layout != 0 && g->w_layout != 1) return MOE_EINVAL;
+  const int64_t most = int64_t(1) << 22;
+  if (g->K > most || g->N > most || g->ldx < 0 || g->ldx > most || g->ldy < 0 || g->ldy > most) return MOE_EINVAL;
+  if ((g->ldx && g->ldx < g->K) || (g->ldy && g->ldy < g->N)) return MOE_EINVAL;
+  const int unit = g->dtype == MOE_F32 ? 4 : 8;
+  return (g->K % unit || g->N % unit || g->ldx % unit || g->ldy % unit) ? MOE_EALIGN : MOE_OK;
 }
 
 }  // namespace
@@ -1012,6 +1051,128 @@ int moe_backward_ring(const moe_shape_t* s, const moe_placement_t* p, const moe_
   e = launch_merge(*s, slot_of, nullptr, recv, dx, cus, st);
   if (e == hipSuccess) e = launch_gate_grad(*s, topk_w, topk_idx, slot_of, dgp, dlogits, cus, st);
   return hip_rc(e);
+}
+
+int moe_norm(const moe_norm_t* n, const void* x, const void* residual, const float* gamma, void* h, void* y,
+             uint8_t* codes, uint8_t* scales, void* stream) {
+  int rc = check_norm(n);
+  if (rc) return rc;
+  if (codes && n->d % 128) return MOE_EALIGN;
+  if (n->rows == 0) return MOE_OK;
+  if ((!h && !y && !codes) || (!codes != !scales) || (h && h == y)) return MOE_EINVAL;
+  if ((rc = check_rows(x)) || (rc = check_optional(residual, 16)) || (rc = check_optional(gamma, 4)) ||
+      (rc = check_optional(h, 16)) || (rc = check_optional(y, 16)) || (rc = check_optional(codes, 16)) ||
+      (rc = check_optional(scales, 4)))
+    return rc;
+  return hip_rc(launch_norm(*n, x, residual, gamma, h, y, codes, scales, cu_count(), static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_norm_backward_workspace_bytes(const moe_norm_t* n) {
+  if (check_norm(n) != MOE_OK) return 0;
+  return align256(size_t(norm_bwd_grid(n->rows, n->d)) * n->d * 4);
+}
+
+int moe_norm_backward(const moe_norm_t* n, const void* dy, const void* h, const float* gamma, const void* dh, void* dx,
+                      float* dgamma, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_norm(n);
+  if (rc) return rc;
+  if (!dx && !dgamma && n->rows > 0) return MOE_EINVAL;
+  if (n->rows > 0 && ((rc = check_rows(dy)) || (rc = check_rows(h)))) return rc;
+  if ((rc = check_optional(gamma, 4)) || (rc = check_optional(dh, 16)) || (rc = check_optional(dx, 16)) ||
+      (rc = check_optional(dgamma, 4)))
+    return rc;
+  if (dgamma && n->rows > 0) {
+    if (!ws) return MOE_EINVAL;
+    if (reinterpret_cast<uintptr_t>(ws) & 255) return MOE_EALIGN;
+    if (ws_bytes < moe_norm_backward_workspace_bytes(n)) return MOE_ENOSPC;
+  }
+  return hip_rc(launch_norm_bwd(*n, dy, h, gamma, dh, dx, dgamma, static_cast<float*>(ws),
+                                static_cast<hipStream_t>(stream)));
+}
+
+int moe_dispatch_pull_codes(const moe_shape_t* s, const moe_placement_t* p, const uint8_t* const* xq,
+                            const uint8_t* const* xq_scales, const int32_t* pull_src, const int32_t* offsets, uint8_t* xe,
+                            uint8_t* xe_scales, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_shape(s, p);
+  if (rc) return rc;
+  if (!is_mx(s)) return MOE_EUNSUP;
+  if (!pull_src || !offsets) return MOE_EINVAL;
+  if ((rc = check_rows(xe)) || (rc = check_scales(xe_scales)) || (rc = check_ptr_table(xq, s->R))) return rc;
+  if (!xq_scales) return MOE_EINVAL;
+  for (int r = 0; r < s->R; ++r) {
+    if ((rc = check_scales(xq_scales[r]))) return rc;
+    if (xq[r] == xe || xq_scales[r] == xe_scales) return MOE_EINVAL;
+  }
+  if ((rc = check_ws(s, p, ws, ws_bytes))) return rc;
+  const WsLayout L = ws_layout(*s, p->E_local);
+  return hip_rc(launch_dispatch_codes(*s, xq, xq_scales, pull_src, xe, xe_scales, L.max_pairs,
+                                      reinterpret_cast<const int32_t*>(static_cast<char*>(ws) + L.ctrl), cu_count(),
+                                      static_cast<hipStream_t>(stream)));
+}
+
+int moe_grouped_gemm(const moe_gemm_t* g, const void* x, const void* w, const int32_t* offsets, void* y,
+                     int32_t* status, void* stream) {
+  int rc = check_gemm(g);
+  if (rc) return rc;
+  if (!offsets) return MOE_EINVAL;
+  if ((rc = check_optional(offsets, 4)) || (rc = check_optional(status, 4))) return rc;
+  if (g->rows > 0) {
+    if ((rc = check_rows(x)) || (rc = check_rows(w)) || (rc = check_rows(y))) return rc;
+    if (y == x || y == w) return MOE_EINVAL;
+  }
+  return hip_rc(launch_grouped(*g, x, w, offsets, y, status, cu_count(), static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_grouped_gemm_wgrad_workspace_bytes(const moe_gemm_t* g) {
+  (void)g;
+  return 0;
+}
+
+int moe_grouped_gemm_wgrad(const moe_gemm_t* g, const void* x, const void* dy, const int32_t* offsets, void* dw,
+                           int32_t dw_dtype, int32_t accumulate, void* ws, size_t ws_bytes, int32_t* status,
+                           void* stream) {
+  int rc = check_gemm(g);
+  if (rc) return rc;
+  if (dw_dtype != MOE_F32 && dw_dtype != g->dtype) return MOE_EUNSUP;
+  if (accumulate && dw_dtype != MOE_F32) return MOE_EINVAL;
+  if (!offsets) return MOE_EINVAL;
+  if ((rc = check_optional(offsets, 4)) || (rc = check_optional(status, 4)) || (rc = check_rows(dw))) return rc;
+  if (g->rows > 0) {
+    if ((rc = check_rows(x)) || (rc = check_rows(dy))) return rc;
+    if (dw == x || dw == dy) return MOE_EINVAL;
+  }
+  if (const size_t need = moe_grouped_gemm_wgrad_workspace_bytes(g)) {
+    if (!ws) return MOE_EINVAL;
+    if (reinterpret_cast<uintptr_t>(ws) & 255) return MOE_EALIGN;
+    if (ws_bytes < need) return MOE_ENOSPC;
+  }
+  return hip_rc(launch_grouped_wgrad(*g, x, dy, offsets, dw, dw_dtype, accumulate != 0, status, cu_count(),
+                                     static_cast<hipStream_t>(stream)));
+}
+
+int moe_adamw(const moe_adamw_t* a, const moe_adamw_tensor_t* tensors, int32_t count, void* stream) {
+  if (!a || count < 0 || (count > 0 && !tensors)) return MOE_EINVAL;
+  const bool eight = a->state_dtype == MOE_MXFP8;
+  if (!eight && a->state_dtype != MOE_F32) return MOE_EUNSUP;
+  if (!isfinite(a->lr) || !(a->beta1 >= 0 && a->beta1 < 1) || !(a->beta2 >= 0 && a->beta2 < 1)) return MOE_EINVAL;
+  if (!(float(a->eps) > 0) || !isfinite(a->eps) || (!a->device_step && a->step < 1)) return MOE_EINVAL;
+  int rc;
+  if ((rc = check_optional(a->grad_scale, 4)) || (rc = check_optional(a->device_lr, 4)) ||
+      (rc = check_optional(a->device_step, 8)))
+    return rc;
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_tensor_t& t = tensors[i];
+    if ((t.param_dtype != MOE_F32 && t.param_dtype != MOE_BF16) || (t.grad_dtype != MOE_F32 && t.grad_dtype != MOE_BF16))
+      return MOE_EUNSUP;
+    if (t.n < 0 || t.n > (int64_t(1) << 40) || !isfinite(t.weight_decay)) return MOE_EINVAL;
+    if (t.n == 0) continue;
+    if (t.master && t.param_dtype == MOE_F32) return MOE_EINVAL;
+    if ((rc = check_rows(t.param)) || (rc = check_rows(t.grad)) || (rc = check_rows(t.m)) || (rc = check_rows(t.v)) ||
+        (rc = check_optional(t.master, 16)))
+      return rc;
+    if (eight && ((rc = check_scales(t.m_scales)) || (rc = check_scales(t.v_scales)))) return rc;
+  }
+  return hip_rc(launch_adamw(*a, tensors, count, cu_count(), static_cast<hipStream_t>(stream)));
 }
 
 int moe_read_status(const void* ws, void* stream) {

@@ -32,6 +32,8 @@ EXPORTS = ["moe_max_pairs", "moe_workspace_bytes", "moe_mx_quantize", "moe_mx_qu
            "moe_combine_pull_reverse", "moe_expert_ffn_backward",
            "moe_dispatch_push_reverse", "moe_backward", "moe_backward_ring", "moe_backward_prepare_mx",
            "moe_backward_mx",
+           "moe_norm", "moe_norm_backward_workspace_bytes", "moe_norm_backward", "moe_dispatch_pull_codes",
+           "moe_grouped_gemm", "moe_grouped_gemm_wgrad_workspace_bytes", "moe_grouped_gemm_wgrad", "moe_adamw",
            "moe_signal_probe_bytes", "moe_signal_probe", "moe_ceiling_probe_bytes", "moe_ceiling_probe",
            "moe_read_status", "moe_strerror", "moe_version"]
 
@@ -61,6 +63,44 @@ class Exec(ctypes.Structure):
     _fields_ = [("minibatch_rows", ctypes.c_int32), ("comm_cus", ctypes.c_int32),
                 ("ring_slots", ctypes.c_int32), ("trace", ctypes.c_int32),
                 ("watchdog_us", ctypes.c_uint64), ("reverse_ring", ctypes.c_int32)]
+
+
+class Norm(ctypes.Structure):
+    """moe_norm_t: Norm(rows, d, dtype, eps)."""
+    _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class Gemm(ctypes.Structure):
+    """moe_gemm_t: Gemm(rows, groups, K, N, dtype, w_layout, ldx, ldy)."""
+    _fields_ = [("rows", ctypes.c_int64), ("groups", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("w_layout", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class AdamW(ctypes.Structure):
+    """moe_adamw_t; grad_scale, device_lr and device_step are addresses (tensor.data_ptr()) or None."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("step", ctypes.c_int64), ("state_dtype", ctypes.c_int32), ("stochastic", ctypes.c_int32),
+                ("seed", ctypes.c_uint64), ("grad_scale", ctypes.c_void_p), ("device_lr", ctypes.c_void_p),
+                ("device_step", ctypes.c_void_p)]
+
+
+class AdamWTensor(ctypes.Structure):
+    """moe_adamw_tensor_t of tensors or addresses."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("weight_decay", ctypes.c_float), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32)]
+
+    def __init__(self, param, grad, n, param_dtype, grad_dtype, m, v, m_scales=None, v_scales=None, master=None,
+                 weight_decay=0.0):
+        super().__init__(_p(param), _p(grad), _p(master), _p(m), _p(v), _p(m_scales), _p(v_scales), int(n), weight_decay,
+                         int(param_dtype), int(grad_dtype))
+
+
+def adamw_table(tensors):
+    """The host array of moe_adamw, to keep from step to step.  It holds addresses: the tensors stay the caller's to keep."""
+    tensors = list(tensors)
+    return (AdamWTensor * len(tensors))(*tensors)
 
 
 _lib = None
@@ -126,6 +166,16 @@ def lib() -> ctypes.CDLL:
         L.moe_backward_prepare_mx.argtypes = [S, PL, VP, VP, VP, VP, VP, VP, VP, VP]
         L.moe_backward_mx.argtypes = [S, PL, VP, VP, VP, VP, VP, VP, VP, MS, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP,
                                       SZ, VP, VP, VP, VP, VP, VP, VP, SZ, VP]
+        L.moe_norm.argtypes = [P(Norm), VP, VP, VP, VP, VP, VP, VP, VP]
+        L.moe_norm_backward_workspace_bytes.argtypes = [P(Norm)]
+        L.moe_norm_backward_workspace_bytes.restype = SZ
+        L.moe_norm_backward.argtypes = [P(Norm), VP, VP, VP, VP, VP, VP, VP, SZ, VP]
+        L.moe_dispatch_pull_codes.argtypes = [S, PL, VP, VP, VP, VP, VP, VP, VP, SZ, VP]
+        L.moe_grouped_gemm.argtypes = [P(Gemm), VP, VP, VP, VP, VP, VP]
+        L.moe_grouped_gemm_wgrad_workspace_bytes.argtypes = [P(Gemm)]
+        L.moe_grouped_gemm_wgrad_workspace_bytes.restype = SZ
+        L.moe_grouped_gemm_wgrad.argtypes = [P(Gemm), VP, VP, VP, VP, ctypes.c_int32, ctypes.c_int32, VP, SZ, VP, VP]
+        L.moe_adamw.argtypes = [P(AdamW), VP, ctypes.c_int32, VP]
         L.moe_signal_probe_bytes.argtypes = [I32]
         L.moe_signal_probe_bytes.restype = SZ
         L.moe_signal_probe.argtypes = [I32, I32, I32, I32, VP, SZ, VP, VP, VP, VP, VP]
@@ -143,7 +193,8 @@ def lib() -> ctypes.CDLL:
                   "moe_forward", "moe_forward_persistent", "moe_persistent_dispatch_ffn_combine",
                   "moe_forward_persistent_noalloc",
                   "moe_combine_pull_reverse", "moe_expert_ffn_backward", "moe_dispatch_push_reverse", "moe_backward", "moe_backward_prepare_mx",
-                  "moe_backward_ring", "moe_backward_mx", "moe_signal_probe", "moe_ceiling_probe", "moe_read_status"):
+                  "moe_backward_ring", "moe_backward_mx", "moe_norm", "moe_norm_backward", "moe_dispatch_pull_codes",
+                  "moe_grouped_gemm", "moe_grouped_gemm_wgrad", "moe_adamw", "moe_signal_probe", "moe_ceiling_probe", "moe_read_status"):
             getattr(L, f).restype = I32
         _lib = L
     return _lib
@@ -197,6 +248,13 @@ def _check(rc: int, where: str) -> int:
     if rc != 0:
         raise MoEError(rc, where)
     return rc
+
+
+def _bytes(ws, ws_bytes):
+    """Bytes of a workspace tensor, unless they are given."""
+    if ws_bytes is not None:
+        return ws_bytes
+    return 0 if ws is None else ws.numel() * ws.element_size()
 
 
 def strerror(code: int) -> str:
@@ -508,6 +566,53 @@ def moe_backward_mx(shape, placement, dy, x, xe, xe_scales, ye, w1q, w3q, w_scal
                                _table(dx), _table(dlogits), _p(dw1), _p(dw3), _p(dw2), _p(bws),
                                bws.numel() if bws_bytes is None else bws_bytes, _stream(stream))
     return _check(rc, "moe_backward_mx") if check else rc
+
+
+def moe_norm(n, x, residual, gamma, h, y, codes=None, scales=None, stream=None, check=True):
+    rc = lib().moe_norm(_ref(n), _p(x), _p(residual), _p(gamma), _p(h), _p(y), _p(codes), _p(scales), _stream(stream))
+    return _check(rc, "moe_norm") if check else rc
+
+
+def moe_norm_backward_workspace_bytes(n: Norm) -> int:
+    return int(lib().moe_norm_backward_workspace_bytes(_ref(n)))
+
+
+def moe_norm_backward(n, dy, h, gamma, dh, dx, dgamma, ws=None, ws_bytes=None, stream=None, check=True):
+    rc = lib().moe_norm_backward(_ref(n), _p(dy), _p(h), _p(gamma), _p(dh), _p(dx), _p(dgamma), _p(ws), _bytes(ws, ws_bytes),
+                                 _stream(stream))
+    return _check(rc, "moe_norm_backward") if check else rc
+
+
+def moe_dispatch_pull_codes(shape, placement, xq, xq_scales, pull_src, offsets, xe, xe_scales, ws, ws_bytes=None,
+                            stream=None, check=True):
+    rc = lib().moe_dispatch_pull_codes(ctypes.byref(shape), ctypes.byref(placement), _table(xq), _table(xq_scales),
+                                       _p(pull_src), _p(offsets), _p(xe), _p(xe_scales), _p(ws), _bytes(ws, ws_bytes),
+                                       _stream(stream))
+    return _check(rc, "moe_dispatch_pull_codes") if check else rc
+
+
+def moe_grouped_gemm(g, x, w, offsets, y, status=None, stream=None, check=True):
+    rc = lib().moe_grouped_gemm(_ref(g), _p(x), _p(w), _p(offsets), _p(y), _p(status), _stream(stream))
+    return _check(rc, "moe_grouped_gemm") if check else rc
+
+
+def moe_grouped_gemm_wgrad_workspace_bytes(g: Gemm) -> int:
+    return int(lib().moe_grouped_gemm_wgrad_workspace_bytes(_ref(g)))
+
+
+def moe_grouped_gemm_wgrad(g, x, dy, offsets, dw, dw_dtype, ws=None, ws_bytes=None, accumulate=False, status=None,
+                           stream=None, check=True):
+    rc = lib().moe_grouped_gemm_wgrad(_ref(g), _p(x), _p(dy), _p(offsets), _p(dw), int(dw_dtype), int(accumulate), _p(ws),
+                                      _bytes(ws, ws_bytes), _p(status), _stream(stream))
+    return _check(rc, "moe_grouped_gemm_wgrad") if check else rc
+
+
+def moe_adamw(step, tensors, stream=None, check=True):
+    """tensors: adamw_table(...), or a list of AdamWTensor."""
+    if not isinstance(tensors, ctypes.Array):
+        tensors = adamw_table(tensors)
+    rc = lib().moe_adamw(_ref(step), tensors, len(tensors), _stream(stream))
+    return _check(rc, "moe_adamw") if check else rc
 
 
 def moe_read_status(ws, stream=None) -> int:

@@ -1,0 +1,207 @@
+"""GPU parity of the products grouped by expert and of their gradients.
+
+Bars.  Whole numbers: inputs are small integers whose sums fp32 holds exactly, so every output is the exact sum, rounded once: no
+tolerance.  Other values: K roundings of 2^-24 of the sum of magnitudes (products of bf16 values are exact in fp32; fp32 ones
+round once more), and finfo.eps / 2 for the one rounding to the output type.
+"""
+import numpy as np
+import pytest
+
+from oracle import more_oracle as M
+from mixture_experts_layer_histogram_amd import moe
+
+pytestmark = pytest.mark.gpu
+
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _kind(dtype):
+    torch = _torch()
+    return (moe.MOE_BF16, torch.bfloat16) if dtype == "bf16" else (moe.MOE_F32, torch.float32)
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _make(shape, dtype, seed, whole, scale=1.0):
+    torch = _torch()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if whole:
+        return torch.randint(-3, 4, shape, generator=g, device="cuda").to(_kind(dtype)[1])
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(_kind(dtype)[1])
+
+
+def _offsets(counts, first=0):
+    torch = _torch()
+    off = np.concatenate([[first], first + np.cumsum(counts)]).astype(np.int32)
+    return off.tolist(), torch.from_numpy(off).cuda()
+
+
+def _strided(rows, cols, pad, dtype, seed, whole):
+    """Rows of `cols` values, `pad` more between them that hold NaN."""
+    torch = _torch()
+    t = torch.full((rows, cols + pad), float("nan"), dtype=_kind(dtype)[1], device="cuda")
+    t[:, :cols] = _make((rows, cols), dtype, seed, whole)
+    return t
+
+
+def _close(got, ref, mag, terms, dtype, whole):
+    got = _np(got)
+    if whole:
+        torch = _torch()
+        want = torch.from_numpy(ref).to(_kind(dtype)[1]).double().numpy()
+        assert np.array_equal(got, want)
+    else:
+        assert (np.abs(got - ref) <= (terms + 1) * 2.0 ** -24 * mag + HALF[dtype] * np.abs(ref)).all()
+
+
+# counts of rows, K, N
+CASES = [
+    ([1], 8, 8), ([0, 1, 0], 16, 8), ([3, 0, 5, 1], 40, 24), ([64, 65, 63], 64, 64), ([7] * 5, 1408, 72), ([130, 0, 257], 200, 264),
+    ([1, 1, 0, 1, 1, 0, 1, 1], 2048, 1408), ([300, 20, 0, 600], 136, 520), ([16] * 32, 512, 256), ([40, 9, 77, 33, 20, 25], 1024, 328),
+    ([2000], 256, 128), ([500, 1, 1, 1, 1], 72, 1032), ([0] * 1023 + [3], 16, 16), ([2] * 1000, 24, 40), ([1100, 900], 2048, 512),
+]
+
+
+@pytest.mark.parametrize("counts,K,N", CASES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("whole", [True, False])
+def test_product(counts, K, N, dtype, layout, whole):
+    torch = _torch()
+    code, kind = _kind(dtype)
+    off, doff = _offsets(counts)
+    rows = off[-1] + 3                       # rows behind the last group: NaN in x, left as they are in y
+    x = _make((rows, K), dtype, 1, whole)
+    x[off[-1]:] = float("nan")
+    w = _make((len(counts), N, K) if layout == 0 else (len(counts), K, N), dtype, 2, whole)
+    y = torch.full((rows, N), 7.0, dtype=kind, device="cuda")
+    status = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    moe.moe_grouped_gemm(moe.Gemm(rows, len(counts), K, N, code, layout), x, w, doff, y, status)
+    assert int(status) == 0
+    ref, mag = M.grouped(_np(x), _np(w), off, layout)
+    _close(y[: off[-1]], ref[: off[-1]], mag[: off[-1]], K + (dtype == "f32"), dtype, whole)
+    assert (y[off[-1]:] == 7).all()
+
+
+@pytest.mark.parametrize("counts,K,N", CASES)
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("whole", [True, False])
+def test_weight_gradient(counts, K, N, dtype, out, layout, whole):
+    torch = _torch()
+    code, kind = _kind(dtype)
+    off, doff = _offsets(counts)
+    rows = off[-1] + 2
+    x, dy = _make((rows, K), dtype, 1, whole), _make((rows, N), dtype, 2, whole)
+    x[off[-1]:] = dy[off[-1]:] = float("nan")
+    g = moe.Gemm(rows, len(counts), K, N, code, layout)
+    size = len(counts) * K * N
+    dw = torch.full((size + 64,), 7.0, dtype=_kind(out)[1], device="cuda")
+    ws = torch.empty(moe.moe_grouped_gemm_wgrad_workspace_bytes(g) + 256, dtype=torch.uint8, device="cuda").fill_(0x5A)
+    status = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    args = (x, dy, doff, dw, _kind(out)[0], ws, ws.numel() - 256)
+    moe.moe_grouped_gemm_wgrad(g, *args, status=status)
+    assert int(status) == 0 and (dw[size:] == 7).all() and (ws[-256:] == 0x5A).all()
+    ref, mag = M.grouped_wgrad(_np(x[: off[-1]]), _np(dy[: off[-1]]), off, layout)
+    _close(dw[:size], ref.reshape(-1), mag.reshape(-1), max(counts) + (dtype == "f32"), out, whole)
+    if out == "f32":                         # and once more on top of it
+        once = dw.clone()
+        moe.moe_grouped_gemm_wgrad(g, *args, accumulate=True)
+        if whole:
+            assert torch.equal(dw[:size], 2 * once[:size])
+        else:
+            assert (np.abs(_np(dw[:size]) - 2 * _np(once[:size])) <= 2.0 ** -24 * 2 * np.abs(_np(once[:size]))).all()
+        assert (dw[size:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("counts", [[5, 0, 40], [300, 31]])
+def test_strided_rows_and_a_first_offset(dtype, layout, counts):
+    """x, y and dy as columns of wider rows (what lies between is NaN and stays), rows of no group ahead of the first."""
+    torch = _torch()
+    code, kind = _kind(dtype)
+    K, N, first = 72, 104, 6
+    off, doff = _offsets(counts, first)
+    rows = off[-1]
+    x, dy = _strided(rows, K, 24, dtype, 1, True), _strided(rows, N, 8, dtype, 2, True)
+    y = torch.full((rows, N + 16), 7.0, dtype=kind, device="cuda")
+    w = _make((len(counts), N, K) if layout == 0 else (len(counts), K, N), dtype, 3, True)
+    g = moe.Gemm(rows, len(counts), K, N, code, layout, K + 24, N + 16)
+    moe.moe_grouped_gemm(g, x, w, doff, y)
+    ref, _ = M.grouped(_np(x[:, :K]), _np(w), off, layout)
+    _close(y[first:, :N], ref[first:], None, K, dtype, True)
+    assert (y[:first] == 7).all() and (y[:, N:] == 7).all()
+    g = moe.Gemm(rows, len(counts), K, N, code, layout, K + 24, N + 8)
+    dw = torch.empty(len(counts), *w.shape[1:], device="cuda")
+    ws = torch.empty(moe.moe_grouped_gemm_wgrad_workspace_bytes(g), dtype=torch.uint8, device="cuda")
+    moe.moe_grouped_gemm_wgrad(g, x, dy, doff, dw, moe.MOE_F32, ws)
+    ref, _ = M.grouped_wgrad(_np(x[:, :K]), _np(dy[:, :N]), off, layout)
+    _close(dw, ref, None, rows, "f32", True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("counts", [[9, 200, 3], [1, 2, 1]])
+def test_a_group_keeps_its_wild_values(dtype, counts):
+    """A NaN or an infinity in one row or one group's weights reaches only that row, or that group's rows, and is not lost."""
+    torch = _torch()
+    code, kind = _kind(dtype)
+    K, N = 88, 136
+    off, doff = _offsets(counts)
+    x, w = _make((off[-1], K), dtype, 1, True), _make((3, N, K), dtype, 2, True)
+    x[0, 87] = float("nan")
+    x[off[1], 5] = float("inf")
+    w[2, 100, 3] = float("nan")
+    w[1, :, 5] = 1.0
+    y = torch.empty(off[-1], N, dtype=kind, device="cuda")
+    moe.moe_grouped_gemm(moe.Gemm(off[-1], 3, K, N, code, 0), x, w, doff, y)
+    y = _np(y)
+    clean_x, clean_w = _np(x), _np(w)
+    clean_x[~np.isfinite(clean_x)] = 0
+    clean_w[~np.isfinite(clean_w)] = 0
+    ref, _ = M.grouped(clean_x, clean_w, off, 0)
+    want = _torch().from_numpy(ref).to(kind).double().numpy()
+    wild = np.zeros(y.shape, bool)
+    wild[0] = True
+    wild[off[1]] = True
+    wild[off[2]:, 100] = True
+    assert np.array_equal(y[~wild], want[~wild])
+    assert np.isnan(y[0]).all() and (y[off[1]] == np.inf).all() and np.isnan(y[off[2]:, 100]).all()
+
+
+@pytest.mark.parametrize("bad", [[0, 5, 3, 9], [-1, 2, 3, 9], [0, 2, 3, 12], [4, 3, 3, 3], [0, 1 << 30, 4, 9]])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bad_offsets_compute_nothing(bad, dtype):
+    torch = _torch()
+    code, kind = _kind(dtype)
+    x, w = _make((11, 64), dtype, 1, True), _make((3, 64, 64), dtype, 2, True)
+    y, dw = torch.full((11, 64), 7.0, dtype=kind, device="cuda"), torch.full((3, 64, 64), 7.0, device="cuda")
+    off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    for call in (lambda s: moe.moe_grouped_gemm(g, x, w, off, y, s), lambda s: moe.moe_grouped_gemm_wgrad(g, x, x, off, dw, moe.MOE_F32, ws, status=s)):
+        g = moe.Gemm(11, 3, 64, 64, code, 0)
+        ws = torch.empty(moe.moe_grouped_gemm_wgrad_workspace_bytes(g), dtype=torch.uint8, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        call(status)
+        assert int(status) == -1
+        call(None)
+    assert (y == 7).all() and (dw == 7).all()
+
+
+def test_no_rows():
+    torch = _torch()
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    g = moe.Gemm(0, 3, 64, 72, moe.MOE_BF16, 0)
+    status = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    moe.moe_grouped_gemm(g, None, None, off, None, status)
+    assert int(status) == 0
+    dw = torch.full((3, 72, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(moe.moe_grouped_gemm_wgrad_workspace_bytes(g), dtype=torch.uint8, device="cuda")
+    moe.moe_grouped_gemm_wgrad(g, None, None, off, dw, moe.MOE_BF16, ws)
+    assert (dw == 0).all()
