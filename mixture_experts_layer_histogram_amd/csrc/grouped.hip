@@ -3,6 +3,7 @@
 //   dW_g = sum over s of dy[s]^T x[s] (or its transpose), the gradient by the weights.
 // The gradient by the rows is the first product in the weights' other orientation.
 #include "grouped.hpp"
+#include "grouped_tile.hpp"
 
 namespace moe {
 
@@ -186,6 +187,117 @@ __global__ __launch_bounds__(256) void grouped_small_wgrad_kernel(WgradArgs g) {
   }
 }
 
+// 256 x 256 tiles in bf16 (grouped_tile.hpp): one workgroup a CU walks them.  The list of tiles is cut into eight contiguous
+// ranges, one for an XCD (workgroup w runs on XCD w mod 8), by group, then column tile, row tiles innermost: the CUs of
+// an XCD share one group's weight panels in their L2.
+template <bool W_KN>
+__global__ __launch_bounds__(kBigThreads, 2) void grouped_big_kernel(GroupedArgs g) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  __shared__ int32_t base[kMaxGroups + 1], part[9];
+  bool bad;
+  const int mtiles = group_tiles<kBigThreads>(g.offsets, g.G, g.rows, 8, base, part, &bad);
+  if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
+  const int NT = (g.N + kBig - 1) / kBig;
+  const int64_t total = int64_t(mtiles) * NT, per_xcd = (total + 7) >> 3;
+  const int xcd = blockIdx.x & 7, wg_per_xcd = gridDim.x >> 3;
+  for (int64_t tt = blockIdx.x >> 3; tt < per_xcd; tt += wg_per_xcd) {
+    const int64_t tau = xcd * per_xcd + tt;
+    if (tau >= total) break;
+    const int mtg = int(tau / NT);
+    const int l = find_expert(base, g.G, mtg);
+    const int mt0 = base[l], mtl = base[l + 1] - mt0;
+    const int i_in = int(tau - int64_t(mt0) * NT);
+    const int nt = i_in / mtl, mt = i_in - nt * mtl;
+    const int64_t row0 = g.offsets[l] + int64_t(mt) * kBig;
+    const int rows = int(min(int64_t(kBig), g.offsets[l + 1] - row0));
+    const int c0 = nt * kBig, cols = min(kBig, g.N - c0);
+    const uint16_t* w = static_cast<const uint16_t*>(g.w) + int64_t(l) * g.N * g.K;
+    BigTile<false, W_KN> t;
+    t.start(smem, BigOperand{static_cast<const uint16_t*>(g.x) + row0 * g.ldx, g.ldx, rows},
+            BigOperand{W_KN ? w + c0 : w + int64_t(c0) * g.K, W_KN ? g.N : g.K, cols}, g.K);
+    t.run(rows, cols);
+    uint16_t* out = static_cast<uint16_t*>(g.y) + row0 * g.ldy + c0;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      const int row = t.half * 128 + m * 16 + t.r16;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int col = t.wn * 64 + n * 16 + 4 * t.g;
+        if (row < rows && col < cols)
+          *reinterpret_cast<uint2*>(out + row * g.ldy + col) =
+              make_uint2(pack_bf16x2(t.acc[m][n][0], t.acc[m][n][1]), pack_bf16x2(t.acc[m][n][2], t.acc[m][n][3]));
+      }
+    }
+  }
+}
+
+// The same for the gradient by the weights: a tile of 256 x 256 of one group's gradient sums over the group's rows.
+template <typename O, bool ADD>
+__global__ __launch_bounds__(kBigThreads, 2) void grouped_big_wgrad_kernel(WgradArgs g) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  __shared__ int32_t base[kMaxGroups + 1], part[9];
+  bool bad;
+  group_tiles<kBigThreads>(g.offsets, g.G, g.rows, 8, base, part, &bad);
+  if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
+  if (bad) return;
+  const int MT = (g.M + kBig - 1) / kBig, NT = (g.N + kBig - 1) / kBig;
+  const int64_t total = int64_t(g.G) * MT * NT, per_xcd = (total + 7) >> 3;
+  const int xcd = blockIdx.x & 7, wg_per_xcd = gridDim.x >> 3;
+  for (int64_t tt = blockIdx.x >> 3; tt < per_xcd; tt += wg_per_xcd) {
+    const int64_t tau = xcd * per_xcd + tt;
+    if (tau >= total) break;
+    const int l = int(tau / (int64_t(MT) * NT));
+    const int rem = int(tau - int64_t(l) * MT * NT);
+    const int nt = rem / MT, mt = rem - nt * MT;
+    const int m0 = mt * kBig, c0 = nt * kBig;
+    const int rows = min(kBig, g.M - m0), cols = min(kBig, g.N - c0);
+    const int64_t r0 = g.offsets[l];
+    const int n = int(g.offsets[l + 1] - r0);
+    if (ADD && n == 0) continue;
+    BigTile<true, true> t;
+    t.start(smem, BigOperand{static_cast<const uint16_t*>(g.a) + r0 * g.lda + m0, g.lda, rows},
+            BigOperand{static_cast<const uint16_t*>(g.b) + r0 * g.ldb + c0, g.ldb, cols}, n);
+    if (n) t.run(rows, cols);
+    else t.zero();
+    O* out = static_cast<O*>(g.dw) + (int64_t(l) * g.M + m0) * g.N + c0;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      const int row = t.half * 128 + m * 16 + t.r16;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = t.wn * 64 + j * 16 + 4 * t.g;
+        if (row < rows && col < cols) {
+          O* p = out + int64_t(row) * g.N + col;
+          if constexpr (sizeof(O) == 2) {
+            *reinterpret_cast<uint2*>(p) =
+                make_uint2(pack_bf16x2(t.acc[m][j][0], t.acc[m][j][1]), pack_bf16x2(t.acc[m][j][2], t.acc[m][j][3]));
+          } else {
+            f32x4 v = t.acc[m][j];
+            if constexpr (ADD) v += *reinterpret_cast<const f32x4*>(p);
+            *reinterpret_cast<f32x4*>(p) = v;
+          }
+        }
+      }
+    }
+  }
+}
+
+static hipError_t set_big_lds() {
+  static std::atomic<uint64_t> done{0};
+  return once_per_device(done, [] {
+    const void* ks[] = {reinterpret_cast<const void*>(grouped_big_kernel<false>),
+                        reinterpret_cast<const void*>(grouped_big_kernel<true>),
+                        reinterpret_cast<const void*>(grouped_big_wgrad_kernel<uint16_t, false>),
+                        reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, false>),
+                        reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, true>)};
+    for (const void* k : ks) {
+      const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kBigLds);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  });
+}
+
 hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, const int32_t* offsets, void* y,
                           int32_t* status, int cus, hipStream_t st) {
   const GroupedArgs g{x, w, y, offsets, status, s.rows, s.ldx ? s.ldx : s.K, s.ldy ? s.ldy : s.N, s.groups, s.K, s.N};
@@ -193,6 +305,12 @@ hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, con
   if (s.dtype == MOE_F32) {
     if (s.w_layout) hipLaunchKernelGGL((grouped_small_kernel<float, true>), grid, threads, 0, st, g);
     else hipLaunchKernelGGL((grouped_small_kernel<float, false>), grid, threads, 0, st, g);
+  } else if (s.rows > int64_t(s.groups) * 64) {
+    const hipError_t e = set_big_lds();
+    if (e != hipSuccess) return e;
+    const dim3 big((cus / 8) * 8);
+    if (s.w_layout) hipLaunchKernelGGL(grouped_big_kernel<true>, big, dim3(kBigThreads), kBigLds, st, g);
+    else hipLaunchKernelGGL(grouped_big_kernel<false>, big, dim3(kBigThreads), kBigLds, st, g);
   } else {
     if (s.w_layout) hipLaunchKernelGGL((grouped_small_kernel<uint16_t, true>), grid, threads, 0, st, g);
     else hipLaunchKernelGGL((grouped_small_kernel<uint16_t, false>), grid, threads, 0, st, g);
@@ -209,11 +327,13 @@ hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* 
   if (s.dtype == MOE_F32) {
     if (accumulate) hipLaunchKernelGGL((grouped_small_wgrad_kernel<float, float, true>), grid, threads, 0, st, g);
     else hipLaunchKernelGGL((grouped_small_wgrad_kernel<float, float, false>), grid, threads, 0, st, g);
-  } else if (dw_dtype == MOE_F32) {
-    if (accumulate) hipLaunchKernelGGL((grouped_small_wgrad_kernel<uint16_t, float, true>), grid, threads, 0, st, g);
-    else hipLaunchKernelGGL((grouped_small_wgrad_kernel<uint16_t, float, false>), grid, threads, 0, st, g);
   } else {
-    hipLaunchKernelGGL((grouped_small_wgrad_kernel<uint16_t, uint16_t, false>), grid, threads, 0, st, g);
+    const hipError_t e = set_big_lds();
+    if (e != hipSuccess) return e;
+    const dim3 big((cus / 8) * 8), many(kBigThreads);
+    if (dw_dtype != MOE_F32) hipLaunchKernelGGL((grouped_big_wgrad_kernel<uint16_t, false>), big, many, kBigLds, st, g);
+    else if (accumulate) hipLaunchKernelGGL((grouped_big_wgrad_kernel<float, true>), big, many, kBigLds, st, g);
+    else hipLaunchKernelGGL((grouped_big_wgrad_kernel<float, false>), big, many, kBigLds, st, g);
   }
   return hipGetLastError();
 }
