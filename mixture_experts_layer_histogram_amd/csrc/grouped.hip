@@ -187,98 +187,140 @@ __global__ __launch_bounds__(256) void grouped_small_wgrad_kernel(WgradArgs g) {
   }
 }
 
-// 256 x 256 tiles in bf16 (grouped_tile.hpp): one workgroup a CU walks them.  The list of tiles is cut into eight contiguous
-// ranges, one for an XCD (workgroup w runs on XCD w mod 8), by group, then column tile, row tiles innermost: the CUs of
-// an XCD share one group's weight panels in their L2.
+// 256 x 256 tiles in bf16 (grouped_tile.hpp): the list of all tiles is cut into eight contiguous ranges, one for an XCD (workgroup w
+// runs on XCD w mod 8), by group, then as big_place says.  A workgroup takes every 32nd tile of its XCD's range, 64 at a
+// time: lane i of each wave looks up the i-th and keeps it.
+template <bool W_KN>
+struct BigProducts {
+  const GroupedArgs& g;
+  uint32_t what;                 // this lane's tile: group | (rows - 1) << 10 | column tile << 18
+  int32_t row0;
+  int n;
+
+  __device__ __forceinline__ uint32_t w_(int i) const { return uint32_t(__builtin_amdgcn_readlane(int(what), i)); }
+  __device__ __forceinline__ int count() const { return n; }
+  __device__ __forceinline__ int K(int) const { return g.K; }
+  __device__ __forceinline__ int rows(int i) const { return int((w_(i) >> 10) & 255) + 1; }
+  __device__ __forceinline__ int cols(int i) const { return min(kBig, g.N - int(w_(i) >> 18) * kBig); }
+  __device__ __forceinline__ BigOperand a(int i) const {
+    return BigOperand{static_cast<const uint16_t*>(g.x) + int64_t(__builtin_amdgcn_readlane(row0, i)) * g.ldx, g.ldx, rows(i)};
+  }
+  __device__ __forceinline__ BigOperand b(int i) const {
+    const int c0 = int(w_(i) >> 18) * kBig;
+    const uint16_t* w = static_cast<const uint16_t*>(g.w) + int64_t(w_(i) & 1023) * g.N * g.K;
+    return BigOperand{W_KN ? w + c0 : w + int64_t(c0) * g.K, W_KN ? g.N : g.K, cols(i)};
+  }
+  template <typename WALK>
+  __device__ __forceinline__ void store(int i, const WALK& walk) const {
+    big_store<uint16_t, false>(walk, static_cast<uint16_t*>(g.y) + int64_t(__builtin_amdgcn_readlane(row0, i)) * g.ldy +
+                               int(w_(i) >> 18) * kBig, g.ldy, rows(i), cols(i));
+  }
+};
+
 template <bool W_KN>
 __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_kernel(GroupedArgs g) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ int32_t base[kMaxGroups + 1], part[9];
-  bool bad;
-  const int mtiles = group_tiles<kBigThreads>(g.offsets, g.G, g.rows, 8, base, part, &bad);
-  if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
   const int NT = (g.N + kBig - 1) / kBig;
-  const int64_t total = int64_t(mtiles) * NT, per_xcd = (total + 7) >> 3;
-  const int xcd = blockIdx.x & 7, wg_per_xcd = gridDim.x >> 3;
-  for (int64_t tt = blockIdx.x >> 3; tt < per_xcd; tt += wg_per_xcd) {
-    const int64_t tau = xcd * per_xcd + tt;
-    if (tau >= total) break;
-    const int mtg = int(tau / NT);
-    const int l = find_expert(base, g.G, mtg);
-    const int mt0 = base[l], mtl = base[l + 1] - mt0;
-    const int i_in = int(tau - int64_t(mt0) * NT);
-    const int nt = i_in / mtl, mt = i_in - nt * mtl;
-    const int64_t row0 = g.offsets[l] + int64_t(mt) * kBig;
-    const int rows = int(min(int64_t(kBig), g.offsets[l + 1] - row0));
-    const int c0 = nt * kBig, cols = min(kBig, g.N - c0);
-    const uint16_t* w = static_cast<const uint16_t*>(g.w) + int64_t(l) * g.N * g.K;
-    BigTile<false, W_KN> t;
-    t.start(smem, BigOperand{static_cast<const uint16_t*>(g.x) + row0 * g.ldx, g.ldx, rows},
-            BigOperand{W_KN ? w + c0 : w + int64_t(c0) * g.K, W_KN ? g.N : g.K, cols}, g.K);
-    t.run(rows, cols);
-    uint16_t* out = static_cast<uint16_t*>(g.y) + row0 * g.ldy + c0;
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      const int row = t.half * 128 + m * 16 + t.r16;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int col = t.wn * 64 + n * 16 + 4 * t.g;
-        if (row < rows && col < cols)
-          *reinterpret_cast<uint2*>(out + row * g.ldy + col) =
-              make_uint2(pack_bf16x2(t.acc[m][n][0], t.acc[m][n][1]), pack_bf16x2(t.acc[m][n][2], t.acc[m][n][3]));
-      }
+  const int xcd = blockIdx.x & 7, wg_per_xcd = gridDim.x >> 3, lane = threadIdx.x & 63;
+  int32_t* base = reinterpret_cast<int32_t*>(smem);
+  int64_t per_xcd = int64_t(1) << 40;     // known after the first look at the offsets
+  for (int64_t t0 = blockIdx.x >> 3; t0 < per_xcd; t0 += 64 * int64_t(wg_per_xcd)) {
+    bool bad;
+    const int mtiles = group_tiles<kBigThreads>(g.offsets, g.G, g.rows, 8, base, base + kMaxGroups + 8, &bad);
+    if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
+    const int64_t total = int64_t(mtiles) * NT;
+    per_xcd = (total + 7) >> 3;
+    const int64_t tt = t0 + int64_t(lane) * wg_per_xcd, tau = xcd * per_xcd + tt;
+    BigProducts<W_KN> tiles{g, 0, 0, 0};
+    const bool mine = tt < per_xcd && tau < total;
+    if (mine) {
+      const int l = find_expert(base, g.G, int(tau / NT));
+      int mt, nt;
+      big_place(tau - int64_t(base[l]) * NT, base[l + 1] - base[l], NT, &mt, &nt);
+      tiles.row0 = g.offsets[l] + mt * kBig;
+      tiles.what = uint32_t(l) | uint32_t(min(kBig, g.offsets[l + 1] - tiles.row0) - 1) << 10 | uint32_t(nt) << 18;
     }
+    tiles.n = __popcll(__ballot(mine));
+    __syncthreads();                      // the tables' LDS becomes the ring's
+    BigWalk<false, W_KN, BigProducts<W_KN>> walk(tiles, smem);
+    walk.run();
+    __syncthreads();
   }
 }
 
 // The same for the gradient by the weights: a tile of 256 x 256 of one group's gradient sums over the group's rows.
 template <typename O, bool ADD>
+struct BigGradients {
+  const WgradArgs& g;
+  uint32_t gm;                   // this lane's tile: group | row tile << 10
+  int nt, n;
+
+  __device__ __forceinline__ int group(int i) const { return __builtin_amdgcn_readlane(int(gm), i) & 1023; }
+  __device__ __forceinline__ int m0(int i) const { return int(uint32_t(__builtin_amdgcn_readlane(int(gm), i)) >> 10) * kBig; }
+  __device__ __forceinline__ int c0(int i) const { return __builtin_amdgcn_readlane(nt, i) * kBig; }
+  __device__ __forceinline__ int count() const { return n; }
+  __device__ __forceinline__ int K(int i) const {
+    const int l = group(i);
+    return __builtin_amdgcn_readfirstlane(g.offsets[l + 1] - g.offsets[l]);
+  }
+  __device__ __forceinline__ int rows(int i) const { return min(kBig, g.M - m0(i)); }
+  __device__ __forceinline__ int cols(int i) const { return min(kBig, g.N - c0(i)); }
+  __device__ __forceinline__ BigOperand a(int i) const {
+    return BigOperand{static_cast<const uint16_t*>(g.a) + int64_t(g.offsets[group(i)]) * g.lda + m0(i), g.lda, rows(i)};
+  }
+  __device__ __forceinline__ BigOperand b(int i) const {
+    return BigOperand{static_cast<const uint16_t*>(g.b) + int64_t(g.offsets[group(i)]) * g.ldb + c0(i), g.ldb, cols(i)};
+  }
+  template <typename WALK>
+  __device__ __forceinline__ void store(int i, const WALK& walk) const {
+    big_store<O, ADD>(walk, static_cast<O*>(g.dw) + (int64_t(group(i)) * g.M + m0(i)) * g.N + c0(i), g.N, rows(i), cols(i));
+  }
+};
+
+template <typename O, bool ADD>
 __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_wgrad_kernel(WgradArgs g) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ int32_t base[kMaxGroups + 1], part[9];
+  int32_t* base = reinterpret_cast<int32_t*>(smem);
   bool bad;
-  group_tiles<kBigThreads>(g.offsets, g.G, g.rows, 8, base, part, &bad);
+  group_tiles<kBigThreads>(g.offsets, g.G, g.rows, 8, base, base + kMaxGroups + 8, &bad);
   if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
   if (bad) return;
+  __syncthreads();
   const int MT = (g.M + kBig - 1) / kBig, NT = (g.N + kBig - 1) / kBig;
   const int64_t total = int64_t(g.G) * MT * NT, per_xcd = (total + 7) >> 3;
-  const int xcd = blockIdx.x & 7, wg_per_xcd = gridDim.x >> 3;
-  for (int64_t tt = blockIdx.x >> 3; tt < per_xcd; tt += wg_per_xcd) {
-    const int64_t tau = xcd * per_xcd + tt;
-    if (tau >= total) break;
-    const int l = int(tau / (int64_t(MT) * NT));
-    const int rem = int(tau - int64_t(l) * MT * NT);
-    const int nt = rem / MT, mt = rem - nt * MT;
-    const int m0 = mt * kBig, c0 = nt * kBig;
-    const int rows = min(kBig, g.M - m0), cols = min(kBig, g.N - c0);
-    const int64_t r0 = g.offsets[l];
-    const int n = int(g.offsets[l + 1] - r0);
-    if (ADD && n == 0) continue;
-    BigTile<true, true> t;
-    t.start(smem, BigOperand{static_cast<const uint16_t*>(g.a) + r0 * g.lda + m0, g.lda, rows},
-            BigOperand{static_cast<const uint16_t*>(g.b) + r0 * g.ldb + c0, g.ldb, cols}, n);
-    if (n) t.run(rows, cols);
-    else t.zero();
-    O* out = static_cast<O*>(g.dw) + (int64_t(l) * g.M + m0) * g.N + c0;
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      const int row = t.half * 128 + m * 16 + t.r16;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col = t.wn * 64 + j * 16 + 4 * t.g;
-        if (row < rows && col < cols) {
-          O* p = out + int64_t(row) * g.N + col;
-          if constexpr (sizeof(O) == 2) {
-            *reinterpret_cast<uint2*>(p) =
-                make_uint2(pack_bf16x2(t.acc[m][j][0], t.acc[m][j][1]), pack_bf16x2(t.acc[m][j][2], t.acc[m][j][3]));
-          } else {
-            f32x4 v = t.acc[m][j];
-            if constexpr (ADD) v += *reinterpret_cast<const f32x4*>(p);
-            *reinterpret_cast<f32x4*>(p) = v;
-          }
+  const int xcd = blockIdx.x & 7, wg_per_xcd = gridDim.x >> 3, lane = threadIdx.x & 63;
+  for (int64_t t0 = blockIdx.x >> 3; t0 < per_xcd; t0 += 64 * int64_t(wg_per_xcd)) {
+    const int64_t tt = t0 + int64_t(lane) * wg_per_xcd, tau = xcd * per_xcd + tt;
+    const bool mine = tt < per_xcd && tau < total;
+    int l = 0, mt = 0, nt = 0, rows = 0;
+    if (mine) {
+      l = int(tau / (int64_t(MT) * NT));
+      big_place(tau - int64_t(l) * MT * NT, MT, NT, &mt, &nt);
+      rows = g.offsets[l + 1] - g.offsets[l];
+    }
+    const uint64_t full = __ballot(mine && rows > 0), empty = __ballot(mine && rows == 0);
+    // tiles of groups with rows first in the lanes' order, the others behind them get zeros
+    const uint64_t below = (uint64_t(1) << lane) - 1;
+    const int to = rows > 0 ? __popcll(full & below) : mine ? __popcll(full) + __popcll(empty & below) : 63;
+    BigGradients<O, ADD> tiles{g, 0, 0, int(__popcll(full))};
+    if (full | empty) {
+      tiles.gm = uint32_t(__builtin_amdgcn_ds_permute(to * 4, mine ? int(uint32_t(l) | uint32_t(mt) << 10) : 0));
+      tiles.nt = __builtin_amdgcn_ds_permute(to * 4, nt);
+    }
+    if constexpr (!ADD) {
+      for (int i = tiles.n; i < tiles.n + int(__popcll(empty)); ++i) {
+        O* out = static_cast<O*>(g.dw) + (int64_t(tiles.group(i)) * g.M + tiles.m0(i)) * g.N + tiles.c0(i);
+        constexpr int V = 16 / sizeof(O);
+        for (int v = threadIdx.x; v < kBig * (kBig / V); v += kBigThreads) {
+          const int row = v / (kBig / V), col = v % (kBig / V) * V;
+          if (row < tiles.rows(i) && col < tiles.cols(i))
+            *reinterpret_cast<u32x4*>(out + int64_t(row) * g.N + col) = u32x4{0, 0, 0, 0};
         }
       }
     }
+    BigWalk<true, true, BigGradients<O, ADD>> walk(tiles, smem);
+    walk.run();
+    __syncthreads();
   }
 }
 

@@ -27,7 +27,9 @@ __device__ __forceinline__ int group_tiles(const int32_t* __restrict__ offsets, 
     }
     sum += n[i];
   }
-  wrong = __syncthreads_or(wrong);
+  if (tid == 0) part[THREADS / 64] = 0;
+  __syncthreads();
+  if (wrong) part[THREADS / 64] = 1;
   int upto = sum;                                   // inclusive over the wave
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -36,6 +38,7 @@ __device__ __forceinline__ int group_tiles(const int32_t* __restrict__ offsets, 
   }
   if (lane == 63) part[wave] = upto;
   __syncthreads();
+  wrong = part[THREADS / 64];
   int before = upto - sum, total = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 64; ++w) {

@@ -1,18 +1,25 @@
-// One 256 x 256 tile of C = A B^T on gfx950 (v_mfma_f32_16x16x32_bf16), A and B each stored with K contiguous or with the
-// row index contiguous.
+// 256 x 256 tiles of C = A B^T on gfx950 (v_mfma_f32_16x16x32_bf16), A and B each stored with K contiguous or with the row
+// index contiguous; one workgroup a CU walks a list of tiles without ever letting its loads run dry.
 //
 // 8 waves as 2 (rows) x 4 (columns), each with 128 x 64 outputs: 8 x 4 blocks of 16 x 16 in 128 accumulators.  K goes by
-// steps of 64 through two LDS stages of 64 KiB, filled by direct global->LDS loads.  The waves of the upper and of the
-// lower half of the tile share SIMDs in pairs (w and w + 4) and take turns, half a step (32 of K) at a time: while one
-// reads its fragments from LDS, the other has the matrix unit, and a barrier ends every turn.  So neither waits for its own
-// reads, and a fill has four turns (about 2000 cycles) to land.
+// steps of 64.  The waves of the upper and of the lower half of the tile share SIMDs in pairs (w and w + 4) and take
+// turns, half a step (32 of K) at a time: while one reads its fragments from LDS, the other has the matrix unit, and a
+// barrier ends every turn (turns are about 512 cycles: 32 MFMAs of 16).
 //
 //   turn        4k          4k + 1      4k + 2      4k + 3      4k + 4
 //   half 0   reads k.0     MFMA k.0    reads k.1   MFMA k.1    reads (k+1).0
 //   half 1   MFMA (k-1).1  reads k.0   MFMA k.0    reads k.1   MFMA k.1
 //
-// Both halves fill stage k + 1 in turn 4k (its last readers were half 1 in turn 4k - 1), and both wait for their fills before
-// the barrier that ends turn 4k + 3.
+// A step's operands are two panels of 32 KiB, and a CU's 160 KiB of LDS hold five: a ring A0 B0 A1 B1 A2 | B2 ...,
+// filled by direct global->LDS loads, two of them a wave and turn.  In step k the places of A and B of step k - 1 take B of
+// step k + 1 (in the first two turns; it has the other two to land) and A of step k + 2 (in the last two).  What this
+// is about: a CU takes in one 1 KiB load in 16 to 23 cycles, 64 of them a step of 2048, and a wave that finds
+// the queue full waits at its issue, MFMAs and all.  8192^3 (rows and columns of K contiguous): two stages of 64 KiB with eight
+// loads at once at a step's start 971 us, spread over three turns 869, the ring of five with two a turn 657 (1674 TFLOP/s; a
+// library's product of that size 670).
+//
+// The loads know nothing of tiles: a cursor for A (two steps ahead) and one for B (one step) walk the list by
+// themselves, so the next tile's first panels land while this one's last products and its stores are on their way.
 #pragma once
 
 #include "gemm_tile.hpp"
@@ -24,10 +31,10 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4_ptr;
 
 constexpr int kBig = 256, kBigBK = 64;
-constexpr int kBigPanel = kBig * kBigBK * 2;          // bytes of one operand's stage
-constexpr int kBigStage = 2 * kBigPanel;
-constexpr int kBigLds = 2 * kBigStage;
+constexpr int kBigPanel = kBig * kBigBK * 2;          // bytes of one operand's step
+constexpr int kBigLds = 5 * kBigPanel;                // all of a CU's LDS
 constexpr int kBigThreads = 512;
+constexpr int kBigBand = 8;                           // row tiles whose column tiles are walked together
 
 // K contiguous: element (r, k) at p + r * ld + k.  Otherwise at p + k * ld + r.  rows: valid ones of the tile (of the row index
 // contiguous: a multiple of 8).
@@ -37,145 +44,158 @@ struct BigOperand {
   int rows;
 };
 
-// The LDS place of 16-byte chunk c of K row k where the row index is contiguous (512 bytes a K row): the eight K rows that half a
-// wave reads at once lie in eight different 32-byte slots of the 64 banks.
+// Tile i of mt x nt: bands of at most kBigBand row tiles (even ones), in a band by column tile, row tiles innermost.  The 32 CUs
+// of an XCD then work on about 8 row and 4 column panels at a time, which its L2 gives 64 times (hit rate 81 %; row tiles
+// innermost over all of 8192 rows 50 %).
+__device__ __forceinline__ void big_place(int64_t i, int mt, int nt, int* m, int* n) {
+  const int bands = (mt + kBigBand - 1) / kBigBand, per = (mt + bands - 1) / bands;
+  const int band = int(i / (int64_t(per) * nt));
+  const int in = int(i - int64_t(band) * per * nt), high = min(per, mt - band * per);
+  *n = in / high;
+  *m = band * per + in - *n * high;
+}
+
+// The LDS place of 16-byte chunk c of K row k where the row index is contiguous (512 bytes a K row) is c ^ this: the eight K rows
+// that half a wave reads at once lie in eight different 32-byte slots of the 64 banks.
 __device__ __forceinline__ int big_mn_swz(int k) { return 2 * ((k & 3) | (((k >> 3) & 1) << 2)); }
 
-#define MOE_VMCNT0() __builtin_amdgcn_s_waitcnt(0x0F70)          // vmcnt(0), the others at their largest
+#define MOE_VMCNT0() __builtin_amdgcn_s_waitcnt(0x0F70)          // vmcnt(0), the other counters at their largest
+#define MOE_VMCNT4() __builtin_amdgcn_s_waitcnt(0x0F74)
 #define MOE_LGKM0() __builtin_amdgcn_s_waitcnt(0xC07F)           // lgkmcnt(0)
 
-template <bool A_MN, bool B_MN>
-struct BigTile {
-  // lane and wave
-  int lane, wave, half, wn, r16, g;
-  uint32_t a_off[4], b_off[4];              // byte offsets of this lane's fills
-  int a_k[4], b_k[4];                       // K of them within a step
-  uint32_t lds_fill;                        // LDS address of this wave's first fill
-  uint32_t a_rd[A_MN ? 8 : 2], b_rd[B_MN ? 4 : 2];
-  const char* abase;
-  const char* bbase;
-  int64_t lda, ldb;
-  int K;
-  bf16x8 fa[8], fb[4];
-  f32x4 acc[8][4];
+// This lane's four fills of a panel
+template <bool MN>
+struct BigFill {
+  const char* p;              // the first value of the cursor's step (K contiguous), or its first K row; the same in every lane
+  int64_t ld;
+  uint32_t off[MN ? 2 : 4];   // byte offsets from it (the third and fourth fill of MN lie 4 K rows behind the first and second)
+  int kb;                     // K of the first fill within a step
+  int tile, left;             // the cursor's tile, and K from its step on
 
-  template <bool MN>
-  __device__ __forceinline__ void fill_offsets(const BigOperand& o, uint32_t* off, int* kk) {
+  __device__ __forceinline__ void at(int wave, int lane, const BigOperand& o, int K) {
+    p = reinterpret_cast<const char*>(wave_uniform(o.p));
+    ld = o.ld;
+    left = K;
+    if constexpr (!MN) {
+      kb = ((lane & 7) ^ (lane >> 4)) * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (!MN) {
-        const int row = (wave * 4 + i) * 8 + (lane >> 3);
-        const int ch = (lane & 7) ^ ((row >> 1) & 7);
-        kk[i] = ch * 8;
-        off[i] = (uint32_t(min(row, o.rows - 1)) * uint32_t(o.ld) + uint32_t(ch * 8)) * 2u;
-      } else {
-        const int k = 8 * wave + 2 * i + (lane >> 5);
-        const int ch = (lane & 31) ^ big_mn_swz(k);
-        kk[i] = k;
-        off[i] = uint32_t(min(ch * 8, o.rows - 8)) * 2u;
-      }
+      for (int i = 0; i < 4; ++i)
+        off[i] = (uint32_t(min((wave * 4 + i) * 8 + (lane >> 3), o.rows - 1)) * uint32_t(ld) + uint32_t(kb ^ ((i & 1) * 32))) * 2u;
+    } else {
+      kb = 8 * wave + (lane >> 5);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        off[i] = (uint32_t(kb + 2 * i) * uint32_t(ld) + uint32_t(min(((lane & 31) ^ big_mn_swz(kb + 2 * i)) * 8, o.rows - 8))) * 2u;
     }
   }
+  // past K: the row's last values, or the last K row, again (zeroed on their way to the products)
+  template <int I>
+  __device__ __forceinline__ void fill(uint32_t lds) const {
+    const lds_void_ptr to = (lds_void_ptr)(uintptr_t)(lds + uint32_t(I * 1024));
+    if constexpr (!MN) {
+      uint32_t o = off[I];
+      if (left < kBigBK) o -= 2u * uint32_t(max(0, (kb ^ ((I & 1) * 32)) - (left - 8)));
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(p + o), to, 16, 0, 0);
+    } else {
+      const char* q = p + (I >> 1) * 8 * ld;
+      uint32_t o = off[I & 1];
+      if (left < kBigBK) {                    // (the offset from p itself, which may be the last row)
+        q = p;
+        o += uint32_t((I >> 1) * 4 - max(0, kb + 2 * I - (left - 1))) * uint32_t(ld) * 2u;
+      }
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(q + o), to, 16, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void step() {
+    p += MN ? ld * (kBigBK * 2) : int64_t(kBigBK * 2);
+    left -= kBigBK;
+  }
+};
 
-  __device__ __forceinline__ void start(char* smem, const BigOperand& A, const BigOperand& B, int K_) {
+// TILES: int count(); K of tile i; its operands a(i) and b(i); rows(i), cols(i) of its output; store(i, walk).
+template <bool A_MN, bool B_MN, typename TILES>
+struct BigWalk {
+  TILES& tiles;
+  int lane, wave, half, wn, r16, g, n_tiles;
+  uint32_t lds_fill;                        // LDS address of this wave's first fill of a panel
+  uint32_t l0, a_rd[A_MN ? 1 : 2], b_rd[B_MN ? 1 : 2];
+  uint32_t pa;                              // the ring's place of A of the step at work
+  BigFill<A_MN> fa_;
+  BigFill<B_MN> fb_;
+  bf16x8 fa[8], fb[4];
+  f32x4 acc[8][4];                          // lane: row half * 128 + m * 16 + r16, columns wn * 64 + n * 16 + 4 g + 0..3
+
+  __device__ __forceinline__ BigWalk(TILES& t, char* smem) : tiles(t) {
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     half = wave >> 2;
     wn = wave & 3;
     r16 = lane & 15;
     g = lane >> 4;
-    K = K_;
-    lda = A.ld;
-    ldb = B.ld;
-    abase = reinterpret_cast<const char*>(wave_uniform(A.p));
-    bbase = reinterpret_cast<const char*>(wave_uniform(B.p));
-    fill_offsets<A_MN>(A, a_off, a_k);
-    fill_offsets<B_MN>(B, b_off, b_k);
-    lds_fill = __builtin_amdgcn_readfirstlane(lds_addr(smem + wave * 4 * 1024));
-    const uint32_t l0 = lds_addr(smem);
+    l0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+    lds_fill = l0 + wave * 4096;
+    pa = 0;
+    // transposing reads: lane 4 c + a of 16 addresses K row c, columns 4 a .. 4 a + 3, and gets four K values of column 4 c + a
+    const int a = r16 & 3, k = 8 * g + (r16 >> 2);
     if constexpr (!A_MN) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) a_rd[h] = l0 + (half * 128 + r16) * 128 + (((h * 4 + g) ^ ((r16 >> 1) & 7)) << 4);
     } else {
-      const int a = r16 & 3, c = r16 >> 2, k = 8 * g + c;
-      const uint32_t b0 = k * 512 + half * 256 + (((a >> 1) ^ big_mn_swz(k)) << 4) + (a & 1) * 8;
-#pragma unroll
-      for (int m = 0; m < 8; ++m) a_rd[m] = l0 + (b0 ^ (m << 5));
+      a_rd[0] = k * 512 + half * 256 + (((a >> 1) ^ big_mn_swz(k)) << 4) + (a & 1) * 8;
     }
     if constexpr (!B_MN) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        b_rd[h] = l0 + kBigPanel + (wn * 64 + r16) * 128 + (((h * 4 + g) ^ ((r16 >> 1) & 7)) << 4);
+      for (int h = 0; h < 2; ++h) b_rd[h] = l0 + (wn * 64 + r16) * 128 + (((h * 4 + g) ^ ((r16 >> 1) & 7)) << 4);
     } else {
-      const int a = r16 & 3, c = r16 >> 2, k = 8 * g + c;
-      const uint32_t b0 = kBigPanel + k * 512 + (wn >> 1) * 256 + ((((wn & 1) * 8 + (a >> 1)) ^ big_mn_swz(k)) << 4) + (a & 1) * 8;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) b_rd[n] = l0 + (b0 ^ (n << 5));
+      b_rd[0] = k * 512 + (wn >> 1) * 256 + (((wn & 1) * 8 + (a >> 1)) ^ big_mn_swz(k)) * 16 + (a & 1) * 8;
     }
   }
 
-  // fills of step ks
-  __device__ __forceinline__ void issue(int ks) {
-    const uint32_t da = lds_fill + uint32_t((ks & 1) * kBigStage), db = da + uint32_t(kBigPanel);
-    const int k0 = ks * kBigBK;
-    const bool tail = k0 + kBigBK > K;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      fill_one<A_MN>(abase, lda, a_off[i], a_k[i], k0, tail, da + uint32_t(i * 1024));
-      fill_one<B_MN>(bbase, ldb, b_off[i], b_k[i], k0, tail, db + uint32_t(i * 1024));
-    }
-  }
-  template <bool MN>
-  __device__ __forceinline__ void fill_one(const char* base, int64_t ld, uint32_t off, int kk, int k0, bool tail, uint32_t lds) {
-    const lds_void_ptr to = (lds_void_ptr)(uintptr_t)lds;
-    if constexpr (!MN) {
-      uint32_t o = off;
-      if (tail) o -= 2u * uint32_t(max(0, k0 + kk - (K - 8)));          // past K: the row's last values again, masked later
-      __builtin_amdgcn_global_load_lds(static_cast<const void*>(base + int64_t(k0) * 2 + o), to, 16, 0, 0);
-    } else {
-      const int k = tail ? min(kk, K - 1 - k0) : kk;
-      __builtin_amdgcn_global_load_lds(static_cast<const void*>(base + int64_t(k0) * ld * 2 + (uint32_t(k) * uint32_t(ld) * 2u + off)),
-                                       to, 16, 0, 0);
-    }
-  }
-
-  // fragments of half a step (32 of K) from LDS, all landed at the end
-  template <int MV>
-  __device__ __forceinline__ void read(int ks, int h, int klim) {
-    const uint32_t st = uint32_t((ks & 1) * kBigStage);
-    if constexpr (!A_MN) {
-      const uint32_t p = a_rd[h] + st;
-      if constexpr (MV > 4)
-        asm volatile("ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:2048\n\tds_read_b128 %2, %8 offset:4096\n\t"
-                     "ds_read_b128 %3, %8 offset:6144\n\tds_read_b128 %4, %8 offset:8192\n\tds_read_b128 %5, %8 offset:10240\n\t"
-                     "ds_read_b128 %6, %8 offset:12288\n\tds_read_b128 %7, %8 offset:14336\n\ts_waitcnt lgkmcnt(0)"
-                     : "=&v"(fa[0]), "=&v"(fa[1]), "=&v"(fa[2]), "=&v"(fa[3]), "=&v"(fa[4]), "=&v"(fa[5]), "=&v"(fa[6]), "=&v"(fa[7])
-                     : "v"(p) : "memory");
-      else if constexpr (MV > 0)
-        asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:2048\n\tds_read_b128 %2, %4 offset:4096\n\t"
-                     "ds_read_b128 %3, %4 offset:6144\n\ts_waitcnt lgkmcnt(0)"
-                     : "=&v"(fa[0]), "=&v"(fa[1]), "=&v"(fa[2]), "=&v"(fa[3]) : "v"(p) : "memory");
-    } else if constexpr (MV > 0) {
-#pragma unroll
-      for (int m = 0; m < MV; ++m) fa[m] = read_tr(a_rd[m] + st + h * 16384);
-    }
-    if constexpr (MV > 0) {
-      if constexpr (!B_MN) {
-        const uint32_t p = b_rd[h] + st;
-        asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:2048\n\tds_read_b128 %2, %4 offset:4096\n\t"
-                     "ds_read_b128 %3, %4 offset:6144\n\ts_waitcnt lgkmcnt(0)"
-                     : "=&v"(fb[0]), "=&v"(fb[1]), "=&v"(fb[2]), "=&v"(fb[3]) : "v"(p) : "memory");
+  // ---- the cursors
+  __device__ __forceinline__ bool on_a() const { return fa_.tile < n_tiles; }
+  __device__ __forceinline__ bool on_b() const { return fb_.tile < n_tiles; }
+  template <bool A, int I>
+  __device__ __forceinline__ void fill(uint32_t place) {
+    if constexpr (A) fa_.template fill<I>(lds_fill + place);
+    else fb_.template fill<I>(lds_fill + place);
+    if constexpr (I == 3) {
+      if constexpr (A) {
+        fa_.step();
+        if (fa_.left <= 0 && ++fa_.tile < n_tiles) fa_.at(wave, lane, tiles.a(fa_.tile), tiles.K(fa_.tile));
       } else {
-#pragma unroll
-        for (int n = 0; n < 4; ++n) fb[n] = read_tr(b_rd[n] + st + h * 16384);
-      }
-      if (klim < h * 32 + 32) {                       // the last step: zeros past K, in both (a NaN there must not count)
-#pragma unroll
-        for (int m = 0; m < MV; ++m) fa[m] = mask(fa[m], klim - h * 32 - 8 * g);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) fb[n] = mask(fb[n], klim - h * 32 - 8 * g);
+        fb_.step();
+        if (fb_.left <= 0 && ++fb_.tile < n_tiles) fb_.at(wave, lane, tiles.b(fb_.tile), tiles.K(fb_.tile));
       }
     }
+  }
+  template <bool A, int I>
+  __device__ __forceinline__ void fill2(uint32_t place) {
+    fill<A, I>(place);
+    fill<A, I + 1>(place);
+  }
+
+  // ---- half a step's fragments from LDS, all landed at the end
+  template <int MV>
+  __device__ __forceinline__ void read(uint32_t pb, int h, int left) {
+    if constexpr (MV > 0) {
+#pragma unroll
+      for (int m = 0; m < MV; ++m) {
+        if constexpr (A_MN) fa[m] = read_tr((a_rd[0] ^ (m << 5)) + (l0 + pa) + h * 16384);       // block m: 32 bytes on, swizzled
+        else fa[m] = *(const __attribute__((address_space(3))) bf16x8*)(uintptr_t)(a_rd[h] + pa + m * 2048);
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        if constexpr (B_MN) fb[n] = read_tr((b_rd[0] ^ (n << 5)) + (l0 + pb) + h * 16384);
+        else fb[n] = *(const __attribute__((address_space(3))) bf16x8*)(uintptr_t)(b_rd[h] + pb + n * 2048);
+      }
+      if (left < h * 32 + 32) {                       // the last step: zeros past K, in both (a NaN there must not count)
+#pragma unroll
+        for (int m = 0; m < MV; ++m) fa[m] = mask(fa[m], left - h * 32 - 8 * g);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) fb[n] = mask(fb[n], left - h * 32 - 8 * g);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
   __device__ static __forceinline__ bf16x8 read_tr(uint32_t p) {
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(uintptr_t)p);
@@ -190,13 +210,25 @@ struct BigTile {
     return __builtin_bit_cast(bf16x8, v);
   }
 
-  template <int MV>
-  __device__ __forceinline__ void mfma() {
+  // ---- half a step's products, with two fills between them.  The weights' (columns') fragment comes first, so that a lane ends up
+  // with four consecutive columns of one row.
+  template <int MV, bool A, int I>
+  __device__ __forceinline__ void mfma(uint32_t place, bool on) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int m = 0; m < MV; ++m)
+    for (int m = 0; m < MV; ++m) {
 #pragma unroll
       for (int n = 0; n < 4; ++n) acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[n], fa[m], acc[m][n], 0, 0, 0);
+      if (m == 0 || m == 3) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (on) {
+          if (m == 0) fill<A, I>(place);
+          else fill<A, I + 1>(place);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (MV == 0 && on) fill2<A, I>(place);
     __builtin_amdgcn_s_setprio(0);
   }
   __device__ static __forceinline__ void turn() {
@@ -206,53 +238,126 @@ struct BigTile {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
   }
-
-  template <int MV>
-  __device__ __forceinline__ void loop(int nk) {
-    for (int ks = 0; ks < nk; ++ks) {
-      const int klim = K - ks * kBigBK;
-      if (half == 0 && ks + 1 < nk) issue(ks + 1);
-      read<MV>(ks, 0, klim);
-      MOE_LGKM0();
-      turn();
-      mfma<MV>();
-      turn();
-      read<MV>(ks, 1, klim);
-      MOE_LGKM0();
-      if (half == 1) MOE_VMCNT0();
-      turn();
-      if (half == 1 && ks + 2 < nk) issue(ks + 2);
-      mfma<MV>();
-      if (half == 0) MOE_VMCNT0();
-      turn();
-    }
+  static __device__ __forceinline__ uint32_t next(uint32_t p, int by) {       // `by` places on in the ring
+    p += uint32_t(by * kBigPanel);
+    return p >= uint32_t(kBigLds) ? p - uint32_t(kBigLds) : p;
   }
 
-  __device__ __forceinline__ void zero() {
+  // ---- the steps of one tile
+  template <int MV, int HALF>
+  __device__ __forceinline__ void steps(int K) {
+    for (int left = K; left > 0; left -= kBigBK) {
+      const uint32_t pb = next(pa, 1), pb1 = next(pa, 3), pa2 = next(pa, 4);
+      read<MV>(pb, 0, left);
+      const bool b = on_b();
+      if (b) fill2<false, HALF == 0 ? 0 : 2>(pb1);
+      MOE_LGKM0();
+      turn();
+      const bool a = on_a();
+      if constexpr (HALF == 0) mfma<MV, false, 2>(pb1, b);
+      else mfma<MV, true, 0>(pa2, a);
+      turn();
+      read<MV>(pb, 1, left);
+      if (a) fill2<true, HALF == 0 ? 0 : 2>(pa2);
+      MOE_LGKM0();
+      if constexpr (HALF == 1) {                       // B of the next step has landed: all but this step's four fills of A
+        if (a) MOE_VMCNT4();
+        else MOE_VMCNT0();
+      }
+      turn();
+      if constexpr (HALF == 0) {
+        mfma<MV, true, 2>(pa2, a);
+        if (a) MOE_VMCNT4();
+        else MOE_VMCNT0();
+      } else {
+        mfma<MV, false, 0>(pa, on_b());                // B of the step after next comes where A of this one lay
+      }
+      turn();
+      pa = next(pa, 2);
+    }
+  }
+  template <int HALF>
+  __device__ __forceinline__ void tile(int i) {
 #pragma unroll
     for (int m = 0; m < 8; ++m)
 #pragma unroll
       for (int n = 0; n < 4; ++n) acc[m][n] = f32x4{0, 0, 0, 0};
+    // 16-row blocks of this wave that hold any of the tile's rows (and columns): the others' products are left out
+    const int mv = wn * 64 >= tiles.cols(i) ? 0 : (tiles.rows(i) - HALF * 128 + 15) >> 4;
+    const int K = tiles.K(i);
+    if (mv > 4) steps<8, HALF>(K);
+    else if (mv > 0) steps<4, HALF>(K);
+    else steps<0, HALF>(K);
+    if (mv > 0) tiles.store(i, *this);
   }
 
-  // The sums of the tile in acc: lane holds row half * 128 + m * 16 + r16, columns wn * 64 + n * 16 + 4 g + 0..3.  Ends on a barrier.
-  __device__ __forceinline__ void run(int rows, int cols) {
-    const int nk = (K + kBigBK - 1) / kBigBK;
-    zero();
-    issue(0);
-    MOE_VMCNT0();
-    turn();
-    if (half == 1) {
-      if (nk > 1) issue(1);
-      turn();
+  // The whole list, every tile with K > 0.  LDS is free before and after.
+  __device__ __forceinline__ void run() {
+    n_tiles = tiles.count();
+    if (n_tiles == 0) return;
+    fa_.tile = fb_.tile = 0;
+    fa_.at(wave, lane, tiles.a(0), tiles.K(0));
+    fb_.at(wave, lane, tiles.b(0), tiles.K(0));
+    fill2<true, 0>(pa);
+    fill2<true, 2>(pa);
+    fill2<false, 0>(next(pa, 1));
+    fill2<false, 2>(next(pa, 1));
+    if (on_a()) {
+      fill2<true, 0>(next(pa, 2));
+      fill2<true, 2>(next(pa, 2));
+      MOE_VMCNT4();
+    } else {
+      MOE_VMCNT0();
     }
-    // 16-row blocks of this wave that hold any of the tile's rows (and columns): the others' products are left out
-    const int mv = wn * 64 >= cols ? 0 : (rows - half * 128 + 15) >> 4;
-    if (mv > 4) loop<8>(nk);
-    else if (mv > 0) loop<4>(nk);
-    else loop<0>(nk);
-    if (half == 0) turn();
+    turn();
+    if (half == 0) {
+      for (int i = 0; i < n_tiles; ++i) tile<0>(i);
+      turn();
+    } else {
+      if (on_b()) fill2<false, 0>(next(pa, 3));
+      turn();
+      for (int i = 0; i < n_tiles; ++i) tile<1>(i);
+    }
   }
 };
+
+// Output rows of a tile from the accumulators: bf16 in 16-byte vectors (two 16-column blocks exchange halves between lane groups, so
+// that a lane has eight consecutive columns), fp32 in 16-byte vectors, added to what is there with ADD.
+template <typename O, bool ADD, typename WALK>
+__device__ __forceinline__ void big_store(const WALK& w, O* out, int64_t ld, int rows, int cols) {
+  int lane = w.lane;
+  asm volatile("" : "+v"(lane));            // the compiler would keep these indices in registers all along the products
+  const int r16 = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int m = 0; m < 8; ++m) {
+    const int row = w.half * 128 + m * 16 + r16;
+    if (row >= rows) continue;
+    O* p = out + row * ld;
+    if constexpr (sizeof(O) == 2) {
+#pragma unroll
+      for (int n = 0; n < 4; n += 2) {
+        u32x4 v;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const auto s = __builtin_amdgcn_permlane16_swap(pack_bf16x2(w.acc[m][n][2 * j], w.acc[m][n][2 * j + 1]),
+                                                          pack_bf16x2(w.acc[m][n + 1][2 * j], w.acc[m][n + 1][2 * j + 1]), false, false);
+          v[j] = s[0];
+          v[2 + j] = s[1];
+        }
+        const int col = w.wn * 64 + (n + (g & 1)) * 16 + (g >> 1) * 8;
+        if (col < cols) *reinterpret_cast<u32x4*>(p + col) = v;
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int col = w.wn * 64 + n * 16 + 4 * g;
+        if (col >= cols) continue;
+        f32x4 v = w.acc[m][n];
+        if constexpr (ADD) v += *reinterpret_cast<const f32x4*>(p + col);
+        *reinterpret_cast<f32x4*>(p + col) = v;
+      }
+    }
+  }
+}
 
 }  // namespace moe
