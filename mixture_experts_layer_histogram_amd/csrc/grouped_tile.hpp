@@ -68,7 +68,7 @@ template <bool MN>
 struct BigFill {
   const char* p;              // the first value of the cursor's step (K contiguous), or its first K row; the same in every lane
   int64_t ld;
-  uint32_t off[MN ? 2 : 4];   // byte offsets from it (the third and fourth fill of MN lie 4 K rows behind the first and second)
+  uint32_t off[4];            // byte offsets from it
   int kb;                     // K of the first fill within a step
   int tile, left;             // the cursor's tile, and K from its step on
 
@@ -84,31 +84,29 @@ struct BigFill {
     } else {
       kb = 8 * wave + (lane >> 5);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 4; ++i)
         off[i] = (uint32_t(kb + 2 * i) * uint32_t(ld) + uint32_t(min(((lane & 31) ^ big_mn_swz(kb + 2 * i)) * 8, o.rows - 8))) * 2u;
     }
+    if (K < kBigBK) cut();
   }
-  // past K: the row's last values, or the last K row, again (zeroed on their way to the products)
   template <int I>
   __device__ __forceinline__ void fill(uint32_t lds) const {
     const lds_void_ptr to = (lds_void_ptr)(uintptr_t)(lds + uint32_t(I * 1024));
-    if constexpr (!MN) {
-      uint32_t o = off[I];
-      if (left < kBigBK) o -= 2u * uint32_t(max(0, (kb ^ ((I & 1) * 32)) - (left - 8)));
-      __builtin_amdgcn_global_load_lds(static_cast<const void*>(p + o), to, 16, 0, 0);
-    } else {
-      const char* q = p + (I >> 1) * 8 * ld;
-      uint32_t o = off[I & 1];
-      if (left < kBigBK) {                    // (the offset from p itself, which may be the last row)
-        q = p;
-        o += uint32_t((I >> 1) * 4 - max(0, kb + 2 * I - (left - 1))) * uint32_t(ld) * 2u;
-      }
-      __builtin_amdgcn_global_load_lds(static_cast<const void*>(q + o), to, 16, 0, 0);
+    __builtin_amdgcn_global_load_lds(static_cast<const void*>(p + off[I]), to, 16, 0, 0);
+  }
+  // the last step of a tile, where K is not a multiple of 64: past K the row's last values, or the last K row, again (zeroed on
+  // their way to the products)
+  __device__ __forceinline__ void cut() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (!MN) off[i] -= 2u * uint32_t(max(0, (kb ^ ((i & 1) * 32)) - (left - 8)));
+      else off[i] -= 2u * uint32_t(max(0, kb + 2 * i - (left - 1))) * uint32_t(ld);
     }
   }
   __device__ __forceinline__ void step() {
     p += MN ? ld * (kBigBK * 2) : int64_t(kBigBK * 2);
     left -= kBigBK;
+    if (left > 0 && left < kBigBK) cut();
   }
 };
 
