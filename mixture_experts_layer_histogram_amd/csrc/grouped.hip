@@ -190,8 +190,9 @@ __global__ __launch_bounds__(256) void grouped_small_wgrad_kernel(WgradArgs g) {
 // 256 x 256 tiles in bf16 (grouped_tile.hpp): the list of all tiles is cut into eight contiguous ranges, one for an XCD (workgroup w
 // runs on XCD w mod 8), by group, then as big_place says.  A workgroup takes every 32nd tile of its XCD's range, 64 at a
 // time: lane i of each wave looks up the i-th and keeps it.
-template <bool W_KN>
+template <bool W_KN, bool CUT>
 struct BigProducts {
+  static constexpr int kCut = CUT;
   const GroupedArgs& g;
   uint32_t what;                 // this lane's tile: group | (rows - 1) << 10 | column tile << 18
   int32_t row0;
@@ -212,12 +213,12 @@ struct BigProducts {
   }
   template <typename WALK>
   __device__ __forceinline__ void store(int i, const WALK& walk) const {
-    big_store<uint16_t, false>(walk, static_cast<uint16_t*>(g.y) + int64_t(__builtin_amdgcn_readlane(row0, i)) * g.ldy +
+    big_store<uint16_t, false, false>(walk, static_cast<uint16_t*>(g.y) + int64_t(__builtin_amdgcn_readlane(row0, i)) * g.ldy +
                                int(w_(i) >> 18) * kBig, g.ldy, rows(i), cols(i));
   }
 };
 
-template <bool W_KN>
+template <bool W_KN, bool CUT>
 __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_kernel(GroupedArgs g) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int NT = (g.N + kBig - 1) / kBig;
@@ -231,7 +232,7 @@ __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_kernel(GroupedArgs
     const int64_t total = int64_t(mtiles) * NT;
     per_xcd = (total + 7) >> 3;
     const int64_t tt = t0 + int64_t(lane) * wg_per_xcd, tau = xcd * per_xcd + tt;
-    BigProducts<W_KN> tiles{g, 0, 0, 0};
+    BigProducts<W_KN, CUT> tiles{g, 0, 0, 0};
     const bool mine = tt < per_xcd && tau < total;
     if (mine) {
       const int l = find_expert(base, g.G, int(tau / NT));
@@ -242,7 +243,7 @@ __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_kernel(GroupedArgs
     }
     tiles.n = __popcll(__ballot(mine));
     __syncthreads();                      // the tables' LDS becomes the ring's
-    BigWalk<false, W_KN, BigProducts<W_KN>> walk(tiles, smem);
+    BigWalk<false, W_KN, BigProducts<W_KN, CUT>> walk(tiles, smem);
     walk.run();
     __syncthreads();
   }
@@ -251,29 +252,29 @@ __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_kernel(GroupedArgs
 // The same for the gradient by the weights: a tile of 256 x 256 of one group's gradient sums over the group's rows.
 template <typename O, bool ADD>
 struct BigGradients {
+  static constexpr int kCut = 2;
   const WgradArgs& g;
   uint32_t gm;                   // this lane's tile: group | row tile << 10
-  int nt, n;
+  int32_t nt, r0, k;             // its column tile, its group's first row and rows
+  int n;
 
   __device__ __forceinline__ int group(int i) const { return __builtin_amdgcn_readlane(int(gm), i) & 1023; }
   __device__ __forceinline__ int m0(int i) const { return int(uint32_t(__builtin_amdgcn_readlane(int(gm), i)) >> 10) * kBig; }
   __device__ __forceinline__ int c0(int i) const { return __builtin_amdgcn_readlane(nt, i) * kBig; }
   __device__ __forceinline__ int count() const { return n; }
-  __device__ __forceinline__ int K(int i) const {
-    const int l = group(i);
-    return __builtin_amdgcn_readfirstlane(g.offsets[l + 1] - g.offsets[l]);
-  }
+  __device__ __forceinline__ int K(int i) const { return __builtin_amdgcn_readlane(k, i); }
+  __device__ __forceinline__ int64_t first(int i) const { return __builtin_amdgcn_readlane(r0, i); }
   __device__ __forceinline__ int rows(int i) const { return min(kBig, g.M - m0(i)); }
   __device__ __forceinline__ int cols(int i) const { return min(kBig, g.N - c0(i)); }
   __device__ __forceinline__ BigOperand a(int i) const {
-    return BigOperand{static_cast<const uint16_t*>(g.a) + int64_t(g.offsets[group(i)]) * g.lda + m0(i), g.lda, rows(i)};
+    return BigOperand{static_cast<const uint16_t*>(g.a) + first(i) * g.lda + m0(i), g.lda, rows(i)};
   }
   __device__ __forceinline__ BigOperand b(int i) const {
-    return BigOperand{static_cast<const uint16_t*>(g.b) + int64_t(g.offsets[group(i)]) * g.ldb + c0(i), g.ldb, cols(i)};
+    return BigOperand{static_cast<const uint16_t*>(g.b) + first(i) * g.ldb + c0(i), g.ldb, cols(i)};
   }
   template <typename WALK>
   __device__ __forceinline__ void store(int i, const WALK& walk) const {
-    big_store<O, ADD>(walk, static_cast<O*>(g.dw) + (int64_t(group(i)) * g.M + m0(i)) * g.N + c0(i), g.N, rows(i), cols(i));
+    big_store<O, ADD, true>(walk, static_cast<O*>(g.dw) + (int64_t(group(i)) * g.M + m0(i)) * g.N + c0(i), g.N, rows(i), cols(i));
   }
 };
 
@@ -292,20 +293,23 @@ __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_wgrad_kernel(Wgrad
   for (int64_t t0 = blockIdx.x >> 3; t0 < per_xcd; t0 += 64 * int64_t(wg_per_xcd)) {
     const int64_t tt = t0 + int64_t(lane) * wg_per_xcd, tau = xcd * per_xcd + tt;
     const bool mine = tt < per_xcd && tau < total;
-    int l = 0, mt = 0, nt = 0, rows = 0;
+    int l = 0, mt = 0, nt = 0, r0 = 0, rows = 0;
     if (mine) {
       l = int(tau / (int64_t(MT) * NT));
       big_place(tau - int64_t(l) * MT * NT, MT, NT, &mt, &nt);
-      rows = g.offsets[l + 1] - g.offsets[l];
+      r0 = g.offsets[l];
+      rows = g.offsets[l + 1] - r0;
     }
     const uint64_t full = __ballot(mine && rows > 0), empty = __ballot(mine && rows == 0);
     // tiles of groups with rows first in the lanes' order, the others behind them get zeros
     const uint64_t below = (uint64_t(1) << lane) - 1;
     const int to = rows > 0 ? __popcll(full & below) : mine ? __popcll(full) + __popcll(empty & below) : 63;
-    BigGradients<O, ADD> tiles{g, 0, 0, int(__popcll(full))};
+    BigGradients<O, ADD> tiles{g, 0, 0, 0, 0, int(__popcll(full))};
     if (full | empty) {
       tiles.gm = uint32_t(__builtin_amdgcn_ds_permute(to * 4, mine ? int(uint32_t(l) | uint32_t(mt) << 10) : 0));
       tiles.nt = __builtin_amdgcn_ds_permute(to * 4, nt);
+      tiles.r0 = __builtin_amdgcn_ds_permute(to * 4, r0);
+      tiles.k = __builtin_amdgcn_ds_permute(to * 4, rows);
     }
     if constexpr (!ADD) {
       for (int i = tiles.n; i < tiles.n + int(__popcll(empty)); ++i) {
@@ -327,8 +331,10 @@ __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_wgrad_kernel(Wgrad
 static hipError_t set_big_lds() {
   static std::atomic<uint64_t> done{0};
   return once_per_device(done, [] {
-    const void* ks[] = {reinterpret_cast<const void*>(grouped_big_kernel<false>),
-                        reinterpret_cast<const void*>(grouped_big_kernel<true>),
+    const void* ks[] = {reinterpret_cast<const void*>(grouped_big_kernel<false, false>),
+                        reinterpret_cast<const void*>(grouped_big_kernel<false, true>),
+                        reinterpret_cast<const void*>(grouped_big_kernel<true, false>),
+                        reinterpret_cast<const void*>(grouped_big_kernel<true, true>),
                         reinterpret_cast<const void*>(grouped_big_wgrad_kernel<uint16_t, false>),
                         reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, false>),
                         reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, true>)};
@@ -351,8 +357,11 @@ hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, con
     const hipError_t e = set_big_lds();
     if (e != hipSuccess) return e;
     const dim3 big((cus / 8) * 8);
-    if (s.w_layout) hipLaunchKernelGGL(grouped_big_kernel<true>, big, dim3(kBigThreads), kBigLds, st, g);
-    else hipLaunchKernelGGL(grouped_big_kernel<false>, big, dim3(kBigThreads), kBigLds, st, g);
+    // K of whole steps: no check at the fills (a tenth of 8192^3)
+    if (s.w_layout && s.K % kBigBK) hipLaunchKernelGGL((grouped_big_kernel<true, true>), big, dim3(kBigThreads), kBigLds, st, g);
+    else if (s.w_layout) hipLaunchKernelGGL((grouped_big_kernel<true, false>), big, dim3(kBigThreads), kBigLds, st, g);
+    else if (s.K % kBigBK) hipLaunchKernelGGL((grouped_big_kernel<false, true>), big, dim3(kBigThreads), kBigLds, st, g);
+    else hipLaunchKernelGGL((grouped_big_kernel<false, false>), big, dim3(kBigThreads), kBigLds, st, g);
   } else {
     if (s.w_layout) hipLaunchKernelGGL((grouped_small_kernel<uint16_t, true>), grid, threads, 0, st, g);
     else hipLaunchKernelGGL((grouped_small_kernel<uint16_t, false>), grid, threads, 0, st, g);

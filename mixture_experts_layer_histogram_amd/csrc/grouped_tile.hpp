@@ -63,6 +63,9 @@ __device__ __forceinline__ int big_mn_swz(int k) { return 2 * ((k & 3) | (((k >>
 #define MOE_VMCNT4() __builtin_amdgcn_s_waitcnt(0x0F74)
 #define MOE_LGKM0() __builtin_amdgcn_s_waitcnt(0xC07F)           // lgkmcnt(0)
 
+// What a tile's last step reads past K: sixteen zero bytes, again and again.
+__device__ const u32x4 kBigZeros = {0, 0, 0, 0};
+
 // This lane's four fills of a panel
 template <bool MN>
 struct BigFill {
@@ -87,30 +90,26 @@ struct BigFill {
       for (int i = 0; i < 4; ++i)
         off[i] = (uint32_t(kb + 2 * i) * uint32_t(ld) + uint32_t(min(((lane & 31) ^ big_mn_swz(kb + 2 * i)) * 8, o.rows - 8))) * 2u;
     }
-    if (K < kBigBK) cut();
   }
-  template <int I>
+  template <int I, bool CUT>
   __device__ __forceinline__ void fill(uint32_t lds) const {
     const lds_void_ptr to = (lds_void_ptr)(uintptr_t)(lds + uint32_t(I * 1024));
-    __builtin_amdgcn_global_load_lds(static_cast<const void*>(p + off[I]), to, 16, 0, 0);
-  }
-  // the last step of a tile, where K is not a multiple of 64: past K the row's last values, or the last K row, again (zeroed on
-  // their way to the products)
-  __device__ __forceinline__ void cut() {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (!MN) off[i] -= 2u * uint32_t(max(0, (kb ^ ((i & 1) * 32)) - (left - 8)));
-      else off[i] -= 2u * uint32_t(max(0, kb + 2 * i - (left - 1))) * uint32_t(ld);
+    if (!CUT || left >= kBigBK) {
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(p + off[I]), to, 16, 0, 0);
+    } else {                  // zeros past K, in both operands: what lies there could be a NaN
+      const int k = MN ? kb + 2 * I : kb ^ ((I & 1) * 32);
+      const char* q = k < left ? p + off[I] : reinterpret_cast<const char*>(&kBigZeros);
+      __builtin_amdgcn_global_load_lds(static_cast<const void*>(q), to, 16, 0, 0);
     }
   }
   __device__ __forceinline__ void step() {
     p += MN ? ld * (kBigBK * 2) : int64_t(kBigBK * 2);
     left -= kBigBK;
-    if (left > 0 && left < kBigBK) cut();
   }
 };
 
-// TILES: int count(); K of tile i; its operands a(i) and b(i); rows(i), cols(i) of its output; store(i, walk).
+// TILES: int count(); K of tile i; its operands a(i) and b(i); rows(i), cols(i) of its output; store(i, walk);
+// kCut: 0 where every K is a multiple of 64; 1: the check at every fill; 2: at every step (few steps, and the code is there twice).
 template <bool A_MN, bool B_MN, typename TILES>
 struct BigWalk {
   TILES& tiles;
@@ -152,10 +151,10 @@ struct BigWalk {
   // ---- the cursors
   __device__ __forceinline__ bool on_a() const { return fa_.tile < n_tiles; }
   __device__ __forceinline__ bool on_b() const { return fb_.tile < n_tiles; }
-  template <bool A, int I>
+  template <bool A, int I, bool CUT>
   __device__ __forceinline__ void fill(uint32_t place) {
-    if constexpr (A) fa_.template fill<I>(lds_fill + place);
-    else fb_.template fill<I>(lds_fill + place);
+    if constexpr (A) fa_.template fill<I, CUT>(lds_fill + place);
+    else fb_.template fill<I, CUT>(lds_fill + place);
     if constexpr (I == 3) {
       if constexpr (A) {
         fa_.step();
@@ -166,31 +165,28 @@ struct BigWalk {
       }
     }
   }
-  template <bool A, int I>
+  template <bool A, int I, bool CUT>
   __device__ __forceinline__ void fill2(uint32_t place) {
-    fill<A, I>(place);
-    fill<A, I + 1>(place);
+    fill<A, I, CUT>(place);
+    fill<A, I + 1, CUT>(place);
   }
 
   // ---- half a step's fragments from LDS, all landed at the end
   template <int MV>
-  __device__ __forceinline__ void read(uint32_t pb, int h, int left) {
+  __device__ __forceinline__ void read(uint32_t pb, int h) {
     if constexpr (MV > 0) {
+      uint32_t ar = a_rd[0], br = b_rd[0];
+      if constexpr (A_MN) asm volatile("" : "+v"(ar));      // the blocks' addresses are not kept in registers of their own
+      if constexpr (B_MN) asm volatile("" : "+v"(br));
 #pragma unroll
       for (int m = 0; m < MV; ++m) {
-        if constexpr (A_MN) fa[m] = read_tr((a_rd[0] ^ (m << 5)) + (l0 + pa) + h * 16384);       // block m: 32 bytes on, swizzled
+        if constexpr (A_MN) fa[m] = read_tr((ar ^ (m << 5)) + (l0 + pa) + h * 16384);       // block m: 32 bytes on, swizzled
         else fa[m] = *(const __attribute__((address_space(3))) bf16x8*)(uintptr_t)(a_rd[h] + pa + m * 2048);
       }
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        if constexpr (B_MN) fb[n] = read_tr((b_rd[0] ^ (n << 5)) + (l0 + pb) + h * 16384);
+        if constexpr (B_MN) fb[n] = read_tr((br ^ (n << 5)) + (l0 + pb) + h * 16384);
         else fb[n] = *(const __attribute__((address_space(3))) bf16x8*)(uintptr_t)(b_rd[h] + pb + n * 2048);
-      }
-      if (left < h * 32 + 32) {                       // the last step: zeros past K, in both (a NaN there must not count)
-#pragma unroll
-        for (int m = 0; m < MV; ++m) fa[m] = mask(fa[m], left - h * 32 - 8 * g);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) fb[n] = mask(fb[n], left - h * 32 - 8 * g);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -200,17 +196,10 @@ struct BigWalk {
     const s16x4 up = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(uintptr_t)(p + 2048));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7));
   }
-  __device__ static __forceinline__ bf16x8 mask(bf16x8 f, int n) {     // the first n values
-    s16x8 v = __builtin_bit_cast(s16x8, f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e >= n) v[e] = 0;
-    return __builtin_bit_cast(bf16x8, v);
-  }
 
   // ---- half a step's products, with two fills between them.  The weights' (columns') fragment comes first, so that a lane ends up
   // with four consecutive columns of one row.
-  template <int MV, bool A, int I>
+  template <int MV, bool A, int I, bool CUT>
   __device__ __forceinline__ void mfma(uint32_t place, bool on) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -220,13 +209,13 @@ struct BigWalk {
       if (m == 0 || m == 3) {
         __builtin_amdgcn_sched_barrier(0);
         if (on) {
-          if (m == 0) fill<A, I>(place);
-          else fill<A, I + 1>(place);
+          if (m == 0) fill<A, I, CUT>(place);
+          else fill<A, I + 1, CUT>(place);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (MV == 0 && on) fill2<A, I>(place);
+    if (MV == 0 && on) fill2<A, I, CUT>(place);
     __builtin_amdgcn_s_setprio(0);
   }
   __device__ static __forceinline__ void turn() {
@@ -241,37 +230,44 @@ struct BigWalk {
     return p >= uint32_t(kBigLds) ? p - uint32_t(kBigLds) : p;
   }
 
-  // ---- the steps of one tile
+  // ---- one step of a tile, and a tile.  CUT: some fill of the step may be of a tile's last, cut step (a branch at each fill: it costs
+  // 8192^3 a tenth).
+  template <int MV, int HALF, bool CUT>
+  __device__ __forceinline__ void step() {
+    const uint32_t pb = next(pa, 1), pb1 = next(pa, 3), pa2 = next(pa, 4);
+    read<MV>(pb, 0);
+    const bool b = on_b();
+    if (b) fill2<false, HALF == 0 ? 0 : 2, CUT>(pb1);
+    MOE_LGKM0();
+    turn();
+    const bool a = on_a();
+    if constexpr (HALF == 0) mfma<MV, false, 2, CUT>(pb1, b);
+    else mfma<MV, true, 0, CUT>(pa2, a);
+    turn();
+    read<MV>(pb, 1);
+    if (a) fill2<true, HALF == 0 ? 0 : 2, CUT>(pa2);
+    MOE_LGKM0();
+    if constexpr (HALF == 1) {                       // B of the next step has landed: all but this step's four fills of A
+      if (a) MOE_VMCNT4();
+      else MOE_VMCNT0();
+    }
+    turn();
+    if constexpr (HALF == 0) {
+      mfma<MV, true, 2, CUT>(pa2, a);
+      if (a) MOE_VMCNT4();
+      else MOE_VMCNT0();
+    } else {
+      mfma<MV, false, 0, CUT>(pa, on_b());         // B of the step after next comes where A of this one lay
+    }
+    turn();
+    pa = next(pa, 2);
+  }
   template <int MV, int HALF>
   __device__ __forceinline__ void steps(int K) {
     for (int left = K; left > 0; left -= kBigBK) {
-      const uint32_t pb = next(pa, 1), pb1 = next(pa, 3), pa2 = next(pa, 4);
-      read<MV>(pb, 0, left);
-      const bool b = on_b();
-      if (b) fill2<false, HALF == 0 ? 0 : 2>(pb1);
-      MOE_LGKM0();
-      turn();
-      const bool a = on_a();
-      if constexpr (HALF == 0) mfma<MV, false, 2>(pb1, b);
-      else mfma<MV, true, 0>(pa2, a);
-      turn();
-      read<MV>(pb, 1, left);
-      if (a) fill2<true, HALF == 0 ? 0 : 2>(pa2);
-      MOE_LGKM0();
-      if constexpr (HALF == 1) {                       // B of the next step has landed: all but this step's four fills of A
-        if (a) MOE_VMCNT4();
-        else MOE_VMCNT0();
-      }
-      turn();
-      if constexpr (HALF == 0) {
-        mfma<MV, true, 2>(pa2, a);
-        if (a) MOE_VMCNT4();
-        else MOE_VMCNT0();
-      } else {
-        mfma<MV, false, 0>(pa, on_b());                // B of the step after next comes where A of this one lay
-      }
-      turn();
-      pa = next(pa, 2);
+      // a step without cut fills needs two whole steps ahead of both cursors
+      if (TILES::kCut == 0 || (TILES::kCut == 2 && min(fa_.left, fb_.left) >= 2 * kBigBK)) step<MV, HALF, false>();
+      else step<MV, HALF, true>();
     }
   }
   template <int HALF>
@@ -296,13 +292,13 @@ struct BigWalk {
     fa_.tile = fb_.tile = 0;
     fa_.at(wave, lane, tiles.a(0), tiles.K(0));
     fb_.at(wave, lane, tiles.b(0), tiles.K(0));
-    fill2<true, 0>(pa);
-    fill2<true, 2>(pa);
-    fill2<false, 0>(next(pa, 1));
-    fill2<false, 2>(next(pa, 1));
+    fill2<true, 0, true>(pa);
+    fill2<true, 2, true>(pa);
+    fill2<false, 0, true>(next(pa, 1));
+    fill2<false, 2, true>(next(pa, 1));
     if (on_a()) {
-      fill2<true, 0>(next(pa, 2));
-      fill2<true, 2>(next(pa, 2));
+      fill2<true, 0, true>(next(pa, 2));
+      fill2<true, 2, true>(next(pa, 2));
       MOE_VMCNT4();
     } else {
       MOE_VMCNT0();
@@ -312,16 +308,23 @@ struct BigWalk {
       for (int i = 0; i < n_tiles; ++i) tile<0>(i);
       turn();
     } else {
-      if (on_b()) fill2<false, 0>(next(pa, 3));
+      if (on_b()) fill2<false, 0, true>(next(pa, 3));
       turn();
       for (int i = 0; i < n_tiles; ++i) tile<1>(i);
     }
   }
 };
 
-// Output rows of a tile from the accumulators: bf16 in 16-byte vectors (two 16-column blocks exchange halves between lane groups, so
-// that a lane has eight consecutive columns), fp32 in 16-byte vectors, added to what is there with ADD.
-template <typename O, bool ADD, typename WALK>
+// Output rows of a tile from the accumulators, in 16-byte vectors.  bf16: two 16-column blocks exchange halves between lane groups, so
+// that a lane has eight consecutive columns, and lanes 8 apart exchange vectors, so that a store covers 128 bytes of each of eight
+// rows.  fp32: added to what is there with ADD.  NT: past the caches.
+template <bool NT>
+__device__ __forceinline__ void big_put(void* p, const u32x4 v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, static_cast<u32x4*>(p));
+  else *static_cast<u32x4*>(p) = v;
+}
+
+template <typename O, bool ADD, bool NT, typename WALK>
 __device__ __forceinline__ void big_store(const WALK& w, O* out, int64_t ld, int rows, int cols) {
   int lane = w.lane;
   asm volatile("" : "+v"(lane));            // the compiler would keep these indices in registers all along the products
@@ -329,22 +332,34 @@ __device__ __forceinline__ void big_store(const WALK& w, O* out, int64_t ld, int
 #pragma unroll
   for (int m = 0; m < 8; ++m) {
     const int row = w.half * 128 + m * 16 + r16;
-    if (row >= rows) continue;
+    if (sizeof(O) == 4 && row >= rows) continue;
     O* p = out + row * ld;
     if constexpr (sizeof(O) == 2) {
+      u32x4 v[2];
 #pragma unroll
-      for (int n = 0; n < 4; n += 2) {
-        u32x4 v;
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const auto s = __builtin_amdgcn_permlane16_swap(pack_bf16x2(w.acc[m][n][2 * j], w.acc[m][n][2 * j + 1]),
-                                                          pack_bf16x2(w.acc[m][n + 1][2 * j], w.acc[m][n + 1][2 * j + 1]), false, false);
-          v[j] = s[0];
-          v[2 + j] = s[1];
+          const auto s = __builtin_amdgcn_permlane16_swap(pack_bf16x2(w.acc[m][2 * n][2 * j], w.acc[m][2 * n][2 * j + 1]),
+                                                          pack_bf16x2(w.acc[m][2 * n + 1][2 * j], w.acc[m][2 * n + 1][2 * j + 1]), false, false);
+          v[n][j] = s[0];
+          v[n][2 + j] = s[1];
         }
-        const int col = w.wn * 64 + (n + (g & 1)) * 16 + (g >> 1) * 8;
-        if (col < cols) *reinterpret_cast<u32x4*>(p + col) = v;
+      // lanes r16 and r16 ^ 8 exchange: then a lane's first vector is of row r16 & 7 and its second of row (r16 & 7) + 8
+      const bool up = r16 >= 8;
+      u32x4 a, b;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t send = up ? v[0][j] : v[1][j];
+        const uint32_t got = uint32_t(__builtin_amdgcn_update_dpp(int(send), int(send), 0x128, 0xF, 0xF, false));
+        a[j] = up ? got : v[0][j];
+        b[j] = up ? v[1][j] : got;
       }
+      const int col = w.wn * 64 + (up ? 32 : 0) + (g & 1) * 16 + (g >> 1) * 8;
+      const int ra = w.half * 128 + m * 16 + (r16 & 7);
+      O* q = out + ra * ld + col;
+      if (col < cols && ra < rows) big_put<NT>(q, a);
+      if (col < cols && ra + 8 < rows) big_put<NT>(q + 8 * ld, b);
     } else {
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
@@ -352,7 +367,7 @@ __device__ __forceinline__ void big_store(const WALK& w, O* out, int64_t ld, int
         if (col >= cols) continue;
         f32x4 v = w.acc[m][n];
         if constexpr (ADD) v += *reinterpret_cast<const f32x4*>(p + col);
-        *reinterpret_cast<f32x4*>(p + col) = v;
+        big_put<NT>(p + col, __builtin_bit_cast(u32x4, v));
       }
     }
   }
