@@ -3,6 +3,7 @@
 //   dW_g = sum over s of dy[s]^T x[s] (or its transpose), the gradient by the weights.
 // The gradient by the rows is the first product in the weights' other orientation.
 #include "grouped.hpp"
+#include "grouped_thin.hpp"
 #include "grouped_tile.hpp"
 
 namespace moe {
@@ -98,16 +99,6 @@ __device__ __forceinline__ f32x16 small_tile(const SmallOperand<T>& A, const Sma
 
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = uint16_t(pack_bf16x2(v, 0.0f)); }
-
-struct GroupedArgs {
-  const void* x;
-  const void* w;
-  void* y;
-  const int32_t* offsets;
-  int32_t* status;
-  int64_t rows, ldx, ldy;
-  int G, K, N;
-};
 
 template <typename T, bool W_KN>
 __global__ __launch_bounds__(256) void grouped_small_kernel(GroupedArgs g) {
@@ -328,44 +319,64 @@ __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_wgrad_kernel(Wgrad
   }
 }
 
-static hipError_t set_big_lds() {
+// the dynamic LDS that each kernel asks for, granted once per device
+static hipError_t set_grouped_lds() {
   static std::atomic<uint64_t> done{0};
   return once_per_device(done, [] {
-    const void* ks[] = {reinterpret_cast<const void*>(grouped_big_kernel<false, false>),
-                        reinterpret_cast<const void*>(grouped_big_kernel<false, true>),
-                        reinterpret_cast<const void*>(grouped_big_kernel<true, false>),
-                        reinterpret_cast<const void*>(grouped_big_kernel<true, true>),
-                        reinterpret_cast<const void*>(grouped_big_wgrad_kernel<uint16_t, false>),
-                        reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, false>),
-                        reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, true>)};
-    for (const void* k : ks) {
-      const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kBigLds);
+    const struct {
+      const void* k;
+      int bytes;
+    } ks[] = {{reinterpret_cast<const void*>(grouped_big_kernel<false, false>), kBigLds},
+              {reinterpret_cast<const void*>(grouped_big_kernel<false, true>), kBigLds},
+              {reinterpret_cast<const void*>(grouped_big_kernel<true, false>), kBigLds},
+              {reinterpret_cast<const void*>(grouped_big_kernel<true, true>), kBigLds},
+              {reinterpret_cast<const void*>(grouped_big_wgrad_kernel<uint16_t, false>), kBigLds},
+              {reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, false>), kBigLds},
+              {reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, true>), kBigLds},
+              {reinterpret_cast<const void*>(grouped_thin_kernel<false>), kThinLds},
+              {reinterpret_cast<const void*>(grouped_thin_kernel<true>), kThinLds}};
+    for (const auto& k : ks) {
+      const hipError_t e = hipFuncSetAttribute(k.k, hipFuncAttributeMaxDynamicSharedMemorySize, k.bytes);
       if (e != hipSuccess) return e;
     }
     return hipSuccess;
   });
 }
 
+// Rows a group on the mean up to which the weights stream past them: 24, or 128 where the 256-column tiles of all groups would leave half
+// of the CUs idle.  us streaming and with tiles: 32 groups of 7168 x 2048, 16 rows a group 149 and 169, 24 rows 181 and 170 (weights
+// stored [K][N]: 163 and 211, 177 and 214), 32 rows 198 and 171 (213 and 216); one group of 7168 x 7168, 1 row 18 and 77, 32 rows 20 and 78,
+// 96 rows 52 and 100.
+static bool thin_rows(const moe_gemm_t& s, int cus) {
+  const int64_t tiles = int64_t(s.groups) * ((s.N + kBig - 1) / kBig);
+  return s.rows <= int64_t(s.groups) * (tiles * 2 < cus ? 128 : 24);
+}
+
 hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, const int32_t* offsets, void* y,
                           int32_t* status, int cus, hipStream_t st) {
   const GroupedArgs g{x, w, y, offsets, status, s.rows, s.ldx ? s.ldx : s.K, s.ldy ? s.ldy : s.N, s.groups, s.K, s.N};
-  const dim3 grid(cus * 4), threads(256);
+  const dim3 threads(256);
   if (s.dtype == MOE_F32) {
-    if (s.w_layout) hipLaunchKernelGGL((grouped_small_kernel<float, true>), grid, threads, 0, st, g);
-    else hipLaunchKernelGGL((grouped_small_kernel<float, false>), grid, threads, 0, st, g);
-  } else if (s.rows > int64_t(s.groups) * 64) {
-    const hipError_t e = set_big_lds();
-    if (e != hipSuccess) return e;
+    if (s.w_layout) hipLaunchKernelGGL((grouped_small_kernel<float, true>), dim3(cus * 4), threads, 0, st, g);
+    else hipLaunchKernelGGL((grouped_small_kernel<float, false>), dim3(cus * 4), threads, 0, st, g);
+    return hipGetLastError();
+  }
+  const hipError_t e = set_grouped_lds();
+  if (e != hipSuccess) return e;
+  if (!thin_rows(s, cus)) {
     const dim3 big((cus / 8) * 8);
     // K of whole steps: no check at the fills (a tenth of 8192^3)
     if (s.w_layout && s.K % kBigBK) hipLaunchKernelGGL((grouped_big_kernel<true, true>), big, dim3(kBigThreads), kBigLds, st, g);
     else if (s.w_layout) hipLaunchKernelGGL((grouped_big_kernel<true, false>), big, dim3(kBigThreads), kBigLds, st, g);
     else if (s.K % kBigBK) hipLaunchKernelGGL((grouped_big_kernel<false, true>), big, dim3(kBigThreads), kBigLds, st, g);
     else hipLaunchKernelGGL((grouped_big_kernel<false, false>), big, dim3(kBigThreads), kBigLds, st, g);
-  } else {
-    if (s.w_layout) hipLaunchKernelGGL((grouped_small_kernel<uint16_t, true>), grid, threads, 0, st, g);
-    else hipLaunchKernelGGL((grouped_small_kernel<uint16_t, false>), grid, threads, 0, st, g);
+    return hipGetLastError();
   }
+  const int64_t tiles = s.rows / kThinRows + (s.rows < s.groups ? s.rows : s.groups);      // at most
+  const int64_t items = tiles * ((s.N + kThinCols - 1) / kThinCols);
+  const dim3 grid(items < 1 ? 1 : int(items < cus ? items : cus));
+  if (s.w_layout) hipLaunchKernelGGL(grouped_thin_kernel<true>, grid, threads, kThinLds, st, g);
+  else hipLaunchKernelGGL(grouped_thin_kernel<false>, grid, threads, kThinLds, st, g);
   return hipGetLastError();
 }
 
@@ -379,7 +390,7 @@ hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* 
     if (accumulate) hipLaunchKernelGGL((grouped_small_wgrad_kernel<float, float, true>), grid, threads, 0, st, g);
     else hipLaunchKernelGGL((grouped_small_wgrad_kernel<float, float, false>), grid, threads, 0, st, g);
   } else {
-    const hipError_t e = set_big_lds();
+    const hipError_t e = set_grouped_lds();
     if (e != hipSuccess) return e;
     const dim3 big((cus / 8) * 8), many(kBigThreads);
     if (dw_dtype != MOE_F32) hipLaunchKernelGGL((grouped_big_wgrad_kernel<uint16_t, false>), big, many, kBigLds, st, g);

@@ -7,6 +7,16 @@ namespace moe {
 
 constexpr int kMaxGroups = 1024;
 
+struct GroupedArgs {
+  const void* x;
+  const void* w;
+  void* y;
+  const int32_t* offsets;
+  int32_t* status;
+  int64_t rows, ldx, ldy;
+  int G, K, N;
+};
+
 // The row tiles of all groups, by one workgroup of THREADS (a multiple of 64) threads: base[g] is the first of group g's
 // ceil(rows / BM) tiles, base[G] their number (returned in every thread).  Offsets that descend or leave [0, rows] give
 // no tiles at all, and *bad is set.  base: G + 1 words of LDS, part: THREADS / 64 + 1.
