@@ -8,126 +8,107 @@
 
 namespace moe {
 
-// A 64 x 64 tile of C = A B^T summed over K, A and B each stored with K contiguous (element (r, k) at r * ld + k) or with
-// the row index contiguous (at k * ld + r).  256 threads, wave w owns the 32 x 32 block (w >> 1, w & 1); K steps of 32
-// staged in LDS with K contiguous, rows padded so that 16 lanes' reads touch all banks.
-constexpr int kSmallBM = 64, kSmallBK = 32;
+// fp32, on the fp32 MFMA (v_mfma_f32_32x32x2_f32): a 64 x 64 tile of C = A B^T, A and B each stored with K contiguous (element (r, k) at
+// r * ld + k) or with the row index contiguous (at k * ld + r).  256 threads, wave w owns the 32 x 32 block (w >> 1, w & 1).  K goes by
+// steps of 128 through LDS, in the order it is stored in (rows padded so that 64 lanes' reads touch all banks), and the next step's loads are on
+// their way in registers while one is at work: small products are a chain of such round trips (509 rows on 8 x (128 x 256), both gradients:
+// 24.9 us with steps of 32 and no loads ahead).
+constexpr int kF32Tile = 64, kF32Step = 128, kF32PitchK = kF32Step + 4, kF32PitchR = kF32Tile + 8;
+constexpr int kF32Panel = kF32Step * kF32PitchR > kF32Tile * kF32PitchK ? kF32Step * kF32PitchR : kF32Tile * kF32PitchK;   // values
+constexpr int kF32Lds = 2 * kF32Panel * 4;
 
-template <typename T>
-struct SmallTile;
-template <>
-struct SmallTile<float> {
-  static constexpr int V = 4, kPitch = kSmallBK + 4;
-};
-template <>
-struct SmallTile<uint16_t> {
-  static constexpr int V = 8, kPitch = kSmallBK + 8;
-};
-
-template <typename T>
-struct SmallOperand {
-  const T* p;
+struct F32Operand {
+  const float* p;
   int64_t ld;
-  int rows, k;         // valid rows of the tile and valid K (multiples of V along the contiguous axis, or cut there)
+  int rows;                    // valid ones of the tile
 };
 
-// 64 x 32 values from k0 on into LDS; zeros past the valid ones
-template <typename T, bool MN>
-__device__ __forceinline__ void small_fill(const SmallOperand<T>& o, int k0, T* lds) {
-  using S = SmallTile<T>;
-  constexpr int V = S::V;
-  if constexpr (!MN) {
-    constexpr int kPerRow = kSmallBK / V;
+template <bool MN>
+struct F32Fill {
+  f32x4 v[8];                  // a thread's share of a step: 64 x 128 values of 256 threads
+
+  // from k0 on, zeros past `left` values of K and past the rows (both multiples of 4 along the contiguous axis)
+  __device__ __forceinline__ void load(const F32Operand& o, int k0, int left) {
 #pragma unroll
-    for (int i = 0; i < kSmallBM * kPerRow / 256; ++i) {
-      const int v = threadIdx.x + i * 256, r = v / kPerRow, k = (v % kPerRow) * V;
-      u32x4 q = {0, 0, 0, 0};
-      if (r < o.rows && k0 + k < o.k) q = *reinterpret_cast<const u32x4*>(o.p + int64_t(r) * o.ld + k0 + k);
-      *reinterpret_cast<u32x4*>(lds + r * S::kPitch + k) = q;
-    }
-  } else {
-    constexpr int kPerRow = kSmallBM / V;
-#pragma unroll
-    for (int i = 0; i < kSmallBK * kPerRow / 256; ++i) {
-      const int v = threadIdx.x + i * 256, k = v / kPerRow, r = (v % kPerRow) * V;
-      union {
-        u32x4 q;
-        T t[V];
-      } u;
-      u.q = u32x4{0, 0, 0, 0};
-      if (r < o.rows && k0 + k < o.k) u.q = *reinterpret_cast<const u32x4*>(o.p + int64_t(k0 + k) * o.ld + r);
-#pragma unroll
-      for (int j = 0; j < V; ++j) lds[(r + j) * S::kPitch + k] = u.t[j];
+    for (int i = 0; i < 8; ++i) {
+      const int t = threadIdx.x + i * 256;
+      const int r = MN ? (t & 15) * 4 : t >> 5, k = MN ? t >> 4 : (t & 31) * 4;
+      v[i] = f32x4{0, 0, 0, 0};
+      if (r < o.rows && k < left)
+        v[i] = *reinterpret_cast<const f32x4*>(o.p + (MN ? int64_t(k0 + k) * o.ld + r : int64_t(r) * o.ld + k0 + k));
     }
   }
-}
+  __device__ __forceinline__ void put(float* lds) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = threadIdx.x + i * 256;
+      *reinterpret_cast<f32x4*>(lds + (MN ? (t >> 4) * kF32PitchR + (t & 15) * 4 : (t >> 5) * kF32PitchK + (t & 31) * 4)) = v[i];
+    }
+  }
+  // lane's four K values of row r: k = 8 c + 4 hi + 0..3
+  static __device__ __forceinline__ f32x4 frag(const float* lds, int r, int c, int hi) {
+    if constexpr (!MN) return *reinterpret_cast<const f32x4*>(lds + r * kF32PitchK + c * 8 + hi * 4);
+    const float* q = lds + (c * 8 + hi * 4) * kF32PitchR + r;
+    return f32x4{q[0], q[kF32PitchR], q[2 * kF32PitchR], q[3 * kF32PitchR]};
+  }
+};
 
-template <typename T, bool A_MN, bool B_MN>
-__device__ __forceinline__ f32x16 small_tile(const SmallOperand<T>& A, const SmallOperand<T>& B, int K, T* sa, T* sb) {
-  using S = SmallTile<T>;
+template <bool A_MN, bool B_MN>
+__device__ __forceinline__ f32x16 f32_tile(const F32Operand& A, const F32Operand& B, int K, float* smem) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, hi = lane >> 5;
+  float *sa = smem, *sb = smem + kF32Panel;
   f32x16 acc;
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-  for (int k0 = 0; k0 < K; k0 += kSmallBK) {
-    small_fill<T, A_MN>(A, k0, sa);
-    small_fill<T, B_MN>(B, k0, sb);
+  F32Fill<A_MN> fa;
+  F32Fill<B_MN> fb;
+  fa.load(A, 0, K);
+  fb.load(B, 0, K);
+  for (int k0 = 0; k0 < K; k0 += kF32Step) {
+    fa.put(sa);
+    fb.put(sb);
     __syncthreads();
-    const T* pa = sa + (wm * 32 + r32) * S::kPitch;
-    const T* pb = sb + (wn * 32 + r32) * S::kPitch;
-    if constexpr (sizeof(T) == 2) {
+    fa.load(A, k0 + kF32Step, K - k0 - kF32Step);
+    fb.load(B, k0 + kF32Step, K - k0 - kF32Step);
+    const int steps = min(kF32Step, K - k0 + 7) >> 3;
+    for (int c = 0; c < steps; ++c) {
+      const f32x4 a = F32Fill<A_MN>::frag(sa, wm * 32 + r32, c, hi);
+      const f32x4 b = F32Fill<B_MN>::frag(sb, wn * 32 + r32, c, hi);
 #pragma unroll
-      for (int c = 0; c < kSmallBK / 16; ++c) {
-        const bf16x8 a = *reinterpret_cast<const bf16x8*>(pa + c * 16 + hi * 8);
-        const bf16x8 b = *reinterpret_cast<const bf16x8*>(pb + c * 16 + hi * 8);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < kSmallBK / 8; ++c) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(pa + c * 8 + hi * 4);
-        const f32x4 b = *reinterpret_cast<const f32x4*>(pb + c * 8 + hi * 4);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[s], b[s], acc, 0, 0, 0);
-      }
+      for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[s], b[s], acc, 0, 0, 0);
     }
-    __syncthreads();
+    __syncthreads();                         // the next step overwrites these
   }
   return acc;
 }
 
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(uint16_t* p, float v) { *p = uint16_t(pack_bf16x2(v, 0.0f)); }
-
-template <typename T, bool W_KN>
-__global__ __launch_bounds__(256) void grouped_small_kernel(GroupedArgs g) {
-  using S = SmallTile<T>;
-  __shared__ __attribute__((aligned(16))) T sa[kSmallBM * S::kPitch];
-  __shared__ __attribute__((aligned(16))) T sb[kSmallBM * S::kPitch];
+template <bool W_KN>
+__global__ __launch_bounds__(256) void grouped_f32_kernel(GroupedArgs g) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ int32_t base[kMaxGroups + 1], part[5];
   bool bad;
   const int mtiles = group_tiles<256>(g.offsets, g.G, g.rows, 6, base, part, &bad);
   if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
-  const int NT = (g.N + kSmallBM - 1) / kSmallBM;
+  const int NT = (g.N + kF32Tile - 1) / kF32Tile;
   const int64_t total = int64_t(mtiles) * NT;
   for (int64_t tau = blockIdx.x; tau < total; tau += gridDim.x) {
     const int mtg = int(tau / NT), nt = int(tau - int64_t(mtg) * NT);
     const int l = find_expert(base, g.G, mtg);
-    const int64_t row0 = g.offsets[l] + int64_t(mtg - base[l]) * kSmallBM;
-    const int rows = int(min(int64_t(kSmallBM), g.offsets[l + 1] - row0));
-    const int c0 = nt * kSmallBM, cols = min(kSmallBM, g.N - c0);
-    const T* w = static_cast<const T*>(g.w) + int64_t(l) * g.N * g.K;
-    const SmallOperand<T> A{static_cast<const T*>(g.x) + row0 * g.ldx, g.ldx, rows, g.K};
-    const SmallOperand<T> B{W_KN ? w + c0 : w + int64_t(c0) * g.K, W_KN ? g.N : g.K, cols, g.K};
-    const f32x16 acc = small_tile<T, false, W_KN>(A, B, g.K, sa, sb);
+    const int64_t row0 = g.offsets[l] + int64_t(mtg - base[l]) * kF32Tile;
+    const int rows = int(min(int64_t(kF32Tile), g.offsets[l + 1] - row0));
+    const int c0 = nt * kF32Tile, cols = min(kF32Tile, g.N - c0);
+    const float* w = static_cast<const float*>(g.w) + int64_t(l) * g.N * g.K;
+    const F32Operand A{static_cast<const float*>(g.x) + row0 * g.ldx, g.ldx, rows};
+    const F32Operand B{W_KN ? w + c0 : w + int64_t(c0) * g.K, W_KN ? g.N : g.K, cols};
+    const f32x16 acc = f32_tile<false, W_KN>(A, B, g.K, reinterpret_cast<float*>(smem));
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = (wave & 1) * 32 + (lane & 31);
-    T* out = static_cast<T*>(g.y) + row0 * g.ldy + c0 + col;
+    float* out = static_cast<float*>(g.y) + row0 * g.ldy + c0 + col;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const int row = (wave >> 1) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-      if (row < rows && col < cols) put(out + row * g.ldy, acc[e]);
+      if (row < rows && col < cols) out[row * g.ldy] = acc[e];
     }
   }
 }
@@ -142,37 +123,35 @@ struct WgradArgs {
   int G, M, N;
 };
 
-template <typename T, typename O, bool ADD>
-__global__ __launch_bounds__(256) void grouped_small_wgrad_kernel(WgradArgs g) {
-  using S = SmallTile<T>;
-  __shared__ __attribute__((aligned(16))) T sa[kSmallBM * S::kPitch];
-  __shared__ __attribute__((aligned(16))) T sb[kSmallBM * S::kPitch];
+template <bool ADD>
+__global__ __launch_bounds__(256) void grouped_f32_wgrad_kernel(WgradArgs g) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ int32_t base[kMaxGroups + 1], part[5];
   bool bad;
   group_tiles<256>(g.offsets, g.G, g.rows, 6, base, part, &bad);
   if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
   if (bad) return;
-  const int MT = (g.M + kSmallBM - 1) / kSmallBM, NT = (g.N + kSmallBM - 1) / kSmallBM;
+  const int MT = (g.M + kF32Tile - 1) / kF32Tile, NT = (g.N + kF32Tile - 1) / kF32Tile;
   const int64_t total = int64_t(g.G) * MT * NT;
   for (int64_t tau = blockIdx.x; tau < total; tau += gridDim.x) {
     const int l = int(tau / (int64_t(MT) * NT));
     const int rem = int(tau - int64_t(l) * MT * NT);
-    const int m0 = (rem % MT) * kSmallBM, c0 = (rem / MT) * kSmallBM;
-    const int mr = min(kSmallBM, g.M - m0), cols = min(kSmallBM, g.N - c0);
+    const int m0 = (rem % MT) * kF32Tile, c0 = (rem / MT) * kF32Tile;
+    const int mr = min(kF32Tile, g.M - m0), cols = min(kF32Tile, g.N - c0);
     const int64_t r0 = g.offsets[l];
     const int n = int(g.offsets[l + 1] - r0);
-    const SmallOperand<T> A{static_cast<const T*>(g.a) + r0 * g.lda + m0, g.lda, mr, n};
-    const SmallOperand<T> B{static_cast<const T*>(g.b) + r0 * g.ldb + c0, g.ldb, cols, n};
-    const f32x16 acc = small_tile<T, true, true>(A, B, n, sa, sb);
+    const F32Operand A{static_cast<const float*>(g.a) + r0 * g.lda + m0, g.lda, mr};
+    const F32Operand B{static_cast<const float*>(g.b) + r0 * g.ldb + c0, g.ldb, cols};
+    const f32x16 acc = f32_tile<true, true>(A, B, n, reinterpret_cast<float*>(smem));
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = (wave & 1) * 32 + (lane & 31);
-    O* out = static_cast<O*>(g.dw) + (int64_t(l) * g.M + m0) * g.N + c0 + col;
+    float* out = static_cast<float*>(g.dw) + (int64_t(l) * g.M + m0) * g.N + c0 + col;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const int row = (wave >> 1) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
       if (row < mr && col < cols) {
         if constexpr (ADD) out[int64_t(row) * g.N] += acc[e];
-        else put(out + int64_t(row) * g.N, acc[e]);
+        else out[int64_t(row) * g.N] = acc[e];
       }
     }
   }
@@ -333,6 +312,10 @@ static hipError_t set_grouped_lds() {
               {reinterpret_cast<const void*>(grouped_big_wgrad_kernel<uint16_t, false>), kBigLds},
               {reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, false>), kBigLds},
               {reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, true>), kBigLds},
+              {reinterpret_cast<const void*>(grouped_f32_kernel<false>), kF32Lds},
+              {reinterpret_cast<const void*>(grouped_f32_kernel<true>), kF32Lds},
+              {reinterpret_cast<const void*>(grouped_f32_wgrad_kernel<false>), kF32Lds},
+              {reinterpret_cast<const void*>(grouped_f32_wgrad_kernel<true>), kF32Lds},
               {reinterpret_cast<const void*>(grouped_thin_kernel<false>), kThinLds},
               {reinterpret_cast<const void*>(grouped_thin_kernel<true>), kThinLds}};
     for (const auto& k : ks) {
@@ -356,13 +339,13 @@ hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, con
                           int32_t* status, int cus, hipStream_t st) {
   const GroupedArgs g{x, w, y, offsets, status, s.rows, s.ldx ? s.ldx : s.K, s.ldy ? s.ldy : s.N, s.groups, s.K, s.N};
   const dim3 threads(256);
-  if (s.dtype == MOE_F32) {
-    if (s.w_layout) hipLaunchKernelGGL((grouped_small_kernel<float, true>), dim3(cus * 4), threads, 0, st, g);
-    else hipLaunchKernelGGL((grouped_small_kernel<float, false>), dim3(cus * 4), threads, 0, st, g);
-    return hipGetLastError();
-  }
   const hipError_t e = set_grouped_lds();
   if (e != hipSuccess) return e;
+  if (s.dtype == MOE_F32) {
+    if (s.w_layout) hipLaunchKernelGGL(grouped_f32_kernel<true>, dim3(cus * 2), threads, kF32Lds, st, g);
+    else hipLaunchKernelGGL(grouped_f32_kernel<false>, dim3(cus * 2), threads, kF32Lds, st, g);
+    return hipGetLastError();
+  }
   if (!thin_rows(s, cus)) {
     const dim3 big((cus / 8) * 8);
     // K of whole steps: no check at the fills (a tenth of 8192^3)
@@ -385,13 +368,12 @@ hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* 
   const int64_t ldx = s.ldx ? s.ldx : s.K, ldy = s.ldy ? s.ldy : s.N;
   const WgradArgs g = s.w_layout ? WgradArgs{x, dy, dw, offsets, status, s.rows, ldx, ldy, s.groups, s.K, s.N}
                                  : WgradArgs{dy, x, dw, offsets, status, s.rows, ldy, ldx, s.groups, s.N, s.K};
-  const dim3 grid(cus * 4), threads(256);
+  const hipError_t e = set_grouped_lds();
+  if (e != hipSuccess) return e;
   if (s.dtype == MOE_F32) {
-    if (accumulate) hipLaunchKernelGGL((grouped_small_wgrad_kernel<float, float, true>), grid, threads, 0, st, g);
-    else hipLaunchKernelGGL((grouped_small_wgrad_kernel<float, float, false>), grid, threads, 0, st, g);
+    if (accumulate) hipLaunchKernelGGL(grouped_f32_wgrad_kernel<true>, dim3(cus * 2), dim3(256), kF32Lds, st, g);
+    else hipLaunchKernelGGL(grouped_f32_wgrad_kernel<false>, dim3(cus * 2), dim3(256), kF32Lds, st, g);
   } else {
-    const hipError_t e = set_grouped_lds();
-    if (e != hipSuccess) return e;
     const dim3 big((cus / 8) * 8), many(kBigThreads);
     if (dw_dtype != MOE_F32) hipLaunchKernelGGL((grouped_big_wgrad_kernel<uint16_t, false>), big, many, kBigLds, st, g);
     else if (accumulate) hipLaunchKernelGGL((grouped_big_wgrad_kernel<float, true>), big, many, kBigLds, st, g);
