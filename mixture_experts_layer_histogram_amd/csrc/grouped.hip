@@ -8,14 +8,15 @@
 
 namespace moe {
 
-// fp32, on the fp32 MFMA (v_mfma_f32_32x32x2_f32): a 64 x 64 tile of C = A B^T, A and B each stored with K contiguous (element (r, k) at
-// r * ld + k) or with the row index contiguous (at k * ld + r).  256 threads, wave w owns the 32 x 32 block (w >> 1, w & 1).  K goes by
-// steps of 128 through LDS, in the order it is stored in (rows padded so that 64 lanes' reads touch all banks), and the next step's loads are on
-// their way in registers while one is at work: small products are a chain of such round trips (509 rows on 8 x (128 x 256), both gradients:
-// 24.9 us with steps of 32 and no loads ahead).
-constexpr int kF32Tile = 64, kF32Step = 128, kF32PitchK = kF32Step + 4, kF32PitchR = kF32Tile + 8;
-constexpr int kF32Panel = kF32Step * kF32PitchR > kF32Tile * kF32PitchK ? kF32Step * kF32PitchR : kF32Tile * kF32PitchK;   // values
-constexpr int kF32Lds = 2 * kF32Panel * 4;
+// fp32, on the fp32 MFMA (v_mfma_f32_32x32x2_f32): a TB x TB tile of C = A B^T, A and B each stored with K contiguous (element (r, k) at
+// r * ld + k) or with the row index contiguous (at k * ld + r), by 256 threads.  TB 64: wave w owns the 32 x 32 block (w >> 1, w & 1).  TB 32:
+// the four waves share the block's K and add up through LDS in wave order, for so few tiles that 64 x 64 would leave most of the card
+// idle (64 MFMAs of 64 cycles a wave and step: half of what a tiny product takes).  K goes by steps of 128 through LDS, in the order it is
+// stored in (rows padded so that 64 lanes' reads touch all banks), and the next step's loads are on their way in registers while one is
+// at work: small products are a chain of such round trips.
+constexpr int kF32Step = 128, kF32PitchK = kF32Step + 4;
+constexpr int f32_panel(int tb) { return kF32Step * (tb + 8) > tb * kF32PitchK ? kF32Step * (tb + 8) : tb * kF32PitchK; }   // values
+constexpr int f32_lds_bytes(int tb) { return 2 * f32_panel(tb) * 4; }
 
 struct F32Operand {
   const float* p;
@@ -23,16 +24,17 @@ struct F32Operand {
   int rows;                    // valid ones of the tile
 };
 
-template <bool MN>
+template <int TB, bool MN>
 struct F32Fill {
-  f32x4 v[8];                  // a thread's share of a step: 64 x 128 values of 256 threads
+  static constexpr int kVecs = TB * kF32Step / 4 / 256, kPitchR = TB + 8, kPerRow = TB / 4;
+  f32x4 v[kVecs];              // a thread's share of a step
 
-  // from k0 on, zeros past `left` values of K and past the rows (both multiples of 4 along the contiguous axis)
+  // from k0 on, zeros past `left` values of K and past the rows (multiples of 4 along the contiguous axis)
   __device__ __forceinline__ void load(const F32Operand& o, int k0, int left) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kVecs; ++i) {
       const int t = threadIdx.x + i * 256;
-      const int r = MN ? (t & 15) * 4 : t >> 5, k = MN ? t >> 4 : (t & 31) * 4;
+      const int r = MN ? t % kPerRow * 4 : t >> 5, k = MN ? t / kPerRow : (t & 31) * 4;
       v[i] = f32x4{0, 0, 0, 0};
       if (r < o.rows && k < left)
         v[i] = *reinterpret_cast<const f32x4*>(o.p + (MN ? int64_t(k0 + k) * o.ld + r : int64_t(r) * o.ld + k0 + k));
@@ -40,29 +42,30 @@ struct F32Fill {
   }
   __device__ __forceinline__ void put(float* lds) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kVecs; ++i) {
       const int t = threadIdx.x + i * 256;
-      *reinterpret_cast<f32x4*>(lds + (MN ? (t >> 4) * kF32PitchR + (t & 15) * 4 : (t >> 5) * kF32PitchK + (t & 31) * 4)) = v[i];
+      *reinterpret_cast<f32x4*>(lds + (MN ? t / kPerRow * kPitchR + t % kPerRow * 4 : (t >> 5) * kF32PitchK + (t & 31) * 4)) = v[i];
     }
   }
   // lane's four K values of row r: k = 8 c + 4 hi + 0..3
   static __device__ __forceinline__ f32x4 frag(const float* lds, int r, int c, int hi) {
     if constexpr (!MN) return *reinterpret_cast<const f32x4*>(lds + r * kF32PitchK + c * 8 + hi * 4);
-    const float* q = lds + (c * 8 + hi * 4) * kF32PitchR + r;
-    return f32x4{q[0], q[kF32PitchR], q[2 * kF32PitchR], q[3 * kF32PitchR]};
+    const float* q = lds + (c * 8 + hi * 4) * kPitchR + r;
+    return f32x4{q[0], q[kPitchR], q[2 * kPitchR], q[3 * kPitchR]};
   }
 };
 
-template <bool A_MN, bool B_MN>
-__device__ __forceinline__ f32x16 f32_tile(const F32Operand& A, const F32Operand& B, int K, float* smem) {
+// out(row, column, value) of the tile's valid values
+template <int TB, bool A_MN, bool B_MN, typename OUT>
+__device__ __forceinline__ void f32_tile(const F32Operand& A, const F32Operand& B, int K, float* smem, OUT out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, hi = lane >> 5;
-  float *sa = smem, *sb = smem + kF32Panel;
+  const int wm = TB == 64 ? wave >> 1 : 0, wn = TB == 64 ? wave & 1 : 0, r32 = lane & 31, hi = lane >> 5;
+  float *sa = smem, *sb = smem + f32_panel(TB);
   f32x16 acc;
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-  F32Fill<A_MN> fa;
-  F32Fill<B_MN> fb;
+  F32Fill<TB, A_MN> fa;
+  F32Fill<TB, B_MN> fb;
   fa.load(A, 0, K);
   fb.load(B, 0, K);
   for (int k0 = 0; k0 < K; k0 += kF32Step) {
@@ -72,44 +75,58 @@ __device__ __forceinline__ f32x16 f32_tile(const F32Operand& A, const F32Operand
     fa.load(A, k0 + kF32Step, K - k0 - kF32Step);
     fb.load(B, k0 + kF32Step, K - k0 - kF32Step);
     const int steps = min(kF32Step, K - k0 + 7) >> 3;
-    for (int c = 0; c < steps; ++c) {
-      const f32x4 a = F32Fill<A_MN>::frag(sa, wm * 32 + r32, c, hi);
-      const f32x4 b = F32Fill<B_MN>::frag(sb, wn * 32 + r32, c, hi);
+    for (int c = TB == 64 ? 0 : wave; c < steps; c += TB == 64 ? 1 : 4) {
+      const f32x4 a = F32Fill<TB, A_MN>::frag(sa, wm * 32 + r32, c, hi);
+      const f32x4 b = F32Fill<TB, B_MN>::frag(sb, wn * 32 + r32, c, hi);
 #pragma unroll
       for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[s], b[s], acc, 0, 0, 0);
     }
     __syncthreads();                         // the next step overwrites these
   }
-  return acc;
+  // lane holds column r32 and rows 8 (e / 4) + 4 hi + e % 4 of its block
+  if constexpr (TB == 64) {
+    const int col = wn * 32 + r32;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int row = wm * 32 + 8 * (e >> 2) + 4 * hi + (e & 3);
+      if (row < A.rows && col < B.rows) out(row, col, acc[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) smem[(wave * 16 + e) * 64 + lane] = acc[e];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = wave * 4 + j, row = 8 * wave + 4 * hi + j;
+      float t = smem[e * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) t += smem[(w * 16 + e) * 64 + lane];
+      if (row < A.rows && r32 < B.rows) out(row, r32, t);
+    }
+    __syncthreads();
+  }
 }
 
-template <bool W_KN>
+template <int TB, bool W_KN>
 __global__ __launch_bounds__(256) void grouped_f32_kernel(GroupedArgs g) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ int32_t base[kMaxGroups + 1], part[5];
   bool bad;
-  const int mtiles = group_tiles<256>(g.offsets, g.G, g.rows, 6, base, part, &bad);
+  const int mtiles = group_tiles<256>(g.offsets, g.G, g.rows, TB == 64 ? 6 : 5, base, part, &bad);
   if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
-  const int NT = (g.N + kF32Tile - 1) / kF32Tile;
+  const int NT = (g.N + TB - 1) / TB;
   const int64_t total = int64_t(mtiles) * NT;
   for (int64_t tau = blockIdx.x; tau < total; tau += gridDim.x) {
     const int mtg = int(tau / NT), nt = int(tau - int64_t(mtg) * NT);
     const int l = find_expert(base, g.G, mtg);
-    const int64_t row0 = g.offsets[l] + int64_t(mtg - base[l]) * kF32Tile;
-    const int rows = int(min(int64_t(kF32Tile), g.offsets[l + 1] - row0));
-    const int c0 = nt * kF32Tile, cols = min(kF32Tile, g.N - c0);
+    const int64_t row0 = g.offsets[l] + int64_t(mtg - base[l]) * TB;
+    const int rows = int(min(int64_t(TB), g.offsets[l + 1] - row0));
+    const int c0 = nt * TB, cols = min(TB, g.N - c0);
     const float* w = static_cast<const float*>(g.w) + int64_t(l) * g.N * g.K;
     const F32Operand A{static_cast<const float*>(g.x) + row0 * g.ldx, g.ldx, rows};
     const F32Operand B{W_KN ? w + c0 : w + int64_t(c0) * g.K, W_KN ? g.N : g.K, cols};
-    const f32x16 acc = f32_tile<false, W_KN>(A, B, g.K, reinterpret_cast<float*>(smem));
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int col = (wave & 1) * 32 + (lane & 31);
-    float* out = static_cast<float*>(g.y) + row0 * g.ldy + c0 + col;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int row = (wave >> 1) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-      if (row < rows && col < cols) out[row * g.ldy] = acc[e];
-    }
+    float* y = static_cast<float*>(g.y) + row0 * g.ldy + c0;
+    f32_tile<TB, false, W_KN>(A, B, g.K, reinterpret_cast<float*>(smem), [&](int r, int c, float v) { y[r * g.ldy + c] = v; });
   }
 }
 
@@ -123,7 +140,7 @@ struct WgradArgs {
   int G, M, N;
 };
 
-template <bool ADD>
+template <int TB, bool ADD>
 __global__ __launch_bounds__(256) void grouped_f32_wgrad_kernel(WgradArgs g) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ int32_t base[kMaxGroups + 1], part[5];
@@ -131,29 +148,21 @@ __global__ __launch_bounds__(256) void grouped_f32_wgrad_kernel(WgradArgs g) {
   group_tiles<256>(g.offsets, g.G, g.rows, 6, base, part, &bad);
   if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
   if (bad) return;
-  const int MT = (g.M + kF32Tile - 1) / kF32Tile, NT = (g.N + kF32Tile - 1) / kF32Tile;
+  const int MT = (g.M + TB - 1) / TB, NT = (g.N + TB - 1) / TB;
   const int64_t total = int64_t(g.G) * MT * NT;
   for (int64_t tau = blockIdx.x; tau < total; tau += gridDim.x) {
     const int l = int(tau / (int64_t(MT) * NT));
     const int rem = int(tau - int64_t(l) * MT * NT);
-    const int m0 = (rem % MT) * kF32Tile, c0 = (rem / MT) * kF32Tile;
-    const int mr = min(kF32Tile, g.M - m0), cols = min(kF32Tile, g.N - c0);
+    const int m0 = (rem % MT) * TB, c0 = (rem / MT) * TB;
     const int64_t r0 = g.offsets[l];
     const int n = int(g.offsets[l + 1] - r0);
-    const F32Operand A{static_cast<const float*>(g.a) + r0 * g.lda + m0, g.lda, mr};
-    const F32Operand B{static_cast<const float*>(g.b) + r0 * g.ldb + c0, g.ldb, cols};
-    const f32x16 acc = f32_tile<true, true>(A, B, n, reinterpret_cast<float*>(smem));
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int col = (wave & 1) * 32 + (lane & 31);
-    float* out = static_cast<float*>(g.dw) + (int64_t(l) * g.M + m0) * g.N + c0 + col;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int row = (wave >> 1) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-      if (row < mr && col < cols) {
-        if constexpr (ADD) out[int64_t(row) * g.N] += acc[e];
-        else out[int64_t(row) * g.N] = acc[e];
-      }
-    }
+    const F32Operand A{static_cast<const float*>(g.a) + r0 * g.lda + m0, g.lda, min(TB, g.M - m0)};
+    const F32Operand B{static_cast<const float*>(g.b) + r0 * g.ldb + c0, g.ldb, min(TB, g.N - c0)};
+    float* dw = static_cast<float*>(g.dw) + (int64_t(l) * g.M + m0) * g.N + c0;
+    f32_tile<TB, true, true>(A, B, n, reinterpret_cast<float*>(smem), [&](int r, int c, float v) {
+      if constexpr (ADD) dw[int64_t(r) * g.N + c] += v;
+      else dw[int64_t(r) * g.N + c] = v;
+    });
   }
 }
 
@@ -312,10 +321,14 @@ static hipError_t set_grouped_lds() {
               {reinterpret_cast<const void*>(grouped_big_wgrad_kernel<uint16_t, false>), kBigLds},
               {reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, false>), kBigLds},
               {reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, true>), kBigLds},
-              {reinterpret_cast<const void*>(grouped_f32_kernel<false>), kF32Lds},
-              {reinterpret_cast<const void*>(grouped_f32_kernel<true>), kF32Lds},
-              {reinterpret_cast<const void*>(grouped_f32_wgrad_kernel<false>), kF32Lds},
-              {reinterpret_cast<const void*>(grouped_f32_wgrad_kernel<true>), kF32Lds},
+              {reinterpret_cast<const void*>(grouped_f32_kernel<32, false>), f32_lds_bytes(32)},
+              {reinterpret_cast<const void*>(grouped_f32_kernel<32, true>), f32_lds_bytes(32)},
+              {reinterpret_cast<const void*>(grouped_f32_kernel<64, false>), f32_lds_bytes(64)},
+              {reinterpret_cast<const void*>(grouped_f32_kernel<64, true>), f32_lds_bytes(64)},
+              {reinterpret_cast<const void*>(grouped_f32_wgrad_kernel<32, false>), f32_lds_bytes(32)},
+              {reinterpret_cast<const void*>(grouped_f32_wgrad_kernel<32, true>), f32_lds_bytes(32)},
+              {reinterpret_cast<const void*>(grouped_f32_wgrad_kernel<64, false>), f32_lds_bytes(64)},
+              {reinterpret_cast<const void*>(grouped_f32_wgrad_kernel<64, true>), f32_lds_bytes(64)},
               {reinterpret_cast<const void*>(grouped_thin_kernel<false>), kThinLds},
               {reinterpret_cast<const void*>(grouped_thin_kernel<true>), kThinLds}};
     for (const auto& k : ks) {
@@ -335,6 +348,12 @@ static bool thin_rows(const moe_gemm_t& s, int cus) {
   return s.rows <= int64_t(s.groups) * (tiles * 2 < cus ? 128 : 24);
 }
 
+// fp32 workgroups for at most `tiles` tiles of 64 x 64 (four times as many of 32 x 32 where they are fewer than the CUs)
+static int f32_grid(int64_t tiles, int cus) {
+  const int64_t n = tiles < cus ? tiles * 4 : tiles;
+  return int(n < 1 ? 1 : n < cus * 2 ? n : cus * 2);
+}
+
 hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, const int32_t* offsets, void* y,
                           int32_t* status, int cus, hipStream_t st) {
   const GroupedArgs g{x, w, y, offsets, status, s.rows, s.ldx ? s.ldx : s.K, s.ldy ? s.ldy : s.N, s.groups, s.K, s.N};
@@ -342,8 +361,13 @@ hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, con
   const hipError_t e = set_grouped_lds();
   if (e != hipSuccess) return e;
   if (s.dtype == MOE_F32) {
-    if (s.w_layout) hipLaunchKernelGGL(grouped_f32_kernel<true>, dim3(cus * 2), threads, kF32Lds, st, g);
-    else hipLaunchKernelGGL(grouped_f32_kernel<false>, dim3(cus * 2), threads, kF32Lds, st, g);
+    const int64_t rows = s.rows / 64 + (s.rows < s.groups ? s.rows : s.groups), tiles = rows * ((s.N + 63) / 64);     // at most
+    const int lds = f32_lds_bytes(tiles < cus ? 32 : 64);
+    const dim3 grid(f32_grid(tiles, cus));
+    if (tiles < cus && s.w_layout) hipLaunchKernelGGL((grouped_f32_kernel<32, true>), grid, threads, lds, st, g);
+    else if (tiles < cus) hipLaunchKernelGGL((grouped_f32_kernel<32, false>), grid, threads, lds, st, g);
+    else if (s.w_layout) hipLaunchKernelGGL((grouped_f32_kernel<64, true>), grid, threads, lds, st, g);
+    else hipLaunchKernelGGL((grouped_f32_kernel<64, false>), grid, threads, lds, st, g);
     return hipGetLastError();
   }
   if (!thin_rows(s, cus)) {
@@ -371,8 +395,13 @@ hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* 
   const hipError_t e = set_grouped_lds();
   if (e != hipSuccess) return e;
   if (s.dtype == MOE_F32) {
-    if (accumulate) hipLaunchKernelGGL(grouped_f32_wgrad_kernel<true>, dim3(cus * 2), dim3(256), kF32Lds, st, g);
-    else hipLaunchKernelGGL(grouped_f32_wgrad_kernel<false>, dim3(cus * 2), dim3(256), kF32Lds, st, g);
+    const int64_t tiles = int64_t(g.G) * ((g.M + 63) / 64) * ((g.N + 63) / 64);
+    const int lds = f32_lds_bytes(tiles < cus ? 32 : 64);
+    const dim3 grid(f32_grid(tiles, cus)), threads(256);
+    if (tiles < cus && accumulate) hipLaunchKernelGGL((grouped_f32_wgrad_kernel<32, true>), grid, threads, lds, st, g);
+    else if (tiles < cus) hipLaunchKernelGGL((grouped_f32_wgrad_kernel<32, false>), grid, threads, lds, st, g);
+    else if (accumulate) hipLaunchKernelGGL((grouped_f32_wgrad_kernel<64, true>), grid, threads, lds, st, g);
+    else hipLaunchKernelGGL((grouped_f32_wgrad_kernel<64, false>), grid, threads, lds, st, g);
   } else {
     const dim3 big((cus / 8) * 8), many(kBigThreads);
     if (dw_dtype != MOE_F32) hipLaunchKernelGGL((grouped_big_wgrad_kernel<uint16_t, false>), big, many, kBigLds, st, g);
