@@ -105,6 +105,8 @@ hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, con
 hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* dy, const int32_t* offsets, void* dw,
                                 int dw_dtype, bool accumulate, int32_t* status, int cus, hipStream_t st);
 hipError_t launch_adamw(const moe_adamw_t& h, const moe_adamw_tensor_t* tensors, int count, int cus, hipStream_t st);
+hipError_t launch_states_values(const uint8_t* codes, const uint8_t* scales, int64_t rows, void* dst, int dst_dtype,
+                                hipStream_t st);
 }  // namespace moe
 
 using namespace moe;
@@ -305,6 +307,8 @@ int moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t forma
   if (K % 128) return MOE_EALIGN;
   if (const int rc = check_codec(dst, codes, scales, rows)) return rc;
   if (rows == 0) return MOE_OK;
+  if (format == MOE_MXFP8 && K == 128)
+    return hip_rc(launch_states_values(codes, scales, rows, dst, dst_dtype, static_cast<hipStream_t>(stream)));
   return hip_rc(launch_mx_dequantize(codes, scales, format, rows, K, dst, dst_dtype,
                                      static_cast<hipStream_t>(stream)));
 }

@@ -161,6 +161,24 @@ def test_values_on_the_device(eight):
     a.check(old, 0, 77, 9, True, scale=0.25)
 
 
+@pytest.mark.parametrize("stochastic", [True, False])
+def test_blocks_of_very_different_values(stochastic):
+    """Gradients over forty powers of ten in one block: codes below E4M3's smallest power of two, zeros, roots that take the smallest
+    code, states below fp32's normal range, blocks of zeros, the largest values."""
+    torch = _torch()
+    for seed in range(3):
+        t = Tensor(4096, "f32", "f32", False, True, 20 + seed, zero=seed == 0, wd=0.0)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        size = 10.0 ** (40 * torch.rand(4096, generator=g, device="cuda") - 34)
+        t.grad[:4096] = torch.randn(4096, generator=g, device="cuda") * size
+        t.grad[64:96] = 0
+        t.grad[96:128] *= 1e-12
+        t.grad[128:160] = 1e18 * torch.sign(t.grad[128:160])
+        old = t.copy()
+        moe.moe_adamw(moe.AdamW(LR, BETA1, BETA2, EPS, 5, moe.MOE_MXFP8, int(stochastic), seed), [t.entry()])
+        t.check(old, 0, 5, seed, stochastic)
+
+
 def test_wild_gradients():
     """NaN and infinite gradients: their values alone in fp32 states, their blocks in 8 bits, for good."""
     torch = _torch()
