@@ -816,9 +816,9 @@ typedef struct {
  * w: [groups][N][K] or [groups][K][N], dense.  K, N, ldx and ldy are multiples of 16 bytes and so are the addresses (else
  * MOE_EALIGN); K * N < 2^31, ldx and ldy <= 2^22.  y may be neither x nor w (MOE_EINVAL) and overlap neither.
  * status: NULL, or a 4-byte-aligned DEVICE int32 that receives 0 or MOE_EINVAL (bad offsets).  No workspace.
- * `rows` (not the rows that the groups have, which the host does not know) chooses between a kernel for few rows a group
- * and one for many; either is right for any number.  Deterministic; a row's result depends on its own values and
- * on `rows` and the sizes only.
+ * `rows` (not the rows that the groups have, which the host does not know) chooses between kernels for few rows a group
+ * and for many; each is right for any number.  Deterministic: the same call gives the same bits.  The order of a row's sum goes
+ * by `rows`, the sizes and the offsets, so that it may change with the rows of other groups (never with their values).
  */
 int moe_grouped_gemm(const moe_gemm_t* g, const void* x, const void* w, const int32_t* offsets, void* y,
                      int32_t* status, void* stream);
@@ -829,7 +829,7 @@ int moe_grouped_gemm(const moe_gemm_t* g, const void* x, const void* w, const in
  * fp32 accumulation, rounded once to dw_dtype: the row type, or MOE_F32.  A group with no rows gets zeros.
  * accumulate != 0: added to what dw holds (MOE_F32 only, else MOE_EINVAL): gradients of several batches.
  * dy: rows of N values with stride ldy.  ws: at least moe_grouped_gemm_wgrad_workspace_bytes() bytes, 256-byte aligned
- * (NULL where that is 0).  Other arguments, limits and errors as moe_grouped_gemm; with bad offsets dw stays as it is.
+ * (NULL where that is 0; the kernels of this version need none).  Other arguments, limits and errors as moe_grouped_gemm; with bad offsets dw stays as it is.
  */
 size_t moe_grouped_gemm_wgrad_workspace_bytes(const moe_gemm_t* g);
 int moe_grouped_gemm_wgrad(const moe_gemm_t* g, const void* x, const void* dy, const int32_t* offsets, void* dw,

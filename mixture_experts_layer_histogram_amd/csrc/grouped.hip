@@ -3,6 +3,7 @@
 //   dW_g = sum over s of dy[s]^T x[s] (or its transpose), the gradient by the weights.
 // The gradient by the rows is the first product in the weights' other orientation.
 #include "grouped.hpp"
+#include "grouped_mid.hpp"
 #include "grouped_thin.hpp"
 #include "grouped_tile.hpp"
 
@@ -169,67 +170,82 @@ __global__ __launch_bounds__(256) void grouped_f32_wgrad_kernel(WgradArgs g) {
 // 256 x 256 tiles in bf16 (grouped_tile.hpp): the list of all tiles is cut into eight contiguous ranges, one for an XCD (workgroup w
 // runs on XCD w mod 8), by group, then as big_place says.  A workgroup takes every 32nd tile of its XCD's range, 64 at a
 // time: lane i of each wave looks up the i-th and keeps it.
-template <bool W_KN, bool CUT>
+template <int T, bool W_KN, bool CUT>
 struct BigProducts {
-  static constexpr int kCut = CUT;
+  static constexpr int kCut = CUT, kAt = T == 256 ? 18 : 17;   // rows - 1 take 8 bits or 7
   const GroupedArgs& g;
-  uint32_t what;                 // this lane's tile: group | (rows - 1) << 10 | column tile << 18
+  uint32_t what;                 // this lane's tile: group | (rows - 1) << 10 | column tile << kAt
   int32_t row0;
   int n;
 
   __device__ __forceinline__ uint32_t w_(int i) const { return uint32_t(__builtin_amdgcn_readlane(int(what), i)); }
   __device__ __forceinline__ int count() const { return n; }
   __device__ __forceinline__ int K(int) const { return g.K; }
-  __device__ __forceinline__ int rows(int i) const { return int((w_(i) >> 10) & 255) + 1; }
-  __device__ __forceinline__ int cols(int i) const { return min(kBig, g.N - int(w_(i) >> 18) * kBig); }
+  __device__ __forceinline__ int rows(int i) const { return int((w_(i) >> 10) & (T - 1)) + 1; }
+  __device__ __forceinline__ int cols(int i) const { return min(T, g.N - int(w_(i) >> kAt) * T); }
   __device__ __forceinline__ BigOperand a(int i) const {
     return BigOperand{static_cast<const uint16_t*>(g.x) + int64_t(__builtin_amdgcn_readlane(row0, i)) * g.ldx, g.ldx, rows(i)};
   }
   __device__ __forceinline__ BigOperand b(int i) const {
-    const int c0 = int(w_(i) >> 18) * kBig;
+    const int c0 = int(w_(i) >> kAt) * T;
     const uint16_t* w = static_cast<const uint16_t*>(g.w) + int64_t(w_(i) & 1023) * g.N * g.K;
     return BigOperand{W_KN ? w + c0 : w + int64_t(c0) * g.K, W_KN ? g.N : g.K, cols(i)};
   }
   template <typename WALK>
   __device__ __forceinline__ void store(int i, const WALK& walk) const {
     big_store<uint16_t, false, false>(walk, static_cast<uint16_t*>(g.y) + int64_t(__builtin_amdgcn_readlane(row0, i)) * g.ldy +
-                               int(w_(i) >> 18) * kBig, g.ldy, rows(i), cols(i));
+                               int(w_(i) >> kAt) * T, g.ldy, rows(i), cols(i));
   }
 };
 
-template <bool W_KN, bool CUT>
-__global__ __launch_bounds__(kBigThreads, 2) void grouped_big_kernel(GroupedArgs g) {
-  extern __shared__ __attribute__((aligned(16))) char smem[];
-  const int NT = (g.N + kBig - 1) / kBig;
+template <int T, int THREADS, bool W_KN, bool CUT>
+__device__ __forceinline__ void grouped_tiles(const GroupedArgs& g, char* smem) {
+  const int NT = (g.N + T - 1) / T;
   const int xcd = blockIdx.x & 7, wg_per_xcd = gridDim.x >> 3, lane = threadIdx.x & 63;
   int32_t* base = reinterpret_cast<int32_t*>(smem);
   int64_t per_xcd = int64_t(1) << 40;     // known after the first look at the offsets
   for (int64_t t0 = blockIdx.x >> 3; t0 < per_xcd; t0 += 64 * int64_t(wg_per_xcd)) {
     bool bad;
-    const int mtiles = group_tiles<kBigThreads>(g.offsets, g.G, g.rows, 8, base, base + kMaxGroups + 8, &bad);
+    const int mtiles = group_tiles<THREADS>(g.offsets, g.G, g.rows, T == 256 ? 8 : 7, base, base + kMaxGroups + 8, &bad);
     if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
     const int64_t total = int64_t(mtiles) * NT;
     per_xcd = (total + 7) >> 3;
     const int64_t tt = t0 + int64_t(lane) * wg_per_xcd, tau = xcd * per_xcd + tt;
-    BigProducts<W_KN, CUT> tiles{g, 0, 0, 0};
+    BigProducts<T, W_KN, CUT> tiles{g, 0, 0, 0};
     const bool mine = tt < per_xcd && tau < total;
     if (mine) {
       const int l = find_expert(base, g.G, int(tau / NT));
       int mt, nt;
       big_place(tau - int64_t(base[l]) * NT, base[l + 1] - base[l], NT, &mt, &nt);
-      tiles.row0 = g.offsets[l] + mt * kBig;
-      tiles.what = uint32_t(l) | uint32_t(min(kBig, g.offsets[l + 1] - tiles.row0) - 1) << 10 | uint32_t(nt) << 18;
+      tiles.row0 = g.offsets[l] + mt * T;
+      tiles.what = uint32_t(l) | uint32_t(min(T, g.offsets[l + 1] - tiles.row0) - 1) << 10 | uint32_t(nt) << tiles.kAt;
     }
     tiles.n = __popcll(__ballot(mine));
     __syncthreads();                      // the tables' LDS becomes the ring's
-    BigWalk<false, W_KN, BigProducts<W_KN, CUT>> walk(tiles, smem);
-    walk.run();
+    if constexpr (T == 256) {
+      BigWalk<false, W_KN, BigProducts<T, W_KN, CUT>> walk(tiles, smem);
+      walk.run();
+    } else {
+      MidWalk<false, W_KN, BigProducts<T, W_KN, CUT>> walk;
+      walk.run(tiles, smem);
+    }
     __syncthreads();
   }
 }
 
+template <bool W_KN, bool CUT>
+__global__ __launch_bounds__(kBigThreads, 2) void grouped_big_kernel(GroupedArgs g) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  grouped_tiles<256, kBigThreads, W_KN, CUT>(g, smem);
+}
+template <bool W_KN>
+__global__ __launch_bounds__(kMidThreads, 1) void grouped_mid_kernel(GroupedArgs g) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  grouped_tiles<128, kMidThreads, W_KN, true>(g, smem);
+}
+
 // The same for the gradient by the weights: a tile of 256 x 256 of one group's gradient sums over the group's rows.
-template <typename O, bool ADD>
+template <int T, typename O, bool ADD>
 struct BigGradients {
   static constexpr int kCut = 2;
   const WgradArgs& g;
@@ -238,13 +254,13 @@ struct BigGradients {
   int n;
 
   __device__ __forceinline__ int group(int i) const { return __builtin_amdgcn_readlane(int(gm), i) & 1023; }
-  __device__ __forceinline__ int m0(int i) const { return int(uint32_t(__builtin_amdgcn_readlane(int(gm), i)) >> 10) * kBig; }
-  __device__ __forceinline__ int c0(int i) const { return __builtin_amdgcn_readlane(nt, i) * kBig; }
+  __device__ __forceinline__ int m0(int i) const { return int(uint32_t(__builtin_amdgcn_readlane(int(gm), i)) >> 10) * T; }
+  __device__ __forceinline__ int c0(int i) const { return __builtin_amdgcn_readlane(nt, i) * T; }
   __device__ __forceinline__ int count() const { return n; }
   __device__ __forceinline__ int K(int i) const { return __builtin_amdgcn_readlane(k, i); }
   __device__ __forceinline__ int64_t first(int i) const { return __builtin_amdgcn_readlane(r0, i); }
-  __device__ __forceinline__ int rows(int i) const { return min(kBig, g.M - m0(i)); }
-  __device__ __forceinline__ int cols(int i) const { return min(kBig, g.N - c0(i)); }
+  __device__ __forceinline__ int rows(int i) const { return min(T, g.M - m0(i)); }
+  __device__ __forceinline__ int cols(int i) const { return min(T, g.N - c0(i)); }
   __device__ __forceinline__ BigOperand a(int i) const {
     return BigOperand{static_cast<const uint16_t*>(g.a) + first(i) * g.lda + m0(i), g.lda, rows(i)};
   }
@@ -257,16 +273,15 @@ struct BigGradients {
   }
 };
 
-template <typename O, bool ADD>
-__global__ __launch_bounds__(kBigThreads, 2) void grouped_big_wgrad_kernel(WgradArgs g) {
-  extern __shared__ __attribute__((aligned(16))) char smem[];
+template <int T, int THREADS, typename O, bool ADD>
+__device__ __forceinline__ void grouped_gradients(const WgradArgs& g, char* smem) {
   int32_t* base = reinterpret_cast<int32_t*>(smem);
   bool bad;
-  group_tiles<kBigThreads>(g.offsets, g.G, g.rows, 8, base, base + kMaxGroups + 8, &bad);
+  group_tiles<THREADS>(g.offsets, g.G, g.rows, 8, base, base + kMaxGroups + 8, &bad);
   if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
   if (bad) return;
   __syncthreads();
-  const int MT = (g.M + kBig - 1) / kBig, NT = (g.N + kBig - 1) / kBig;
+  const int MT = (g.M + T - 1) / T, NT = (g.N + T - 1) / T;
   const int64_t total = int64_t(g.G) * MT * NT, per_xcd = (total + 7) >> 3;
   const int xcd = blockIdx.x & 7, wg_per_xcd = gridDim.x >> 3, lane = threadIdx.x & 63;
   for (int64_t t0 = blockIdx.x >> 3; t0 < per_xcd; t0 += 64 * int64_t(wg_per_xcd)) {
@@ -283,7 +298,7 @@ __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_wgrad_kernel(Wgrad
     // tiles of groups with rows first in the lanes' order, the others behind them get zeros
     const uint64_t below = (uint64_t(1) << lane) - 1;
     const int to = rows > 0 ? __popcll(full & below) : mine ? __popcll(full) + __popcll(empty & below) : 63;
-    BigGradients<O, ADD> tiles{g, 0, 0, 0, 0, int(__popcll(full))};
+    BigGradients<T, O, ADD> tiles{g, 0, 0, 0, 0, int(__popcll(full))};
     if (full | empty) {
       tiles.gm = uint32_t(__builtin_amdgcn_ds_permute(to * 4, mine ? int(uint32_t(l) | uint32_t(mt) << 10) : 0));
       tiles.nt = __builtin_amdgcn_ds_permute(to * 4, nt);
@@ -294,17 +309,33 @@ __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_wgrad_kernel(Wgrad
       for (int i = tiles.n; i < tiles.n + int(__popcll(empty)); ++i) {
         O* out = static_cast<O*>(g.dw) + (int64_t(tiles.group(i)) * g.M + tiles.m0(i)) * g.N + tiles.c0(i);
         constexpr int V = 16 / sizeof(O);
-        for (int v = threadIdx.x; v < kBig * (kBig / V); v += kBigThreads) {
-          const int row = v / (kBig / V), col = v % (kBig / V) * V;
+        for (int v = threadIdx.x; v < T * (T / V); v += THREADS) {
+          const int row = v / (T / V), col = v % (T / V) * V;
           if (row < tiles.rows(i) && col < tiles.cols(i))
             *reinterpret_cast<u32x4*>(out + int64_t(row) * g.N + col) = u32x4{0, 0, 0, 0};
         }
       }
     }
-    BigWalk<true, true, BigGradients<O, ADD>> walk(tiles, smem);
-    walk.run();
+    if constexpr (T == 256) {
+      BigWalk<true, true, BigGradients<T, O, ADD>> walk(tiles, smem);
+      walk.run();
+    } else {
+      MidWalk<true, true, BigGradients<T, O, ADD>> walk;
+      walk.run(tiles, smem);
+    }
     __syncthreads();
   }
+}
+
+template <typename O, bool ADD>
+__global__ __launch_bounds__(kBigThreads, 2) void grouped_big_wgrad_kernel(WgradArgs g) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  grouped_gradients<256, kBigThreads, O, ADD>(g, smem);
+}
+template <typename O, bool ADD>
+__global__ __launch_bounds__(kMidThreads, 1) void grouped_mid_wgrad_kernel(WgradArgs g) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  grouped_gradients<128, kMidThreads, O, ADD>(g, smem);
 }
 
 // the dynamic LDS that each kernel asks for, granted once per device
@@ -321,6 +352,11 @@ static hipError_t set_grouped_lds() {
               {reinterpret_cast<const void*>(grouped_big_wgrad_kernel<uint16_t, false>), kBigLds},
               {reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, false>), kBigLds},
               {reinterpret_cast<const void*>(grouped_big_wgrad_kernel<float, true>), kBigLds},
+              {reinterpret_cast<const void*>(grouped_mid_kernel<false>), kMidLds},
+              {reinterpret_cast<const void*>(grouped_mid_kernel<true>), kMidLds},
+              {reinterpret_cast<const void*>(grouped_mid_wgrad_kernel<uint16_t, false>), kMidLds},
+              {reinterpret_cast<const void*>(grouped_mid_wgrad_kernel<float, false>), kMidLds},
+              {reinterpret_cast<const void*>(grouped_mid_wgrad_kernel<float, true>), kMidLds},
               {reinterpret_cast<const void*>(grouped_f32_kernel<32, false>), f32_lds_bytes(32)},
               {reinterpret_cast<const void*>(grouped_f32_kernel<32, true>), f32_lds_bytes(32)},
               {reinterpret_cast<const void*>(grouped_f32_kernel<64, false>), f32_lds_bytes(64)},
@@ -339,13 +375,21 @@ static hipError_t set_grouped_lds() {
   });
 }
 
-// Rows a group on the mean up to which the weights stream past them: 24, or 128 where the 256-column tiles of all groups would leave half
-// of the CUs idle.  us streaming and with tiles: 32 groups of 7168 x 2048, 16 rows a group 149 and 169, 24 rows 181 and 170 (weights
-// stored [K][N]: 163 and 211, 177 and 214), 32 rows 198 and 171 (213 and 216); one group of 7168 x 7168, 1 row 18 and 77, 32 rows 20 and 78,
-// 96 rows 52 and 100.
-static bool thin_rows(const moe_gemm_t& s, int cus) {
-  const int64_t tiles = int64_t(s.groups) * ((s.N + kBig - 1) / kBig);
-  return s.rows <= int64_t(s.groups) * (tiles * 2 < cus ? 128 : 24);
+// How a bf16 product goes.  us streaming the weights past the rows, with tiles of 128 and of 256 (weights stored [K][N] in brackets):
+// - up to 24 rows a group on the mean, streaming: 32 groups of 7168 x 2048, 16 rows a group 149, -, 169; 24 rows 181, -, 170 (163, -, 211;
+//   177, -, 214); 32 rows 198, -, 171 (213, -, 216).
+// - where the tiles of 256 take no more than half of the CUs, streaming up to 4096 outputs a CU: 512 x 2048 x 2048 16, 27, 44 (22, 30, 47), 8 groups,
+//   256 x 2048 x 1408 13, 26, 27 (19, 26, 27), 2000 x 2048 x 1408 60, 28, 46.
+// - past those, tiles of 128: 2048 x 2048 x 2048 52, 29, 47 (70, 40, 49), 8 groups, 1024 x 7168 x 2048 160, 79, 131.  Weights stored [K][N] take
+//   two LDS reads for one there, and the tiles may be a third of the CUs (8 groups, 2000 x 1408 x 2048, 120 tiles: (69, 48, 38)).
+// - tiles of 256 else: 8 groups, 8000 x 2048 x 1408 140, 75, 52 (204, 118, 72).
+enum class Rows { kThin, kMid, kBig };
+static Rows rows_way(const moe_gemm_t& s, int cus) {
+  if (s.rows <= int64_t(s.groups) * 24) return Rows::kThin;
+  const int64_t tiles = (s.rows / kBig + s.groups) * ((s.N + kBig - 1) / kBig);        // at most
+  if (tiles * 2 > cus) return Rows::kBig;
+  if (s.rows * s.N <= int64_t(cus) * 4096) return Rows::kThin;
+  return s.w_layout && tiles * 3 > cus ? Rows::kBig : Rows::kMid;
 }
 
 // fp32 workgroups for at most `tiles` tiles of 64 x 64 (four times as many of 32 x 32 where they are fewer than the CUs)
@@ -370,7 +414,14 @@ hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, con
     else hipLaunchKernelGGL((grouped_f32_kernel<64, false>), grid, threads, lds, st, g);
     return hipGetLastError();
   }
-  if (!thin_rows(s, cus)) {
+  const Rows way = rows_way(s, cus);
+  if (way == Rows::kMid) {
+    const dim3 big((cus / 8) * 8);
+    if (s.w_layout) hipLaunchKernelGGL(grouped_mid_kernel<true>, big, dim3(kMidThreads), kMidLds, st, g);
+    else hipLaunchKernelGGL(grouped_mid_kernel<false>, big, dim3(kMidThreads), kMidLds, st, g);
+    return hipGetLastError();
+  }
+  if (way == Rows::kBig) {
     const dim3 big((cus / 8) * 8);
     // K of whole steps: no check at the fills (a tenth of 8192^3)
     if (s.w_layout && s.K % kBigBK) hipLaunchKernelGGL((grouped_big_kernel<true, true>), big, dim3(kBigThreads), kBigLds, st, g);
@@ -404,6 +455,14 @@ hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* 
     else hipLaunchKernelGGL((grouped_f32_wgrad_kernel<64, false>), grid, threads, lds, st, g);
   } else {
     const dim3 big((cus / 8) * 8), many(kBigThreads);
+    // 512 rows of 2048 x 2048 (64 tiles of 256) 13 us with tiles of 128, 20 with those; 2048 rows 39 and 51; 8 groups of 2048 x 1408 (384) 46 and 33
+    const int64_t tiles = int64_t(s.groups) * ((s.K + kBig - 1) / kBig) * ((s.N + kBig - 1) / kBig);
+    if (tiles * 4 <= cus) {
+      if (dw_dtype != MOE_F32) hipLaunchKernelGGL((grouped_mid_wgrad_kernel<uint16_t, false>), big, dim3(kMidThreads), kMidLds, st, g);
+      else if (accumulate) hipLaunchKernelGGL((grouped_mid_wgrad_kernel<float, true>), big, dim3(kMidThreads), kMidLds, st, g);
+      else hipLaunchKernelGGL((grouped_mid_wgrad_kernel<float, false>), big, dim3(kMidThreads), kMidLds, st, g);
+      return hipGetLastError();
+    }
     if (dw_dtype != MOE_F32) hipLaunchKernelGGL((grouped_big_wgrad_kernel<uint16_t, false>), big, many, kBigLds, st, g);
     else if (accumulate) hipLaunchKernelGGL((grouped_big_wgrad_kernel<float, true>), big, many, kBigLds, st, g);
     else hipLaunchKernelGGL((grouped_big_wgrad_kernel<float, false>), big, many, kBigLds, st, g);

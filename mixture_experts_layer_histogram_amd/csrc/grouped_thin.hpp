@@ -6,7 +6,7 @@
 // ends up with four consecutive columns of one row.
 //
 // SPLIT 1: a wave takes an item alone.  SPLIT 4: the workgroup's four waves share an item's K and add up through LDS in wave order (two
-// stages each), where the items do not come out even on the waves; thin_split has the figures.
+// stages each), where the items do not come out even on the waves; thin_alone has the figures.
 #pragma once
 
 #include "grouped.hpp"
@@ -41,7 +41,7 @@ __device__ __forceinline__ void thin_run(const GroupedArgs& g, const int32_t* ba
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q = lane >> 4;
   const int ncb = (g.N + kThinCols - 1) / kThinCols, nst = (g.K + kThinK - 1) / kThinK;
-  const int items = mtiles * ncb;                     // fewer than (1024 * 48 / 32 + 1024) * 2^16: rows a group are few here
+  const int items = mtiles * ncb;                     // below 2^29: rows a group are few here, and the weights, 16 bytes a column at least, fit in memory
   const int it0 = SPLIT == 1 ? int(blockIdx.x) * 4 + wave : int(blockIdx.x);
   const int it_step = SPLIT == 1 ? int(gridDim.x) * 4 : int(gridDim.x);
   const int s0 = SPLIT == 1 ? 0 : nst * wave / 4, s1 = SPLIT == 1 ? nst : nst * (wave + 1) / 4;

@@ -15,8 +15,8 @@
 // step k + 1 (in the first two turns; it has the other two to land) and A of step k + 2 (in the last two).  What this
 // is about: a CU takes in one 1 KiB load in 16 to 23 cycles, 64 of them a step of 2048, and a wave that finds
 // the queue full waits at its issue, MFMAs and all.  8192^3 (rows and columns of K contiguous): two stages of 64 KiB with eight
-// loads at once at a step's start 971 us, spread over three turns 869, the ring of five with two a turn 657 (1674 TFLOP/s; a
-// library's product of that size 670).
+// loads at once at a step's start 971 us, spread over three turns 869, the ring of five with two a turn 764 (1440 TFLOP/s; a
+// library's product of that size 670 to 687).
 //
 // The loads know nothing of tiles: a cursor for A (two steps ahead) and one for B (one step) walk the list by
 // themselves, so the next tile's first panels land while this one's last products and its stores are on their way.
@@ -112,8 +112,9 @@ struct BigFill {
 // kCut: 0 where every K is a multiple of 64; 1: the check at every fill; 2: at every step (few steps, and the code is there twice).
 template <bool A_MN, bool B_MN, typename TILES>
 struct BigWalk {
+  static constexpr int kBlocks = 8;
   TILES& tiles;
-  int lane, wave, half, wn, r16, g, n_tiles;
+  int lane, wave, half, wn, r16, g, n_tiles, row_base, col_base;
   uint32_t lds_fill;                        // LDS address of this wave's first fill of a panel
   uint32_t l0, a_rd[A_MN ? 1 : 2], b_rd[B_MN ? 1 : 2];
   uint32_t pa;                              // the ring's place of A of the step at work
@@ -127,6 +128,8 @@ struct BigWalk {
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     half = wave >> 2;
     wn = wave & 3;
+    row_base = half * 128;
+    col_base = wn * 64;
     r16 = lane & 15;
     g = lane >> 4;
     l0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
@@ -330,8 +333,8 @@ __device__ __forceinline__ void big_store(const WALK& w, O* out, int64_t ld, int
   asm volatile("" : "+v"(lane));            // the compiler would keep these indices in registers all along the products
   const int r16 = lane & 15, g = lane >> 4;
 #pragma unroll
-  for (int m = 0; m < 8; ++m) {
-    const int row = w.half * 128 + m * 16 + r16;
+  for (int m = 0; m < WALK::kBlocks; ++m) {
+    const int row = w.row_base + m * 16 + r16;
     if (sizeof(O) == 4 && row >= rows) continue;
     O* p = out + row * ld;
     if constexpr (sizeof(O) == 2) {
@@ -355,15 +358,15 @@ __device__ __forceinline__ void big_store(const WALK& w, O* out, int64_t ld, int
         a[j] = up ? got : v[0][j];
         b[j] = up ? v[1][j] : got;
       }
-      const int col = w.wn * 64 + (up ? 32 : 0) + (g & 1) * 16 + (g >> 1) * 8;
-      const int ra = w.half * 128 + m * 16 + (r16 & 7);
+      const int col = w.col_base + (up ? 32 : 0) + (g & 1) * 16 + (g >> 1) * 8;
+      const int ra = w.row_base + m * 16 + (r16 & 7);
       O* q = out + ra * ld + col;
       if (col < cols && ra < rows) big_put<NT>(q, a);
       if (col < cols && ra + 8 < rows) big_put<NT>(q + 8 * ld, b);
     } else {
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        const int col = w.wn * 64 + n * 16 + 4 * g;
+        const int col = w.col_base + n * 16 + 4 * g;
         if (col >= cols) continue;
         f32x4 v = w.acc[m][n];
         if constexpr (ADD) v += *reinterpret_cast<const f32x4*>(p + col);

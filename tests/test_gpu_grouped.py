@@ -66,6 +66,8 @@ CASES = [
     ([1], 8, 8), ([0, 1, 0], 16, 8), ([3, 0, 5, 1], 40, 24), ([64, 65, 63], 64, 64), ([7] * 5, 1408, 72), ([130, 0, 257], 200, 264),
     ([1, 1, 0, 1, 1, 0, 1, 1], 2048, 1408), ([300, 20, 0, 600], 136, 520), ([16] * 32, 512, 256), ([40, 9, 77, 33, 20, 25], 1024, 328),
     ([2000], 256, 128), ([500, 1, 1, 1, 1], 72, 1032), ([0] * 1023 + [3], 16, 16), ([2] * 1000, 24, 40), ([1100, 900], 2048, 512),
+    ([1500, 548], 136, 1304), ([1500, 548], 192, 1304), ([300, 20, 0, 600, 77, 256, 3, 129], 520, 776),
+    ([300, 20, 0, 600, 77, 256, 3, 129], 72, 4104), ([260, 257, 9], 8, 9000), ([700, 0, 350], 320, 8712),
 ]
 
 
