@@ -1,0 +1,395 @@
+"""The norm, the dispatch of codes, the products grouped by expert and the AdamW step as they are used: between the layer's own calls, in
+a serving pass with MXFP8 experts and in training steps of experts of another form, eager, captured, on streams and at once.
+
+Bars.  Serving: none, the layer's own path from the same codes gives the same bits.  Training in fp32 against 64-bit gradients:
+four products in a row with sums of at most K = 768 terms, each off by K * 2^-24 of its terms' magnitudes, which are at most
+sqrt(K) of a row's largest value: 4 * 768 * 28 * 2^-24 = 5e-3 of a row's largest value in the worst case; 1e-3 is asked (of
+a hundredth of the tensor's largest value where a row's own are smaller: terms that cancel leave errors of their own size).
+"""
+import numpy as np
+import pytest
+
+from oracle import more_oracle as M
+from mixture_experts_layer_histogram_amd import configs, inputs, moe
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+BETA1, BETA2, LR, TINY = 0.9, 0.95, 1e-2, 1e-8
+
+
+def _torch():
+    import torch
+    return torch
+
+
+# ------------------------------------------------------------------------------------------------ serving
+@pytest.mark.parametrize("T", [1, 130])
+def test_norm_then_mxfp8_experts(T):
+    """residual + norm -> codes -> layout of choices -> dispatch of codes -> experts -> merge -> the next norm: from the codes on the
+    bits that the layer makes of the rows that the codes stand for."""
+    torch = _torch()
+    from mixture_experts_layer_histogram_amd.device import DeviceProblem
+    cfg = configs.MoEConfig(f"norm-mx T{T} d512 E16/8 k3 F256", R=2, T=T, d=512, E=16, E_local=8, k=3, F=256, dtype="mxfp8")
+    P = DeviceProblem(cfg, inputs.make_inputs(cfg, seed=4))
+    g = torch.Generator(device="cuda").manual_seed(T)
+    bf = torch.bfloat16
+    x = [torch.randn(T, 512, generator=g, device="cuda").to(bf) for _ in range(2)]
+    res = [torch.randn(T, 512, generator=g, device="cuda").to(bf) for _ in range(2)]
+    gamma = 1 + 0.1 * torch.randn(512, generator=g, device="cuda")
+    idx = torch.topk(torch.rand(2, T, 16, generator=g, device="cuda"), 3).indices.int()
+    w = torch.rand(2, T, 3, generator=g, device="cuda")
+    n = moe.Norm(T, 512, moe.MOE_BF16, EPS)
+    h, q, qs = [[torch.empty(*s, dtype=t, device="cuda") for _ in range(2)]
+                for s, t in (((T, 512), bf), ((T, 512), torch.uint8), ((4, T, 4), torch.uint8))]
+    for r in range(2):
+        moe.moe_norm(n, x[r], res[r], gamma, h[r], None, q[r], qs[r])
+    moe.moe_layout_choices(P.shape, P.placement, None, idx, P.counts, P.offsets, P.pull_src, P.slot_of, P.ws)
+    moe.moe_dispatch_pull_codes(P.shape, P.placement, q, qs, P.pull_src, P.offsets, P.xe, P.xe_scales, P.ws)
+    P.ffn()
+    y = [torch.empty_like(t) for t in x]
+    moe.moe_combine_merge(P.shape, P.placement, P.ye, P.slot_of, w, y)
+    nxt = [torch.empty_like(t) for t in x]
+    for r in range(2):
+        moe.moe_norm(n, y[r], h[r], gamma, h[r], nxt[r])       # h in place: the stream of residuals
+    assert P.status() == 0
+    for r in range(2):                                         # E4M3 codes times a power of two are bf16 values
+        moe.moe_mx_dequantize(q[r], qs[r], moe.MOE_MXFP8, T, 512, P.x[r], moe.MOE_BF16)
+    P.forward_choices(idx, w)
+    for r in range(2):
+        assert torch.equal(P.y[r], y[r]) and (T == 1 or (y[r] != 0).any())
+        s = (x[r].float() + res[r].float()).to(bf).double().cpu().numpy()
+        _, ref, _ = M.norm(y[r].double().cpu().numpy(), s, gamma.double().cpu().numpy(), EPS)
+        assert (np.abs(nxt[r].double().cpu().numpy() - ref) <= (2.0 ** -8 + 33 * 2.0 ** -24) * np.abs(ref)).all()
+
+
+# ------------------------------------------------------------------------------------------------ training
+class Net:
+    """Tokens, their choices, and experts relu(y wu^T)^2 wd^T behind a norm; one step with its gradients and AdamW."""
+
+    def __init__(self, T, d, F, E, k, dtype, seed, eight=False):
+        torch = _torch()
+        self.g = g = torch.Generator(device="cuda").manual_seed(seed)
+        self.kind, self.code = (torch.bfloat16, moe.MOE_BF16) if dtype == "bf16" else (torch.float32, moe.MOE_F32)
+        self.dims, self.eight = (T, d, F, E, k), eight
+        rnd = lambda *s, f=1.0: torch.randn(*s, generator=g, device="cuda") * f        # noqa: E731
+        self.x, self.res, self.dz = (rnd(T, d).to(self.kind) for _ in range(3))
+        self.idx = torch.topk(torch.rand(1, T, E, generator=g, device="cuda"), k).indices.int()
+        self.idx[torch.rand(1, T, k, generator=g, device="cuda") < 0.1] = -1
+        self.w = torch.rand(1, T, k, generator=g, device="cuda")
+        self.gamma = 1 + rnd(d, f=0.1)
+        masters = [rnd(E, F, d, f=d ** -0.5), rnd(E, d, F, f=F ** -0.5)]
+        self.wu, self.wd = (m.to(self.kind) for m in masters)
+        self.masters = masters if dtype == "bf16" else [None, None]
+        self.shape = moe.Shape(1, T, d, E, k, F, self.code)
+        self.e2l = torch.arange(E, dtype=torch.int32, device="cuda")
+        self.pl = moe.Placement(self.e2l.data_ptr(), E)
+        N = moe.moe_max_pairs(self.shape, self.pl)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        self.counts, self.off = torch.zeros(E, **i32), torch.zeros(E + 1, **i32)
+        self.src, self.slot = torch.zeros(N, 2, **i32), torch.zeros(1, T, k, **i32)
+        self.ws = torch.empty(moe.moe_workspace_bytes(self.shape, self.pl), dtype=torch.uint8, device="cuda")
+        new = lambda *s: torch.full(s, float("nan"), dtype=self.kind, device="cuda")   # noqa: E731
+        self.h, self.y, self.z, self.dyn, self.dx = (new(T, d) for _ in range(5))
+        self.xe, self.ye, self.dye, self.dxe = (new(N, d) for _ in range(4))
+        self.a, self.b, self.db = (new(N, F) for _ in range(3))
+        self.dw = torch.empty(1, T, k, device="cuda")
+        f32 = dict(dtype=torch.float32, device="cuda")
+        self.dgamma, self.dwu, self.dwd = torch.empty(d, **f32), torch.empty(E, F, d, **f32), torch.empty(E, d, F, **f32)
+        self.norm = moe.Norm(T, d, self.code, EPS)
+        self.nws = torch.empty(moe.moe_norm_backward_workspace_bytes(self.norm), dtype=torch.uint8, device="cuda")
+        self.up, self.down = moe.Gemm(N, E, d, F, self.code, 0), moe.Gemm(N, E, F, d, self.code, 0)
+        self.up_t, self.down_t = moe.Gemm(N, E, F, d, self.code, 1), moe.Gemm(N, E, d, F, self.code, 1)
+        self.at, self.lr = torch.ones(1, dtype=torch.int64, device="cuda"), torch.full((1,), LR, device="cuda")
+        self.states = []
+        for p in (self.gamma, self.wu, self.wd):
+            n = -(-p.numel() // 128) * 128
+            u8 = dict(dtype=torch.uint8, device="cuda")
+            self.states.append([torch.zeros(n, **u8), torch.zeros(n, **u8), torch.zeros(n // 32, **u8), torch.zeros(n // 32, **u8)]
+                               if eight else [torch.zeros_like(p, dtype=torch.float32), torch.zeros_like(p, dtype=torch.float32), None, None])
+        lst = [(self.gamma, self.dgamma, moe.MOE_F32, None), (self.wu, self.dwu, self.code, self.masters[0]),
+               (self.wd, self.dwd, self.code, self.masters[1])]
+        self.table = moe.adamw_table(moe.AdamWTensor(p, gr, p.numel(), c, moe.MOE_F32, *s, m, 0.1)
+                                     for (p, gr, c, m), s in zip(lst, self.states))
+
+    def kept(self):
+        """What a step leaves to the next one, and its results."""
+        out = [self.z, self.dx, self.dw, self.dgamma, self.dwu, self.dwd, self.gamma, self.wu, self.wd]
+        return out + [t for t in self.masters if t is not None] + [t for s in self.states for t in s if t is not None]
+
+    def step(self):
+        torch = _torch()
+        moe.moe_norm(self.norm, self.x, self.res, self.gamma, self.h, self.y)
+        moe.moe_layout_choices(self.shape, self.pl, None, self.idx, self.counts, self.off, self.src, self.slot, self.ws)
+        moe.moe_dispatch_pull(self.shape, self.pl, [self.y], self.src, self.off, self.xe, self.ws)
+        moe.moe_grouped_gemm(self.up, self.xe, self.wu, self.off, self.a)
+        torch.clamp(self.a, min=0, out=self.a)
+        torch.mul(self.a, self.a, out=self.b)
+        moe.moe_grouped_gemm(self.down, self.b, self.wd, self.off, self.ye)
+        moe.moe_combine_merge(self.shape, self.pl, self.ye, self.slot, self.w, [self.z])
+        moe.moe_combine_merge_backward(self.shape, self.pl, [self.dz], self.ye, self.slot, self.w, self.dye, self.dw)
+        moe.moe_grouped_gemm_wgrad(self.down, self.b, self.dye, self.off, self.dwd, moe.MOE_F32)
+        moe.moe_grouped_gemm(self.down_t, self.dye, self.wd, self.off, self.db)
+        torch.mul(self.db, self.a, out=self.db)
+        torch.mul(self.db, 2, out=self.db)
+        moe.moe_grouped_gemm_wgrad(self.up, self.xe, self.db, self.off, self.dwu, moe.MOE_F32)
+        moe.moe_grouped_gemm(self.up_t, self.db, self.wu, self.off, self.dxe)
+        moe.moe_dispatch_pull_backward(self.shape, self.pl, self.dxe, self.slot, [self.dyn])
+        moe.moe_norm_backward(self.norm, self.dyn, self.h, self.gamma, self.dz, self.dx, self.dgamma, self.nws)
+        moe.moe_adamw(moe.AdamW(LR, BETA1, BETA2, TINY, 0, moe.MOE_MXFP8 if self.eight else moe.MOE_F32, int(self.eight), 5, None,
+                                self.lr.data_ptr(), self.at.data_ptr()), self.table)
+
+
+# T, d, F, E, k: few rows a group, tiles of 128, tiles of 256 (in bf16)
+SIZES = [(5, 256, 384, 8, 2), (700, 512, 768, 8, 2), (3000, 512, 1600, 32, 2)]
+
+
+@pytest.mark.parametrize("T,d,F,E,k", SIZES[:2])
+def test_training_step_against_64_bits(T, d, F, E, k):
+    torch = _torch()
+    net = Net(T, d, F, E, k, "f32", 1)
+    start = [t.clone() for t in (net.gamma, net.wu, net.wd)]
+    leaves = [t.double().requires_grad_() for t in (net.x, net.gamma, net.wu, net.wd, net.w)]
+    x, gamma, wu, wd, w = leaves
+    net.step()
+    assert moe.moe_read_status(net.ws) == 0
+    s = x + net.res.double()
+    y = s * torch.rsqrt((s * s).mean(-1, keepdim=True) + float(np.float32(EPS))) * gamma
+    z = torch.zeros_like(s)
+    for e in range(E):
+        t, j = (net.idx[0] == e).nonzero(as_tuple=True)
+        z = z.index_add(0, t, w[0, t, j, None] * (torch.relu(y[t] @ wu[e].t()) ** 2 @ wd[e].t()))
+    ((s + z) * net.dz.double()).sum().backward()
+    assert T < 10 or ((net.idx < 0).any() and (net.counts > 0).all())
+
+    def near(got, want):
+        a, b = got.double().reshape(-1, got.shape[-1]), want.detach().reshape(-1, got.shape[-1])
+        assert ((a - b).abs().amax(-1) <= 1e-3 * b.abs().amax(-1).clamp(min=1e-2 * float(b.abs().max()))).all()
+
+    near(net.z, z)
+    near(net.dx, x.grad)
+    near(net.dgamma, gamma.grad)
+    near(net.dwu, wu.grad)
+    near(net.dwd, wd.grad)
+    near(net.dw, w.grad)
+    n = lambda t: t.detach().float().cpu().numpy()              # noqa: E731
+    for p, old, gr in zip((net.gamma, net.wu, net.wd), start, (net.dgamma, net.dwu, net.dwd)):
+        m, v = M.moments(0 * n(gr), 0 * n(gr), n(gr), BETA1, BETA2)
+        ref, away = M.adamw(n(old), m, v, LR, BETA1, BETA2, TINY, 1, 0.1)
+        assert (np.abs(n(p) - ref) <= 2.0 ** -24 * (16 * away + 3 * (np.abs(ref) + away))).all()
+
+
+def _restore(net, kept):
+    for t, o in zip(net.kept(), kept):
+        t.copy_(o)
+
+
+@pytest.mark.parametrize("T,d,F,E,k", SIZES)
+@pytest.mark.parametrize("dtype,eight", [("f32", False), ("bf16", False), ("bf16", True)])
+def test_steps_captured_and_replayed(T, d, F, E, k, dtype, eight):
+    """Four steps eager, then the same four from a captured one, with eager work of the same operators between the replays."""
+    torch = _torch()
+    net, other = Net(T, d, F, E, k, dtype, 2, eight), Net(40, 256, 320, 4, 2, dtype, 3, eight)
+    start = [t.clone() for t in net.kept()]
+    want = []
+    for i in range(4):
+        net.at.fill_(i + 1)
+        net.step()
+        want.append([t.clone() for t in net.kept()])
+    assert not torch.equal(want[0][7], want[3][7]) and all(torch.isfinite(t.float()).all() for t in want[3])
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        net.step()
+    _restore(net, start)
+    for i in range(4):
+        net.at.fill_(i + 1)
+        g.replay()
+        other.step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want[i], net.kept())), i
+
+
+@pytest.mark.parametrize("T,d,F,E,k", SIZES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_two_nets_at_once(T, d, F, E, k, dtype):
+    """Two nets on two streams, their steps enqueued in turn, neither on the stream that made the tensors."""
+    torch = _torch()
+    nets = [Net(T, d, F, E, k, dtype, 4, dtype == "bf16"), Net(T + 3, d, F, E, k, dtype, 5)]
+    start = [[t.clone() for t in n.kept()] for n in nets]
+    want = []
+    for n in nets:
+        for _ in range(3):
+            n.step()
+        want.append([t.clone() for t in n.kept()])
+    for n, s in zip(nets, start):
+        _restore(n, s)
+    streams = [torch.cuda.Stream() for _ in nets]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for n, s in zip(nets, streams):
+            with torch.cuda.stream(s):
+                n.step()
+    torch.cuda.synchronize()
+    for n, w in zip(nets, want):
+        assert all(torch.equal(a, b) for a, b in zip(w, n.kept()))
+
+
+def test_two_graphs_over_one_norm_workspace():
+    """Two layers' norm gradients captured over one workspace, replayed in turn, with an eager call of another size between."""
+    torch = _torch()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    sizes = [(3001, 1024), (77, 4096), (500, 512)]
+    norms = [moe.Norm(r, d, moe.MOE_BF16, EPS) for r, d in sizes]
+    ws = torch.empty(max(moe.moe_norm_backward_workspace_bytes(n) for n in norms), dtype=torch.uint8, device="cuda")
+    data = [[torch.randn(r, d, generator=g, device="cuda").bfloat16() for _ in range(2)] for r, d in sizes]
+    out = [(torch.empty_like(t[0]), torch.empty(t[0].shape[1], device="cuda")) for t in data]
+
+    def run(i):
+        moe.moe_norm_backward(norms[i], data[i][0], data[i][1], None, None, out[i][0], out[i][1], ws)
+
+    want = []
+    for i in range(3):
+        run(i)
+        want.append([t.clone() for t in out[i]])
+    graphs, s = [], torch.cuda.Stream()
+    for i in range(2):
+        s.wait_stream(torch.cuda.current_stream())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i], stream=s):
+            run(i)
+    for i in (0, 1, 2, 1, 0, 0, 2, 1):
+        for t in out[i]:
+            t.fill_(float("nan"))
+        graphs[i].replay() if i < 2 else run(i)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want[i], out[i])), i
+
+
+# ------------------------------------------------------------------------------------------------ sizes past 32 bits
+def test_norm_past_4_gib():
+    """Rows whose byte offsets pass 32 bits: the last ones as in a call of their own."""
+    torch = _torch()
+    rows, d, some = 300000, 8192, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    tail = [torch.randn(some, d, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    x, dy = (torch.ones(rows, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[-some:], dy[-some:] = tail
+    gamma = torch.rand(d, generator=g, device="cuda")
+    big, small = moe.Norm(rows, d, moe.MOE_BF16, EPS), moe.Norm(some, d, moe.MOE_BF16, EPS)
+    y, q, sc = torch.empty_like(x), torch.empty(rows, d, dtype=torch.uint8, device="cuda"), torch.empty(d // 128, rows, 4, dtype=torch.uint8, device="cuda")
+    moe.moe_norm(big, x, None, gamma, None, y, q, sc)
+    ty, tq, ts = torch.empty_like(tail[0]), torch.empty(some, d, dtype=torch.uint8, device="cuda"), torch.empty(d // 128, some, 4, dtype=torch.uint8, device="cuda")
+    moe.moe_norm(small, tail[0], None, gamma, None, ty, tq, ts)
+    assert torch.equal(y[-some:], ty) and torch.equal(q[-some:], tq) and torch.equal(sc[:, -some:], ts)
+    moe.moe_norm_backward(big, dy, x, gamma, None, y, None)
+    moe.moe_norm_backward(small, tail[1], tail[0], gamma, None, ty, None)
+    assert torch.equal(y[-some:], ty)
+    assert bool((y[:-some] == y[0]).all())                      # rows of ones all come out alike
+
+
+def test_codes_past_4_gib():
+    """640000 rows of 7168 codes, gathered from tokens: every row its token's, at both ends."""
+    torch = _torch()
+    T, d, k = 80000, 7168, 8
+    sh, e2l = moe.Shape(1, T, d, 8, k, 128, moe.MOE_MXFP8), torch.arange(8, dtype=torch.int32, device="cuda")
+    p = moe.Placement(e2l.data_ptr(), 8)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    idx = torch.arange(8, **i32).repeat(T, 1).reshape(1, T, 8).contiguous()
+    off, src, slot = torch.empty(9, **i32), torch.empty(T * k, 2, **i32), torch.empty(1, T, k, **i32)
+    ws = torch.empty(moe.moe_workspace_bytes(sh, p), dtype=torch.uint8, device="cuda")
+    moe.moe_layout_choices(sh, p, None, idx, torch.empty(8, **i32), off, src, slot, ws)
+    xq = torch.randint(0, 256, (T, d), dtype=torch.uint8, device="cuda")
+    xs = torch.randint(0, 256, (d // 128, T, 4), dtype=torch.uint8, device="cuda")
+    xe, xes = torch.zeros(T * k, d, dtype=torch.uint8, device="cuda"), torch.zeros(d // 128, T * k, 4, dtype=torch.uint8, device="cuda")
+    moe.moe_dispatch_pull_codes(sh, p, [xq], [xs], src, off, xe, xes, ws)
+    assert moe.moe_read_status(ws) == 0 and int(off[-1]) == T * k
+    for e in range(8):                                          # expert e's rows are the tokens in order
+        assert torch.equal(xe[e * T:(e + 1) * T], xq) and torch.equal(xes[:, e * T:(e + 1) * T], xs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", [0, 1])
+def test_products_past_4_gib(dtype, layout):
+    """x and y as columns of rows 2^22 values apart, and many dense rows: whole numbers, so every bit is known."""
+    torch = _torch()
+    kind, code = (torch.bfloat16, moe.MOE_BF16) if dtype == "bf16" else (torch.float32, moe.MOE_F32)
+    for rows, ld, K, N in ((600, 1 << 22, 72, 136), (9000000, 256, 256, 264)):
+        counts = [rows - 290, 0, 290] if ld > K else [rows - 300, 300]
+        off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32), device="cuda")
+        wide = ld > K
+        x = torch.zeros(rows, ld, dtype=kind, device="cuda")
+        x[-600:, :K] = torch.randint(-2, 3, (600, K), device="cuda").to(kind)
+        w = torch.randint(-2, 3, (len(counts), N, K) if layout == 0 else (len(counts), K, N), device="cuda").to(kind)
+        y = torch.full((rows, ld if wide else N), 7.0, dtype=kind, device="cuda")
+        g = moe.Gemm(rows, len(counts), K, N, code, layout, ld if wide else 0, ld if wide else 0)
+        moe.moe_grouped_gemm(g, x, w, off, y)
+        m = w.float() if layout else w.float().transpose(1, 2).contiguous()
+        xs = x[-600:, :K].float()
+        at = 600 - counts[-1]
+        want = torch.cat((xs[:at] @ m[0], xs[at:] @ m[-1]))
+        assert torch.equal(y[-600:, :N], want.to(kind)) and (not wide or bool((y[:, N:] == 7).all()))
+        assert wide or bool((y[:-600] == 0).all())
+        dw = torch.empty_like(w, dtype=torch.float32)
+        y[:, :N].zero_()
+        y[-600:, :N] = torch.randint(-2, 3, (600, N), device="cuda").to(kind)
+        moe.moe_grouped_gemm_wgrad(g, x, y, off, dw, moe.MOE_F32)
+        ys = y[-600:, :N].float()
+        for i, (a, b) in ((0, (0, at)), (len(counts) - 1, (at, 600))):
+            dm = xs[a:b].t() @ ys[a:b]
+            assert torch.equal(dw[i], dm if layout else dm.t())
+        del x, y
+
+
+def test_more_tiles_than_a_workgroup_lists_at_once():
+    """1024 groups whose tiles of 256 are more than 64 for every CU, for the product and both of its gradients."""
+    torch = _torch()
+    counts = [24] * 900 + [300] * 124
+    K, N, G = 8, 5000, 1024
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    rows, doff = int(off[-1]), torch.from_numpy(off).cuda()
+    pick = lambda *s: torch.randint(-3, 4, s, device="cuda").bfloat16()                # noqa: E731
+    x, w, dy = pick(rows, K), pick(G, N, K), pick(rows, N)
+    y, dx, dw = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda"), torch.empty_like(x), torch.empty_like(w)
+    g = moe.Gemm(rows, G, K, N, moe.MOE_BF16, 0)
+    moe.moe_grouped_gemm(g, x, w, doff, y)
+    moe.moe_grouped_gemm(moe.Gemm(rows, G, N, K, moe.MOE_BF16, 1), dy, w, doff, dx)
+    moe.moe_grouped_gemm_wgrad(g, x, dy, doff, dw, moe.MOE_BF16)
+    for i in range(G):
+        a, b = int(off[i]), int(off[i + 1])
+        xs, ws, ds = x[a:b].float(), w[i].float(), dy[a:b].float()
+        assert torch.equal(y[a:b], (xs @ ws.t()).bfloat16()), i
+        assert torch.equal(dx[a:b], (ds @ ws).bfloat16()), i
+        assert torch.equal(dw[i], (ds.t() @ xs).bfloat16()), i
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_a_tensor_past_4_gib(eight):
+    """2^31 + 70001 values: the last ones as in a tensor of their own (no random bits, which go by the place)."""
+    torch = _torch()
+    n, some = 2 ** 31 + 70001, 128 * 100 + 70001 % 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    bf = torch.bfloat16
+
+    def make(n, p, gr):
+        param, grad = torch.ones(n, dtype=bf, device="cuda"), torch.zeros(n, dtype=bf, device="cuda")
+        param[-some:], grad[-some:] = p, gr
+        pad = -(-n // 128) * 128
+        kind = torch.uint8 if eight else torch.float32
+        st = [torch.zeros(pad, dtype=kind, device="cuda") for _ in range(2)]
+        st += [torch.zeros(pad // 32, dtype=torch.uint8, device="cuda") for _ in range(2)] if eight else [None, None]
+        return param, grad, st
+
+    tail = [torch.randn(some, generator=g, device="cuda").to(bf) for _ in range(2)]
+    sets = [make(n, *tail), make(some, *tail)]
+    for step in (1, 2):
+        for p, gr, st in sets:
+            moe.moe_adamw(moe.AdamW(LR, BETA1, BETA2, TINY, step, moe.MOE_MXFP8 if eight else moe.MOE_F32, 0, 5),
+                          [moe.AdamWTensor(p, gr, p.numel(), moe.MOE_BF16, moe.MOE_BF16, *st, None, 0.0)])
+    (p, _, st), (q, _, su) = sets
+    assert torch.equal(p[-some:], q) and not torch.equal(q, tail[0])
+    pad = len(su[0])
+    assert all(torch.equal(a[-pad:], b) for a, b in zip(st[:2], su[:2]))
+    if eight:
+        assert all(torch.equal(a[-pad // 32:], b) for a, b in zip(st[2:], su[2:]))
+    assert bool((p[:-some] == 1).all()) and bool((st[0][:-pad] == 0).all())
