@@ -20,11 +20,10 @@
 namespace moe {
 
 constexpr int kAdamThreads = 256;
-// Parts (of 4 values a lane) that a workgroup loads together, and values of a tensor that it takes at a time: 4096 are a line of scale
-// bytes, and one look at the tensors for 65 KiB; 1024 where there are few, so that more workgroups share them (61 tensors of 260000
-// values in two launches: 5.8 + 5.3 us, with 4096 8.6 + 7.8).
+// Four values a lane, so a part of a tensor is 1024.  A workgroup takes one at a time, and with states in 8 bits two, one after the other, where
+// that leaves every workgroup that the card holds a chunk: 61 tensors of 4096 values 12 us with one, 15 with two, 500000 values 102 and 94,
+// 9 million 1577 and 1479 (fp32 states 136 and 147, 2824 and 2964).
 constexpr int kAdamPart = kAdamThreads * 4;
-constexpr int adam_chunk(int parts) { return parts == 1 ? kAdamPart : 4 * kAdamPart; }
 
 struct AdamScales {
   uint8_t *m, *v;
@@ -229,7 +228,7 @@ struct AdamPart {
 template <bool EIGHT, bool STOCHASTIC, int PARTS>
 __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamArgs<EIGHT> a) {
 #pragma clang fp contract(off)
-  constexpr int kChunk = adam_chunk(PARTS);
+  constexpr int kChunk = PARTS * kAdamPart;
   const int64_t step = a.device_step ? *a.device_step : a.step;
   const float lr = a.device_lr ? *a.device_lr : a.lr;
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
@@ -260,62 +259,57 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamArgs<EIGHT> a) 
       key1 = mix32(key + 2);
     }
     // the values' places count on within 2^32 (a chunk never crosses such a border)
-    for (int64_t i0 = first; i0 < first + kChunk && i0 < n; i0 += PARTS * kAdamPart) {
-      AdamPart<EIGHT> part[PARTS];
+    for (int64_t i0 = first; i0 < min(first + kChunk, n); i0 += kAdamPart) {
+      const int64_t i = i0 + threadIdx.x * 4;
+      AdamPart<EIGHT> w;
+      w.load(t, sc, i, n, pb, gb, mast);
+      float r[4];
 #pragma unroll
-      for (int q = 0; q < PARTS; ++q) part[q].load(t, sc, i0 + q * kAdamPart + threadIdx.x * 4, n, pb, gb, mast);
+      for (int j = 0; j < 4; ++j) {
+        const float gj = w.g[j] * gs;
+        w.m[j] = b1 * w.m[j] + c1 * gj;
+        w.v[j] = b2 * w.v[j] + (c2 * gj) * gj;
+        r[j] = root_of(w.v[j]);
+        w.p[j] = w.p[j] * keep - lr * ((w.m[j] * by_m) * __builtin_amdgcn_rcpf(r[j] * by_r + a.eps));
+      }
+      if (mast) store_f32(t.master, i, n, w.p);
+      if (pb) {
+        uint32_t b[4];
+        if (up) {
 #pragma unroll
-      for (int q = 0; q < PARTS; ++q) {
-        AdamPart<EIGHT>& w = part[q];
-        const int64_t i = i0 + q * kAdamPart + threadIdx.x * 4;
-        float r[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float gj = w.g[j] * gs;
-          w.m[j] = b1 * w.m[j] + c1 * gj;
-          w.v[j] = b2 * w.v[j] + (c2 * gj) * gj;
-          r[j] = root_of(w.v[j]);
-          w.p[j] = w.p[j] * keep - lr * ((w.m[j] * by_m) * __builtin_amdgcn_rcpf(r[j] * by_r + a.eps));
-        }
-        if (mast) store_f32(t.master, i, n, w.p);
-        if (pb) {
-          uint32_t b[4];
-          if (up) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = bf16_up(w.p[j], mix32(key1 + uint32_t(i) + j) & 0xFFFFu);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              const uint32_t two = pack_bf16x2(w.p[j], w.p[j + 1]);
-              b[j] = two & 0xFFFFu;
-              b[j + 1] = two >> 16;
-            }
-          }
-          store_bf16(reinterpret_cast<uint16_t*>(t.param), i, n, b);
+          for (int j = 0; j < 4; ++j) b[j] = bf16_up(w.p[j], mix32(key1 + uint32_t(i) + j) & 0xFFFFu);
         } else {
-          store_f32(reinterpret_cast<float*>(t.param), i, n, w.p);
-        }
-        if constexpr (EIGHT) {
-          uint32_t rand[4];
-          if constexpr (STOCHASTIC) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) rand[j] = mix32(key0 + uint32_t(i) + j);
+          for (int j = 0; j < 4; j += 2) {
+            const uint32_t two = pack_bf16x2(w.p[j], w.p[j + 1]);
+            b[j] = two & 0xFFFFu;
+            b[j + 1] = two >> 16;
           }
-          uint32_t scm, scv;
-          const uint32_t qm = state_quant<false, STOCHASTIC>(w.m, rand, &scm);    // all lanes: eight of them agree on a block
-          const uint32_t qv = state_quant<true, STOCHASTIC>(r, rand, &scv);
-          if (i < ((n + 127) & ~int64_t(127))) {
-            __builtin_nontemporal_store(qm, reinterpret_cast<uint32_t*>(t.m + i));
-            __builtin_nontemporal_store(qv, reinterpret_cast<uint32_t*>(t.v + i));
-            if ((i & 31) == 0) {
-              sc.m[i >> 5] = uint8_t(scm);
-              sc.v[i >> 5] = uint8_t(scv);
-            }
-          }
-        } else {
-          store_f32(reinterpret_cast<float*>(t.m), i, n, w.m);
-          store_f32(reinterpret_cast<float*>(t.v), i, n, w.v);
         }
+        store_bf16(reinterpret_cast<uint16_t*>(t.param), i, n, b);
+      } else {
+        store_f32(reinterpret_cast<float*>(t.param), i, n, w.p);
+      }
+      if constexpr (EIGHT) {
+        uint32_t rand[4];
+        if constexpr (STOCHASTIC) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) rand[j] = mix32(key0 + uint32_t(i) + j);
+        }
+        uint32_t scm, scv;
+        const uint32_t qm = state_quant<false, STOCHASTIC>(w.m, rand, &scm);    // all lanes: eight of them agree on a block
+        const uint32_t qv = state_quant<true, STOCHASTIC>(r, rand, &scv);
+        if (i < ((n + 127) & ~int64_t(127))) {
+          __builtin_nontemporal_store(qm, reinterpret_cast<uint32_t*>(t.m + i));
+          __builtin_nontemporal_store(qv, reinterpret_cast<uint32_t*>(t.v + i));
+          if ((i & 31) == 0) {
+            sc.m[i >> 5] = uint8_t(scm);
+            sc.v[i >> 5] = uint8_t(scv);
+          }
+        }
+      } else {
+        store_f32(reinterpret_cast<float*>(t.m), i, n, w.m);
+        store_f32(reinterpret_cast<float*>(t.v), i, n, w.v);
       }
     }
   }
@@ -365,15 +359,15 @@ template <bool EIGHT>
 static hipError_t adamw_launches(const moe_adamw_t& h, const moe_adamw_tensor_t* tensors, int count, int cus, hipStream_t st) {
   int64_t values = 0;
   for (int i = 0; i < count; ++i) values += tensors[i].n;
-  const bool few = values < int64_t(cus) * 8 * adam_chunk(2);
-  const int chunk = adam_chunk(few ? 1 : 2);
+  const bool two = EIGHT && values >= int64_t(cus) * 8 * 2 * kAdamPart;
+  const int chunk = two ? 2 * kAdamPart : kAdamPart;
   for (int i = 0; i < count;) {
     AdamArgs<EIGHT> a{};
     a.first = i;
     int64_t chunks = 0;
     for (; i < count && a.count < adam_tensors(EIGHT); ++i) {
       const moe_adamw_tensor_t& t = tensors[i];
-      const int64_t mine = (t.n + chunk - 1) / chunk;          // at most 2^28
+      const int64_t mine = (t.n + chunk - 1) / chunk;          // at most 2^30
       if (chunks + mine >= int64_t(1) << 31) break;
       AdamTensor<EIGHT>& d = a.t[a.count];
       d.param = static_cast<char*>(t.param);
@@ -403,10 +397,10 @@ static hipError_t adamw_launches(const moe_adamw_t& h, const moe_adamw_tensor_t*
     a.by_r = float(1.0 / sqrt(1.0 - pow(h.beta2, double(h.step))));
     // a workgroup a chunk (553 M values: 1726 us; sixteen workgroups a CU that loop 1814)
     const dim3 grid(int(chunks < (1 << 22) ? chunks : 1 << 22)), threads(kAdamThreads);
-    if (few && h.stochastic) hipLaunchKernelGGL((adamw_kernel<EIGHT, true, 1>), grid, threads, 0, st, a);
-    else if (few) hipLaunchKernelGGL((adamw_kernel<EIGHT, false, 1>), grid, threads, 0, st, a);
-    else if (h.stochastic) hipLaunchKernelGGL((adamw_kernel<EIGHT, true, 2>), grid, threads, 0, st, a);
-    else hipLaunchKernelGGL((adamw_kernel<EIGHT, false, 2>), grid, threads, 0, st, a);
+    if (two && h.stochastic) hipLaunchKernelGGL((adamw_kernel<EIGHT, true, EIGHT ? 2 : 1>), grid, threads, 0, st, a);
+    else if (two) hipLaunchKernelGGL((adamw_kernel<EIGHT, false, EIGHT ? 2 : 1>), grid, threads, 0, st, a);
+    else if (h.stochastic) hipLaunchKernelGGL((adamw_kernel<EIGHT, true, 1>), grid, threads, 0, st, a);
+    else hipLaunchKernelGGL((adamw_kernel<EIGHT, false, 1>), grid, threads, 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -4,16 +4,17 @@
 //   xe[s] = xq[r][t], xe_scales[:, s] = xq_scales[r][:, t] with (r, t) = pull_src[s].
 //
 // Half (a quarter) of the bytes that the bf16 rows would cost on the way to their experts, and a token is quantised once
-// instead of at every expert that it goes to.  Bound by bytes: a wave copies a row's codes in 16-byte vectors, all of
-// them in flight at once.  The scale words of a row lie in d / 128 planes; a workgroup collects those of its chunk of
+// instead of at every expert that it goes to.  Bound by bytes: a wave copies a row's codes in 16-byte vectors, four a lane
+// in flight at once.  The scale words of a row lie in d / 128 planes; a workgroup collects those of its chunk of
 // rows in LDS and writes each plane's words as one run.
 #include "common.hpp"
 
 namespace moe {
 
 constexpr int kCodesRows = 32;            // rows of a workgroup's chunk
+// Vectors that a lane has in flight: 16384 rows of 7168 bytes to two experts each 70.7 us with two, 70.0 with four, 73 with seven (a whole row)
+constexpr int U = 4;
 
-template <int U>
 __global__ __launch_bounds__(256) void dispatch_codes_kernel(RankPtrs<const char*> xq, RankPtrs<const uint32_t*> xs,
                                                              const int32_t* __restrict__ pull_src,
                                                              const int32_t* __restrict__ ctrl, char* __restrict__ xe,
@@ -67,12 +68,7 @@ hipError_t launch_dispatch_codes(const moe_shape_t& s, const uint8_t* const* xq,
   const dim3 grid(int(need < cus * 8 ? need : cus * 8));
   char* out = reinterpret_cast<char*>(xe);
   uint32_t* words = reinterpret_cast<uint32_t*>(xe_scales);
-  if (row_bytes <= 64 * 16 * 2)
-    hipLaunchKernelGGL(dispatch_codes_kernel<2>, grid, dim3(256), 0, st, q, w, pull_src, ctrl, out, words, row_bytes,
-                       s.d >> 7, s.T, nmax);
-  else
-    hipLaunchKernelGGL(dispatch_codes_kernel<7>, grid, dim3(256), 0, st, q, w, pull_src, ctrl, out, words, row_bytes,
-                       s.d >> 7, s.T, nmax);
+  hipLaunchKernelGGL(dispatch_codes_kernel, grid, dim3(256), 0, st, q, w, pull_src, ctrl, out, words, row_bytes, s.d >> 7, s.T, nmax);
   return hipGetLastError();
 }
 

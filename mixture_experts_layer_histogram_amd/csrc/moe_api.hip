@@ -1175,6 +1175,10 @@ int moe_adamw(const moe_adamw_t* a, const moe_adamw_tensor_t* tensors, int32_t c
         (rc = check_optional(t.master, 16)))
       return rc;
     if (eight && ((rc = check_scales(t.m_scales)) || (rc = check_scales(t.v_scales)))) return rc;
+    const void* const own[] = {t.param, t.grad, t.m, t.v, t.master, eight ? t.m_scales : nullptr, eight ? t.v_scales : nullptr};
+    for (int j = 1; j < 7; ++j)
+      for (int l = 0; l < j; ++l)
+        if (own[j] && own[j] == own[l]) return MOE_EINVAL;
   }
   return hip_rc(launch_adamw(*a, tensors, count, cu_count(), static_cast<hipStream_t>(stream)));
 }

@@ -39,9 +39,9 @@ struct RowVec {
   }
 };
 
-// Rows from kNormPast bytes on go past the caches, which do not hold them until somebody reads them: 32768 x 7168 bf16 with residual and
-// MXFP8 449 -> 398 us, the backward 382 -> 347.
-constexpr int64_t kNormPast = int64_t(64) << 20;
+// Rows from kNormPast bytes on go past the caches, which do not hold them until somebody reads them.  us of two norms on end, bf16, past
+// them and through them: 4096 x 7168 80.7 and 76.7, 8192 x 7168 124 and 114, 32768 x 7168 393 and 413 (with residual and MXFP8 398 and 449).
+constexpr int64_t kNormPast = int64_t(256) << 20;
 
 // (a template: of two stores in the arms of a branch the compiler makes one, through the caches)
 template <bool PAST>
@@ -337,52 +337,46 @@ __global__ __launch_bounds__(1024) void norm_gamma_kernel(const float* __restric
   }
 }
 
-// Waves a row: up to 32 values a lane
-int norm_waves(int d) { return d <= 2048 ? 1 : d <= 8192 ? 4 : 16; }
+// Waves a row.  Few values a lane keep enough rows in flight, many waves a row wait for each other.  us of two norms on end and of the
+// gradients, bf16: 4096 x 2048, one wave 39.2 and 31.5, four 29.7 and 22.5; 2048 x 4096, four 39.0, eight 27.8 (gradients 21.0, 21.1); 4096 x 7168,
+// four 76.7 and 43.5, eight 65.0 and 41.7, sixteen 66.1 and 47.4; 32768 x 7168, four 393 and 256, eight 387 and 250, sixteen 443 and 291.
+int norm_waves(int d) { return d <= 512 ? 1 : d <= 2048 ? 4 : d <= 8192 ? 8 : 16; }
 
-// Workgroups of the backward, each of which leaves one partial sum of dgamma
+// Workgroups of the backward, each of which leaves one partial sum of dgamma: 4096 waves.  Twice as many write and read those sums for longer
+// (4096 x 7168 51.5 us instead of 43.5, with four waves a row), half as many leave too few rows in flight (48.1 instead of 41.7, 32768 x 7168
+// 296 instead of 250).
 int norm_bwd_grid(int64_t rows, int d) {
-  const int per = norm_waves(d) == 1 ? 4 : 1;
+  const int W = norm_waves(d), per = W == 1 ? 4 : 1, most = W <= 4 ? 1024 : 4096 / W;
   const int64_t need = (rows + per - 1) / per;
-  return int(need < 1024 ? need : 1024);
+  return int(need < most ? need : most);
 }
 
-template <bool BF16, int W, bool PAST>
+template <bool BF16, int W, int E, bool PAST>
 static void norm_launch(const NormArgs& a, int grid, size_t lds, hipStream_t st) {
-  const int per_lane = (a.d + 64 * W - 1) / (64 * W);
-  const dim3 threads(W < 4 ? 256 : 64 * W);
-  if (per_lane <= 8) hipLaunchKernelGGL((norm_kernel<BF16, W, 8, PAST>), dim3(grid), threads, lds, st, a);
-  else if (per_lane <= 16) hipLaunchKernelGGL((norm_kernel<BF16, W, 16, PAST>), dim3(grid), threads, lds, st, a);
-  else hipLaunchKernelGGL((norm_kernel<BF16, W, 32, PAST>), dim3(grid), threads, lds, st, a);
+  hipLaunchKernelGGL((norm_kernel<BF16, W, E, PAST>), dim3(grid), dim3(W < 4 ? 256 : 64 * W), lds, st, a);
 }
-
-template <bool BF16, int W, bool PAST>
+template <bool BF16, int W, int E, bool PAST>
 static void norm_launch(const NormBwdArgs& a, int grid, size_t lds, hipStream_t st) {
-  const int per_lane = (a.d + 64 * W - 1) / (64 * W);
-  const dim3 threads(W < 4 ? 256 : 64 * W);
-  if (per_lane <= 8) hipLaunchKernelGGL((norm_bwd_kernel<BF16, W, 8, PAST>), dim3(grid), threads, lds, st, a);
-  else if (per_lane <= 16) hipLaunchKernelGGL((norm_bwd_kernel<BF16, W, 16, PAST>), dim3(grid), threads, lds, st, a);
-  else hipLaunchKernelGGL((norm_bwd_kernel<BF16, W, 32, PAST>), dim3(grid), threads, lds, st, a);
+  hipLaunchKernelGGL((norm_bwd_kernel<BF16, W, E, PAST>), dim3(grid), dim3(W < 4 ? 256 : 64 * W), lds, st, a);
 }
 
 template <typename ARGS>
 static hipError_t norm_pick(const ARGS& a, int dtype, int grid, size_t lds, hipStream_t st) {
-  const int W = norm_waves(a.d);
-  const bool past = a.rows * a.d * (dtype == MOE_BF16 ? 2 : 4) >= kNormPast;
-  auto pick = [&](auto bf16) {
-    constexpr bool B = decltype(bf16)::value;
-    if (past) {
-      if (W == 1) norm_launch<B, 1, true>(a, grid, lds, st);
-      else if (W == 4) norm_launch<B, 4, true>(a, grid, lds, st);
-      else norm_launch<B, 16, true>(a, grid, lds, st);
-    } else {
-      if (W == 1) norm_launch<B, 1, false>(a, grid, lds, st);
-      else if (W == 4) norm_launch<B, 4, false>(a, grid, lds, st);
-      else norm_launch<B, 16, false>(a, grid, lds, st);
-    }
+  const int W = norm_waves(a.d), lane = (a.d + 64 * W - 1) / (64 * W);           // values a lane: 8, 16 or 32
+  auto pick = [&](auto bf16, auto past) {
+    constexpr bool B = decltype(bf16)::value, P = decltype(past)::value;
+    if (W == 1) norm_launch<B, 1, 8, P>(a, grid, lds, st);
+    else if (W == 4) norm_launch<B, 4, 8, P>(a, grid, lds, st);
+    else if (W == 8 && lane <= 8) norm_launch<B, 8, 8, P>(a, grid, lds, st);
+    else if (W == 8) norm_launch<B, 8, 16, P>(a, grid, lds, st);
+    else if (lane <= 16) norm_launch<B, 16, 16, P>(a, grid, lds, st);
+    else norm_launch<B, 16, 32, P>(a, grid, lds, st);
   };
-  if (dtype == MOE_BF16) pick(std::true_type{});
-  else pick(std::false_type{});
+  const bool past = a.rows * a.d * (dtype == MOE_BF16 ? 2 : 4) >= kNormPast;
+  if (dtype == MOE_BF16 && past) pick(std::true_type{}, std::true_type{});
+  else if (dtype == MOE_BF16) pick(std::true_type{}, std::false_type{});
+  else if (past) pick(std::false_type{}, std::true_type{});
+  else pick(std::false_type{}, std::false_type{});
   return hipGetLastError();
 }
 
@@ -392,7 +386,7 @@ hipError_t launch_norm(const moe_norm_t& n, const void* x, const void* residual,
   const NormArgs a{static_cast<const char*>(x), static_cast<const char*>(residual), gamma, static_cast<char*>(h),
                    static_cast<char*>(y), codes, scales, n.rows, n.d, n.eps};
   const int W = norm_waves(n.d), per = W == 1 ? 4 : 1;
-  const int64_t need = (n.rows + per - 1) / per, most = int64_t(cus) * (W == 16 ? 2 : 8);
+  const int64_t need = (n.rows + per - 1) / per, most = int64_t(cus) * (W <= 4 ? 8 : 32 / W);      // 32 waves a CU
   const int grid = int(need < most ? need : most);
   const size_t lds = codes ? size_t(kNormChunk) * ((n.d >> 7) + 1) * 4 : 0;
   return norm_pick(a, n.dtype, grid, lds, st);

@@ -166,6 +166,12 @@ def test_adamw_refusals(kw, code):
     assert _adamw(**kw) == code
 
 
+@pytest.mark.parametrize("kw", [dict(grad=A), dict(m=A), dict(m=B), dict(v=C), dict(v=B), dict(master=A), dict(master=D), dict(m_scales=C),
+                                dict(v_scales=E), dict(state_dtype=moe.MOE_F32, v=C)])
+def test_adamw_refuses_a_buffer_in_two_places(kw):
+    assert _adamw(**kw) == -1
+
+
 def test_adamw_of_nothing():
     step = moe.AdamW(*STEP.values())
     assert moe.moe_adamw(step, [], stream=0) == 0

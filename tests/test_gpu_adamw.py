@@ -225,3 +225,27 @@ def test_eight_bit_states_follow_fp32_states():
     assert -0.02 < vb.mean() / va.mean() - 1 < 0.045 + 0.02
     moved = _np(a.param[:n]) - _np(b.param[:n])
     assert np.abs(moved).mean() < 500 * LR * 0.1
+
+
+def test_a_step_of_millions():
+    """So many values that a workgroup takes two parts of a tensor at a time, beside tensors that end in either."""
+    ts = [Tensor(n, "bf16", "bf16", True, True, 30 + i) for i, n in enumerate((4300001, 1025, 2048, 1, 3073, 1024))]
+    old = [t.copy() for t in ts]
+    _step(ts, 5, 3, True, True)
+    for i, (t, o) in enumerate(zip(ts, old)):
+        t.check(o, i, 5, 3, True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_values_of_states_for_every_code_and_scale(dtype):
+    """Rows of 128 go their own way in moe_mx_dequantize: the same bits as rows of 256, for all 256 codes under all 256 scales."""
+    torch = _torch()
+    kind, code = (torch.bfloat16, moe.MOE_BF16) if dtype == "bf16" else (torch.float32, moe.MOE_F32)
+    codes = torch.arange(256, device="cuda").repeat(256, 1).to(torch.uint8)                        # [scale][code]
+    scales = torch.arange(256, device="cuda").to(torch.uint8)
+    wide, rows = torch.empty(256, 256, dtype=kind, device="cuda"), torch.empty(512, 128, dtype=kind, device="cuda")
+    moe.moe_mx_dequantize(codes, scales.repeat_interleave(4).repeat(2).contiguous(), moe.MOE_MXFP8, 256, 256, wide, code)
+    moe.moe_mx_dequantize(codes, scales.repeat_interleave(8).contiguous(), moe.MOE_MXFP8, 512, 128, rows, code)
+    a, b = wide.reshape(-1).float(), rows.reshape(-1).float()
+    nan = torch.isnan(a)
+    assert torch.equal(nan, torch.isnan(b)) and torch.equal(a[~nan], b[~nan]) and int(nan.sum()) == 256 + 2 * 255
