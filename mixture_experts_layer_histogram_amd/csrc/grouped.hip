@@ -273,24 +273,40 @@ struct BigGradients {
   }
 };
 
+constexpr int kTileSteps = 3;            // what a tile's stores take, in steps
 template <int T, int THREADS, typename O, bool ADD>
 __device__ __forceinline__ void grouped_gradients(const WgradArgs& g, char* smem) {
   int32_t* base = reinterpret_cast<int32_t*>(smem);
   bool bad;
-  group_tiles<THREADS>(g.offsets, g.G, g.rows, 8, base, base + kMaxGroups + 8, &bad);
+  group_tiles<THREADS>(g.offsets, g.G, g.rows, 6, base, base + kMaxGroups + 8, &bad);
   if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
   if (bad) return;
   __syncthreads();
-  const int MT = (g.M + T - 1) / T, NT = (g.N + T - 1) / T;
-  const int64_t total = int64_t(g.G) * MT * NT, per_xcd = (total + 7) >> 3;
+  const int MT = (g.M + T - 1) / T, NT = (g.N + T - 1) / T, per_group = MT * NT;
+  // Every XCD gets consecutive tiles of an eighth of the work, by the K steps of 64 that its groups' rows make.
+  auto ahead = [&](int l) { return int64_t(per_group) * (base[l] + kTileSteps * l); };
+  auto tile_at = [&](int64_t work) -> int64_t {
+    int l = 0;
+    for (int hi = g.G - 1; l < hi;) {
+      const int mid = (l + hi + 1) >> 1;
+      if (ahead(mid) <= work) l = mid;
+      else hi = mid - 1;
+    }
+    const int64_t one = base[l + 1] - base[l] + kTileSteps, in = (work - ahead(l) + one - 1) / one;
+    return int64_t(l) * per_group + (in < per_group ? in : per_group);
+  };
   const int xcd = blockIdx.x & 7, wg_per_xcd = gridDim.x >> 3, lane = threadIdx.x & 63;
-  for (int64_t t0 = blockIdx.x >> 3; t0 < per_xcd; t0 += 64 * int64_t(wg_per_xcd)) {
-    const int64_t tt = t0 + int64_t(lane) * wg_per_xcd, tau = xcd * per_xcd + tt;
-    const bool mine = tt < per_xcd && tau < total;
+  const int64_t work = ahead(g.G), first = tile_at(work * xcd / 8), past = tile_at(work * (xcd + 1) / 8);
+  __syncthreads();                        // the tables' LDS becomes the ring's
+  for (int64_t t0 = first + (blockIdx.x >> 3); t0 < past; t0 += 64 * int64_t(wg_per_xcd)) {
+    const int64_t tau = t0 + int64_t(lane) * wg_per_xcd;
+    const bool mine = tau < past;
     int l = 0, mt = 0, nt = 0, r0 = 0, rows = 0;
     if (mine) {
-      l = int(tau / (int64_t(MT) * NT));
-      big_place(tau - int64_t(l) * MT * NT, MT, NT, &mt, &nt);
+      l = int(tau / per_group);
+      // Bands over the longer axis: 32 groups of about 512 rows, 7168 x 2048 545 us, 2048 x 7168 544, over the shorter one 649 and 677; as long: the same
+      if (MT >= NT) big_place(tau - int64_t(l) * per_group, MT, NT, &mt, &nt);
+      else big_place(tau - int64_t(l) * per_group, NT, MT, &nt, &mt);
       r0 = g.offsets[l];
       rows = g.offsets[l + 1] - r0;
     }
