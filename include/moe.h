@@ -801,7 +801,7 @@ int moe_dispatch_pull_codes(const moe_shape_t* s, const moe_placement_t* p, cons
  * descend or leave that range are found on the device: the call then computes nothing and sets *status to MOE_EINVAL.
  */
 typedef struct {
-  int64_t rows;      /* rows that x and y have, at least offsets[groups]; < 2^31 */
+  int64_t rows;      /* rows that x and y have, at least offsets[groups]; <= 2^30 */
   int32_t groups;    /* 1 .. 1024 */
   int32_t K, N;      /* values of an x row and of a y row */
   int32_t dtype;     /* MOE_BF16 or MOE_F32 (else MOE_EUNSUP), of x, w and y */
@@ -829,7 +829,8 @@ int moe_grouped_gemm(const moe_gemm_t* g, const void* x, const void* w, const in
  * fp32 accumulation, rounded once to dw_dtype: the row type, or MOE_F32.  A group with no rows gets zeros.
  * accumulate != 0: added to what dw holds (MOE_F32 only, else MOE_EINVAL): gradients of several batches.
  * dy: rows of N values with stride ldy.  ws: at least moe_grouped_gemm_wgrad_workspace_bytes() bytes, 256-byte aligned
- * (NULL where that is 0; the kernels of this version need none).  Other arguments, limits and errors as moe_grouped_gemm; with bad offsets dw stays as it is.
+ * (may be NULL where that is 0): few small matrices with many rows are summed in pieces there, whose number goes by `rows` and the
+ * sizes alone.  Deterministic, as moe_grouped_gemm.  Other arguments, limits and errors as there; with bad offsets dw stays as it is.
  */
 size_t moe_grouped_gemm_wgrad_workspace_bytes(const moe_gemm_t* g);
 int moe_grouped_gemm_wgrad(const moe_gemm_t* g, const void* x, const void* dy, const int32_t* offsets, void* dw,

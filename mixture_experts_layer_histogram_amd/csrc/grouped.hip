@@ -455,7 +455,68 @@ hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, con
   return hipGetLastError();
 }
 
-hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* dy, const int32_t* offsets, void* dw,
+// ---- gradients of so few tiles that they would leave most of the card idle: the rows of a group go in `parts` pieces, as if they were groups of
+// their own, into fp32 gradients of theirs in the workspace, which are added up in order.  us whole and in pieces, bf16:
+// one matrix of 256 x 512 with 100000 rows 1626 and 72, 7168 x 256 with 32768 rows 648 and 170, 2048 x 2048 with 4096 rows 74 and 69, with 2048 rows 41 and
+// 48 (pieces of 1024 rows), 8 of 1024 x 1024 with 16384 rows 54 and 66 (likewise); fp32: 64 x 64 with 100000 rows 875 and 36, 256 x 256 with 2048 rows 22
+// and 14.
+constexpr int kSplitCUs = 256;
+
+// Pieces of a group, by the sizes alone
+int wgrad_parts(const moe_gemm_t& s) {
+  const bool f32 = s.dtype == MOE_F32;
+  const int T = f32 ? 32 : kBig, least = f32 ? 512 : 2048;        // rows of a piece on the mean, at least
+  const int64_t tiles = int64_t(s.groups) * ((s.K + T - 1) / T) * ((s.N + T - 1) / T);
+  int64_t n = (f32 ? 2 : 1) * kSplitCUs / tiles;
+  n = n < s.rows / (int64_t(s.groups) * least) ? n : s.rows / (int64_t(s.groups) * least);
+  n = n < kMaxGroups / s.groups ? n : kMaxGroups / s.groups;
+  return n < 2 ? 1 : int(n);
+}
+
+static size_t parts_bytes(const moe_gemm_t& s, int parts) { return align256(size_t(4) * (size_t(s.groups) * parts + 1)); }
+
+size_t wgrad_workspace(const moe_gemm_t& s) {
+  const int parts = wgrad_parts(s);
+  return parts == 1 ? 0 : parts_bytes(s, parts) + align256(size_t(s.groups) * parts * s.K * s.N * 4);
+}
+
+// The offsets of the pieces, by one workgroup; bad ones (to whoever reads these, too) where the groups' are.
+__global__ __launch_bounds__(1024) void wgrad_parts_kernel(const int32_t* __restrict__ offsets, int G, int parts, int64_t rows,
+                                                           int32_t* __restrict__ out) {
+  __shared__ int wrong;
+  if (threadIdx.x == 0) wrong = 0;
+  __syncthreads();
+  for (int g = threadIdx.x; g < G; g += 1024)
+    if (offsets[g] < 0 || offsets[g + 1] < offsets[g] || offsets[g + 1] > rows) wrong = 1;
+  __syncthreads();
+  for (int v = threadIdx.x; v <= G * parts; v += 1024) {
+    const int g = v / parts, i = v - g * parts, first = offsets[g], n = i ? offsets[g + 1] - first : 0;
+    const int len = ((n + parts - 1) / parts + kBigBK - 1) & ~(kBigBK - 1);
+    out[v] = wrong ? -1 : first + int(min(int64_t(n), int64_t(i) * len));
+  }
+}
+
+// dw = sum over the pieces, in order
+template <typename O, bool ADD>
+__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict__ sums, const int32_t* __restrict__ bounds, int parts, int64_t size,
+                                                         int64_t vectors, O* __restrict__ dw) {
+  if (bounds[0] < 0) return;
+  for (int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x; t < vectors; t += int64_t(gridDim.x) * 256) {
+    const int64_t g = t * 4 / size;
+    const float* p = sums + g * size * (parts - 1) + t * 4;
+    f32x4 v = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll 4
+    for (int i = 1; i < parts; ++i) v += *reinterpret_cast<const f32x4*>(p + i * size);
+    if constexpr (sizeof(O) == 2) {
+      *reinterpret_cast<uint2*>(dw + t * 4) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    } else {
+      if constexpr (ADD) v += *reinterpret_cast<const f32x4*>(dw + t * 4);
+      *reinterpret_cast<f32x4*>(dw + t * 4) = v;
+    }
+  }
+}
+
+static hipError_t launch_wgrad_whole(const moe_gemm_t& s, const void* x, const void* dy, const int32_t* offsets, void* dw,
                                 int dw_dtype, bool accumulate, int32_t* status, int cus, hipStream_t st) {
   const int64_t ldx = s.ldx ? s.ldx : s.K, ldy = s.ldy ? s.ldy : s.N;
   const WgradArgs g = s.w_layout ? WgradArgs{x, dy, dw, offsets, status, s.rows, ldx, ldy, s.groups, s.K, s.N}
@@ -484,6 +545,29 @@ hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* 
     else if (accumulate) hipLaunchKernelGGL((grouped_big_wgrad_kernel<float, true>), big, many, kBigLds, st, g);
     else hipLaunchKernelGGL((grouped_big_wgrad_kernel<float, false>), big, many, kBigLds, st, g);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* dy, const int32_t* offsets, void* dw,
+                                int dw_dtype, bool accumulate, void* ws, int32_t* status, int cus, hipStream_t st) {
+  const int parts = wgrad_parts(s);
+  if (parts == 1) return launch_wgrad_whole(s, x, dy, offsets, dw, dw_dtype, accumulate, status, cus, st);
+  int32_t* const bounds = static_cast<int32_t*>(ws);
+  float* const sums = reinterpret_cast<float*>(static_cast<char*>(ws) + parts_bytes(s, parts));
+  hipLaunchKernelGGL(wgrad_parts_kernel, dim3(1), dim3(1024), 0, st, offsets, s.groups, parts, s.rows, bounds);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  moe_gemm_t pieces = s;
+  pieces.groups = s.groups * parts;
+  if ((e = launch_wgrad_whole(pieces, x, dy, bounds, sums, MOE_F32, false, status, cus, st)) != hipSuccess) return e;
+  const int64_t size = int64_t(s.K) * s.N, vectors = s.groups * size / 4, need = (vectors + 255) / 256;
+  const dim3 grid(int(need < (1 << 20) ? need : 1 << 20)), threads(256);
+  if (dw_dtype != MOE_F32)
+    hipLaunchKernelGGL((wgrad_join_kernel<uint16_t, false>), grid, threads, 0, st, sums, bounds, parts, size, vectors, static_cast<uint16_t*>(dw));
+  else if (accumulate)
+    hipLaunchKernelGGL((wgrad_join_kernel<float, true>), grid, threads, 0, st, sums, bounds, parts, size, vectors, static_cast<float*>(dw));
+  else
+    hipLaunchKernelGGL((wgrad_join_kernel<float, false>), grid, threads, 0, st, sums, bounds, parts, size, vectors, static_cast<float*>(dw));
   return hipGetLastError();
 }
 

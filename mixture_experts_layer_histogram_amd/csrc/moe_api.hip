@@ -103,7 +103,8 @@ hipError_t launch_dispatch_codes(const moe_shape_t& s, const uint8_t* const* xq,
 hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, const int32_t* offsets, void* y,
                           int32_t* status, int cus, hipStream_t st);
 hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* dy, const int32_t* offsets, void* dw,
-                                int dw_dtype, bool accumulate, int32_t* status, int cus, hipStream_t st);
+                                int dw_dtype, bool accumulate, void* ws, int32_t* status, int cus, hipStream_t st);
+size_t wgrad_workspace(const moe_gemm_t& s);
 hipError_t launch_adamw(const moe_adamw_t& h, const moe_adamw_tensor_t* tensors, int count, int cus, hipStream_t st);
 hipError_t launch_states_values(const uint8_t* codes, const uint8_t* scales, int64_t rows, void* dst, int dst_dtype,
                                 hipStream_t st);
@@ -251,7 +252,7 @@ int check_norm(const moe_norm_t* n) {
 int check_gemm(const moe_gemm_t* g) {
   if (!g) return MOE_EINVAL;
   if (g->dtype != MOE_F32 && g->dtype != MOE_BF16) return MOE_EUNSUP;
-  if (g->rows < 0 || g->rows >= (int64_t(1) << 31) || g->groups < 1 || g->groups > 1024) return MOE_EINVAL;
+  if (g->rows < 0 || g->rows > (int64_t(1) << 30) || g->groups < 1 || g->groups > 1024) return MOE_EINVAL;
   if (g->K < 1 || g->N < 1 || int64_t(g->K) * g->N >= (int64_t(1) << 31)) return MOE_EINVAL;
   if (g->w_layout != 0 && g->w_layout != 1) return MOE_EINVAL;
   const int64_t most = int64_t(1) << 22;
@@ -1128,8 +1129,7 @@ int moe_grouped_gemm(const moe_gemm_t* g, const void* x, const void* w, const in
 }
 
 size_t moe_grouped_gemm_wgrad_workspace_bytes(const moe_gemm_t* g) {
-  (void)g;
-  return 0;
+  return check_gemm(g) == MOE_OK ? wgrad_workspace(*g) : 0;
 }
 
 int moe_grouped_gemm_wgrad(const moe_gemm_t* g, const void* x, const void* dy, const int32_t* offsets, void* dw,
@@ -1150,7 +1150,7 @@ int moe_grouped_gemm_wgrad(const moe_gemm_t* g, const void* x, const void* dy, c
     if (reinterpret_cast<uintptr_t>(ws) & 255) return MOE_EALIGN;
     if (ws_bytes < need) return MOE_ENOSPC;
   }
-  return hip_rc(launch_grouped_wgrad(*g, x, dy, offsets, dw, dw_dtype, accumulate != 0, status, cu_count(),
+  return hip_rc(launch_grouped_wgrad(*g, x, dy, offsets, dw, dw_dtype, accumulate != 0, ws, status, cu_count(),
                                      static_cast<hipStream_t>(stream)));
 }
 

@@ -115,7 +115,7 @@ def _wgrad(**kw):
 
 @pytest.mark.parametrize("call", [_gemm, _wgrad])
 @pytest.mark.parametrize("kw,code", [
-    (dict(rows=-1), -1), (dict(rows=1 << 31), -1), (dict(groups=0), -1), (dict(groups=1025), -1), (dict(K=0), -1), (dict(N=0), -1),
+    (dict(rows=-1), -1), (dict(rows=1 << 31), -1), (dict(rows=(1 << 30) + 1), -1), (dict(groups=0), -1), (dict(groups=1025), -1), (dict(K=0), -1), (dict(N=0), -1),
     (dict(K=1 << 16, N=1 << 15), -1), (dict(K=(1 << 22) + 8, N=8), -1), (dict(w_layout=2), -1), (dict(w_layout=-1), -1),
     (dict(dtype=moe.MOE_MXFP8), -6), (dict(dtype=7), -6), (dict(K=60), -2), (dict(N=68), -2), (dict(dtype=moe.MOE_F32, K=62), -2),
     (dict(ldx=56), -1), (dict(ldy=64), -1), (dict(ldx=68), -2), (dict(ldy=76), -2), (dict(ldx=-8), -1), (dict(ldx=(1 << 22) + 8), -1),
@@ -179,3 +179,14 @@ def test_adamw_of_nothing():
     assert moe.moe_adamw(step, (moe.AdamWTensor(**empty) for _ in range(50)), stream=0) == 0
     assert moe.lib().moe_adamw(ctypes.byref(step), None, 1, None) == -1
     assert moe.lib().moe_adamw(ctypes.byref(step), None, -1, None) == -1
+
+
+def test_wgrad_in_pieces_asks_for_its_workspace():
+    """One matrix of 256 x 512 (2 tiles) with 100000 rows: 48 pieces; groups that fill the card, or few rows: none."""
+    g = moe.Gemm(100000, 1, 256, 512, moe.MOE_BF16, 0)
+    need = moe.moe_grouped_gemm_wgrad_workspace_bytes(g)
+    assert need == 256 + 48 * 256 * 512 * 4
+    call = lambda **kw: moe.moe_grouped_gemm_wgrad(g, A, B, C, D, moe.MOE_BF16, stream=0, check=False, **kw)       # noqa: E731
+    assert call() == -1 and call(ws=E + 64, ws_bytes=need) == -2 and call(ws=E, ws_bytes=need - 1) == -3
+    assert moe.moe_grouped_gemm_wgrad_workspace_bytes(moe.Gemm(100000, 64, 1024, 512, moe.MOE_BF16, 0)) == 0
+    assert moe.moe_grouped_gemm_wgrad_workspace_bytes(moe.Gemm(4095, 1, 256, 512, moe.MOE_BF16, 0)) == 0

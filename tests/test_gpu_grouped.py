@@ -68,6 +68,7 @@ CASES = [
     ([2000], 256, 128), ([500, 1, 1, 1, 1], 72, 1032), ([0] * 1023 + [3], 16, 16), ([2] * 1000, 24, 40), ([1100, 900], 2048, 512),
     ([1500, 548], 136, 1304), ([1500, 548], 192, 1304), ([300, 20, 0, 600, 77, 256, 3, 129], 520, 776),
     ([300, 20, 0, 600, 77, 256, 3, 129], 72, 4104), ([260, 257, 9], 8, 9000), ([700, 0, 350], 320, 8712),
+    ([4100], 72, 136), ([3000, 0, 5, 9000], 64, 256), ([2048, 2047], 264, 40), ([0, 0, 9000], 8, 16), ([12300, 0, 5], 40, 264), ([100, 16500], 72, 8),
 ]
 
 
@@ -207,3 +208,52 @@ def test_no_rows():
     ws = torch.empty(moe.moe_grouped_gemm_wgrad_workspace_bytes(g), dtype=torch.uint8, device="cuda")
     moe.moe_grouped_gemm_wgrad(g, None, None, off, dw, moe.MOE_BF16, ws)
     assert (dw == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bad_offsets_of_a_gradient_in_pieces(dtype):
+    """Nothing is computed, in the workspace's pieces or behind them; the next call with good ones is whole."""
+    torch = _torch()
+    code, kind = _kind(dtype)
+    g = moe.Gemm(9000, 1, 64, 64, code, 0)
+    x, dy = _make((9000, 64), dtype, 1, True), _make((9000, 64), dtype, 2, True)
+    ws = torch.empty(moe.moe_grouped_gemm_wgrad_workspace_bytes(g), dtype=torch.uint8, device="cuda").fill_(0x5A)
+    assert ws.numel() > 0
+    dw, status = torch.full((64, 64), 7.0, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for bad in ([0, 9001], [10, 9], [-1, 9000]):
+        moe.moe_grouped_gemm_wgrad(g, x, dy, torch.tensor(bad, dtype=torch.int32, device="cuda"), dw, moe.MOE_F32, ws, status=status)
+        assert int(status) == -1 and (dw == 7).all()
+        status.zero_()
+    moe.moe_grouped_gemm_wgrad(g, x, dy, torch.tensor([0, 9000], dtype=torch.int32, device="cuda"), dw, moe.MOE_F32, ws, status=status)
+    assert int(status) == 0 and torch.equal(dw, dy.float().t() @ x.float())
+
+
+def test_gradients_in_pieces_of_two_graphs_over_one_workspace():
+    torch = _torch()
+    sizes = [(9000, 1, 64, 128), (20000, 2, 256, 72), (5000, 1, 40, 40)]
+    gs = [moe.Gemm(*s, moe.MOE_BF16, 1) for s in sizes]
+    ws = torch.empty(max(moe.moe_grouped_gemm_wgrad_workspace_bytes(g) for g in gs), dtype=torch.uint8, device="cuda")
+    data = [(_make((r, K), "bf16", i, True), _make((r, N), "bf16", i + 9, True), torch.tensor([0, r // 3, r] if G == 2 else [0, r],
+             dtype=torch.int32, device="cuda"), torch.empty(G, K, N, device="cuda")) for i, (r, G, K, N) in enumerate(sizes)]
+
+    def run(i):
+        moe.moe_grouped_gemm_wgrad(gs[i], data[i][0], data[i][1], data[i][2], data[i][3], moe.MOE_F32, ws)
+
+    want = []
+    for i in range(3):
+        run(i)
+        want.append(data[i][3].clone())
+        off = data[i][2].tolist()
+        for j, (a, b) in enumerate(zip(off, off[1:])):
+            assert torch.equal(want[i][j], data[i][0][a:b].float().t() @ data[i][1][a:b].float())
+    graphs, s = [], torch.cuda.Stream()
+    for i in range(2):
+        s.wait_stream(torch.cuda.current_stream())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i], stream=s):
+            run(i)
+    for i in (0, 1, 2, 1, 0, 0, 2, 1):
+        data[i][3].fill_(float("nan"))
+        graphs[i].replay() if i < 2 else run(i)
+        torch.cuda.synchronize()
+        assert torch.equal(data[i][3], want[i]), i

@@ -2,8 +2,8 @@
 a serving pass with MXFP8 experts and in training steps of experts of another form, eager, captured, on streams and at once.
 
 Bars.  Serving: none, the layer's own path from the same codes gives the same bits.  Training in fp32 against 64-bit gradients:
-four products in a row with sums of at most K = 768 terms, each off by K * 2^-24 of its terms' magnitudes, which are at most
-sqrt(K) of a row's largest value: 4 * 768 * 28 * 2^-24 = 5e-3 of a row's largest value in the worst case; 1e-3 is asked (of
+four products in a row with sums of at most K = 768 terms (a weight gradient's
+of 4700 rows in pieces), each off by K * 2^-24 of its terms' magnitudes, which are at most sqrt(K) of a row's largest value: 4 * 768 * 28 * 2^-24 = 5e-3 of a row's largest value in the worst case; 1e-3 is asked (of
 a hundredth of the tensor's largest value where a row's own are smaller: terms that cancel leave errors of their own size).
 """
 import numpy as np
@@ -100,6 +100,8 @@ class Net:
         self.nws = torch.empty(moe.moe_norm_backward_workspace_bytes(self.norm), dtype=torch.uint8, device="cuda")
         self.up, self.down = moe.Gemm(N, E, d, F, self.code, 0), moe.Gemm(N, E, F, d, self.code, 0)
         self.up_t, self.down_t = moe.Gemm(N, E, F, d, self.code, 1), moe.Gemm(N, E, d, F, self.code, 1)
+        need = max(moe.moe_grouped_gemm_wgrad_workspace_bytes(m) for m in (self.up, self.down))
+        self.gws = torch.empty(need, dtype=torch.uint8, device="cuda")
         self.at, self.lr = torch.ones(1, dtype=torch.int64, device="cuda"), torch.full((1,), LR, device="cuda")
         self.states = []
         for p in (self.gamma, self.wu, self.wd):
@@ -128,11 +130,11 @@ class Net:
         moe.moe_grouped_gemm(self.down, self.b, self.wd, self.off, self.ye)
         moe.moe_combine_merge(self.shape, self.pl, self.ye, self.slot, self.w, [self.z])
         moe.moe_combine_merge_backward(self.shape, self.pl, [self.dz], self.ye, self.slot, self.w, self.dye, self.dw)
-        moe.moe_grouped_gemm_wgrad(self.down, self.b, self.dye, self.off, self.dwd, moe.MOE_F32)
+        moe.moe_grouped_gemm_wgrad(self.down, self.b, self.dye, self.off, self.dwd, moe.MOE_F32, self.gws)
         moe.moe_grouped_gemm(self.down_t, self.dye, self.wd, self.off, self.db)
         torch.mul(self.db, self.a, out=self.db)
         torch.mul(self.db, 2, out=self.db)
-        moe.moe_grouped_gemm_wgrad(self.up, self.xe, self.db, self.off, self.dwu, moe.MOE_F32)
+        moe.moe_grouped_gemm_wgrad(self.up, self.xe, self.db, self.off, self.dwu, moe.MOE_F32, self.gws)
         moe.moe_grouped_gemm(self.up_t, self.db, self.wu, self.off, self.dxe)
         moe.moe_dispatch_pull_backward(self.shape, self.pl, self.dxe, self.slot, [self.dyn])
         moe.moe_norm_backward(self.norm, self.dyn, self.h, self.gamma, self.dz, self.dx, self.dgamma, self.nws)
@@ -140,11 +142,11 @@ class Net:
                                 self.lr.data_ptr(), self.at.data_ptr()), self.table)
 
 
-# T, d, F, E, k: few rows a group, tiles of 128, tiles of 256 (in bf16)
-SIZES = [(5, 256, 384, 8, 2), (700, 512, 768, 8, 2), (3000, 512, 1600, 32, 2)]
+# T, d, F, E, k: few rows a group, tiles of 128, tiles of 256 (in bf16), weight gradients in pieces
+SIZES = [(5, 256, 384, 8, 2), (700, 512, 768, 8, 2), (3000, 512, 1600, 32, 2), (7000, 256, 256, 3, 2)]
 
 
-@pytest.mark.parametrize("T,d,F,E,k", SIZES[:2])
+@pytest.mark.parametrize("T,d,F,E,k", SIZES[:2] + SIZES[3:])
 def test_training_step_against_64_bits(T, d, F, E, k):
     torch = _torch()
     net = Net(T, d, F, E, k, "f32", 1)
@@ -333,7 +335,8 @@ def test_products_past_4_gib(dtype, layout):
         dw = torch.empty_like(w, dtype=torch.float32)
         y[:, :N].zero_()
         y[-600:, :N] = torch.randint(-2, 3, (600, N), device="cuda").to(kind)
-        moe.moe_grouped_gemm_wgrad(g, x, y, off, dw, moe.MOE_F32)
+        ws = torch.empty(moe.moe_grouped_gemm_wgrad_workspace_bytes(g), dtype=torch.uint8, device="cuda")
+        moe.moe_grouped_gemm_wgrad(g, x, y, off, dw, moe.MOE_F32, ws)
         ys = y[-600:, :N].float()
         for i, (a, b) in ((0, (0, at)), (len(counts) - 1, (at, 600))):
             dm = xs[a:b].t() @ ys[a:b]
