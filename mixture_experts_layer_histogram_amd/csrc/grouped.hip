@@ -140,6 +140,7 @@ struct WgradArgs {
   int32_t* status;
   int64_t rows, lda, ldb;
   int G, M, N;
+  const int32_t* used;         // null, or where the number of groups is (at most G)
 };
 
 template <int TB, bool ADD>
@@ -147,6 +148,7 @@ __global__ __launch_bounds__(256) void grouped_f32_wgrad_kernel(WgradArgs g) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ int32_t base[kMaxGroups + 1], part[5];
   bool bad;
+  if (g.used) g.G = *g.used;
   group_tiles<256>(g.offsets, g.G, g.rows, 6, base, part, &bad);
   if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
   if (bad) return;
@@ -276,12 +278,13 @@ struct BigGradients {
 
 constexpr int kTileSteps = 3;            // what a tile's stores take, in steps
 template <int T, int THREADS, typename O, bool ADD>
-__device__ __forceinline__ void grouped_gradients(const WgradArgs& g, char* smem) {
+__device__ __forceinline__ void grouped_gradients(WgradArgs& g, char* smem) {
   int32_t* base = reinterpret_cast<int32_t*>(smem);
   bool bad;
+  if (g.used) g.G = *g.used;
   group_tiles<THREADS>(g.offsets, g.G, g.rows, 6, base, base + kMaxGroups + 8, &bad);
   if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
-  if (bad) return;
+  if (bad || g.G == 0) return;
   __syncthreads();
   const int MT = (g.M + T - 1) / T, NT = (g.N + T - 1) / T, per_group = MT * NT;
   // Every XCD gets consecutive tiles of an eighth of the work, by the K steps of 64 that its groups' rows make.
@@ -455,58 +458,71 @@ hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, con
   return hipGetLastError();
 }
 
-// ---- gradients of so few tiles that they would leave most of the card idle: the rows of a group go in `parts` pieces, as if they were groups of
-// their own, into fp32 gradients of theirs in the workspace, which are added up in order.  us whole and in pieces, bf16:
-// one matrix of 256 x 512 with 100000 rows 1626 and 72, 7168 x 256 with 32768 rows 648 and 170, 2048 x 2048 with 4096 rows 74 and 69, with 2048 rows 41 and
-// 48 (pieces of 1024 rows), 8 of 1024 x 1024 with 16384 rows 54 and 66 (likewise); fp32: 64 x 64 with 100000 rows 875 and 36, 256 x 256 with 2048 rows 22
-// and 14.
-constexpr int kSplitCUs = 256;
+// ---- gradients in pieces: the rows of every group go in pieces of `piece` rows, as if they were groups of their own, into fp32 gradients of
+// theirs in the workspace, which are added up in order.  For matrices of few tiles, which would leave most of the card idle or wait for the
+// group with the most rows, where writing and reading the pieces' gradients takes 20 us at most, or half of what groups of equal sizes take.
+// us whole and in pieces, bf16: one matrix of 256 x 512 with 100000 rows 1626 and 67, 7168 x 256 with 32768 rows 648 and 173; 12 of 440 x 368 with 26401 rows,
+// uneven (softmax of normal numbers) 208 and 57, even 46 and 43; 8 of 512 x 512 with 16384 rows 133 and 39, even 34 and 39; 36 of 128 x 96, even 16 and 24.
+// Left whole: 2048 x 2048 with 2048 rows 41 and 48, 8 of 1024 x 1024 with 16384 rows, even 54 and 66.  fp32: 64 x 64 with 100000 rows 875 and 37, 104 of
+// 28 x 164 with 31015 rows 77 and 34, even 20 and 26.
+constexpr int kPieceCUs = 256;
 
-// Pieces of a group, by the sizes alone
-int wgrad_parts(const moe_gemm_t& s) {
+// Rows of a piece, a power of two, by the sizes alone; 0 for whole groups
+static int64_t wgrad_piece(const moe_gemm_t& s) {
   const bool f32 = s.dtype == MOE_F32;
-  const int T = f32 ? 32 : kBig, least = f32 ? 512 : 2048;        // rows of a piece on the mean, at least
-  const int64_t tiles = int64_t(s.groups) * ((s.K + T - 1) / T) * ((s.N + T - 1) / T);
-  int64_t n = (f32 ? 2 : 1) * kSplitCUs / tiles;
-  n = n < s.rows / (int64_t(s.groups) * least) ? n : s.rows / (int64_t(s.groups) * least);
-  n = n < kMaxGroups / s.groups ? n : kMaxGroups / s.groups;
-  return n < 2 ? 1 : int(n);
+  const int T = f32 ? 32 : kBig, wgs = f32 ? 2 * kPieceCUs : kPieceCUs;
+  const int64_t matrix = int64_t((s.K + T - 1) / T) * ((s.N + T - 1) / T), tiles = matrix * s.groups;
+  int64_t piece = 512;
+  while (piece < s.rows * matrix / wgs || s.rows / piece + s.groups > kMaxGroups) {
+    if (piece > s.rows) return 0;
+    piece *= 2;
+  }
+  if (s.rows < 4 * piece) return 0;
+  const double turns = double((tiles + wgs - 1) / wgs), rows = double(s.rows) / s.groups;
+  const double even = f32 ? rows / 128 * turns : rows / 64 * (tiles * 4 <= kPieceCUs ? 0.6 : 1.5 * turns);       // us
+  const double join = double(s.rows / piece + s.groups) * s.K * s.N * 8 / 5e6;
+  return join <= (even > 40 ? even / 2 : 20) ? piece : 0;
 }
+static int most_pieces(const moe_gemm_t& s, int64_t piece) { return int(s.rows / piece + s.groups); }
 
-static size_t parts_bytes(const moe_gemm_t& s, int parts) { return align256(size_t(4) * (size_t(s.groups) * parts + 1)); }
-
+// The workspace: the pieces' bounds, the first piece of every group, their number; the pieces' gradients
+static size_t piece_table(const moe_gemm_t& s, int64_t piece) { return align256(size_t(4) * (most_pieces(s, piece) + 1 + s.groups + 1)); }
 size_t wgrad_workspace(const moe_gemm_t& s) {
-  const int parts = wgrad_parts(s);
-  return parts == 1 ? 0 : parts_bytes(s, parts) + align256(size_t(s.groups) * parts * s.K * s.N * 4);
+  const int64_t piece = wgrad_piece(s);
+  return piece == 0 ? 0 : piece_table(s, piece) + align256(size_t(most_pieces(s, piece)) * s.K * s.N * 4);
 }
 
-// The offsets of the pieces, by one workgroup; bad ones (to whoever reads these, too) where the groups' are.
-__global__ __launch_bounds__(1024) void wgrad_parts_kernel(const int32_t* __restrict__ offsets, int G, int parts, int64_t rows,
-                                                           int32_t* __restrict__ out) {
-  __shared__ int wrong;
-  if (threadIdx.x == 0) wrong = 0;
+// By one workgroup.  first[G] is the pieces' number; where the offsets are bad, one piece with bad bounds.
+__global__ __launch_bounds__(256) void wgrad_pieces_kernel(const int32_t* __restrict__ offsets, int G, int piece_log2, int64_t rows,
+                                                           int32_t* __restrict__ bounds, int32_t* __restrict__ first) {
+  __shared__ int32_t base[kMaxGroups + 1], part[5];
+  bool bad;
+  int n = group_tiles<256>(offsets, G, rows, piece_log2, base, part, &bad);
   __syncthreads();
-  for (int g = threadIdx.x; g < G; g += 1024)
-    if (offsets[g] < 0 || offsets[g + 1] < offsets[g] || offsets[g + 1] > rows) wrong = 1;
-  __syncthreads();
-  for (int v = threadIdx.x; v <= G * parts; v += 1024) {
-    const int g = v / parts, i = v - g * parts, first = offsets[g], n = i ? offsets[g + 1] - first : 0;
-    const int len = ((n + parts - 1) / parts + kBigBK - 1) & ~(kBigBK - 1);
-    out[v] = wrong ? -1 : first + int(min(int64_t(n), int64_t(i) * len));
+  for (int g = threadIdx.x; g < G; g += 256) first[g] = base[g];
+  for (int v = threadIdx.x; v < n; v += 256) {
+    const int g = find_expert(base, G, v);
+    bounds[v] = offsets[g] + ((v - base[g]) << piece_log2);
+  }
+  if (bad) n = 1;
+  if (threadIdx.x == 0) {
+    first[G] = n;
+    bounds[n] = offsets[G];
+    if (bad) bounds[0] = -1;
   }
 }
 
 // dw = sum over the pieces, in order
 template <typename O, bool ADD>
-__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict__ sums, const int32_t* __restrict__ bounds, int parts, int64_t size,
-                                                         int64_t vectors, O* __restrict__ dw) {
+__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict__ sums, const int32_t* __restrict__ bounds,
+                                                         const int32_t* __restrict__ first, int64_t size, int64_t vectors, O* __restrict__ dw) {
   if (bounds[0] < 0) return;
   for (int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x; t < vectors; t += int64_t(gridDim.x) * 256) {
     const int64_t g = t * 4 / size;
-    const float* p = sums + g * size * (parts - 1) + t * 4;
-    f32x4 v = *reinterpret_cast<const f32x4*>(p);
+    const int b = first[g + 1];
+    f32x4 v{0, 0, 0, 0};
 #pragma unroll 4
-    for (int i = 1; i < parts; ++i) v += *reinterpret_cast<const f32x4*>(p + i * size);
+    for (int i = first[g]; i < b; ++i) v += *reinterpret_cast<const f32x4*>(sums + i * size + (t * 4 - g * size));
     if constexpr (sizeof(O) == 2) {
       *reinterpret_cast<uint2*>(dw + t * 4) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     } else {
@@ -517,10 +533,10 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict
 }
 
 static hipError_t launch_wgrad_whole(const moe_gemm_t& s, const void* x, const void* dy, const int32_t* offsets, void* dw,
-                                int dw_dtype, bool accumulate, int32_t* status, int cus, hipStream_t st) {
+                                int dw_dtype, bool accumulate, int32_t* status, const int32_t* used, int cus, hipStream_t st) {
   const int64_t ldx = s.ldx ? s.ldx : s.K, ldy = s.ldy ? s.ldy : s.N;
-  const WgradArgs g = s.w_layout ? WgradArgs{x, dy, dw, offsets, status, s.rows, ldx, ldy, s.groups, s.K, s.N}
-                                 : WgradArgs{dy, x, dw, offsets, status, s.rows, ldy, ldx, s.groups, s.N, s.K};
+  const WgradArgs g = s.w_layout ? WgradArgs{x, dy, dw, offsets, status, s.rows, ldx, ldy, s.groups, s.K, s.N, used}
+                                 : WgradArgs{dy, x, dw, offsets, status, s.rows, ldy, ldx, s.groups, s.N, s.K, used};
   const hipError_t e = set_grouped_lds();
   if (e != hipSuccess) return e;
   if (s.dtype == MOE_F32) {
@@ -550,24 +566,25 @@ static hipError_t launch_wgrad_whole(const moe_gemm_t& s, const void* x, const v
 
 hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* dy, const int32_t* offsets, void* dw,
                                 int dw_dtype, bool accumulate, void* ws, int32_t* status, int cus, hipStream_t st) {
-  const int parts = wgrad_parts(s);
-  if (parts == 1) return launch_wgrad_whole(s, x, dy, offsets, dw, dw_dtype, accumulate, status, cus, st);
+  const int64_t piece = wgrad_piece(s);
+  if (piece == 0) return launch_wgrad_whole(s, x, dy, offsets, dw, dw_dtype, accumulate, status, nullptr, cus, st);
+  moe_gemm_t pieces = s;
+  pieces.groups = most_pieces(s, piece);
   int32_t* const bounds = static_cast<int32_t*>(ws);
-  float* const sums = reinterpret_cast<float*>(static_cast<char*>(ws) + parts_bytes(s, parts));
-  hipLaunchKernelGGL(wgrad_parts_kernel, dim3(1), dim3(1024), 0, st, offsets, s.groups, parts, s.rows, bounds);
+  int32_t* const first = bounds + pieces.groups + 1;
+  float* const sums = reinterpret_cast<float*>(static_cast<char*>(ws) + piece_table(s, piece));
+  hipLaunchKernelGGL(wgrad_pieces_kernel, dim3(1), dim3(256), 0, st, offsets, s.groups, __builtin_ctzll(uint64_t(piece)), s.rows, bounds, first);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  moe_gemm_t pieces = s;
-  pieces.groups = s.groups * parts;
-  if ((e = launch_wgrad_whole(pieces, x, dy, bounds, sums, MOE_F32, false, status, cus, st)) != hipSuccess) return e;
+  if ((e = launch_wgrad_whole(pieces, x, dy, bounds, sums, MOE_F32, false, status, first + s.groups, cus, st)) != hipSuccess) return e;
   const int64_t size = int64_t(s.K) * s.N, vectors = s.groups * size / 4, need = (vectors + 255) / 256;
   const dim3 grid(int(need < (1 << 20) ? need : 1 << 20)), threads(256);
   if (dw_dtype != MOE_F32)
-    hipLaunchKernelGGL((wgrad_join_kernel<uint16_t, false>), grid, threads, 0, st, sums, bounds, parts, size, vectors, static_cast<uint16_t*>(dw));
+    hipLaunchKernelGGL((wgrad_join_kernel<uint16_t, false>), grid, threads, 0, st, sums, bounds, first, size, vectors, static_cast<uint16_t*>(dw));
   else if (accumulate)
-    hipLaunchKernelGGL((wgrad_join_kernel<float, true>), grid, threads, 0, st, sums, bounds, parts, size, vectors, static_cast<float*>(dw));
+    hipLaunchKernelGGL((wgrad_join_kernel<float, true>), grid, threads, 0, st, sums, bounds, first, size, vectors, static_cast<float*>(dw));
   else
-    hipLaunchKernelGGL((wgrad_join_kernel<float, false>), grid, threads, 0, st, sums, bounds, parts, size, vectors, static_cast<float*>(dw));
+    hipLaunchKernelGGL((wgrad_join_kernel<float, false>), grid, threads, 0, st, sums, bounds, first, size, vectors, static_cast<float*>(dw));
   return hipGetLastError();
 }
 

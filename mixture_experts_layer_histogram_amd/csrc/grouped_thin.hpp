@@ -27,7 +27,10 @@ constexpr int kThinLds = thin_lds_bytes(1) > thin_lds_bytes(4) ? thin_lds_bytes(
 // stored [N][K]) to a quarter ([K][N], where four waves far apart in K read 128 bytes of a row each) to sums and shorter queues.  32 groups of
 // 7168 x 2048, us alone and split: 1024 items 149 and 159, in the other layout 163 and 205; 1056 items 237 and 181; 3584 items 202
 // and 169; 64 groups of 2048 x 1408, one row each (1408 items): 84 and 69; 132 items: 16 and 9.
-__device__ __forceinline__ bool thin_alone(int items, int wgs, bool w_kn) {
+// Of few K steps there is little to share: always alone below 8 (us split and alone: 91 groups of 16 x 5040, 438 rows 64 and 22, 64 of 128 x 2048,
+// 1024 rows 23 and 13, of 448 x 2048 31 and 27).
+__device__ __forceinline__ bool thin_alone(int items, int wgs, int steps, bool w_kn) {
+  if (steps < 8) return true;
   const int one = (items + 4 * wgs - 1) / (4 * wgs), four = (items + wgs - 1) / wgs;
   return one * (w_kn ? 16 : 37) <= four * (w_kn ? 5 : 10);
 }
@@ -231,7 +234,7 @@ __global__ __launch_bounds__(256, 1) void grouped_thin_kernel(GroupedArgs g) {
   const int mtiles = group_tiles<256>(g.offsets, g.G, g.rows, 5, base, part, &bad);
   if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
   const int items = mtiles * ((g.N + kThinCols - 1) / kThinCols);
-  if (thin_alone(items, gridDim.x, W_KN)) thin_run<W_KN, 1>(g, base, mtiles, smem);
+  if (thin_alone(items, gridDim.x, (g.K + kThinK - 1) / kThinK, W_KN)) thin_run<W_KN, 1>(g, base, mtiles, smem);
   else thin_run<W_KN, 4>(g, base, mtiles, smem);
 }
 

@@ -182,11 +182,11 @@ def test_adamw_of_nothing():
 
 
 def test_wgrad_in_pieces_asks_for_its_workspace():
-    """One matrix of 256 x 512 (2 tiles) with 100000 rows: 48 pieces; groups that fill the card, or few rows: none."""
+    """One matrix of 256 x 512 (2 tiles) with 100000 rows: pieces of 1024; groups that fill the card, or few rows: none."""
     g = moe.Gemm(100000, 1, 256, 512, moe.MOE_BF16, 0)
     need = moe.moe_grouped_gemm_wgrad_workspace_bytes(g)
-    assert need == 256 + 48 * 256 * 512 * 4
+    assert need == 512 + 98 * 256 * 512 * 4
     call = lambda **kw: moe.moe_grouped_gemm_wgrad(g, A, B, C, D, moe.MOE_BF16, stream=0, check=False, **kw)       # noqa: E731
     assert call() == -1 and call(ws=E + 64, ws_bytes=need) == -2 and call(ws=E, ws_bytes=need - 1) == -3
     assert moe.moe_grouped_gemm_wgrad_workspace_bytes(moe.Gemm(100000, 64, 1024, 512, moe.MOE_BF16, 0)) == 0
-    assert moe.moe_grouped_gemm_wgrad_workspace_bytes(moe.Gemm(4095, 1, 256, 512, moe.MOE_BF16, 0)) == 0
+    assert moe.moe_grouped_gemm_wgrad_workspace_bytes(moe.Gemm(2047, 1, 256, 512, moe.MOE_BF16, 0)) == 0

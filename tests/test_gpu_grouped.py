@@ -69,6 +69,7 @@ CASES = [
     ([1500, 548], 136, 1304), ([1500, 548], 192, 1304), ([300, 20, 0, 600, 77, 256, 3, 129], 520, 776),
     ([300, 20, 0, 600, 77, 256, 3, 129], 72, 4104), ([260, 257, 9], 8, 9000), ([700, 0, 350], 320, 8712),
     ([4100], 72, 136), ([3000, 0, 5, 9000], 64, 256), ([2048, 2047], 264, 40), ([0, 0, 9000], 8, 16), ([12300, 0, 5], 40, 264), ([100, 16500], 72, 8),
+    ([0, 700, 1, 4000, 0, 64, 0], 136, 88), ([20] * 100 + [5000] + [0] * 20, 64, 24),
 ]
 
 
@@ -215,17 +216,17 @@ def test_bad_offsets_of_a_gradient_in_pieces(dtype):
     """Nothing is computed, in the workspace's pieces or behind them; the next call with good ones is whole."""
     torch = _torch()
     code, kind = _kind(dtype)
-    g = moe.Gemm(9000, 1, 64, 64, code, 0)
+    g = moe.Gemm(9000, 3, 64, 64, code, 0)
     x, dy = _make((9000, 64), dtype, 1, True), _make((9000, 64), dtype, 2, True)
     ws = torch.empty(moe.moe_grouped_gemm_wgrad_workspace_bytes(g), dtype=torch.uint8, device="cuda").fill_(0x5A)
     assert ws.numel() > 0
-    dw, status = torch.full((64, 64), 7.0, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
-    for bad in ([0, 9001], [10, 9], [-1, 9000]):
+    dw, status = torch.full((3, 64, 64), 7.0, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for bad in ([0, 5, 5, 9001], [10, 9, 20, 30], [-1, 0, 0, 9000], [0, 0, 9000, 8999]):
         moe.moe_grouped_gemm_wgrad(g, x, dy, torch.tensor(bad, dtype=torch.int32, device="cuda"), dw, moe.MOE_F32, ws, status=status)
         assert int(status) == -1 and (dw == 7).all()
         status.zero_()
-    moe.moe_grouped_gemm_wgrad(g, x, dy, torch.tensor([0, 9000], dtype=torch.int32, device="cuda"), dw, moe.MOE_F32, ws, status=status)
-    assert int(status) == 0 and torch.equal(dw, dy.float().t() @ x.float())
+    moe.moe_grouped_gemm_wgrad(g, x, dy, torch.tensor([8, 8, 9000, 9000], dtype=torch.int32, device="cuda"), dw, moe.MOE_F32, ws, status=status)
+    assert int(status) == 0 and torch.equal(dw[1], dy[8:].float().t() @ x[8:].float()) and (dw[::2] == 0).all()
 
 
 def test_gradients_in_pieces_of_two_graphs_over_one_workspace():
