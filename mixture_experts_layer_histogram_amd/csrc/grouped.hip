@@ -132,6 +132,59 @@ __global__ __launch_bounds__(256) void grouped_f32_kernel(GroupedArgs g) {
   }
 }
 
+// fp32 products of few rows and columns (a latency): tiles of 16 x 16 (v_mfma_f32_16x16x4_f32), whose K sixteen waves share, 16 values at a time straight into
+// registers, four such loads in flight, and add up through LDS in wave order.
+template <bool W_KN>
+__global__ __launch_bounds__(1024) void grouped_f32_thin_kernel(GroupedArgs g) {
+  __shared__ int32_t base[kMaxGroups + 1], part[17];
+  __shared__ f32x4 sums[16][64];
+  bool bad;
+  const int mtiles = group_tiles<1024>(g.offsets, g.G, g.rows, 4, base, part, &bad);
+  if (g.status && blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? MOE_EINVAL : MOE_OK;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, q = lane >> 4;
+  const int NT = (g.N + 15) >> 4;
+  const int64_t total = int64_t(mtiles) * NT;
+  for (int64_t tau = blockIdx.x; tau < total; tau += gridDim.x) {
+    const int mtg = int(tau / NT), c0 = int(tau - int64_t(mtg) * NT) * 16;
+    const int l = find_expert(base, g.G, mtg);
+    const int64_t row0 = g.offsets[l] + int64_t(mtg - base[l]) * 16;
+    const int rows = int(min(int64_t(16), g.offsets[l + 1] - row0));
+    const float* x = static_cast<const float*>(g.x) + (row0 + min(r16, rows - 1)) * g.ldx;
+    const int64_t c = min(c0 + r16, g.N - 1);
+    const float* w = static_cast<const float*>(g.w) + int64_t(l) * g.N * g.K + (W_KN ? c : c * g.K);
+    f32x4 acc{0, 0, 0, 0};
+    for (int k0 = wave * 16 + q * 4; k0 - q * 4 < g.K; k0 += 1024) {
+      f32x4 a[4], b[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = min(k0 + u * 256, g.K - 4);             // past K: some values of the row, which become zeros
+        b[u] = *reinterpret_cast<const f32x4*>(x + k);
+        if constexpr (W_KN) {
+          const float* p = w + int64_t(k) * g.N;
+          a[u] = f32x4{p[0], p[g.N], p[2 * int64_t(g.N)], p[3 * int64_t(g.N)]};
+        } else {
+          a[u] = *reinterpret_cast<const f32x4*>(w + k);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool in = k0 + u * 256 < g.K;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)                            // columns first: a lane gets four of them of one row
+          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(in ? a[u][e] : 0.0f, in ? b[u][e] : 0.0f, acc, 0, 0, 0);
+      }
+    }
+    sums[wave][lane] = acc;
+    __syncthreads();
+    if (threadIdx.x < 64 && r16 < rows && c0 + 4 * q < g.N) {
+#pragma unroll
+      for (int v = 1; v < 16; ++v) acc += sums[v][lane];
+      *reinterpret_cast<f32x4*>(static_cast<float*>(g.y) + (row0 + r16) * g.ldy + c0 + 4 * q) = acc;
+    }
+    __syncthreads();
+  }
+}
+
 struct WgradArgs {
   const void* a;               // the rows whose columns become the gradient's rows
   const void* b;
@@ -426,6 +479,16 @@ hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, con
   if (e != hipSuccess) return e;
   if (s.dtype == MOE_F32) {
     const int64_t rows = s.rows / 64 + (s.rows < s.groups ? s.rows : s.groups), tiles = rows * ((s.N + 63) / 64);     // at most
+    const int64_t small = (s.rows / 16 + (s.rows < s.groups ? s.rows : s.groups)) * ((s.N + 15) / 16);                 // tiles of 16 x 16
+    // us with those and with tiles of 32: 5 groups, 5 rows of 7108 x 96 (30) 16 and 58; 1 group, 80 rows of 6652 x 212 (84) 23 and 55; 35 groups, 2 rows of
+    // 4244 x 848 (106) 12 and 37; 64 groups, 64 rows of 2048 x 128 (544) 17 and 23, weights stored [K][N] 25 and 23; 8 groups, 509 rows of 256 x 128
+    // (312) 11 and 7
+    if (small <= cus && s.K >= 512) {
+      const dim3 few(int(small < 1 ? 1 : small));
+      if (s.w_layout) hipLaunchKernelGGL(grouped_f32_thin_kernel<true>, few, dim3(1024), 0, st, g);
+      else hipLaunchKernelGGL(grouped_f32_thin_kernel<false>, few, dim3(1024), 0, st, g);
+      return hipGetLastError();
+    }
     const int lds = f32_lds_bytes(tiles < cus ? 32 : 64);
     const dim3 grid(f32_grid(tiles, cus));
     if (tiles < cus && s.w_layout) hipLaunchKernelGGL((grouped_f32_kernel<32, true>), grid, threads, lds, st, g);

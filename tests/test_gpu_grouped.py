@@ -69,7 +69,8 @@ CASES = [
     ([1500, 548], 136, 1304), ([1500, 548], 192, 1304), ([300, 20, 0, 600, 77, 256, 3, 129], 520, 776),
     ([300, 20, 0, 600, 77, 256, 3, 129], 72, 4104), ([260, 257, 9], 8, 9000), ([700, 0, 350], 320, 8712),
     ([4100], 72, 136), ([3000, 0, 5, 9000], 64, 256), ([2048, 2047], 264, 40), ([0, 0, 9000], 8, 16), ([12300, 0, 5], 40, 264), ([100, 16500], 72, 8),
-    ([0, 700, 1, 4000, 0, 64, 0], 136, 88), ([20] * 100 + [5000] + [0] * 20, 64, 24),
+    ([0, 700, 1, 4000, 0, 64, 0], 136, 88), ([20] * 100 + [5000] + [0] * 20, 64, 24), ([1, 0, 17], 1032, 24),
+    ([0, 40, 3], 2056, 40), ([1] * 7, 4104, 8),
 ]
 
 
@@ -258,3 +259,29 @@ def test_gradients_in_pieces_of_two_graphs_over_one_workspace():
         graphs[i].replay() if i < 2 else run(i)
         torch.cuda.synchronize()
         assert torch.equal(data[i][3], want[i]), i
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_few_rows_of_long_sums_keep_to_themselves(dtype, layout):
+    """Rows and groups beside a NaN, strided rows with NaN between, rows ahead of the first group; then bad offsets."""
+    torch = _torch()
+    code, kind = _kind(dtype)
+    K, N, counts, first = 1032, 40, [2, 0, 19], 3
+    off, doff = _offsets(counts, first)
+    rows = off[-1] + 1
+    x = _strided(rows, K, 8, dtype, 1, True)
+    x[first - 1] = x[first + 1] = x[rows - 1] = float("nan")
+    w = _make((3, N, K) if layout == 0 else (3, K, N), dtype, 2, True)
+    w[1] = float("nan")
+    y = torch.full((rows, N + 16), 7.0, dtype=kind, device="cuda")
+    g, status = moe.Gemm(rows, 3, K, N, code, layout, K + 8, N + 16), torch.zeros(1, dtype=torch.int32, device="cuda")
+    moe.moe_grouped_gemm(g, x, w, doff, y, status)
+    ref, _ = M.grouped(_np(x[:, :K]), _np(w), off, layout)
+    keep = [i for i in range(first, off[-1]) if i != first + 1]
+    _close(y[keep, :N], ref[keep], None, K, dtype, True)
+    assert torch.isnan(y[first + 1, :N]).all() and (y[:, N:] == 7).all() and (y[:first] == 7).all() and (y[off[-1]:] == 7).all()
+    y.fill_(7)
+    for bad in ([3, 5, 5, rows + 1], [3, 5, 4, 24], [-1, 5, 5, 24]):
+        moe.moe_grouped_gemm(g, x, w, torch.tensor(bad, dtype=torch.int32, device="cuda"), y, status)
+        assert int(status) == -1 and (y == 7).all()
