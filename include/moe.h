@@ -830,7 +830,7 @@ int moe_grouped_gemm(const moe_gemm_t* g, const void* x, const void* w, const in
  * accumulate != 0: added to what dw holds (MOE_F32 only, else MOE_EINVAL): gradients of several batches.
  * dy: rows of N values with stride ldy.  ws: at least moe_grouped_gemm_wgrad_workspace_bytes() bytes, 256-byte aligned
  * (may be NULL where that is 0): few small matrices with many rows are summed in pieces there, whose number goes by `rows` and the
- * sizes alone.  Deterministic, as moe_grouped_gemm.  Other arguments, limits and errors as there; with bad offsets dw stays as it is.
+ * sizes alone.  A workspace for more rows serves fewer.  Deterministic, as moe_grouped_gemm.  Other arguments, limits and errors as there; with bad offsets dw stays as it is.
  */
 size_t moe_grouped_gemm_wgrad_workspace_bytes(const moe_gemm_t* g);
 int moe_grouped_gemm_wgrad(const moe_gemm_t* g, const void* x, const void* dy, const int32_t* offsets, void* dw,

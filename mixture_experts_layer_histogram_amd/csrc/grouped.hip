@@ -530,29 +530,46 @@ hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, con
 // 28 x 164 with 31015 rows 77 and 34, even 20 and 26.
 constexpr int kPieceCUs = 256;
 
-// Rows of a piece, a power of two, by the sizes alone; 0 for whole groups
-static int64_t wgrad_piece(const moe_gemm_t& s) {
+struct Pieces {
+  int wgs;                     // workgroups that take tiles at a time
+  int64_t matrix;              // tiles of a matrix
+  double most_join;            // us that writing and reading the pieces' gradients may take
+};
+static Pieces pieces_of(const moe_gemm_t& s) {
   const bool f32 = s.dtype == MOE_F32;
   const int T = f32 ? 32 : kBig, wgs = f32 ? 2 * kPieceCUs : kPieceCUs;
   const int64_t matrix = int64_t((s.K + T - 1) / T) * ((s.N + T - 1) / T), tiles = matrix * s.groups;
+  const double turns = double((tiles + wgs - 1) / wgs), rows = double(s.rows) / s.groups;
+  const double even = f32 ? rows / 128 * turns : rows / 64 * (tiles * 4 <= kPieceCUs ? 0.6 : 1.5 * turns);       // us
+  return {wgs, matrix, even > 40 ? even / 2 : 20};
+}
+static double join_us(const moe_gemm_t& s, int64_t pieces) { return double(pieces) * s.K * s.N * 8 / 5e6; }
+
+// Rows of a piece, a power of two, by the sizes alone; 0 for whole groups
+static int64_t wgrad_piece(const moe_gemm_t& s) {
+  const Pieces p = pieces_of(s);
   int64_t piece = 512;
-  while (piece < s.rows * matrix / wgs || s.rows / piece + s.groups > kMaxGroups) {
+  while (piece < s.rows * p.matrix / p.wgs || s.rows / piece + s.groups > kMaxGroups) {
     if (piece > s.rows) return 0;
     piece *= 2;
   }
-  if (s.rows < 4 * piece) return 0;
-  const double turns = double((tiles + wgs - 1) / wgs), rows = double(s.rows) / s.groups;
-  const double even = f32 ? rows / 128 * turns : rows / 64 * (tiles * 4 <= kPieceCUs ? 0.6 : 1.5 * turns);       // us
-  const double join = double(s.rows / piece + s.groups) * s.K * s.N * 8 / 5e6;
-  return join <= (even > 40 ? even / 2 : 20) ? piece : 0;
+  return s.rows >= 4 * piece && join_us(s, s.rows / piece + s.groups) <= p.most_join ? piece : 0;
 }
 static int most_pieces(const moe_gemm_t& s, int64_t piece) { return int(s.rows / piece + s.groups); }
 
 // The workspace: the pieces' bounds, the first piece of every group, their number; the pieces' gradients
-static size_t piece_table(const moe_gemm_t& s, int64_t piece) { return align256(size_t(4) * (most_pieces(s, piece) + 1 + s.groups + 1)); }
-size_t wgrad_workspace(const moe_gemm_t& s) {
+static size_t piece_table(const moe_gemm_t& s, int64_t pieces) { return align256(size_t(4) * (pieces + 1 + s.groups + 1)); }
+static size_t piece_bytes(const moe_gemm_t& s, int64_t pieces) { return piece_table(s, pieces) + align256(size_t(pieces) * s.K * s.N * 4); }
+size_t wgrad_need(const moe_gemm_t& s) {
   const int64_t piece = wgrad_piece(s);
-  return piece == 0 ? 0 : piece_table(s, piece) + align256(size_t(most_pieces(s, piece)) * s.K * s.N * 4);
+  return piece == 0 ? 0 : piece_bytes(s, most_pieces(s, piece));
+}
+// What any number of rows up to these needs: a piece has at least its share of the rows and 512 of them, and there are at least four
+size_t wgrad_workspace(const moe_gemm_t& s) {
+  const Pieces p = pieces_of(s);
+  if (s.rows < 4 * 512 || join_us(s, s.groups + 4) > p.most_join) return 0;
+  const int64_t share = p.wgs / p.matrix + 1, most = (s.rows / 512 < share ? s.rows / 512 : share) + s.groups;
+  return piece_bytes(s, most < kMaxGroups ? most : kMaxGroups);
 }
 
 // By one workgroup.  first[G] is the pieces' number; where the offsets are bad, one piece with bad bounds.
@@ -635,7 +652,7 @@ hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* 
   pieces.groups = most_pieces(s, piece);
   int32_t* const bounds = static_cast<int32_t*>(ws);
   int32_t* const first = bounds + pieces.groups + 1;
-  float* const sums = reinterpret_cast<float*>(static_cast<char*>(ws) + piece_table(s, piece));
+  float* const sums = reinterpret_cast<float*>(static_cast<char*>(ws) + piece_table(s, pieces.groups));
   hipLaunchKernelGGL(wgrad_pieces_kernel, dim3(1), dim3(256), 0, st, offsets, s.groups, __builtin_ctzll(uint64_t(piece)), s.rows, bounds, first);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

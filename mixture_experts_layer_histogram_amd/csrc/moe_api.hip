@@ -105,6 +105,7 @@ hipError_t launch_grouped(const moe_gemm_t& s, const void* x, const void* w, con
 hipError_t launch_grouped_wgrad(const moe_gemm_t& s, const void* x, const void* dy, const int32_t* offsets, void* dw,
                                 int dw_dtype, bool accumulate, void* ws, int32_t* status, int cus, hipStream_t st);
 size_t wgrad_workspace(const moe_gemm_t& s);
+size_t wgrad_need(const moe_gemm_t& s);
 hipError_t launch_adamw(const moe_adamw_t& h, const moe_adamw_tensor_t* tensors, int count, int cus, hipStream_t st);
 hipError_t launch_states_values(const uint8_t* codes, const uint8_t* scales, int64_t rows, void* dst, int dst_dtype,
                                 hipStream_t st);
@@ -1145,7 +1146,7 @@ int moe_grouped_gemm_wgrad(const moe_gemm_t* g, const void* x, const void* dy, c
     if ((rc = check_rows(x)) || (rc = check_rows(dy))) return rc;
     if (dw == x || dw == dy) return MOE_EINVAL;
   }
-  if (const size_t need = moe_grouped_gemm_wgrad_workspace_bytes(g)) {
+  if (const size_t need = wgrad_need(*g)) {             // at most the workspace of these rows, or of more
     if (!ws) return MOE_EINVAL;
     if (reinterpret_cast<uintptr_t>(ws) & 255) return MOE_EALIGN;
     if (ws_bytes < need) return MOE_ENOSPC;

@@ -182,11 +182,21 @@ def test_adamw_of_nothing():
 
 
 def test_wgrad_in_pieces_asks_for_its_workspace():
-    """One matrix of 256 x 512 (2 tiles) with 100000 rows: pieces of 1024; groups that fill the card, or few rows: none."""
+    """One matrix of 256 x 512 (2 tiles) with 100000 rows: pieces of 1024, 129 at most for any number of rows; groups that fill the card, or few
+    rows: none."""
     g = moe.Gemm(100000, 1, 256, 512, moe.MOE_BF16, 0)
     need = moe.moe_grouped_gemm_wgrad_workspace_bytes(g)
-    assert need == 512 + 98 * 256 * 512 * 4
+    assert need == 768 + 130 * 256 * 512 * 4
     call = lambda **kw: moe.moe_grouped_gemm_wgrad(g, A, B, C, D, moe.MOE_BF16, stream=0, check=False, **kw)       # noqa: E731
-    assert call() == -1 and call(ws=E + 64, ws_bytes=need) == -2 and call(ws=E, ws_bytes=need - 1) == -3
-    assert moe.moe_grouped_gemm_wgrad_workspace_bytes(moe.Gemm(100000, 64, 1024, 512, moe.MOE_BF16, 0)) == 0
+    assert call() == -1 and call(ws=E + 64, ws_bytes=need) == -2 and call(ws=E, ws_bytes=98 * 256 * 512 * 4) == -3
+    assert moe.moe_grouped_gemm_wgrad_workspace_bytes(moe.Gemm(100000, 64, 7168, 2048, moe.MOE_BF16, 0)) == 0
     assert moe.moe_grouped_gemm_wgrad_workspace_bytes(moe.Gemm(2047, 1, 256, 512, moe.MOE_BF16, 0)) == 0
+
+
+@pytest.mark.parametrize("dtype", [moe.MOE_BF16, moe.MOE_F32])
+@pytest.mark.parametrize("G,K,N", [(1, 256, 512), (1, 7168, 256), (12, 440, 368), (8, 1024, 1024), (1000, 64, 64), (1023, 8, 8), (3, 2048, 2048)])
+def test_a_wgrad_workspace_for_more_rows_serves_fewer(dtype, G, K, N):
+    size = lambda rows: moe.moe_grouped_gemm_wgrad_workspace_bytes(moe.Gemm(rows, G, K, N, dtype, 0))              # noqa: E731
+    rows = sorted({int(1.03 ** i) + d for i in range(60, 700) for d in (-1, 0, 1) if 1.03 ** i < 1 << 29} | {1 << i for i in range(6, 30)})
+    sizes = [size(r) for r in rows]
+    assert sizes == sorted(sizes)

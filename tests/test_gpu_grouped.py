@@ -285,3 +285,22 @@ def test_few_rows_of_long_sums_keep_to_themselves(dtype, layout):
     for bad in ([3, 5, 5, rows + 1], [3, 5, 4, 24], [-1, 5, 5, 24]):
         moe.moe_grouped_gemm(g, x, w, torch.tensor(bad, dtype=torch.int32, device="cuda"), y, status)
         assert int(status) == -1 and (y == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,K,N", [(1, 256, 512), (12, 104, 200), (2, 1024, 264), (700, 8, 16)])
+def test_a_gradients_workspace_for_more_rows(dtype, G, K, N):
+    """The workspace of 40000 rows, for calls with fewer: none is refused, and nothing behind it is touched."""
+    torch = _torch()
+    code, kind = _kind(dtype)
+    need = moe.moe_grouped_gemm_wgrad_workspace_bytes(moe.Gemm(40000, G, K, N, code, 1))
+    ws = torch.full((need + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+    for rows in (40000, 39999, 33000, 20481, 20479, 9000, 4097, 2048, 2047, 700):
+        c = [rows // G] * G
+        c[-1] += rows - sum(c)
+        off, doff = _offsets(c)
+        x, dy, dw = _make((rows, K), dtype, 1, True), _make((rows, N), dtype, 2, True), torch.empty(G, K, N, device="cuda")
+        moe.moe_grouped_gemm_wgrad(moe.Gemm(rows, G, K, N, code, 1), x, dy, doff, dw, moe.MOE_F32, ws, need)
+        for i in (0, G - 1):
+            assert torch.equal(dw[i], x[off[i]:off[i + 1]].float().t() @ dy[off[i]:off[i + 1]].float())
+        assert (ws[need:] == 0x5A).all()
