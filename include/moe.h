@@ -853,6 +853,8 @@ int moe_grouped_gemm_wgrad(const moe_gemm_t* g, const void* x, const void* dy, c
  * nearest even, which loses small changes.  The root is rounded without bias, so v, its square, gains the rounding's variance:
  * up to a twentieth with beta2 = 0.999.
  * A gradient that is NaN or infinite makes its value (and in 8 bits its block of states) NaN.
+ * A finite one whose v passes fp32's range (|g| from about 5e20 on with beta2 = 0.999) leaves v infinite: the change is 0 from then on, and p decays by
+ * weight_decay alone; in 8 bits its block of v is NaN from the next step on.
  * tensors: a HOST array, read during the call only; a launch for every 70 tensors (54 with states in 8 bits).  Pointers 16-byte aligned, scales
  * 4-byte aligned; buffers of a tensor overlap neither each other (the same address twice: MOE_EINVAL) nor another tensor's.
  * MOE_EINVAL: a NULL pointer of a tensor with n > 0, n outside [0, 2^40], master != NULL beside an fp32 param, count < 0, step < 1

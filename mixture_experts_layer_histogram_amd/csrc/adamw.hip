@@ -71,13 +71,14 @@ __device__ __forceinline__ uint32_t mix32(uint32_t z) {
   return z ^ (z >> 16);
 }
 
-// Correctly rounded square roots of values that are zero or at least 2^-100: the instruction's (a unit off at most), once corrected by its
-// residual.  Smaller ones take the general function: a branch that hardly any wave takes.
+// Correctly rounded square roots of values that are zero or between 2^-100 and infinity: the instruction's (a unit off at most), once corrected
+// by its residual.  Smaller ones, and an infinity, whose residual is a NaN, take the general function: a branch that hardly any wave takes.
 __device__ __forceinline__ float root_of(float v) {
   float s = __builtin_amdgcn_sqrtf(v);
   const float e = __builtin_fmaf(-s, s, v);
   s = __builtin_fmaf(e, 0.5f * __builtin_amdgcn_rcpf(fmaxf(s, 0x1p-60f)), s);
-  if (__float_as_uint(v) - 1u < 0x0D800000u - 1u) s = sqrtf(v);      // 0 < v < 2^-100
+  const uint32_t bits = __float_as_uint(v);
+  if (bits - 1u < 0x0D800000u - 1u || bits >= 0x7F800000u) s = sqrtf(v);      // 0 < v < 2^-100, or not finite
   return s;
 }
 

@@ -249,3 +249,29 @@ def test_values_of_states_for_every_code_and_scale(dtype):
     a, b = wide.reshape(-1).float(), rows.reshape(-1).float()
     nan = torch.isnan(a)
     assert torch.equal(nan, torch.isnan(b)) and torch.equal(a[~nan], b[~nan]) and int(nan.sum()) == 256 + 2 * 255
+
+
+@pytest.mark.parametrize("param,grad,master", [("f32", "f32", False), ("bf16", "f32", True), ("bf16", "bf16", True), ("bf16", "bf16", False)])
+@pytest.mark.parametrize("eight,stochastic", [(False, False), (False, True), (True, True), (True, False)])
+def test_finite_gradients_whose_squares_pass_fp32(param, grad, master, eight, stochastic):
+    """v and its root are infinite then, so the change is zero and the param decays only; fp32 states go on like that in later steps, a
+    block of 8-bit roots with an infinity is NaN from the next step on.  Gradients just within the range beside them."""
+    torch = _torch()
+    big = torch.tensor([1e21, -1e30, 3e38, 7e20, -5e20, 1e21, 1e21], device="cuda")
+    at = [0, 7, 33, 130, 131, 200, 299]
+    for step, zero in ((1, True), (1000, False)):
+        t = Tensor(300, param, grad, master, eight, 40, zero=zero)
+        t.grad[at] = big.to(t.grad.dtype)
+        old = t.copy()
+        _step([t], step, 5, eight, stochastic)
+        t.check(old, 0, step, 5, stochastic)
+        again = t.copy()
+        _step([t], step + 1, 5, eight, stochastic)
+        if eight:
+            lost = torch.zeros(300, dtype=torch.bool, device="cuda")
+            for block in (0, 1, 4, 6, 9):
+                lost[32 * block: 32 * block + 32] = True
+            p = t.param[:300] if t.master is None else t.master[:300]
+            assert torch.equal(torch.isnan(p), lost)
+        else:
+            t.check(again, 0, step + 1, 5, stochastic)
