@@ -200,3 +200,9 @@ def test_a_wgrad_workspace_for_more_rows_serves_fewer(dtype, G, K, N):
     rows = sorted({int(1.03 ** i) + d for i in range(60, 700) for d in (-1, 0, 1) if 1.03 ** i < 1 << 29} | {1 << i for i in range(6, 30)})
     sizes = [size(r) for r in rows]
     assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("eps,code", [(2.0 ** -126, 0), (1.1e-38, -1), (1e-39, -1), (1e-45, -1), (2.0 ** 126, 0), (1e38, -1), (1e39, -1), (1e300, -1)])
+def test_adamw_takes_an_eps_whose_reciprocal_is_a_normal_float(eps, code):
+    """The step multiplies by the reciprocal of root + eps: of a subnormal eps it would be infinite, and 0 times it a NaN; of a larger one zero."""
+    assert moe.moe_adamw(moe.AdamW(*dict(STEP, eps=eps).values()), [], stream=0, check=False) == code

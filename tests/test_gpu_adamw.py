@@ -275,3 +275,17 @@ def test_finite_gradients_whose_squares_pass_fp32(param, grad, master, eight, st
             assert torch.equal(torch.isnan(p), lost)
         else:
             t.check(again, 0, step + 1, 5, stochastic)
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("eps", [2.0 ** -126, 2.0 ** -100, 2.0 ** 126])
+def test_the_smallest_and_the_largest_eps(eight, eps):
+    """Values without a gradient and without states do not move but by the decay; with one, the change is at most one unit's rounding of
+    lr m' / (r' + eps) off (as in the bars above)."""
+    t = Tensor(300, "f32", "f32", False, eight, 41, zero=True)
+    t.grad[:200] = 0
+    old = t.copy()
+    moe.moe_adamw(moe.AdamW(LR, BETA1, BETA2, eps, 1, moe.MOE_MXFP8 if eight else moe.MOE_F32, 0, 0), [t.entry()])
+    p0, got = _np(old.param[:300]), _np(t.param[:300])
+    m, v = M.moments(np.zeros(300), np.zeros(300), _np(t.grad[:300]), BETA1, BETA2)
+    p, away = M.adamw(p0, m, v, LR, BETA1, BETA2, eps, 1, t.wd)
+    assert (away[:200] == 0).all() and (np.abs(got - p) <= 16 * U * away + 3 * U * (np.abs(p0) + away)).all()
