@@ -756,8 +756,9 @@ int moe_backward_mx(const moe_shape_t* s, const moe_placement_t* p, const void* 
  * x, residual, h, y: dense rows of d values of `dtype` (MOE_F32 or MOE_BF16), 16-byte aligned; gamma: [d] fp32, 4-byte
  * aligned; codes 16-byte, scales 4-byte aligned.  h or y may be x or residual themselves (a row is read before it is
  * written), but not each other (MOE_EINVAL), and the buffers may not overlap otherwise.  The sum of squares is held in fp32:
- * rows with values from about 1e18 on pass its range.  1 <= d <= 32768, rows >= 0, rows * d < 2^40, eps >= 0 and finite
- * (else MOE_EINVAL), one output at least (else MOE_EINVAL).  Deterministic.
+ * a row's has to stay below 3.4e38 (values of 1e17 in the widest rows, of 1e18 in rows of 300), and its mean with eps above 1e-36 (for an eps of 0:
+ * values of 1e-18 on the mean; rows of 1e-23 are infinite then, and a row of zeros is 0 / 0, NaN).  1 <= d <= 32768, rows >= 0,
+ * rows * d < 2^40, eps >= 0 and finite (else MOE_EINVAL), one output at least (else MOE_EINVAL).  Deterministic.
  */
 typedef struct {
   int64_t rows;

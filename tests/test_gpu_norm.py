@@ -241,3 +241,52 @@ def test_dispatch_of_codes_with_no_local_pair():
     xe, xes = torch.full((16, 128), GUARD, **u8), torch.full((1, 16, 4), GUARD, **u8)
     moe.moe_dispatch_pull_codes(sh, p, [torch.zeros(16, 128, **u8)], [torch.zeros(1, 16, 4, **u8)], src, offsets, xe, xes, ws)
     assert (xe == GUARD).all() and (xes == GUARD).all()
+
+
+# ------------------------------------------------------------------------------------------------ the range that the header names
+SIZES = [1.0, 2e-18, 2e16, 1e-16, 3.0, 1e8, 2.0 ** -50]
+RANGE = [(15, 4, "f32"), (15, 8, "bf16"), (9001, 64, "f32"), (29, 512, "bf16"), (4203, 2048, "bf16"), (29, 1408, "f32"), (15, 4096, "f32"), (1100, 7168, "bf16"),
+         (15, 8200, "bf16"), (15, 32768, "f32")]
+
+
+def _sized(rows, d, dtype, seed):
+    """Rows of sizes in turn, side by side in a workgroup: from the smallest whose squares fp32 holds (a mean of 4e-36, of which each value's
+    2^-150 is less than 2^-31) to values of 1e17, 32768 of which add up to less than 3.4e38."""
+    torch = _torch()
+    size = torch.tensor([SIZES[i % len(SIZES)] for i in range(rows)], device="cuda")
+    return (_rows(rows, d, "f32", seed).clamp(-5, 5) * size[:, None]).to(_kind(dtype)[1])
+
+
+@pytest.mark.parametrize("rows,d,dtype", RANGE)
+def test_norm_without_eps_over_its_range(rows, d, dtype):
+    torch = _torch()
+    code, kind = _kind(dtype)
+    x, res = _sized(rows, d, dtype, 1), _sized(rows, d, dtype, 2)
+    gamma = 1 + 0.1 * torch.randn(d, device="cuda")
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    q = torch.empty(rows, d, dtype=torch.uint8, device="cuda") if d % 128 == 0 else None
+    sc = torch.empty(rows * d // 32, dtype=torch.uint8, device="cuda") if d % 128 == 0 else None
+    moe.moe_norm(moe.Norm(rows, d, code, 0.0), x, res, gamma, h, y, q, sc)
+    s, ref, _ = M.norm(_np(x), _np(res), _np(gamma), 0.0)
+    assert (np.abs(_np(h) - s) <= (HALF[dtype] + U) * np.abs(s)).all()
+    bad = ~(np.abs(_np(y) - ref) <= (HALF[dtype] + FWD) * np.abs(ref))
+    assert not bad.any(), sorted({int(i) % len(SIZES) for i in np.nonzero(bad)[0]})
+    if q is not None:
+        _check_codes(q.cpu().numpy(), sc.cpu().numpy(), ref, FWD)
+
+
+@pytest.mark.parametrize("rows,d,dtype", RANGE)
+def test_norm_gradients_without_eps_over_its_range(rows, d, dtype):
+    torch = _torch()
+    code, kind = _kind(dtype)
+    h, dy, dh = _sized(rows, d, dtype, 1), _rows(rows, d, dtype, 2), _rows(rows, d, dtype, 3)
+    gamma = 1 + 0.1 * torch.randn(d, device="cuda")
+    n = moe.Norm(rows, d, code, 0.0)
+    ws = torch.empty(moe.moe_norm_backward_workspace_bytes(n), dtype=torch.uint8, device="cuda")
+    dx, dgamma = torch.empty_like(h), torch.empty(d, device="cuda")
+    moe.moe_norm_backward(n, dy, h, gamma, dh, dx, dgamma, ws)
+    rx, rg, bx, bg = M.norm_backward(_np(dy), _np(h), _np(gamma), _np(dh), 0.0)
+    bad = ~(np.abs(_np(dx) - rx) <= HALF[dtype] * np.abs(rx) + BWD * bx)
+    assert not bad.any(), sorted({int(i) % len(SIZES) for i in np.nonzero(bad)[0]})
+    chain = rows / 1024 + 4 + 64 + 16 + 30 + 4
+    assert (np.abs(_np(dgamma) - rg) <= chain * U * bg).all()
