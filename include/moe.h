@@ -859,7 +859,7 @@ int moe_grouped_gemm_wgrad(const moe_gemm_t* g, const void* x, const void* dy, c
  * tensors: a HOST array, read during the call only; a launch for every 70 tensors (54 with states in 8 bits).  Pointers 16-byte aligned, scales
  * 4-byte aligned; buffers of a tensor overlap neither each other (the same address twice: MOE_EINVAL) nor another tensor's.
  * MOE_EINVAL: a NULL pointer of a tensor with n > 0, n outside [0, 2^40], master != NULL beside an fp32 param, count < 0, step < 1
- * (without device_step), beta1 or beta2 outside [0, 1), eps outside [2^-126, 2^126], a value that is not finite.  MOE_EUNSUP: a dtype other than
+ * (without device_step), beta1 or beta2 outside [0, 1), eps outside [2^-126, 2^126], a value that is not finite in fp32.  MOE_EUNSUP: a dtype other than
  * named here.  Deterministic.
  */
 typedef struct {

@@ -1159,7 +1159,7 @@ int moe_adamw(const moe_adamw_t* a, const moe_adamw_tensor_t* tensors, int32_t c
   if (!a || count < 0 || (count > 0 && !tensors)) return MOE_EINVAL;
   const bool eight = a->state_dtype == MOE_MXFP8;
   if (!eight && a->state_dtype != MOE_F32) return MOE_EUNSUP;
-  if (!isfinite(a->lr) || !(a->beta1 >= 0 && a->beta1 < 1) || !(a->beta2 >= 0 && a->beta2 < 1)) return MOE_EINVAL;
+  if (!isfinite(float(a->lr)) || !(a->beta1 >= 0 && a->beta1 < 1) || !(a->beta2 >= 0 && a->beta2 < 1)) return MOE_EINVAL;
   // the step multiplies by the reciprocal of root + eps, whose instruction takes and gives normal numbers only
   if (!(float(a->eps) >= 0x1p-126f && float(a->eps) <= 0x1p126f) || (!a->device_step && a->step < 1)) return MOE_EINVAL;
   int rc;

@@ -206,3 +206,8 @@ def test_a_wgrad_workspace_for_more_rows_serves_fewer(dtype, G, K, N):
 def test_adamw_takes_an_eps_whose_reciprocal_is_a_normal_float(eps, code):
     """The step multiplies by the reciprocal of root + eps: of a subnormal eps it would be infinite, and 0 times it a NaN; of a larger one zero."""
     assert moe.moe_adamw(moe.AdamW(*dict(STEP, eps=eps).values()), [], stream=0, check=False) == code
+
+
+@pytest.mark.parametrize("lr,code", [(3e38, 0), (4e38, -1), (-4e38, -1), (1e300, -1)])
+def test_adamw_takes_a_rate_that_fp32_holds(lr, code):
+    assert moe.moe_adamw(moe.AdamW(*dict(STEP, lr=lr).values()), [], stream=0, check=False) == code
