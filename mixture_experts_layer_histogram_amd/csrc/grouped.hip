@@ -564,12 +564,26 @@ size_t wgrad_need(const moe_gemm_t& s) {
   const int64_t piece = wgrad_piece(s);
   return piece == 0 ? 0 : piece_bytes(s, most_pieces(s, piece));
 }
-// What any number of rows up to these needs: a piece has at least its share of the rows and 512 of them, and there are at least four
+// What any number of rows up to these needs, none where none of them goes in pieces.  Pieces of one length and of one number of whole ones are
+// judged at the most rows that have them, since what joining may cost grows with the rows; a piece holds its share of the rows, so that
+// there are at most wgs / matrix whole ones.  (One piece more than the most is asked for.)
 size_t wgrad_workspace(const moe_gemm_t& s) {
   const Pieces p = pieces_of(s);
   if (s.rows < 4 * 512 || join_us(s, s.groups + 4) > p.most_join) return 0;
-  const int64_t share = p.wgs / p.matrix + 1, most = (s.rows / 512 < share ? s.rows / 512 : share) + s.groups;
-  return piece_bytes(s, most < kMaxGroups ? most : kMaxGroups);
+  int64_t most = 0;
+  for (int64_t piece = 512; 4 * piece <= s.rows; piece *= 2) {
+    const int64_t fit = ((piece + 1) * p.wgs - 1) / p.matrix, top = s.rows < fit ? s.rows : fit;
+    const int64_t room = kMaxGroups - s.groups;
+    for (int64_t whole = top / piece < room ? top / piece : room; whole > most && whole >= 4; --whole) {
+      moe_gemm_t r = s;
+      r.rows = top < (whole + 1) * piece - 1 ? top : (whole + 1) * piece - 1;
+      if (wgrad_piece(r) == piece) most = whole;
+    }
+  }
+  if (most == 0) return 0;
+  const int64_t share = p.wgs / p.matrix + 1, bound = s.rows / 512 < share ? s.rows / 512 : share;
+  const int64_t pieces = (most < bound ? most + 1 : bound) + s.groups;
+  return piece_bytes(s, pieces < kMaxGroups ? pieces : kMaxGroups);
 }
 
 // By one workgroup.  first[G] is the pieces' number; where the offsets are bad, one piece with bad bounds.

@@ -211,3 +211,12 @@ def test_adamw_takes_an_eps_whose_reciprocal_is_a_normal_float(eps, code):
 @pytest.mark.parametrize("lr,code", [(3e38, 0), (4e38, -1), (-4e38, -1), (1e300, -1)])
 def test_adamw_takes_a_rate_that_fp32_holds(lr, code):
     assert moe.moe_adamw(moe.AdamW(*dict(STEP, lr=lr).values()), [], stream=0, check=False) == code
+
+
+@pytest.mark.parametrize("dtype,rows,G,K,N", [(moe.MOE_BF16, 32768, 8, 7168, 2048), (moe.MOE_BF16, 32768, 1, 8192, 8192),
+                                              (moe.MOE_BF16, 131072, 32, 7168, 2048), (moe.MOE_BF16, 16384, 8, 1024, 1024),
+                                              (moe.MOE_BF16, 262144, 1, 4096, 4096), (moe.MOE_F32, 54882, 162, 2016, 7176),
+                                              (moe.MOE_F32, 16563, 17, 7620, 2336), (moe.MOE_BF16, 1 << 30, 1024, 8, 8)])
+def test_no_workspace_where_no_rows_use_one(dtype, rows, G, K, N):
+    """Matrices of so many tiles, or with so large sums, that no number of rows up to these goes in pieces."""
+    assert moe.moe_grouped_gemm_wgrad_workspace_bytes(moe.Gemm(rows, G, K, N, dtype, 0)) == 0
