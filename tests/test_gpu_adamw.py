@@ -289,3 +289,71 @@ def test_the_smallest_and_the_largest_eps(eight, eps):
     m, v = M.moments(np.zeros(300), np.zeros(300), _np(t.grad[:300]), BETA1, BETA2)
     p, away = M.adamw(p0, m, v, LR, BETA1, BETA2, eps, 1, t.wd)
     assert (away[:200] == 0).all() and (np.abs(got - p) <= 16 * U * away + 3 * U * (np.abs(p0) + away)).all()
+
+
+def test_params_move_with_eight_bit_states_as_with_fp32_states():
+    """500 steps of the same gradients, which move a param by 500^1/2 lr (m' adds up to the gradients, over their size).  What 8 bits add, of
+    that: m's roundings have at most a variance of (|m| / 16)^2 and count ten times (1 / (1 - 0.9)), |m| is (0.1 / 1.9)^1/2 of the root:
+    10 * 0.23 / 16 = 0.144; v is off by 0.35 of itself and 0.065 on the mean at most (above), its root by half of that: 0.21.  A param that
+    stands still is off by 1, one that goes the other way by 2."""
+    torch = _torch()
+    n = 8192
+    a, b = Tensor(n, "f32", "f32", False, False, 6, zero=True), Tensor(n, "f32", "f32", False, True, 6, zero=True)
+    start = _np(a.param[:n])
+    g = torch.Generator(device="cuda").manual_seed(8)
+    for step in range(1, 501):
+        grad = torch.randn(n + 16, generator=g, device="cuda") * 1e-3
+        a.grad, b.grad = grad, grad
+        _step([a], step, 0, False, False)
+        _step([b], step, 11, True, True)
+    pa, pb = _np(a.param[:n]), _np(b.param[:n])
+    moved = np.abs(pa - start).mean()
+    assert 10 * LR < moved < 25 * LR
+    assert np.abs(pa - pb).mean() <= 0.36 * moved
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("grad", ["bf16", "f32"])
+def test_the_random_bits_of_a_bf16_param(eight, grad):
+    """A param without a master: its 16 random bits (a word of their own) are added to what bf16 cuts off.  The codes of both ends of what the
+    param's bar allows before that; most values have one."""
+    torch = _torch()
+    step, seed, n = 9, (5 << 35) + 77, 50001
+    ts = [Tensor(k, "bf16", grad, False, eight, 50 + i) for i, k in enumerate((3, n))]
+    old = [t.copy() for t in ts]
+    _step(ts, step, seed, eight, True)
+    for place, (t, o) in enumerate(zip(ts, old)):
+        k = t.n
+        if eight:
+            pad = _pad(k)
+            m = M.state_values(o.m[:pad].cpu().numpy(), o.ms[:pad // 32].cpu().numpy())[:k]
+            v = np.float32(M.state_values(o.v[:pad].cpu().numpy(), o.vs[:pad // 32].cpu().numpy())[:k]) ** 2
+        else:
+            m, v = o.m[:k].cpu().numpy(), o.v[:k].cpu().numpy()
+        m, v = M.moments(m, v, _np(o.grad[:k]), BETA1, BETA2)
+        p0 = _np(o.param[:k])
+        p, away = M.adamw(p0, m, v, LR, BETA1, BETA2, EPS, step, t.wd)
+        bar = 16 * U * away + 3 * U * (np.abs(p0) + away)
+        sure = np.abs(p) > 4 * bar
+        r16 = (M.random_bits(seed, step, place, k, 1) & np.uint64(0xFFFF)).astype(np.uint32)
+        f = np.float32
+        least = (np.nextafter(f(np.abs(p) - bar), f(0)).view(np.uint32) + r16) >> 16
+        most = (np.nextafter(f(np.abs(p) + bar), f(np.inf)).view(np.uint32) + r16) >> 16
+        got = t.param[:k].view(torch.int16).cpu().numpy().view(np.uint16).astype(np.uint32)
+        assert ((got >> 15).astype(bool) == (p < 0))[sure].all()
+        assert ((least <= (got & 0x7FFF)) & ((got & 0x7FFF) <= most))[sure].all()
+        assert sure.mean() > 0.99 and (least == most)[sure].mean() > 0.99
+
+
+def test_small_changes_of_a_bf16_param_add_up():
+    """100 changes of lr = 1e-4 (a constant gradient) to params of 1, whose bf16 neighbour below is 2^-8 away: to nearest none would stay.  Each is a
+    step with the chance 1e-4 * 2^8: 100 of them vary by 100 * 1e-4 * 2^-8, 0.0063 a value and 6.9e-5 for the mean of 8192, of which five are
+    allowed (the rest, m' / (r' + eps) and bf16's smaller steps above 1, below a thousandth of the 0.01)."""
+    torch = _torch()
+    t = Tensor(8192, "bf16", "f32", False, False, 60, wd=0.0, zero=True)
+    t.param[:] = 1.0
+    t.grad[:] = 1.0
+    for step in range(1, 101):
+        moe.moe_adamw(moe.AdamW(1e-4, BETA1, BETA2, EPS, step, moe.MOE_F32, 1, 3), [t.entry()])
+    moved = 1.0 - _np(t.param[:8192])
+    assert abs(moved.mean() - 0.01) <= 5 * 6.9e-5 + 1e-5
