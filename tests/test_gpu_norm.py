@@ -244,7 +244,7 @@ def test_dispatch_of_codes_with_no_local_pair():
 
 
 # ------------------------------------------------------------------------------------------------ the range that the header names
-SIZES = [1.0, 2e-18, 2e16, 1e-16, 3.0, 1e8, 2.0 ** -50]
+SPREAD = [1.0, 2e-18, 2e16, 1e-16, 3.0, 1e8, 2.0 ** -50]
 RANGE = [(15, 4, "f32"), (15, 8, "bf16"), (9001, 64, "f32"), (29, 512, "bf16"), (4203, 2048, "bf16"), (29, 1408, "f32"), (15, 4096, "f32"), (1100, 7168, "bf16"),
          (15, 8200, "bf16"), (15, 32768, "f32")]
 
@@ -253,7 +253,7 @@ def _sized(rows, d, dtype, seed):
     """Rows of sizes in turn, side by side in a workgroup: from the smallest whose squares fp32 holds (a mean of 4e-36, of which each value's
     2^-150 is less than 2^-31) to values of 1e17, 32768 of which add up to less than 3.4e38."""
     torch = _torch()
-    size = torch.tensor([SIZES[i % len(SIZES)] for i in range(rows)], device="cuda")
+    size = torch.tensor([SPREAD[i % len(SPREAD)] for i in range(rows)], device="cuda")
     return (_rows(rows, d, "f32", seed).clamp(-5, 5) * size[:, None]).to(_kind(dtype)[1])
 
 
@@ -270,7 +270,7 @@ def test_norm_without_eps_over_its_range(rows, d, dtype):
     s, ref, _ = M.norm(_np(x), _np(res), _np(gamma), 0.0)
     assert (np.abs(_np(h) - s) <= (HALF[dtype] + U) * np.abs(s)).all()
     bad = ~(np.abs(_np(y) - ref) <= (HALF[dtype] + FWD) * np.abs(ref))
-    assert not bad.any(), sorted({int(i) % len(SIZES) for i in np.nonzero(bad)[0]})
+    assert not bad.any(), sorted({int(i) % len(SPREAD) for i in np.nonzero(bad)[0]})
     if q is not None:
         _check_codes(q.cpu().numpy(), sc.cpu().numpy(), ref, FWD)
 
@@ -287,6 +287,55 @@ def test_norm_gradients_without_eps_over_its_range(rows, d, dtype):
     moe.moe_norm_backward(n, dy, h, gamma, dh, dx, dgamma, ws)
     rx, rg, bx, bg = M.norm_backward(_np(dy), _np(h), _np(gamma), _np(dh), 0.0)
     bad = ~(np.abs(_np(dx) - rx) <= HALF[dtype] * np.abs(rx) + BWD * bx)
-    assert not bad.any(), sorted({int(i) % len(SIZES) for i in np.nonzero(bad)[0]})
+    assert not bad.any(), sorted({int(i) % len(SPREAD) for i in np.nonzero(bad)[0]})
     chain = rows / 1024 + 4 + 64 + 16 + 30 + 4
     assert (np.abs(_np(dgamma) - rg) <= chain * U * bg).all()
+
+
+@pytest.mark.parametrize("d,dtype", [(512, "bf16"), (2048, "bf16"), (4096, "bf16"), (8192, "bf16"), (16384, "bf16"), (32768, "bf16"),
+                                     (512, "f32"), (2048, "f32"), (4096, "f32"), (8192, "f32"), (16384, "f32"), (32768, "f32")])
+def test_rows_past_the_caches(d, dtype):
+    """Rows of 256 MiB and more go past the caches: the same bits as in two calls that do not, with one, four, eight and sixteen waves a row,
+    residual, codes and dh; gamma's gradient against 64 bits."""
+    torch = _torch()
+    code, kind = _kind(dtype)
+    rows = (1 << 28) // (d * (2 if dtype == "bf16" else 4)) + 5
+    half = rows // 2
+    x, res = _rows(rows, d, dtype, 1), _rows(rows, d, dtype, 2)
+    gamma = 1 + 0.1 * torch.randn(d, device="cuda")
+
+    def forward(lo, hi):
+        k = hi - lo
+        h, y = _guarded(k, d, kind), _guarded(k, d, kind)
+        q = torch.full((k + 1, d), GUARD, dtype=torch.uint8, device="cuda")
+        sc = torch.full((k * d // 32 + 64,), GUARD, dtype=torch.uint8, device="cuda")
+        moe.moe_norm(moe.Norm(k, d, code, EPS), x[lo:hi], res[lo:hi], gamma, h, y, q, sc)
+        assert (h[k] == 7).all() and (y[k] == 7).all() and (q[k] == GUARD).all() and (sc[k * d // 32:] == GUARD).all()
+        return h[:k], y[:k], q[:k], sc[:k * d // 32].view(d // 128, k, 4).transpose(0, 1)
+
+    whole, parts = forward(0, rows), (forward(0, half), forward(half, rows))
+    for i, t in enumerate(whole):
+        assert torch.equal(t[:half], parts[0][i]) and torch.equal(t[half:], parts[1][i])
+    h = whole[0]
+    del parts, whole
+
+    def backward(lo, hi, dgamma):
+        n = moe.Norm(hi - lo, d, code, EPS)
+        ws = torch.empty(moe.moe_norm_backward_workspace_bytes(n), dtype=torch.uint8, device="cuda")
+        dx = _guarded(hi - lo, d, kind)
+        moe.moe_norm_backward(n, x[lo:hi], h[lo:hi], gamma, res[lo:hi], dx, dgamma, ws)
+        assert (dx[hi - lo] == 7).all()
+        return dx[:hi - lo]
+
+    dgamma = torch.empty(d, device="cuda")
+    dx = backward(0, rows, dgamma)
+    assert torch.equal(dx[:half], backward(0, half, None)) and torch.equal(dx[half:], backward(half, rows, None))
+    ref, mag = torch.zeros(d, dtype=torch.double, device="cuda"), torch.zeros(d, dtype=torch.double, device="cuda")
+    for lo in range(0, rows, 8192):
+        a, b = h[lo:lo + 8192].double(), x[lo:lo + 8192].double()
+        t = b * a / torch.sqrt((a * a).mean(-1, keepdim=True) + EPS)
+        ref += t.sum(0)
+        mag += t.abs().sum(0)
+    # as in test_norm_backward, of the workgroups that share the rows: 1024, 512 with eight waves a row, 256 with sixteen
+    chain = rows / (1024 if d <= 2048 else 512 if d <= 8192 else 256) + 4 + 64 + 16 + 30 + 4
+    assert ((dgamma.double() - ref).abs() <= chain * U * mag).all()
