@@ -304,3 +304,51 @@ def test_a_gradients_workspace_for_more_rows(dtype, G, K, N):
         for i in (0, G - 1):
             assert torch.equal(dw[i], x[off[i]:off[i + 1]].float().t() @ dy[off[i]:off[i + 1]].float())
         assert (ws[need:] == 0x5A).all()
+
+
+# counts of rows, the rows that the buffers have, K, N: few rows of long buffers, as a layer's own are, whose rows nobody knows on the host
+LONG = [([16] * 32, 4096, 512, 2048), ([3, 0, 2, 0, 0, 0, 1, 0], 4096, 264, 256), ([5, 0, 17], 6000, 200, 256), ([1], 20000, 1032, 40),
+        ([0] * 64, 3000, 64, 72), ([0, 2, 0, 700, 0], 9000, 64, 128), ([0] * 255 + [6000], 6001, 64, 72), ([0, 40, 0], 30000, 16, 24)]
+
+
+@pytest.mark.parametrize("counts,rows,K,N", LONG)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", [0, 1])
+def test_buffers_with_far_more_rows_than_the_groups(counts, rows, K, N, dtype, layout):
+    """What lies behind the groups is NaN in x and dy and stays in y; groups without rows get zeros."""
+    torch = _torch()
+    code, kind = _kind(dtype)
+    off, doff = _offsets(counts)
+    used = off[-1]
+    x, dy = _make((rows, K), dtype, 1, True), _make((rows, N), dtype, 2, True)
+    x[used:] = dy[used:] = float("nan")
+    w = _make((len(counts), N, K) if layout == 0 else (len(counts), K, N), dtype, 3, True)
+    y = torch.full((rows, N), 7.0, dtype=kind, device="cuda")
+    g, status = moe.Gemm(rows, len(counts), K, N, code, layout), torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    moe.moe_grouped_gemm(g, x, w, doff, y, status)
+    assert int(status) == 0 and (y[used:] == 7).all()
+    ref, _ = M.grouped(_np(x[:used]), _np(w), off, layout)
+    _close(y[:used], ref, None, K, dtype, True)
+    dw = torch.full(w.shape, 7.0, device="cuda")
+    ws = torch.empty(moe.moe_grouped_gemm_wgrad_workspace_bytes(g), dtype=torch.uint8, device="cuda")
+    moe.moe_grouped_gemm_wgrad(g, x, dy, doff, dw, moe.MOE_F32, ws, status=status)
+    ref, _ = M.grouped_wgrad(_np(x[:used]), _np(dy[:used]), off, layout)
+    assert int(status) == 0
+    _close(dw, ref, None, max(counts), "f32", True)
+
+
+@pytest.mark.parametrize("G,K,N,rows", [(53, 840, 232, (76906, 6143, 5632, 5631)), (16, 360, 1504, (21700, 4095, 3584)), (11, 896, 784, (13350, 3583, 3072))])
+def test_a_gradients_workspace_where_few_pieces_are_worth_it(G, K, N, rows):
+    """Shapes whose pieces' sums are large: the workspace of the most rows, which holds a few pieces, at the numbers of rows that take all of it."""
+    torch = _torch()
+    need = moe.moe_grouped_gemm_wgrad_workspace_bytes(moe.Gemm(rows[0], G, K, N, moe.MOE_BF16, 0))
+    ws = torch.full((need + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+    for r in rows:
+        c = [r // G] * G
+        c[-1] += r - sum(c)
+        off, doff = _offsets(c)
+        x, dy, dw = _make((r, K), "bf16", 1, True), _make((r, N), "bf16", 2, True), torch.empty(G, N, K, device="cuda")
+        moe.moe_grouped_gemm_wgrad(moe.Gemm(r, G, K, N, moe.MOE_BF16, 0), x, dy, doff, dw, moe.MOE_F32, ws, need)
+        for i in range(G):
+            assert torch.equal(dw[i], dy[off[i]:off[i + 1]].float().t() @ x[off[i]:off[i + 1]].float())
+        assert (ws[need:] == 0x5A).all()
