@@ -5,8 +5,8 @@
 //
 // Bound by bytes: 28 a value with bf16 weights, fp32 masters and fp32 states, 16.1 with states in 8 bits.  Workgroups walk
 // chunks of all tensors of a launch in turn, so small tensors share a launch with large ones; every array passes by once
-// (non-temporal).  553 M values with fp32 masters and 8-bit states 1639 us (5.5 TB/s), 549 M with fp32 states 2824 us (5.4 TB/s); 61 tensors of
-// 260000 values in all 5.6 us, a launch's submission.
+// (non-temporal).  553 M values with fp32 masters and 8-bit states 1616 us (5.5 TB/s), with fp32 states 2734 us (5.7 TB/s); 61 tensors of
+// 260000 values in all 5.8 us, a launch's submission.
 //
 // States in 8 bits are MXFP8 matrices of rows of 128 values: m, and the root of v (which halves the powers of ten that v
 // spans).  A step changes v by a thousandth, E4M3 has steps of a sixteenth: rounded to nearest, most changes would be

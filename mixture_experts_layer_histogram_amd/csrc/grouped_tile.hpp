@@ -20,8 +20,8 @@
 //
 // The loads know nothing of tiles: a cursor for A (two steps ahead) and one for B (one step) walk the list by
 // themselves, so the next tile's first panels land while this one's last products and its stores are on their way.
-// 32 groups of 7168 x 2048 (bf16): 32749 rows from 2048 values to 7168 868 us (1.1 PFLOP/s; one group of 32768 rows 729: the tiles at the
-// groups' ends), 16381 rows back to 7168 values 500, their weight gradients 545 (8 steps a tile and 128 KiB stored).  Not faster: workgroups set
+// 32 groups of 7168 x 2048 (bf16): 32749 rows from 2048 values to 7168 845 us (1.1 PFLOP/s; one group of 32768 rows 699: the tiles at the
+// groups' ends), 16381 rows back to 7168 values 497, their weight gradients 551 (8 steps a tile and 128 KiB stored); some 3 % more on other cards.  Not faster: workgroups set
 // off by parts of a tile, other places for the short tiles, bands over the longer axis in the products.
 #pragma once
 

@@ -7,7 +7,7 @@
 // Both are bound by the rows' bytes: a row is read once, stays in registers as fp32 (E values a lane, W waves a row) and is
 // written once.  A workgroup takes consecutive rows, so a lane keeps its columns: gamma is read once a workgroup, the
 // gradient of gamma adds up in registers, and the scale words of a chunk of rows leave through LDS as runs.  32768 x 7168 bf16 with residual, both
-// rows out and MXFP8: 380 us (5.6 TB/s); its gradients 347 us (5.4 TB/s); 37 x 1408 fp32 5.3 us, a launch's submission.
+// rows out and MXFP8: 379 us (5.6 TB/s); its gradients 345 us (5.4 TB/s); 37 x 1408 fp32 5.4 us, a launch's submission.
 #include <type_traits>
 
 #include "mx.hpp"

@@ -98,7 +98,8 @@ class AdamWTensor(ctypes.Structure):
 
 
 def adamw_table(tensors):
-    """The host array of moe_adamw, to keep from step to step.  It holds addresses: the tensors stay the caller's to keep."""
+    """The host array of moe_adamw, to keep from step to step.  It holds addresses: the tensors stay the caller's to keep, and where one has moved
+    (gradients that were freed between steps), table[i].grad = tensor.data_ptr() puts the new address into it."""
     tensors = list(tensors)
     return (AdamWTensor * len(tensors))(*tensors)
 

@@ -220,3 +220,12 @@ def test_adamw_takes_a_rate_that_fp32_holds(lr, code):
 def test_no_workspace_where_no_rows_use_one(dtype, rows, G, K, N):
     """Matrices of so many tiles, or with so large sums, that no number of rows up to these goes in pieces."""
     assert moe.moe_grouped_gemm_wgrad_workspace_bytes(moe.Gemm(rows, G, K, N, dtype, 0)) == 0
+
+
+def test_a_kept_table_takes_new_gradients():
+    table = moe.adamw_table([moe.AdamWTensor(**TENSOR), moe.AdamWTensor(**dict(TENSOR, n=0))])
+    step = moe.AdamW(*STEP.values())
+    table[0].grad = B + 8
+    assert moe.moe_adamw(step, table, stream=0, check=False) == -2
+    table[0].grad = A
+    assert moe.moe_adamw(step, table, stream=0, check=False) == -1 and table[0].param == A and table[0].n == 100
